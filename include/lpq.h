@@ -279,6 +279,95 @@ typedef struct {
 lpq_status lpq_gemm_ex(int32_t layout, const lpq_qview *a, const lpq_qview *b, void *c, int32_t c_is_fp32,
                        int64_t m, int64_t n, int64_t k, const lpq_gemm_opts *opts, lpq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around the linear layers: the norm in front of them, the loss
+ * behind the last one, and their product for the few tokens of decoding.
+ * Sums, row statistics and softmax statistics are held in FP32. */
+
+/* Element types of the norm's tensors. */
+typedef enum { LPQ_TYPE_BF16 = 0, LPQ_TYPE_FP32 = 1 } lpq_type;
+
+/* Layer norm of every row of x [rows, cols] (rows ldx elements apart):
+ *   mean = sum(x) / cols,  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ *   x_type       type of x and y; w_type that of weight and bias.
+ *   weight, bias [cols]; NULL weight = 1, NULL bias = 0.
+ *   y            [rows, cols], rows ldy elements apart; rounded once.
+ *   mean, rstd   [rows] FP32, what lpq_layer_norm_backward reads; either may
+ *                be NULL.
+ *   amax         one FP32, max |y| over the rounded outputs (NaN ignored,
+ *                infinities counted, 0 without rows): the value lpq_amax gives
+ *                for y, so that lpq_quantize with LPQ_GIVEN_AMAX needs no amax
+ *                pass.  NULL: not computed.
+ * Any rows >= 0, cols >= 1, ldx and ldy >= cols and eps >= 0.  Pointers need
+ * their element's alignment; 16-byte aligned rows (of x and y) of a multiple
+ * of 16 bytes, with 16-byte aligned weight and bias, take 16-byte accesses.  x
+ * and y must not overlap. */
+lpq_status lpq_layer_norm(const void *x, int64_t ldx, int32_t x_type, const void *weight, const void *bias,
+                          int32_t w_type, int64_t rows, int64_t cols, float eps, void *y, int64_t ldy, float *mean,
+                          float *rstd, float *amax, lpq_stream_t stream);
+
+/* Bytes of lpq_layer_norm_backward's workspace (16-byte aligned device
+ * memory).  Host-only. */
+lpq_status lpq_layer_norm_workspace(int64_t rows, int64_t cols, size_t *bytes);
+
+/* Backward pass of lpq_layer_norm from dy [rows, cols] and the forward's x,
+ * mean and rstd.  With xhat = (x - mean) * rstd and g = dy * weight:
+ *   dx      = rstd * (g - sum(g) / cols - xhat * sum(g * xhat) / cols)
+ *   dweight = sum over the rows of dy * xhat,  dbias = that of dy   (FP32)
+ * dx has x's type and rows lddx elements apart.  dweight and dbias may be
+ * NULL.  The sums over the rows are split into a fixed number of parts joined
+ * in a fixed order: the same inputs give the same bits.  Alignment as for
+ * lpq_layer_norm; dy, x and dx must not overlap.  0 rows give zero gradients. */
+lpq_status lpq_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t x_type,
+                                   const float *mean, const float *rstd, const void *weight, int32_t w_type,
+                                   int64_t rows, int64_t cols, void *dx, int64_t lddx, float *dweight, float *dbias,
+                                   void *workspace, size_t workspace_bytes, lpq_stream_t stream);
+
+/* Softmax cross entropy of a vocabulary projection, logits not kept.  For
+ * hidden states h [t, d] and weights w [v, d] (bf16, rows ldh / ldw elements
+ * apart) and the logits l = h w^T (FP32):
+ *   lse[i]  = log(sum_j exp(l[i, j])),   loss[i] = lse[i] - l[i, labels[i]].
+ * labels [t] are int64; a label outside 0 .. v - 1 (-100, say) marks a row
+ * without target: its loss is 0 and its gradients vanish, its lse is computed.
+ * Any t >= 0, v >= 1; d >= 8 a multiple of 8; ldh and ldw >= d multiples of 8;
+ * h, w and the workspace 16-byte aligned.  A row whose logits hold a NaN has
+ * lse NaN; one with a +infinity has lse +infinity. */
+lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels, int64_t t,
+                         int64_t v, int64_t d, float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                         lpq_stream_t stream);
+
+/* Gradients of sum_i dloss[i] * loss[i]: with the forward's lse and
+ *   dl[i, j] = dloss[i] * (exp(l[i, j] - lse[i]) - (j == labels[i]))
+ * (0 in rows without target, whatever their dloss and lse hold)
+ *   dh [t, d] = dl w,   dw [v, d] = dl^T h,
+ * contiguous, bf16 (grads_fp32 = 0) or FP32.  The logits are computed again,
+ * vocab_piece words at a time (0: the library's choice; else a positive
+ * multiple of 64), so that only t * vocab_piece values of dl exist at once.
+ * They are divided by max |dloss| and rounded to bf16, which the tensor cores
+ * read; all sums are FP32 and the factor is put back before the final
+ * rounding.  The same inputs give the same bits.  0 rows give dw = 0. */
+lpq_status lpq_linear_ce_backward(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels,
+                                  const float *lse, const float *dloss, int64_t t, int64_t v, int64_t d, void *dh,
+                                  void *dw, int32_t grads_fp32, int64_t vocab_piece, void *workspace,
+                                  size_t workspace_bytes, lpq_stream_t stream);
+
+/* Workspace bytes of lpq_linear_ce (backward = 0) and lpq_linear_ce_backward
+ * (backward = 1, with the same vocab_piece).  Host-only. */
+lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t backward, int64_t vocab_piece,
+                                   size_t *bytes);
+
+/* y[i, n] = sum_k x[i, k] * deq(w)[n, k] for a few tokens i on 4-bit weights:
+ * w is a row-wise copy [n, k] of NVFP4, NVFP4_2D or MXFP4 as lpq_quantize
+ * writes it (either scale layout; codes 16-byte aligned, scales 4-byte
+ * aligned), x [m, k] is bf16 and not quantized (rows ldx elements apart, ldx
+ * a multiple of 8, 16-byte aligned), y [m, n] contiguous bf16 or FP32.  Codes
+ * times scales are exact, products are summed in FP32 and the tensor scale is
+ * applied to the sum.  k must be a multiple of 32; m and n are arbitrary
+ * (>= 0), but m is meant to be small: the weights are read once per 8 tokens. */
+lpq_status lpq_matvec(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,
+                      lpq_stream_t stream);
+
 /* Transformer configuration ([TE] "model configuration and training input"). */
 typedef struct {
   int64_t hidden, intermediate, heads, layers, micro_batch, seq;

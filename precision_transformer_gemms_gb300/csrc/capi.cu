@@ -327,6 +327,187 @@ lpq_status lpq_gemm_ex(int32_t layout, const lpq_qview* a, const lpq_qview* b, v
   return launch_gemm(a, b, c, c_is_fp32, m, n, k, opts, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+bool valid_type(int32_t t) { return t == LPQ_TYPE_BF16 || t == LPQ_TYPE_FP32; }
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+uintptr_t type_bytes(int32_t t) { return t == LPQ_TYPE_FP32 ? 4 : 2; }
+
+// What both directions of the norm check.
+lpq_status check_norm(int32_t x_type, int32_t w_type, int64_t rows, int64_t cols) {
+  if (!valid_type(x_type)) return set_error(LPQ_ERR_INVALID_ARG, "x_type %d", x_type);
+  if (!valid_type(w_type)) return set_error(LPQ_ERR_INVALID_ARG, "w_type %d", w_type);
+  if (rows < 0 || cols < 1) return set_error(LPQ_ERR_SHAPE, "layer norm of %lld x %lld", (long long)rows, (long long)cols);
+  if (cols > (int64_t)1 << 30 || rows > (int64_t)1 << 40) return set_error(LPQ_ERR_SHAPE, "layer norm: too large");
+  return LPQ_OK;
+}
+lpq_status check_matrix(const void* p, const char* name, int64_t ld, int64_t rows, int64_t cols, uintptr_t elem) {
+  if (ld < cols) return set_error(LPQ_ERR_SHAPE, "%s: leading dimension %lld below %lld", name, (long long)ld, (long long)cols);
+  if (rows > 0 && !p) return set_error(LPQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned_to(p, elem)) return set_error(LPQ_ERR_ALIGN, "%s not aligned to its elements", name);
+  return LPQ_OK;
+}
+
+// What both directions of the vocabulary loss check.
+lpq_status check_ce_shape(int64_t t, int64_t v, int64_t d) {
+  if (t < 0 || v < 1) return set_error(LPQ_ERR_SHAPE, "t %lld, v %lld", (long long)t, (long long)v);
+  if (d < 8 || d % 8) return set_error(LPQ_ERR_SHAPE, "d %lld not a positive multiple of 8", (long long)d);
+  const int64_t most = (int64_t)1 << 30;
+  if (t > most || v > most || d > most) return set_error(LPQ_ERR_SHAPE, "dimension beyond 2^30");
+  return LPQ_OK;
+}
+lpq_status check_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* labels, int64_t t,
+                    int64_t v, int64_t d) {
+  lpq_status st = check_ce_shape(t, v, d);
+  if (st != LPQ_OK) return st;
+  if (ldh < d || ldw < d || ldh % 8 || ldw % 8)
+    return set_error(LPQ_ERR_SHAPE, "ldh %lld and ldw %lld must be multiples of 8, at least d = %lld", (long long)ldh,
+                     (long long)ldw, (long long)d);
+  if (ldh > (int64_t)1 << 38 || ldw > (int64_t)1 << 38) return set_error(LPQ_ERR_SHAPE, "leading dimension beyond 2^38");
+  if ((t > 0 && (!h || !labels)) || !w) return set_error(LPQ_ERR_INVALID_ARG, "h, w or labels is NULL");
+  if (!aligned16(h) || !aligned16(w)) return set_error(LPQ_ERR_ALIGN, "h or w not 16-byte aligned");
+  if (!aligned_to(labels, 8)) return set_error(LPQ_ERR_ALIGN, "labels not 8-byte aligned");
+  return LPQ_OK;
+}
+lpq_status check_piece(int64_t piece) {
+  if (piece < 0 || piece % 64) return set_error(LPQ_ERR_SHAPE, "vocab_piece %lld not a multiple of 64", (long long)piece);
+  return LPQ_OK;
+}
+lpq_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (have < need) return set_error(LPQ_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", have, need);
+  if (need > 0 && !ws) return set_error(LPQ_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned16(ws)) return set_error(LPQ_ERR_ALIGN, "workspace not 16-byte aligned");
+  return LPQ_OK;
+}
+}  // namespace
+
+lpq_status lpq_layer_norm(const void* x, int64_t ldx, int32_t x_type, const void* weight, const void* bias,
+                          int32_t w_type, int64_t rows, int64_t cols, float eps, void* y, int64_t ldy, float* mean,
+                          float* rstd, float* amax, lpq_stream_t stream) {
+  lpq_status st = check_norm(x_type, w_type, rows, cols);
+  if (st != LPQ_OK) return st;
+  if (!(eps >= 0.f)) return set_error(LPQ_ERR_INVALID_ARG, "eps must be at least 0");
+  if ((st = check_matrix(x, "x", ldx, rows, cols, type_bytes(x_type))) != LPQ_OK) return st;
+  if ((st = check_matrix(y, "y", ldy, rows, cols, type_bytes(x_type))) != LPQ_OK) return st;
+  if (!aligned_to(weight, type_bytes(w_type)) || !aligned_to(bias, type_bytes(w_type)))
+    return set_error(LPQ_ERR_ALIGN, "weight or bias not aligned to its elements");
+  if (!aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(amax, 4))
+    return set_error(LPQ_ERR_ALIGN, "mean, rstd or amax not 4-byte aligned");
+  if ((st = check_arch()) != LPQ_OK) return st;
+  NormArgs a{};
+  a.x = x; a.ldx = ldx; a.weight = weight; a.bias = bias; a.rows = rows; a.cols = cols; a.eps = eps;
+  a.out = y; a.ldo = ldy; a.mean = mean; a.rstd = rstd; a.amax = amax;
+  return launch_norm(a, x_type, w_type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_layer_norm_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return set_error(LPQ_ERR_INVALID_ARG, "NULL output pointer");
+  lpq_status st = check_norm(LPQ_TYPE_BF16, LPQ_TYPE_BF16, rows, cols);
+  if (st != LPQ_OK) return st;
+  *bytes = (size_t)norm_parts(rows, cols) * 2 * (size_t)cols * sizeof(float);
+  return LPQ_OK;
+}
+
+lpq_status lpq_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int32_t x_type,
+                                   const float* mean, const float* rstd, const void* weight, int32_t w_type,
+                                   int64_t rows, int64_t cols, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                   void* workspace, size_t workspace_bytes, lpq_stream_t stream) {
+  size_t need = 0;
+  lpq_status st = check_norm(x_type, w_type, rows, cols);
+  if (st != LPQ_OK) return st;
+  if ((st = check_matrix(dy, "dy", lddy, rows, cols, type_bytes(x_type))) != LPQ_OK) return st;
+  if ((st = check_matrix(x, "x", ldx, rows, cols, type_bytes(x_type))) != LPQ_OK) return st;
+  if ((st = check_matrix(dx, "dx", lddx, rows, cols, type_bytes(x_type))) != LPQ_OK) return st;
+  if (rows > 0 && (!mean || !rstd)) return set_error(LPQ_ERR_INVALID_ARG, "mean or rstd is NULL");
+  if (!aligned_to(weight, type_bytes(w_type))) return set_error(LPQ_ERR_ALIGN, "weight not aligned to its elements");
+  if (!aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dweight, 4) || !aligned_to(dbias, 4))
+    return set_error(LPQ_ERR_ALIGN, "mean, rstd, dweight or dbias not 4-byte aligned");
+  if ((st = lpq_layer_norm_workspace(rows, cols, &need)) != LPQ_OK) return st;
+  if (dweight || dbias)
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  NormArgs a{};
+  a.dy = dy; a.lddy = lddy; a.x = x; a.ldx = ldx; a.weight = weight; a.rows = rows; a.cols = cols;
+  a.mean_in = mean; a.rstd_in = rstd; a.out = dx; a.ldo = lddx; a.dweight = dweight; a.dbias = dbias;
+  a.parts = static_cast<float*>(workspace);
+  return launch_norm_backward(a, x_type, w_type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t backward, int64_t vocab_piece,
+                                   size_t* bytes) {
+  if (!bytes) return set_error(LPQ_ERR_INVALID_ARG, "NULL output pointer");
+  lpq_status st = check_ce_shape(t, v, d);
+  if (st != LPQ_OK) return st;
+  if ((st = check_piece(vocab_piece)) != LPQ_OK) return st;
+  *bytes = ce_workspace(t, v, d, backward != 0, vocab_piece);
+  return LPQ_OK;
+}
+
+lpq_status lpq_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* labels, int64_t t,
+                         int64_t v, int64_t d, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                         lpq_stream_t stream) {
+  lpq_status st = check_ce(h, ldh, w, ldw, labels, t, v, d);
+  if (st != LPQ_OK) return st;
+  if (t > 0 && (!loss || !lse)) return set_error(LPQ_ERR_INVALID_ARG, "loss or lse is NULL");
+  if (!aligned_to(loss, 4) || !aligned_to(lse, 4)) return set_error(LPQ_ERR_ALIGN, "loss or lse not 4-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, false, 0))) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  CeArgs a{};
+  a.h = h; a.w = w; a.labels = labels; a.ldh = ldh; a.ldw = ldw; a.t = t; a.v = v; a.d = d;
+  a.loss = loss; a.lse_out = lse; a.workspace = static_cast<uint8_t*>(workspace);
+  return launch_ce(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_linear_ce_backward(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* labels,
+                                  const float* lse, const float* dloss, int64_t t, int64_t v, int64_t d, void* dh,
+                                  void* dw, int32_t grads_fp32, int64_t vocab_piece, void* workspace,
+                                  size_t workspace_bytes, lpq_stream_t stream) {
+  lpq_status st = check_ce(h, ldh, w, ldw, labels, t, v, d);
+  if (st != LPQ_OK) return st;
+  if ((st = check_piece(vocab_piece)) != LPQ_OK) return st;
+  if (grads_fp32 < 0 || grads_fp32 > 1) return set_error(LPQ_ERR_INVALID_ARG, "grads_fp32 %d", grads_fp32);
+  if ((t > 0 && (!lse || !dloss || !dh)) || !dw) return set_error(LPQ_ERR_INVALID_ARG, "lse, dloss, dh or dw is NULL");
+  if (!aligned_to(lse, 4) || !aligned_to(dloss, 4)) return set_error(LPQ_ERR_ALIGN, "lse or dloss not 4-byte aligned");
+  if (!aligned16(dh) || !aligned16(dw)) return set_error(LPQ_ERR_ALIGN, "dh or dw not 16-byte aligned");
+  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, true, vocab_piece))) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  CeArgs a{};
+  a.h = h; a.w = w; a.labels = labels; a.ldh = ldh; a.ldw = ldw; a.t = t; a.v = v; a.d = d;
+  a.lse = lse; a.dloss = dloss; a.dh = dh; a.dw = dw; a.grads_fp32 = grads_fp32; a.piece = vocab_piece;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  return launch_ce_backward(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
+                      lpq_stream_t stream) {
+  if (!w) return set_error(LPQ_ERR_INVALID_ARG, "w is NULL");
+  if (!(is_nvfp4(w->fmt) || w->fmt == LPQ_MXFP4))
+    return set_error(LPQ_ERR_UNSUPPORTED, "lpq_matvec reads NVFP4, NVFP4_2D and MXFP4 weights, not format %d", w->fmt);
+  if (w->colwise) return set_error(LPQ_ERR_INVALID_ARG, "lpq_matvec reads a row-wise copy");
+  if (w->sf_layout != LPQ_SF_PLAIN && w->sf_layout != LPQ_SF_GEMM)
+    return set_error(LPQ_ERR_INVALID_ARG, "w.sf_layout %d", w->sf_layout);
+  if (y_is_fp32 < 0 || y_is_fp32 > 1) return set_error(LPQ_ERR_INVALID_ARG, "y_is_fp32 %d", y_is_fp32);
+  if (m < 0 || w->rows < 0 || w->cols < 0) return set_error(LPQ_ERR_SHAPE, "negative dimension");
+  if (w->cols % 32) return set_error(LPQ_ERR_SHAPE, "k %lld not a multiple of 32", (long long)w->cols);
+  if (w->rows > (int64_t)1 << 30 || w->cols > (int64_t)1 << 30 || m > (int64_t)1 << 30)
+    return set_error(LPQ_ERR_SHAPE, "dimension beyond 2^30");
+  if (m > 0 && w->cols > 0 && (ldx < w->cols || ldx % 8))
+    return set_error(LPQ_ERR_SHAPE, "ldx %lld must be a multiple of 8, at least k = %lld", (long long)ldx, (long long)w->cols);
+  if (m > 0 && w->rows > 0) {
+    if (!y) return set_error(LPQ_ERR_INVALID_ARG, "y is NULL");
+    if (!aligned16(y)) return set_error(LPQ_ERR_ALIGN, "y not 16-byte aligned");
+    if (w->cols > 0) {
+      if (!x || !w->codes || !w->scales) return set_error(LPQ_ERR_INVALID_ARG, "x, w.codes or w.scales is NULL");
+      if (is_nvfp4(w->fmt) && !w->tensor_scale) return set_error(LPQ_ERR_INVALID_ARG, "w.tensor_scale is NULL");
+      if (!aligned16(x) || !aligned16(w->codes)) return set_error(LPQ_ERR_ALIGN, "x or w.codes not 16-byte aligned");
+      if (!aligned_to(w->scales, 4) || !aligned_to(w->tensor_scale, 4))
+        return set_error(LPQ_ERR_ALIGN, "w.scales or w.tensor_scale not 4-byte aligned");
+    }
+  }
+  lpq_status st = check_arch();
+  if (st != LPQ_OK) return st;
+  return launch_matvec(w, x, ldx, m, y, y_is_fp32, reinterpret_cast<cudaStream_t>(stream));
+}
+
 lpq_status lpq_layer_shapes(const lpq_transformer_cfg* cfg, lpq_gemm_shape out[12], int32_t* count) {
   if (!cfg || !out || !count) return set_error(LPQ_ERR_INVALID_ARG, "NULL argument");
   if (cfg->hidden <= 0 || cfg->intermediate <= 0 || cfg->micro_batch <= 0 || cfg->seq <= 0)

@@ -54,6 +54,54 @@ lpq_status launch_scale_update(const lpq_delayed_state* state, const float* amax
 lpq_status launch_gemm(const lpq_qview* a, const lpq_qview* b, void* c, int32_t c_is_fp32, int64_t m,
                        int64_t n, int64_t k, const lpq_gemm_opts* opts, cudaStream_t stream);
 
+// Layer norm launchers (norm.cu).  Arguments validated.
+struct NormArgs {
+  const void* x;
+  const void* weight;  // may be NULL
+  const void* bias;    // may be NULL (forward only)
+  const void* dy;      // backward only
+  void* out;           // y or dx
+  int64_t ldx, ldo, lddy;
+  int64_t rows, cols;
+  float eps;
+  const float* mean_in;  // backward
+  const float* rstd_in;
+  float* mean;  // forward; may be NULL
+  float* rstd;
+  float* amax;     // forward; may be NULL
+  float* dweight;  // backward; may be NULL
+  float* dbias;
+  float* parts;  // backward workspace
+};
+int64_t norm_parts(int64_t rows, int64_t cols);  // row parts of the parameter gradients' partial sums
+lpq_status launch_norm(const NormArgs& a, int32_t x_type, int32_t w_type, cudaStream_t stream);
+lpq_status launch_norm_backward(const NormArgs& a, int32_t x_type, int32_t w_type, cudaStream_t stream);
+
+// Vocabulary cross-entropy launchers (loss.cu).  Arguments validated.
+struct CeArgs {
+  const void* h;
+  const void* w;
+  const int64_t* labels;
+  int64_t ldh, ldw;
+  int64_t t, v, d;
+  float* loss;  // forward
+  float* lse_out;
+  const float* lse;  // backward
+  const float* dloss;
+  void* dh;
+  void* dw;
+  int32_t grads_fp32;
+  int64_t piece;  // backward: words per piece, 0 = choose
+  uint8_t* workspace;
+};
+size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece);
+lpq_status launch_ce(const CeArgs& a, cudaStream_t stream);
+lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t stream);
+
+// 4-bit matrix-vector launcher (matvec.cu).  Arguments validated.
+lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
+                         cudaStream_t stream);
+
 // Device error word (gemm.cu owns it).
 lpq_status read_and_clear_device_error(cudaStream_t stream, int32_t* code);
 lpq_status launch_selftest_wait(uint64_t limit_ns, cudaStream_t stream);

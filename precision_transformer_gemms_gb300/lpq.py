@@ -20,6 +20,7 @@ SCALING_CURRENT, SCALING_DELAYED = 0, 1
 ROWWISE, COLWISE, RHT_COLWISE, STOCHASTIC, GIVEN_AMAX = 1, 2, 4, 8, 16
 SF_PLAIN, SF_GEMM = 0, 1
 FPROP, DGRAD, WGRAD = 0, 1, 2
+TYPE_BF16, TYPE_FP32 = 0, 1
 
 STATUS_NAMES = {OK: "OK", ERR_INVALID_ARG: "INVALID_ARG", ERR_SHAPE: "SHAPE", ERR_ALIGN: "ALIGN",
                 ERR_UNSUPPORTED: "UNSUPPORTED", ERR_ARCH: "ARCH", ERR_CUDA: "CUDA", ERR_TIMEOUT: "TIMEOUT"}
@@ -104,6 +105,14 @@ def lib():
         L.lpq_gemm.argtypes = [I32, ctypes.POINTER(QView), ctypes.POINTER(QView), P, I32, I64, I64, I64, P]
         L.lpq_gemm_ex.argtypes = [I32, ctypes.POINTER(QView), ctypes.POINTER(QView), P, I32, I64, I64, I64,
                                   ctypes.POINTER(GemmOpts), P]
+        SZ, PSZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        L.lpq_layer_norm.argtypes = [P, I64, I32, P, P, I32, I64, I64, F, P, I64, P, P, P, P]
+        L.lpq_layer_norm_workspace.argtypes = [I64, I64, PSZ]
+        L.lpq_layer_norm_backward.argtypes = [P, I64, P, I64, I32, P, P, P, I32, I64, I64, P, I64, P, P, P, SZ, P]
+        L.lpq_linear_ce_workspace.argtypes = [I64, I64, I64, I32, I64, PSZ]
+        L.lpq_linear_ce.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, SZ, P]
+        L.lpq_linear_ce_backward.argtypes = [P, I64, P, I64, P, P, P, I64, I64, I64, P, P, I32, I64, P, SZ, P]
+        L.lpq_matvec.argtypes = [ctypes.POINTER(QView), P, I64, I64, P, I32, P]
         L.lpq_layer_shapes.argtypes = [ctypes.POINTER(TransformerCfg), ctypes.POINTER(GemmShape),
                                        ctypes.POINTER(I32)]
         L.lpq_last_error.restype = ctypes.c_char_p
@@ -113,7 +122,9 @@ def lib():
         L.lpq_selftest_arith.argtypes = [I32, U64, U64, U32, P, P]
         L.lpq_version.restype = I32
         for name in ("lpq_copy_bytes", "lpq_quantize", "lpq_scale_update", "lpq_gemm", "lpq_gemm_ex", "lpq_amax", "lpq_layer_shapes",
-                     "lpq_device_status", "lpq_selftest_wait", "lpq_mma_peak", "lpq_selftest_arith"):
+                     "lpq_device_status", "lpq_selftest_wait", "lpq_mma_peak", "lpq_selftest_arith", "lpq_layer_norm",
+                     "lpq_layer_norm_workspace", "lpq_layer_norm_backward", "lpq_linear_ce_workspace", "lpq_linear_ce",
+                     "lpq_linear_ce_backward", "lpq_matvec"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -184,6 +195,14 @@ class Copy:
         c = cls.__new__(cls)
         c.fmt, c.rows, c.cols, c.colwise, c.sf_layout = BF16, x.shape[0], x.shape[1], int(colwise), SF_PLAIN
         c.codes, c.scales, c.tensor_scale, c.amax = x.contiguous(), None, None, None
+        return c
+
+    @classmethod
+    def of_parts(cls, fmt, rows, cols, codes, scales, tensor_scale=None, sf_layout=SF_GEMM, colwise=False):
+        """Wraps existing codes (uint8), block scales and tensor scale as a copy, e.g. from a checkpoint."""
+        c = cls.__new__(cls)
+        c.fmt, c.rows, c.cols, c.colwise, c.sf_layout = fmt, rows, cols, int(colwise), sf_layout
+        c.codes, c.scales, c.tensor_scale, c.amax = codes, scales, tensor_scale, None
         return c
 
     def view(self):
@@ -271,6 +290,141 @@ def gemm(layout, a, b, c=None, out_fp32=False, stream=None, path=None):
         _check(lib().lpq_gemm_ex(layout, ctypes.byref(va), ctypes.byref(vb), _ptr(c), int(out_fp32), m, n, k,
                                  ctypes.byref(opts), _stream(stream)))
     return c
+
+
+# ----------------------------------------------------------------- around the linear layers
+_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
+
+
+def _new(stream, shape, dtype, device):
+    """A device buffer the call writes: on a stream other than the current one
+    its memory is not reused before that stream is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _rows(x, name):
+    """Checks a [rows, cols] matrix with contiguous rows and returns its leading dimension."""
+    assert x.is_cuda and x.dim() == 2, f"{name} must be a CUDA matrix"
+    assert x.shape[1] <= 1 or x.stride(1) == 1, f"{name} must have contiguous rows"
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]  # the library refuses rows that overlap
+
+
+def _vector(v, n, name, dtype=None):
+    assert v.is_cuda and v.is_contiguous() and v.numel() == n, f"{name} must be a contiguous CUDA vector of {n}"
+    assert dtype is None or v.dtype == dtype, f"{name} must be {dtype}"
+
+
+def _norm_params(x, weight, bias):
+    assert x.dtype in _TYPES, "layer norm runs on bf16 and fp32"
+    w_type = TYPE_FP32
+    for name, v in (("weight", weight), ("bias", bias)):
+        if v is not None:
+            _vector(v, x.shape[1], name)
+            assert v.dtype in _TYPES, f"{name} must be bf16 or fp32"
+            w_type = _TYPES[v.dtype]
+    assert weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias must have one type"
+    return w_type
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, amax=None, out=None, stream=None):
+    """lpq_layer_norm on a bf16 or fp32 CUDA tensor x [rows, cols]: returns
+    (y, mean, rstd).  `amax` (one FP32, optional) receives max |y|, ready for
+    quantize(..., lpq.GIVEN_AMAX)."""
+    ldx = _rows(x, "x")
+    w_type = _norm_params(x, weight, bias)
+    rows, cols = x.shape
+    if out is None:
+        out = _new(stream, (rows, cols), x.dtype, x.device)
+    assert out.dtype == x.dtype and out.shape == x.shape
+    if amax is not None:
+        _vector(amax, 1, "amax", torch.float32)
+    stats = _new(stream, (2, rows), torch.float32, x.device)
+    mean, rstd = stats[0], stats[1]
+    _check(lib().lpq_layer_norm(x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(weight), _ptr(bias), w_type, rows, cols, eps,
+                                out.data_ptr(), _rows(out, "out"), mean.data_ptr(), rstd.data_ptr(), _ptr(amax),
+                                _stream(stream)))
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, param_grads=True, stream=None):
+    """lpq_layer_norm_backward: returns (dx, dweight, dbias); the parameter
+    gradients are FP32 (None, None without `param_grads`)."""
+    assert dy.shape == x.shape and dy.dtype == x.dtype, "dy must be like x"
+    lddy, ldx = _rows(dy, "dy"), _rows(x, "x")
+    w_type = _norm_params(x, weight, None)
+    rows, cols = x.shape
+    _vector(mean, rows, "mean", torch.float32)
+    _vector(rstd, rows, "rstd", torch.float32)
+    dx = _new(stream, (rows, cols), x.dtype, x.device)
+    dweight = dbias = ws = None
+    need = 0
+    if param_grads:
+        n = ctypes.c_size_t()
+        _check(lib().lpq_layer_norm_workspace(rows, cols, ctypes.byref(n)))
+        need = n.value
+        dweight, dbias = _new(stream, (2, cols), torch.float32, x.device).unbind(0)
+        ws = _new(stream, need, torch.uint8, x.device)
+    _check(lib().lpq_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, _TYPES[x.dtype], mean.data_ptr(),
+                                         rstd.data_ptr(), _ptr(weight), w_type, rows, cols, dx.data_ptr(), cols,
+                                         _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream(stream)))
+    return dx, dweight, dbias
+
+
+def _ce_args(h, w, labels):
+    assert h.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, "h and w must be bf16"
+    ldh, ldw = _rows(h, "h"), _rows(w, "w")
+    assert h.shape[1] == w.shape[1], "h and w must have the same number of columns"
+    _vector(labels, h.shape[0], "labels", torch.int64)
+    return ldh, ldw
+
+
+def _ce_workspace(t, v, d, backward, piece, stream, device):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_linear_ce_workspace(t, v, d, backward, piece, ctypes.byref(n)))
+    return _new(stream, n.value, torch.uint8, device), n.value
+
+
+def linear_cross_entropy(h, w, labels, stream=None):
+    """lpq_linear_ce: the softmax cross entropy of the logits h w^T for hidden
+    states h [t, d] and vocabulary weights w [v, d] (bf16) against labels [t]
+    (int64; outside 0 .. v - 1: no target, loss 0).  Returns (loss, lse) [t] FP32."""
+    ldh, ldw = _ce_args(h, w, labels)
+    (t, d), v = h.shape, w.shape[0]
+    loss, lse = _new(stream, (2, t), torch.float32, h.device).unbind(0)
+    ws, need = _ce_workspace(t, v, d, 0, 0, stream, h.device)
+    _check(lib().lpq_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), t, v, d, loss.data_ptr(),
+                               lse.data_ptr(), ws.data_ptr(), need, _stream(stream)))
+    return loss, lse
+
+
+def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, vocab_piece=0, stream=None):
+    """lpq_linear_ce_backward: the gradients (dh [t, d], dw [v, d]) of
+    sum(dloss * loss) for dloss [t] FP32 and the forward's lse."""
+    ldh, ldw = _ce_args(h, w, labels)
+    (t, d), v = h.shape, w.shape[0]
+    _vector(lse, t, "lse", torch.float32)
+    _vector(dloss, t, "dloss", torch.float32)
+    dtype = torch.float32 if out_fp32 else torch.bfloat16
+    dh, dw = _new(stream, (t, d), dtype, h.device), _new(stream, (v, d), dtype, h.device)
+    ws, need = _ce_workspace(t, v, d, 1, vocab_piece, stream, h.device)
+    _check(lib().lpq_linear_ce_backward(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
+                                        dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32),
+                                        vocab_piece, ws.data_ptr(), need, _stream(stream)))
+    return dh, dw
+
+
+def matvec(x, w, out_fp32=False, stream=None):
+    """lpq_matvec: x [m, k] bf16 (a few tokens, not quantized) times the 4-bit
+    weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n]."""
+    ldx = _rows(x, "x")
+    assert x.dtype == torch.bfloat16 and x.shape[1] == w.cols, "x must be bf16 [m, k]"
+    m = x.shape[0]
+    y = _new(stream, (m, w.rows), torch.float32 if out_fp32 else torch.bfloat16, x.device)
+    _check(lib().lpq_matvec(ctypes.byref(w.view()), x.data_ptr(), ldx, m, y.data_ptr(), int(out_fp32), _stream(stream)))
+    return y
 
 
 def device_status(stream=None):
