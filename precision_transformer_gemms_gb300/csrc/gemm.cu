@@ -442,6 +442,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // 2D map over a row-major [rows, inner] matrix whose rows are `row_bytes`
 // apart; box = box_inner x box_rows, 128-byte swizzle, zero fill outside.
 lpq_status make_map(CUtensorMap* map, const void* base, bool bf16, int64_t inner, int64_t rows, int64_t row_bytes,
@@ -458,6 +460,8 @@ lpq_status make_map(CUtensorMap* map, const void* base, bool bf16, int64_t inner
   if (r != CUDA_SUCCESS) return set_error(LPQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return LPQ_OK;
 }
+
+namespace {
 
 // Instruction descriptors (tcgen05): D format F32 in bits 4-5 (dense kinds),
 // A/B formats in 7-9 / 10-12, K-major A and B (bits 15, 16 clear), N >> 3 in
@@ -1678,6 +1682,27 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns) {
 lpq_status launch_selftest_wait(uint64_t limit_ns, cudaStream_t s) {
   selftest_wait_kernel<<<1, 32, 0, s>>>(limit_ns);
   return cuda_check(cudaGetLastError(), "selftest kernel launch");
+}
+
+lpq_status device_error_word(int** word) {
+  static std::mutex mu;
+  static int* known[256] = {};  // per device
+  int dev = 0;
+  lpq_status st = cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != LPQ_OK) return st;
+  std::lock_guard<std::mutex> lock(mu);
+  const bool keep = dev >= 0 && dev < 256;
+  if (!keep || !known[dev]) {
+    void* p = nullptr;
+    if ((st = cuda_check(cudaGetSymbolAddress(&p, g_device_error), "cudaGetSymbolAddress")) != LPQ_OK) return st;
+    if (!keep) {
+      *word = static_cast<int*>(p);
+      return LPQ_OK;
+    }
+    known[dev] = static_cast<int*>(p);
+  }
+  *word = known[dev];
+  return LPQ_OK;
 }
 
 lpq_status read_and_clear_device_error(cudaStream_t s, int32_t* code) {

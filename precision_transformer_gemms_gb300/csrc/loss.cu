@@ -1,17 +1,23 @@
 // Softmax cross entropy of a vocabulary projection and its gradients on
 // sm_103a.  The logits l = h w^T exist tile by tile only:
 //
-//   forward   each tile leaves every row's maximum m and sum of exp(l - m);
-//             a second kernel joins them: lse = log sum_j exp(l_j),
-//             loss = lse - l[label].
+//   forward   each tile leaves, for every row, the maximum m and the sum of
+//             exp(l - m) over its columns; a second kernel joins them:
+//             lse = log sum_j exp(l_j), loss = lse - l[label].
 //   backward  per piece of the vocabulary the logits are computed again and
 //             turned into dl = (exp(l - lse) - onehot) dloss in bf16; then
 //             dh += dl w (FP32 sums across pieces) and dw = dl^T h.
+//
+// All four products run on one kernel: a CTA pair (cta_group::2) per 256 x 256
+// output tile, operands staged by TMA (128-byte swizzle), FP32 accumulators in
+// TMEM.  The operand that a product sums along its rows (w in dl w; dl and h
+// in dl^T h) is read as it lies, as an MN-major operand: no transposed copies.
 //
 // dl is divided by s = max |dloss| before its rounding to bf16 (what the
 // tensor cores read) and s multiplies the FP32 sums: with equal dloss, the
 // mean over the tokens say, the entry p - 1 of a label is then rounded as it
 // is instead of after a product with 1 / t.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -21,117 +27,402 @@
 namespace lpq {
 namespace {
 
-constexpr int kTile = 64, kTileK = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLog2e = 1.4426950408889634f;
 
-enum { kStats, kDlogits, kDh, kDw };
+constexpr int kTile = 256;   // rows and columns of an output tile (one CTA pair)
+constexpr int kHalf = 128;   // of each operand and of the rows, per CTA
+constexpr int kStepK = 64;   // one 128-byte swizzle row of bf16
+constexpr int kGroupM = 16;  // tiles along M that share a band of B tiles (L2 reuse)
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kOperand = kHalf * kStepK * 2;  // bytes of one operand per CTA and step
+constexpr int kStgWarp = 32 * 128;            // epilogue staging: 32 rows x 64 bf16 per warp
+constexpr int kStg = kEpiWarps * kStgWarp;
+constexpr int kStages = (232448 - 2048 - 512 - kStg) / (2 * kOperand);
+constexpr int kSmem = kStages * 2 * kOperand + 2048 + 512 + kStg;
+constexpr int kNacc = 2;  // accumulators: one tile's epilogue under the next tile's products
+static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budgets");
+
+// What the epilogue makes of a tile.
+//   kStats    row maxima and sums of exponentials of the logits
+//   kDlogits  dl in bf16
+//   kPart     FP32 partial sums of dh (one slab per split of K), added to across pieces
+//   kOut      a finished gradient: times the scale, bf16 or FP32
+enum { kStats, kDlogits, kPart, kOut };
 
 struct CeTile {
-  const __nv_bfloat16* a;  // element (i, k) at a[i * ai + k * ak]
-  const __nv_bfloat16* b;  // element (j, k) at b[j * bj + k * bk]
-  int64_t ai, ak, bj, bk;
-  int64_t M, N, K;
-  int64_t col0;  // first word of the piece
+  int64_t M, N;
+  int num_k;  // steps of kStepK along K
+  int tiles_m, tiles_n, splits;
+  uint32_t idesc;
+  int* err;
   const int64_t* labels;
   int64_t vocab;
-  float2* stats;    // [tiles_n][M]
+  int64_t col0;     // first word of the piece
+  float2* stats;    // [M][stat_cols] (maximum, sum) per 128 columns
+  int64_t stat_cols;
   float* at_label;  // [M]
   const float* lse;
   const float* dloss;
   const float* scale;
-  __nv_bfloat16* dl;
-  int64_t ldl;
-  float* acc;  // dh sums [M, N]
-  int first;
+  float* acc;  // [splits][M][N]
+  int add;     // 1: add to acc
   void* out;
   int out_fp32;
 };
 
-__device__ __forceinline__ void store(void* out, int fp32, int64_t at, float v) {
-  if (fp32) static_cast<float*>(out)[at] = v;
-  else static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(256) ce_tile_kernel(const CeTile g) {
-  __shared__ float sa[kTileK][kTile + 1], sb[kTileK][kTile + 1], sc[kTile][kTile + 1];
-  const int64_t m0 = (int64_t)blockIdx.y * kTile, n0 = (int64_t)blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < g.K; k0 += kTileK) {
-    for (int e = threadIdx.x; e < kTile * kTileK; e += 256) {
-      const int i = e / kTileK, k = e % kTileK;
-      sa[k][i] = (m0 + i < g.M && k0 + k < g.K) ? __bfloat162float(g.a[(m0 + i) * g.ai + (k0 + k) * g.ak]) : 0.f;
-      sb[k][i] = (n0 + i < g.N && k0 + k < g.K) ? __bfloat162float(g.b[(n0 + i) * g.bj + (k0 + k) * g.bk]) : 0.f;
+// Work item w -> tile and split; consecutive tiles walk down a band of kGroupM
+// m-tiles, all splits of a tile run together.
+__device__ __forceinline__ void item_coords(int w, const CeTile& g, int& mt, int& nt, int& split) {
+  split = w % g.splits;
+  const int t = w / g.splits;
+  const int per_group = kGroupM * g.tiles_n;
+  const int group = t / per_group;
+  const int first = group * kGroupM;
+  const int size = min(kGroupM, g.tiles_m - first);
+  const int r = t - group * per_group;
+  mt = first + r % size;
+  nt = r / size;
+}
+__device__ __forceinline__ void split_range(int split, const CeTile& g, int& k0, int& k1) {
+  k0 = (int)((int64_t)g.num_k * split / g.splits);
+  k1 = (int)((int64_t)g.num_k * (split + 1) / g.splits);
+}
+
+// After an abort: wait (bounded) for the loads of ring uses [from, to).
+__device__ __forceinline__ void drain(uint64_t* bars, uint32_t from, uint32_t to, int* err) {
+  volatile int no_abort = 0;
+  for (uint32_t k = from; k < to; ++k) mbar_wait_bounded(&bars[k % kStages], (k / kStages) & 1u, &no_abort, err);
+}
+
+// Persistent: each CTA pair takes work items in turn.  Warp 0 (one lane)
+// streams the operands into a ring of shared-memory stages, warp 1 of the even
+// CTA (one lane) issues the pair MMAs, eight epilogue warps per CTA (two per
+// TMEM lane quarter, 128 columns each) finish the tile.
+// MN-major operands (A_MN, B_MN): the matrix lies with K along its rows; a
+// stage holds two 64 x 64 blocks (64 k-rows of 128 bytes each).
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
+    ce_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmC, const CeTile g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + kStages * kOperand;
+  uint8_t* stage_c = sB + kStages * kOperand;
+  uint64_t* full = reinterpret_cast<uint64_t*>(stage_c + kStg);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + kNacc;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + kNacc);
+  uint32_t* peer_base = tmem_slot + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int total = g.tiles_m * g.tiles_n * g.splits;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-    for (int k = 0; k < kTileK; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty * 4 + i] * sb[k][tx * 4 + j];
-    __syncthreads();
+    for (int a = 0; a < kNacc; ++a) {
+      mbar_init(&acc_full[a], 1);
+      mbar_init(&acc_empty[a], 2 * kEpiWarps);  // the epilogue warps of both CTAs
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
   }
-  if constexpr (EPI == kStats) {
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) sc[ty * 4 + i][tx * 4 + j] = acc[i][j];
-    __syncthreads();
-    const int64_t row = m0 + threadIdx.x;
-    if (threadIdx.x < kTile && row < g.M) {
-      const int cols = (int)min((int64_t)kTile, g.N - n0);
-      float m = kNegInf, s = 0.f;
-      bool nan = false;
-      for (int j = 0; j < cols; ++j) {
-        nan |= sc[threadIdx.x][j] != sc[threadIdx.x][j];
-        m = fmaxf(m, sc[threadIdx.x][j]);
-      }
-      for (int j = 0; j < cols; ++j) s += isinf(m) ? (sc[threadIdx.x][j] == m && m > 0.f) : expf(sc[threadIdx.x][j] - m);
-      g.stats[blockIdx.x * g.M + row] = make_float2(nan ? __int_as_float(0x7FC00000) : m, s);
-      const int64_t label = g.labels[row];
-      if (label >= n0 && label < n0 + cols) g.at_label[row] = sc[threadIdx.x][label - n0];
-    }
-  } else {
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-        if (r >= g.M || c >= g.N) continue;
-        if constexpr (EPI == kDlogits) {
-          const int64_t label = g.labels[r];
-          float v = 0.f;
-          if (label >= 0 && label < g.vocab)
-            v = (expf(acc[i][j] - g.lse[r]) - (g.col0 + c == label ? 1.f : 0.f)) * (g.dloss[r] / *g.scale);
-          g.dl[r * g.ldl + c] = __float2bfloat16_rn(v);
-        } else if constexpr (EPI == kDh) {
-          float* p = g.acc + r * g.N + c;
-          *p = (g.first ? 0.f : *p) + acc[i][j];
-        } else {
-          store(g.out, g.out_fp32, r * g.N + c, acc[i][j] * *g.scale);
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  // Both CTAs must see the same TMEM address; otherwise stop cleanly.
+  if (threadIdx.x == 0) st_shared_remote_u32(mapa_shared(smem_u32(peer_base), rank ^ 1u), tmem_base);
+  cluster_sync_all();
+  if (*peer_base != tmem_base) {
+    if (threadIdx.x == 0) atomicCAS(g.err, 0, (int)LPQ_ERR_UNSUPPORTED);
+    *abort_flag = 1;
+  }
+  const bool run = *peer_base == tmem_base;
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+  const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+
+  if (run && warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, it = 0;
+      bool ok = true;
+      for (int w = pair; w < total && ok; w += npairs) {
+        int mt, nt, split, k0, k1;
+        item_coords(w, g, mt, nt, split);
+        split_range(split, g, k0, k1);
+        const int32_t arow = mt * kTile + (int32_t)rank * kHalf, brow = nt * kTile + (int32_t)rank * kHalf;
+        for (int kt = k0; kt < k1; ++kt) {
+          if (!(ok = mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, g.err))) break;
+          if (leader) mbar_arrive_expect_tx(&full[s], 4 * kOperand);
+          const uint32_t fb = full_leader + 8 * s;
+          uint8_t* da = sA + s * kOperand;
+          uint8_t* db = sB + s * kOperand;
+          if constexpr (A_MN) {
+            tma_load_2d_pair(da, &tmA, arow, kt * kStepK, fb);
+            tma_load_2d_pair(da + kOperand / 2, &tmA, arow + 64, kt * kStepK, fb);
+          } else {
+            tma_load_2d_pair(da, &tmA, kt * kStepK, arow, fb);
+          }
+          if constexpr (B_MN) {
+            tma_load_2d_pair(db, &tmB, brow, kt * kStepK, fb);
+            tma_load_2d_pair(db + kOperand / 2, &tmB, brow + 64, kt * kStepK, fb);
+          } else {
+            tma_load_2d_pair(db, &tmB, kt * kStepK, brow, fb);
+          }
+          ++it;
+          if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
         }
       }
+      // After an abort, the even CTA lets the pair's loads in flight land
+      // (they all signal its full barriers) before either CTA exits.
+      if (!ok && leader) drain(full, it > (uint32_t)kStages ? it - kStages : 0u, it, g.err);
+    }
+  } else if (run && warp == 1) {
+    if (lane == 0 && leader) {
+      // K-major: 8-row groups of 1024 bytes, 16 values along K = 32 bytes on.
+      // MN-major: 64-value blocks kOperand / 2 bytes apart, 8-row groups of K of
+      // 1024 bytes, 16 rows along K = 2048 bytes on.
+      const uint64_t ad0 = smem_desc(smem_u32(sA), A_MN ? kOperand / 2 : 16, 1024, 2);
+      const uint64_t bd0 = smem_desc(smem_u32(sB), B_MN ? kOperand / 2 : 16, 1024, 2);
+      uint32_t s = 0, ph = 0, lt = 0;
+      bool ok = true;
+      for (int w = pair; w < total && ok; w += npairs, ++lt) {
+        int mt, nt, split, k0, k1;
+        item_coords(w, g, mt, nt, split);
+        split_range(split, g, k0, k1);
+        const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
+        if (!(ok = mbar_wait_bounded(&acc_empty[a], aph ^ 1u, abort_flag, g.err))) break;
+        tc_fence_after();
+        const uint32_t tmem_d = tmem_base + a * kTile;
+        for (int kt = k0; kt < k1; ++kt) {
+          if (!(ok = mbar_wait_bounded(&full[s], ph, abort_flag, g.err))) break;
+          tc_fence_after();
+          const uint64_t ad = ad0 + (uint64_t)(s * (kOperand >> 4)), bd = bd0 + (uint64_t)(s * (kOperand >> 4));
+#pragma unroll
+          for (int j = 0; j < kStepK / 16; ++j)
+            mma_pair<kKindF16>(tmem_d, ad + (uint64_t)(j * (A_MN ? 128 : 2)), bd + (uint64_t)(j * (B_MN ? 128 : 2)),
+                               g.idesc, (kt > k0 || j > 0) ? 1u : 0u);
+          tc_commit_pair(&empty[s], 0x3);
+          if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
+        }
+        if (ok) tc_commit_pair(&acc_full[a], 0x3);
+      }
+    }
+  } else if (run && warp >= 2) {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* stg = stage_c + (warp - 2) * kStgWarp;
+    float scale = 1.f;
+    if constexpr (EPI == kDlogits || EPI == kOut) scale = *g.scale;
+    uint32_t lt = 0;
+    for (int w = pair; w < total; w += npairs, ++lt) {
+      int mt, nt, split;
+      item_coords(w, g, mt, nt, split);
+      const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
+      const int64_t row = (int64_t)mt * kTile + rank * kHalf + q * 32 + lane;
+      const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
+      const bool live = row < g.M;
+      const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, g.N - c0));  // columns of this warp inside the matrix
+      // what the row needs is fetched before the accumulator is waited for
+      int64_t label = -1;
+      float lse2 = 0.f, gs = 0.f;
+      bool target = false;
+      if constexpr (EPI == kStats || EPI == kDlogits) {
+        if (live) label = g.labels[row];
+        target = label >= 0 && label < g.vocab;
+        label -= g.col0 + c0;  // column of the label among this warp's 128
+      }
+      if constexpr (EPI == kDlogits) {
+        if (target) {
+          lse2 = g.lse[row] * kLog2e;
+          gs = g.dloss[row] / scale;
+        }
+      }
+      if (!mbar_wait_bounded(&acc_full[a], aph, abort_flag, g.err)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + a * kTile + half * kHalf + ((uint32_t)(q * 32) << 16);
+      float m = kNegInf, sum = 0.f;
+      bool some = true;
+      if constexpr (EPI == kPart) {  // a ragged last piece can leave a split without steps: nothing to add
+        int k0, k1;
+        split_range(split, g, k0, k1);
+        some = k0 < k1;
+      }
+#pragma unroll 1
+      for (int cc = 0; cc < kHalf / 32; ++cc) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(tbase + (uint32_t)(cc * 32), v);
+        if (cc == kHalf / 32 - 1) {  // the accumulator is read: hand it back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader) mbar_arrive(&acc_empty[a]); else mbar_arrive_remote_relaxed(acc_empty_leader + 8 * a);
+          }
+        }
+        if constexpr (EPI == kStats) {
+          if (cc * 32 >= ncols) continue;
+          if (cc * 32 + 32 > ncols)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (cc * 32 + i >= ncols) v[i] = __float_as_uint(kNegInf);
+          if (target && label >= cc * 32 && label < cc * 32 + 32) {
+            float at = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (label == cc * 32 + i) at = __uint_as_float(v[i]);
+            g.at_label[row] = at;
+          }
+          float top = m;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = max_nan(top, __uint_as_float(v[i]));
+          // -inf so far: every exponent is taken against 0, and each term is exp(-inf) = 0
+          const float base = top == kNegInf ? 0.f : top * kLog2e;
+          float part = sum * ex2(__fmaf_rn(m, kLog2e, -base));
+#pragma unroll
+          for (int i = 0; i < 32; ++i) part += ex2(__fmaf_rn(__uint_as_float(v[i]), kLog2e, -base));
+          m = top;
+          sum = part;
+        } else if constexpr (EPI == kPart) {
+          if (live && some && cc * 32 < ncols) {
+            float* p = g.acc + ((int64_t)split * g.M + row) * g.N + c0 + cc * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (cc * 32 + 4 * i >= ncols) break;
+              float4 o = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                     __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+              if (g.add) {
+                const float4 b = reinterpret_cast<const float4*>(p)[i];
+                o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
+              }
+              reinterpret_cast<float4*>(p)[i] = o;
+            }
+          }
+        } else if (EPI == kOut && g.out_fp32) {
+          if (live && cc * 32 < ncols) {
+            float* p = static_cast<float*>(g.out) + row * g.N + c0 + cc * 32;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (cc * 32 + 4 * i >= ncols) break;
+              reinterpret_cast<float4*>(p)[i] =
+                  make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
+                              __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale);
+            }
+          }
+        } else {
+          // bf16 tile: 32 rows x 64 columns staged (128-byte swizzle: 16-byte
+          // chunk i of row r at chunk i ^ (r & 7)) and stored by TMA, which
+          // clips at the matrix's edges
+          if constexpr (EPI == kDlogits) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              v[i] = __float_as_uint(target ? ex2(__fmaf_rn(__uint_as_float(v[i]), kLog2e, -lse2)) * gs : 0.f);
+            if (target && label >= cc * 32 && label < cc * 32 + 32)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (label == cc * 32 + i) v[i] = __float_as_uint(__uint_as_float(v[i]) - gs);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+          }
+          if ((cc & 1) == 0) {
+            if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
+            __syncwarp();
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+              pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            const int chunk = (cc & 1) * 4 + i;
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          if (cc & 1) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmC, stg, (int32_t)(c0 + (cc - 1) * 32), mt * kTile + (int32_t)rank * kHalf + q * 32);
+              bulk_commit_group();
+            }
+          }
+        }
+      }
+      if constexpr (EPI == kStats) {
+        if (live && ncols > 0) g.stats[row * g.stat_cols + nt * 2 + half] = make_float2(m, sum);
+      }
+    }
+    if (lane == 0) bulk_wait_group0();  // this warp's TMA stores complete before the CTA exits
+    __syncwarp();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal its barriers
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
   }
 }
 
-// lse and loss of a row from its tiles' maxima and sums; one thread per row.
-__global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64_t tiles, const float* at_label,
+// Joins (m, s) pairs: the sum of s exp(m - M) under the common maximum M.  A
+// maximum that is NaN, +inf or -inf is the result by itself.
+__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
+  const float top = max_nan(m, m2);
+  const float base = top == kNegInf ? 0.f : top * kLog2e;
+  s = s * ex2(__fmaf_rn(m, kLog2e, -base)) + s2 * ex2(__fmaf_rn(m2, kLog2e, -base));
+  m = top;
+}
+
+// lse and loss of a row from its column blocks' maxima and sums; one warp per row.
+__global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64_t cols, const float* at_label,
                                                       const int64_t* labels, int64_t t, int64_t v, float* loss,
                                                       float* lse) {
-  const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= t) return;
-  float m = kNegInf;
-  bool nan = false;
-  for (int64_t i = 0; i < tiles; ++i) {
-    const float x = stats[i * t + row].x;
-    nan |= x != x;
-    m = fmaxf(m, x);
+  const int lane = threadIdx.x & 31;
+  float m = kNegInf, s = 0.f;
+#pragma unroll 4
+  for (int64_t i = lane; i < cols; i += 32) {
+    const float2 x = stats[row * cols + i];
+    join_stats(m, s, x.x, x.y);
   }
-  float s = 0.f;
-  if (!isinf(m))
-    for (int64_t i = 0; i < tiles; ++i) {
-      const float2 x = stats[i * t + row];
-      if (x.y > 0.f) s += x.y * expf(x.x - m);
-    }
-  const float l = nan ? __int_as_float(0x7FC00000) : isinf(m) ? m : m + logf(s);
-  lse[row] = l;
-  const int64_t label = labels[row];
-  loss[row] = label >= 0 && label < v ? l - at_label[row] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    join_stats(m, s, m2, s2);
+  }
+  if (lane == 0) {
+    const float l = (m == m && fabsf(m) != -kNegInf) ? m + logf(s) : m;
+    const int64_t label = labels[row];
+    lse[row] = l;
+    loss[row] = label >= 0 && label < v ? l - at_label[row] : 0.f;
+  }
 }
 
 // s = max |dloss| over the rows with a target; 1 where that is 0 or not finite.
@@ -150,81 +441,174 @@ __global__ void __launch_bounds__(1024) ce_scale_kernel(const float* dloss, cons
   }
 }
 
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float* acc, int64_t n, const float* scale, void* out,
-                                                        int fp32) {
+// dh from its partial sums: the splits in order, times the scale.
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int64_t n4, int splits, const float* scale,
+                                                        void* out, int fp32) {
   const float s = *scale;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
-    store(out, fp32, i, acc[i] * s);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    float4 a = acc[i];
+    for (int k = 1; k < splits; ++k) {
+      const float4 b = acc[k * n4 + i];
+      a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+    }
+    if (fp32) {
+      static_cast<float4*>(out)[i] = make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * s, a.y * s), hi = __floats2bfloat162_rn(a.z * s, a.w * s);
+      static_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+  }
 }
 
+// ------------------------------------------------------------------ host side
 int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+int64_t cdiv(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// Words per piece of the backward pass: dl takes at most 2^28 values (512 MiB)
+// unless 64 words of it are more.
 int64_t piece_of(int64_t t, int64_t v, int64_t piece) {
   if (piece == 0) piece = std::max<int64_t>(64, (((int64_t)1 << 28) / std::max<int64_t>(t, 1)) / 64 * 64);
   return std::min(piece, round_up(v, 64));
 }
 
-template <int EPI>
-lpq_status run_tile(const CeTile& g, cudaStream_t s) {
-  const dim3 grid((unsigned)((g.N + kTile - 1) / kTile), (unsigned)((g.M + kTile - 1) / kTile));
-  ce_tile_kernel<EPI><<<grid, 256, 0, s>>>(g);
+// Splits of dh's sum over a piece's words.  dh has few tiles when t is small
+// and its sum is long, so the sum is split until the pairs are busy; each
+// split costs its slab of FP32 partial sums written and read once.  The
+// estimate: a step of a pair tile takes 0.33 us, a tile's start and end 1 us,
+// memory 6.5 TB/s.
+int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
+  const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK);
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 64 && s <= steps; ++s) {
+    const double us = (double)cdiv(tiles * s, pairs) * ((double)cdiv(steps, s) * 0.33 + 1.0) +
+                      (s > 1 ? (double)s * (double)t * (double)d * 8.0 / 6.5e6 : 0.0);
+    if (s == 1 || us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
+}
+
+struct Operand {
+  const void* p;
+  int64_t ld;  // elements
+};
+
+// Launches one product: A [M, K] (K-major) or [K, M] (A_MN), B likewise; C the
+// bf16 output of the kinds that store one.
+template <int EPI, bool A_MN, bool B_MN>
+lpq_status run_pair(CeTile g, Operand a, Operand b, int64_t K, void* c, int64_t ldc, int splits, cudaStream_t s) {
+  CUtensorMap ta, tb, tc;
+  lpq_status st;
+  if ((st = A_MN ? make_map(&ta, a.p, true, g.M, K, a.ld * 2, 64, kStepK)
+                 : make_map(&ta, a.p, true, K, g.M, a.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+  if ((st = B_MN ? make_map(&tb, b.p, true, g.N, K, b.ld * 2, 64, kStepK)
+                 : make_map(&tb, b.p, true, K, g.N, b.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+  tc = ta;
+  if (c && (st = make_map(&tc, c, true, g.N, g.M, ldc * 2, 64, 32)) != LPQ_OK) return st;
+  const int64_t tm = cdiv(g.M, kTile), tn = cdiv(g.N, kTile);
+  if (tm * tn * splits > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "too many output tiles");
+  g.num_k = (int)cdiv(K, kStepK);
+  g.tiles_m = (int)tm;
+  g.tiles_n = (int)tn;
+  g.splits = splits;
+  // F32 accumulator, BF16 x BF16, MN-major flags, N = 256, M = 256
+  g.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
+            ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+  if ((st = device_error_word(&g.err)) != LPQ_OK) return st;
+  if ((st = set_smem_attr(reinterpret_cast<const void*>(ce_pair_kernel<EPI, A_MN, B_MN>), kSmem)) != LPQ_OK) return st;
+  const int pairs = (int)std::min<int64_t>(tm * tn * splits, std::max(1, device_sms() / 2));
+  ce_pair_kernel<EPI, A_MN, B_MN><<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, tc, g);
   return cuda_check(cudaGetLastError(), "cross entropy launch");
 }
+
+// Workspace of the backward pass: scale, dl, partial sums of dh.
+struct BackwardPlan {
+  int64_t piece, dl_ld;
+  int splits;
+  bool direct;  // one piece, one split: dh is stored by its product
+  size_t dl_at, acc_at, bytes;
+  BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked) {
+    piece = piece_of(t, v, asked);
+    dl_ld = std::min(piece, round_up(v, 8));
+    // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
+    splits = dh_splits(t, d, std::min(piece, v), 76);
+    direct = splits == 1 && piece >= v;
+    dl_at = 256;
+    acc_at = dl_at + (size_t)round_up(t * dl_ld * 2, 256);
+    bytes = acc_at + (direct ? 0 : (size_t)splits * (size_t)t * (size_t)d * 4);
+  }
+};
 
 }  // namespace
 
 size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece) {
   if (t == 0) return 0;
-  if (!backward) return (size_t)round_up(t * 4, 256) + (size_t)((v + kTile - 1) / kTile) * (size_t)t * sizeof(float2);
-  return 256 + (size_t)round_up(t * d * 4, 256) + (size_t)t * (size_t)piece_of(t, v, piece) * 2;
+  if (!backward) return (size_t)round_up(t * 4, 256) + (size_t)cdiv(v, kHalf) * (size_t)t * sizeof(float2);
+  return BackwardPlan(t, v, d, piece).bytes;
 }
 
 lpq_status launch_ce(const CeArgs& a, cudaStream_t s) {
   if (a.t == 0) return LPQ_OK;
   CeTile g{};
-  g.a = static_cast<const __nv_bfloat16*>(a.h);
-  g.b = static_cast<const __nv_bfloat16*>(a.w);
-  g.ai = a.ldh; g.ak = 1; g.bj = a.ldw; g.bk = 1;
-  g.M = a.t; g.N = a.v; g.K = a.d;
+  g.M = a.t;
+  g.N = a.v;
   g.labels = a.labels;
+  g.vocab = a.v;
   g.at_label = reinterpret_cast<float*>(a.workspace);
   g.stats = reinterpret_cast<float2*>(a.workspace + round_up(a.t * 4, 256));
-  lpq_status st = run_tile<kStats>(g, s);
+  g.stat_cols = cdiv(a.v, kHalf);
+  lpq_status st = run_pair<kStats, false, false>(g, {a.h, a.ldh}, {a.w, a.ldw}, a.d, nullptr, 0, 1, s);
   if (st != LPQ_OK) return st;
-  ce_join_kernel<<<(unsigned)((a.t + 255) / 256), 256, 0, s>>>(g.stats, (a.v + kTile - 1) / kTile, g.at_label, a.labels,
-                                                               a.t, a.v, a.loss, a.lse_out);
+  ce_join_kernel<<<(unsigned)cdiv(a.t, 8), 256, 0, s>>>(g.stats, g.stat_cols, g.at_label, a.labels, a.t, a.v, a.loss,
+                                                       a.lse_out);
   return cuda_check(cudaGetLastError(), "cross entropy join launch");
 }
 
 lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
-  const size_t out_elem = a.grads_fp32 ? 4 : 2;
-  if (a.t == 0) return cuda_check(cudaMemsetAsync(a.dw, 0, (size_t)a.v * (size_t)a.d * out_elem, s), "cudaMemsetAsync(dw)");
+  const size_t elem = a.grads_fp32 ? 4 : 2;
+  if (a.t == 0) return cuda_check(cudaMemsetAsync(a.dw, 0, (size_t)a.v * (size_t)a.d * elem, s), "cudaMemsetAsync(dw)");
+  const BackwardPlan plan(a.t, a.v, a.d, a.piece);
   float* scale = reinterpret_cast<float*>(a.workspace);
-  float* acc = reinterpret_cast<float*>(a.workspace + 256);
-  __nv_bfloat16* dl = reinterpret_cast<__nv_bfloat16*>(a.workspace + 256 + round_up(a.t * a.d * 4, 256));
-  const int64_t piece = piece_of(a.t, a.v, a.piece);
+  void* dl = a.workspace + plan.dl_at;
+  CeTile g{};
+  g.labels = a.labels;
+  g.vocab = a.v;
+  g.lse = a.lse;
+  g.dloss = a.dloss;
+  g.scale = scale;
+  g.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
+  g.out_fp32 = a.grads_fp32;
   ce_scale_kernel<<<1, 1024, 0, s>>>(a.dloss, a.labels, a.t, a.v, scale);
   lpq_status st = cuda_check(cudaGetLastError(), "cross entropy scale launch");
   if (st != LPQ_OK) return st;
-  const __nv_bfloat16* h = static_cast<const __nv_bfloat16*>(a.h);
-  for (int64_t v0 = 0; v0 < a.v; v0 += piece) {
-    const int64_t width = std::min(piece, a.v - v0);
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(a.w) + v0 * a.ldw;
-    CeTile g{};
-    g.labels = a.labels; g.vocab = a.v; g.lse = a.lse; g.dloss = a.dloss; g.scale = scale; g.col0 = v0;
-    g.dl = dl; g.ldl = piece; g.acc = acc; g.first = v0 == 0; g.out_fp32 = a.grads_fp32;
-    g.a = h; g.ai = a.ldh; g.ak = 1; g.b = w; g.bj = a.ldw; g.bk = 1;
-    g.M = a.t; g.N = width; g.K = a.d;
-    if ((st = run_tile<kDlogits>(g, s)) != LPQ_OK) return st;
-    g.a = dl; g.ai = piece; g.ak = 1; g.b = w; g.bj = 1; g.bk = a.ldw;
-    g.M = a.t; g.N = a.d; g.K = width;
-    if ((st = run_tile<kDh>(g, s)) != LPQ_OK) return st;
-    g.a = dl; g.ai = 1; g.ak = piece; g.b = h; g.bj = 1; g.bk = a.ldh;
-    g.M = width; g.N = a.d; g.K = a.t;
-    g.out = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * out_elem;
-    if ((st = run_tile<kDw>(g, s)) != LPQ_OK) return st;
+  for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
+    const int64_t width = std::min(plan.piece, a.v - v0);
+    const Operand w{static_cast<const uint8_t*>(a.w) + (size_t)v0 * (size_t)a.ldw * 2, a.ldw};
+    const Operand h{a.h, a.ldh}, l{dl, plan.dl_ld};
+    // dl = (exp(h w^T - lse) - onehot) dloss / s
+    g.M = a.t; g.N = width; g.col0 = v0;
+    if ((st = run_pair<kDlogits, false, false>(g, h, w, a.d, dl, plan.dl_ld, 1, s)) != LPQ_OK) return st;
+    // dh (+)= dl w
+    g.M = a.t; g.N = a.d; g.add = v0 > 0;
+    if (plan.direct) {
+      g.out = a.dh;
+      st = run_pair<kOut, false, true>(g, l, w, width, a.grads_fp32 ? nullptr : a.dh, a.d, 1, s);
+    } else {
+      st = run_pair<kPart, false, true>(g, l, w, width, nullptr, 0, plan.splits, s);
+    }
+    if (st != LPQ_OK) return st;
+    // dw = dl^T h
+    g.M = width; g.N = a.d;
+    g.out = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
+    if ((st = run_pair<kOut, true, true>(g, l, h, a.t, a.grads_fp32 ? nullptr : g.out, a.d, 1, s)) != LPQ_OK) return st;
   }
-  ce_finish_kernel<<<device_sms() * 8, 256, 0, s>>>(acc, a.t * a.d, scale, a.dh, a.grads_fp32);
+  if (plan.direct) return LPQ_OK;
+  const int64_t n4 = a.t * a.d / 4;
+  ce_finish_kernel<<<(unsigned)std::min<int64_t>(cdiv(n4, 256), (int64_t)device_sms() * 8), 256, 0, s>>>(
+      reinterpret_cast<const float4*>(g.acc), n4, plan.splits, scale, a.dh, a.grads_fp32);
   return cuda_check(cudaGetLastError(), "cross entropy finish launch");
 }
 

@@ -11,6 +11,10 @@
 
 namespace lpq {
 
+// 2D tensor map with 128-byte swizzle (gemm.cu).
+lpq_status make_map(CUtensorMap* map, const void* base, bool bf16, int64_t inner, int64_t rows, int64_t row_bytes,
+                    uint32_t box_inner, uint32_t box_rows);
+
 // ------------------------------------------------------------------ bf16 / fp32
 __device__ __forceinline__ float bf16_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t pair) { return __uint_as_float(pair & 0xFFFF0000u); }

@@ -103,6 +103,7 @@ lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t
                          cudaStream_t stream);
 
 // Device error word (gemm.cu owns it).
+lpq_status device_error_word(int** word);
 lpq_status read_and_clear_device_error(cudaStream_t stream, int32_t* code);
 lpq_status launch_selftest_wait(uint64_t limit_ns, cudaStream_t stream);
 lpq_status launch_mma_peak(int32_t kind, int32_t iters, int32_t with_sf, cudaStream_t stream);
