@@ -44,6 +44,14 @@ constexpr int kSmem = kStages * 2 * kOperand + 2048 + 512 + kStg;
 constexpr int kNacc = 2;  // accumulators: one tile's epilogue under the next tile's products
 static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budgets");
 
+// The tensor core cuts (does not round) the FP32 sum at every 16 products, so
+// a long sum drifts towards zero: measured 2.5e-6 of the loss over d = 4096.
+// The logits of the forward pass are therefore summed in TMEM over kChunk
+// steps (1024 values) at a time and across chunks in the epilogue's registers:
+// 2% of the time at 7936 x 4096 x 32000, a fifth to an eighth of the drift;
+// the gradients' sums carry dl's bf16 rounding, far above that drift.
+constexpr int kChunk = 16;
+
 // What the epilogue makes of a tile.
 //   kStats    row maxima and sums of exponentials of the logits
 //   kDlogits  dl in bf16
@@ -211,26 +219,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       const uint64_t bd0 = smem_desc(smem_u32(sB), B_MN ? kOperand / 2 : 16, 1024, 2);
       uint32_t s = 0, ph = 0, lt = 0;
       bool ok = true;
-      for (int w = pair; w < total && ok; w += npairs, ++lt) {
+      for (int w = pair; w < total && ok; w += npairs) {
         int mt, nt, split, k0, k1;
         item_coords(w, g, mt, nt, split);
         split_range(split, g, k0, k1);
-        const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
-        if (!(ok = mbar_wait_bounded(&acc_empty[a], aph ^ 1u, abort_flag, g.err))) break;
-        tc_fence_after();
-        const uint32_t tmem_d = tmem_base + a * kTile;
-        for (int kt = k0; kt < k1; ++kt) {
-          if (!(ok = mbar_wait_bounded(&full[s], ph, abort_flag, g.err))) break;
+        int kt = k0;
+        do {  // one accumulator per chunk of the sum (a split without steps still hands one over)
+          const int kend = EPI == kStats ? min(k1, kt + kChunk) : k1;
+          const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
+          ++lt;
+          if (!(ok = mbar_wait_bounded(&acc_empty[a], aph ^ 1u, abort_flag, g.err))) break;
           tc_fence_after();
-          const uint64_t ad = ad0 + (uint64_t)(s * (kOperand >> 4)), bd = bd0 + (uint64_t)(s * (kOperand >> 4));
+          const uint32_t tmem_d = tmem_base + a * kTile;
+          for (const int first = kt; kt < kend; ++kt) {
+            if (!(ok = mbar_wait_bounded(&full[s], ph, abort_flag, g.err))) break;
+            tc_fence_after();
+            const uint64_t ad = ad0 + (uint64_t)(s * (kOperand >> 4)), bd = bd0 + (uint64_t)(s * (kOperand >> 4));
 #pragma unroll
-          for (int j = 0; j < kStepK / 16; ++j)
-            mma_pair<kKindF16>(tmem_d, ad + (uint64_t)(j * (A_MN ? 128 : 2)), bd + (uint64_t)(j * (B_MN ? 128 : 2)),
-                               g.idesc, (kt > k0 || j > 0) ? 1u : 0u);
-          tc_commit_pair(&empty[s], 0x3);
-          if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
-        }
-        if (ok) tc_commit_pair(&acc_full[a], 0x3);
+            for (int j = 0; j < kStepK / 16; ++j)
+              mma_pair<kKindF16>(tmem_d, ad + (uint64_t)(j * (A_MN ? 128 : 2)), bd + (uint64_t)(j * (B_MN ? 128 : 2)),
+                                 g.idesc, (kt > first || j > 0) ? 1u : 0u);
+            tc_commit_pair(&empty[s], 0x3);
+            if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
+          }
+          if (ok) tc_commit_pair(&acc_full[a], 0x3);
+        } while (ok && kt < k1);
       }
     }
   } else if (run && warp >= 2) {
@@ -239,22 +252,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     float scale = 1.f;
     if constexpr (EPI == kDlogits || EPI == kOut) scale = *g.scale;
     uint32_t lt = 0;
-    for (int w = pair; w < total; w += npairs, ++lt) {
+    for (int w = pair; w < total; w += npairs) {
       int mt, nt, split;
       item_coords(w, g, mt, nt, split);
-      const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
       const int64_t row = (int64_t)mt * kTile + rank * kHalf + q * 32 + lane;
       const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
       const bool live = row < g.M;
       const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, g.N - c0));  // columns of this warp inside the matrix
       // what the row needs is fetched before the accumulator is waited for
-      int64_t label = -1;
+      int label = -1;  // its column among this warp's 128, -1: not here
       float lse2 = 0.f, gs = 0.f;
       bool target = false;
       if constexpr (EPI == kStats || EPI == kDlogits) {
-        if (live) label = g.labels[row];
-        target = label >= 0 && label < g.vocab;
-        label -= g.col0 + c0;  // column of the label among this warp's 128
+        const int64_t word = live ? g.labels[row] : -1;
+        target = word >= 0 && word < g.vocab;
+        const int64_t col = word - (g.col0 + c0);
+        if (target && col >= 0 && col < kHalf) label = (int)col;
       }
       if constexpr (EPI == kDlogits) {
         if (target) {
@@ -262,53 +275,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           gs = g.dloss[row] / scale;
         }
       }
-      if (!mbar_wait_bounded(&acc_full[a], aph, abort_flag, g.err)) break;
-      __syncwarp();
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + a * kTile + half * kHalf + ((uint32_t)(q * 32) << 16);
-      float m = kNegInf, sum = 0.f;
+      // Waits for the next accumulator; hands it back once its values are in registers.
+      uint32_t tbase = 0, a = 0;
+      auto take = [&]() {
+        a = lt % kNacc;
+        const bool ok = mbar_wait_bounded(&acc_full[a], (lt / kNacc) & 1u, abort_flag, g.err);
+        ++lt;
+        __syncwarp();
+        tc_fence_after();
+        tbase = tmem_base + a * kTile + half * kHalf + ((uint32_t)(q * 32) << 16);
+        return __all_sync(0xFFFFFFFFu, ok);
+      };
+      auto give = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&acc_empty[a]); else mbar_arrive_remote_relaxed(acc_empty_leader + 8 * a);
+        }
+      };
+      if constexpr (EPI == kStats) {
+        float l[kHalf];
+        bool ok = true;
+        for (int kt = 0; kt < g.num_k && ok; kt += kChunk) {
+          if (!(ok = take())) break;
+#pragma unroll
+          for (int cc = 0; cc < kHalf / 32; ++cc) {
+            uint32_t v[32];
+            tmem_ld32(tbase + (uint32_t)(cc * 32), v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) l[cc * 32 + i] = (kt ? l[cc * 32 + i] : 0.f) + __uint_as_float(v[i]);
+          }
+          give();
+        }
+        if (!ok) break;
+        if (ncols < kHalf)
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i)
+            if (i >= ncols) l[i] = kNegInf;
+        if (label >= 0) {
+          float at = 0.f;
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i)
+            if (label == i) at = l[i];
+          g.at_label[row] = at;
+        }
+        float m = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) m = max_nan(m, l[i]);
+        // all -inf: the exponents are taken against 0, and each term is exp(-inf) = 0
+        const float base = m == kNegInf ? 0.f : m * kLog2e;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) sum += ex2(__fmaf_rn(l[i], kLog2e, -base));
+        if (live && ncols > 0) g.stats[row * g.stat_cols + nt * 2 + half] = make_float2(m, sum);
+        __syncwarp();
+        continue;
+      }
       bool some = true;
       if constexpr (EPI == kPart) {  // a ragged last piece can leave a split without steps: nothing to add
         int k0, k1;
         split_range(split, g, k0, k1);
         some = k0 < k1;
       }
+      if (!take()) break;
 #pragma unroll 1
       for (int cc = 0; cc < kHalf / 32; ++cc) {
         uint32_t v[32];
         __syncwarp();
         tmem_ld32(tbase + (uint32_t)(cc * 32), v);
-        if (cc == kHalf / 32 - 1) {  // the accumulator is read: hand it back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (leader) mbar_arrive(&acc_empty[a]); else mbar_arrive_remote_relaxed(acc_empty_leader + 8 * a);
-          }
-        }
-        if constexpr (EPI == kStats) {
-          if (cc * 32 >= ncols) continue;
-          if (cc * 32 + 32 > ncols)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (cc * 32 + i >= ncols) v[i] = __float_as_uint(kNegInf);
-          if (target && label >= cc * 32 && label < cc * 32 + 32) {
-            float at = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (label == cc * 32 + i) at = __uint_as_float(v[i]);
-            g.at_label[row] = at;
-          }
-          float top = m;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) top = max_nan(top, __uint_as_float(v[i]));
-          // -inf so far: every exponent is taken against 0, and each term is exp(-inf) = 0
-          const float base = top == kNegInf ? 0.f : top * kLog2e;
-          float part = sum * ex2(__fmaf_rn(m, kLog2e, -base));
-#pragma unroll
-          for (int i = 0; i < 32; ++i) part += ex2(__fmaf_rn(__uint_as_float(v[i]), kLog2e, -base));
-          m = top;
-          sum = part;
-        } else if constexpr (EPI == kPart) {
+        if (cc == kHalf / 32 - 1) give();
+        if constexpr (EPI == kPart) {
           if (live && some && cc * 32 < ncols) {
             float* p = g.acc + ((int64_t)split * g.M + row) * g.N + c0 + cc * 32;
 #pragma unroll
@@ -342,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               v[i] = __float_as_uint(target ? ex2(__fmaf_rn(__uint_as_float(v[i]), kLog2e, -lse2)) * gs : 0.f);
-            if (target && label >= cc * 32 && label < cc * 32 + 32)
+            if (label >= cc * 32 && label < cc * 32 + 32)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (label == cc * 32 + i) v[i] = __float_as_uint(__uint_as_float(v[i]) - gs);
@@ -374,9 +409,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             }
           }
         }
-      }
-      if constexpr (EPI == kStats) {
-        if (live && ncols > 0) g.stats[row * g.stat_cols + nt * 2 + half] = make_float2(m, sum);
       }
     }
     if (lane == 0) bulk_wait_group0();  // this warp's TMA stores complete before the CTA exits
