@@ -127,7 +127,7 @@ int device_sms() {
   return n;
 }
 
-int resident_ctas(const void* kernel, int threads) {
+int resident_ctas(const void* kernel, int threads, int smem) {
   int dev = 0;
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lock(g_dev_mu);
@@ -135,7 +135,7 @@ int resident_ctas(const void* kernel, int threads) {
   auto it = g_resident->find({dev, kernel});
   if (it != g_resident->end()) return it->second;
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) n = 1;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) n = 1;
   (*g_resident)[{dev, kernel}] = n;
   return n;
 }
@@ -488,8 +488,8 @@ lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m,
   if (y_is_fp32 < 0 || y_is_fp32 > 1) return set_error(LPQ_ERR_INVALID_ARG, "y_is_fp32 %d", y_is_fp32);
   if (m < 0 || w->rows < 0 || w->cols < 0) return set_error(LPQ_ERR_SHAPE, "negative dimension");
   if (w->cols % 32) return set_error(LPQ_ERR_SHAPE, "k %lld not a multiple of 32", (long long)w->cols);
-  if (w->rows > (int64_t)1 << 30 || w->cols > (int64_t)1 << 30 || m > (int64_t)1 << 30)
-    return set_error(LPQ_ERR_SHAPE, "dimension beyond 2^30");
+  if (w->rows > (int64_t)1 << 30 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "dimension beyond 2^30");
+  if (w->cols > (int64_t)1 << 19) return set_error(LPQ_ERR_SHAPE, "k %lld beyond 2^19", (long long)w->cols);
   if (m > 0 && w->cols > 0 && (ldx < w->cols || ldx % 8))
     return set_error(LPQ_ERR_SHAPE, "ldx %lld must be a multiple of 8, at least k = %lld", (long long)ldx, (long long)w->cols);
   if (m > 0 && w->rows > 0) {

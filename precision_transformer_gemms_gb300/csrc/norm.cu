@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lpq_device.cuh"
 
@@ -24,10 +25,29 @@ __device__ __forceinline__ T from_f32(float v) {
   if constexpr (sizeof(T) == 4) return v; else return __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ float load_param(const void* p, int w_fp32, int c) {
+  return w_fp32 ? static_cast<const float*>(p)[c] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c]);
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// The launch's max |y|: a single CTA stores it, several raise the value that
+// was set to 0 before the launch.
+__device__ __forceinline__ void store_amax(float* amax, float top) {
+  __shared__ float sh[32];
+  top = warp_max_xor(top, 32);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    top = warp_max_xor(threadIdx.x < blockDim.x / 32 ? sh[threadIdx.x] : 0.f, 32);
+    if (threadIdx.x == 0) {
+      if (gridDim.x == 1) *amax = top; else atomic_max_nonneg(amax, top);
+    }
+  }
 }
 
 constexpr int kRowThreads = 256;
@@ -45,13 +65,12 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
   return s;
 }
 
+// ------------------------------------------------------------------ rows beyond 16384 columns
 // One CTA per row, element by element: any size, stride and alignment.
-template <typename T, typename W>
-__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a, int w_fp32) {
   __shared__ float sh[kRowThreads / 32];
   const int n = (int)a.cols;
-  const W* w = static_cast<const W*>(a.weight);
-  const W* b = static_cast<const W*>(a.bias);
   float top = 0.f;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
@@ -67,7 +86,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a)
     const float rstd = 1.0f / sqrtf(block_sum(s, sh) / (float)n + a.eps);
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
       const float c = (to_f32(x[i]) - mean) * rstd;
-      const T o = from_f32<T>(c * (w ? to_f32(w[i]) : 1.0f) + (b ? to_f32(b[i]) : 0.0f));
+      const T o = from_f32<T>(c * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f) + (a.bias ? load_param(a.bias, w_fp32, i) : 0.0f));
       y[i] = o;
       top = absmax_acc(top, to_f32(o));
     }
@@ -76,17 +95,13 @@ __global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a)
       if (a.rstd) a.rstd[r] = rstd;
     }
   }
-  if (a.amax) {
-    top = warp_max_xor(top, 32);
-    if ((threadIdx.x & 31) == 0) atomic_max_nonneg(a.amax, top);
-  }
+  if (a.amax) store_amax(a.amax, top);
 }
 
-template <typename T, typename W>
-__global__ void __launch_bounds__(kRowThreads) norm_dx_row_kernel(const NormArgs a) {
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads) norm_dx_row_kernel(const NormArgs a, int w_fp32) {
   __shared__ float sh[kRowThreads / 32];
   const int n = (int)a.cols;
-  const W* w = static_cast<const W*>(a.weight);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
     const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
@@ -94,14 +109,14 @@ __global__ void __launch_bounds__(kRowThreads) norm_dx_row_kernel(const NormArgs
     const float mean = a.mean_in[r], rstd = a.rstd_in[r];
     float s1 = 0.f, s2 = 0.f;
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float g = to_f32(dy[i]) * (w ? to_f32(w[i]) : 1.0f);
+      const float g = to_f32(dy[i]) * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f);
       s1 += g;
       s2 += g * ((to_f32(x[i]) - mean) * rstd);
     }
     const float m1 = block_sum(s1, sh) / (float)n;
     const float m2 = block_sum(s2, sh) / (float)n;
     for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float g = to_f32(dy[i]) * (w ? to_f32(w[i]) : 1.0f);
+      const float g = to_f32(dy[i]) * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f);
       const float xh = (to_f32(x[i]) - mean) * rstd;
       dx[i] = from_f32<T>(rstd * (g - m1 - xh * m2));
     }
@@ -126,44 +141,566 @@ __global__ void __launch_bounds__(kRowThreads) norm_parts_kernel(const NormArgs 
   }
 }
 
-// Joins the parts: 32 columns per CTA, its 8 warps each summing every eighth
-// part, then the 8 sums in order.
-__global__ void __launch_bounds__(256) norm_join_kernel(const float* parts, int nparts, int64_t cols, float* dweight,
-                                                        float* dbias) {
-  __shared__ float sh[8][33];
+// Joins the parts: 32 columns per CTA, its 16 warps each summing every 16th
+// part, then the 16 sums in order.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float* parts, int nparts, int64_t cols,
+                                                                    float* dweight, float* dbias) {
+  __shared__ float sh[kJoinWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   const int which = blockIdx.y;  // 0: dweight, 1: dbias
   float* out = which ? dbias : dweight;
   if (!out) return;
   float s = 0.f;
-  if (c < cols)
-    for (int p = warp; p < nparts; p += 8) s += parts[((int64_t)p * 2 + which) * cols + c];
+  if (c < cols) {
+    const float* p = parts + which * cols + c;
+#pragma unroll 10
+    for (int i = warp; i < nparts; i += kJoinWarps) s += p[(int64_t)i * 2 * cols];
+  }
   sh[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < cols) {
-    for (int i = 1; i < 8; ++i) s += sh[i][lane];
+#pragma unroll
+    for (int i = 1; i < kJoinWarps; ++i) s += sh[i][lane];
     out[c] = s;
   }
 }
 
-template <typename T, typename W>
-lpq_status forward_t(const NormArgs& a, cudaStream_t s) {
-  const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
-  norm_row_kernel<T, W><<<grid, kRowThreads, 0, s>>>(a);
+// ------------------------------------------------------------------ rows in registers
+// A row belongs to TPR threads, each holding NE of its elements in FP32; a CTA
+// works on kBlock / TPR rows at a time and loops over the rest.  Vector form
+// (16-byte aligned rows of whole 16-byte vectors): every thread streams its own
+// vectors of the next rows through a ring in shared memory with cp.async, so
+// that the loads in flight take no registers and need no barrier (a thread
+// reads back only what it copied itself, and refills a slot after its values
+// have entered a sum).  Scalar form: any alignment and length.
+
+// Rows in flight for a ring stage of this many bytes: two CTAs of it fit an SM
+// while three stages do.
+constexpr int rows_ahead(int stage) {
+  return 4 * stage <= 98304 ? 4 : 3 * stage <= 98304 ? 3 : 2 * stage <= 200000 ? 2 : 1;
+}
+
+template <int TPR>
+struct RowGroup {
+  static constexpr int kBlock = TPR > 256 ? TPR : 256;
+  static constexpr int kGroups = kBlock / TPR;
+};
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sums of the N values of v over the TPR threads of a row group.  `sh`
+// alternates between two places from call to call, so one barrier is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (*sh)[32]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+  if constexpr (TPR > 32) {
+    constexpr int kW = TPR / 32;
+    const int w0 = (int)threadIdx.x / TPR * kW;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) sh[i][threadIdx.x / 32] = v[i];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+      if constexpr (kW >= 4) {
+#pragma unroll
+        for (int j = 0; j < kW; j += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(&sh[i][w0 + j]);
+          s += (q.x + q.y) + (q.z + q.w);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) s += sh[i][w0 + j];
+      }
+      v[i] = s;
+    }
+  }
+}
+
+// Column of element i of thread `tid` of a row: vectors are dealt out in turn.
+template <typename T, bool VEC, int TPR>
+__device__ __forceinline__ int column_of(int tid, int i) {
+  if constexpr (VEC) {
+    constexpr int V = 16 / (int)sizeof(T);
+    return ((i / V) * TPR + tid) * V + i % V;
+  } else {
+    return i * TPR + tid;
+  }
+}
+
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+
+// 16 bytes <-> FP32 pairs (8 bf16 values or 4 floats).
+template <typename T>
+__device__ __forceinline__ void unpack_vector(const uint4& v, float2* f) {
+  if constexpr (sizeof(T) == 2) {
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
+  } else {
+    f[0] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_vector(const float2* f) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __float22bfloat162_rn(f[j]);
+      u[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+  }
+}
+
+// 2 NP consecutive parameters from column c on (weight or bias, bf16 or FP32).
+template <int NP>
+__device__ __forceinline__ void load_params(const void* p, int w_fp32, int c, float2* f) {
+  if (w_fp32) {
+#pragma unroll
+    for (int j = 0; j < NP; j += 2)
+      unpack_vector<float>(__ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + c + 2 * j)), f + j);
+  } else if constexpr (NP == 4) {
+    unpack_vector<__nv_bfloat16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + c)), f);
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + c));
+    f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+  }
+}
+
+// The parameters of a thread's vectors.  HELD (parameters of the rows' own
+// type): kept as they are in registers over all rows; else read for each row
+// (both would be 2 registers per element and cost resident warps).
+template <typename T, int TPR, int NE, bool HELD>
+struct Params {
+  static constexpr int V = 16 / (int)sizeof(T), NV = NE / V;
+  uint4 held[HELD ? NV : 1];
+  const void* p;
+  int w_fp32;
+  __device__ __forceinline__ Params(const void* param, int fp32, int tid, int n, uint32_t fill) : p(param), w_fp32(fp32) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        held[v] = make_uint4(fill, fill, fill, fill);
+        if (p && c < n) held[v] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + c));
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int v, int c, float2 (&f)[V / 2], float none) const {
+    if constexpr (HELD) {
+      unpack_vector<T>(held[v], f);
+    } else if (p) {
+      load_params<V / 2>(p, w_fp32, c, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) f[j] = pair_of(none);
+    }
+  }
+};
+// 1.0 in every element of a register of T.
+template <typename T>
+constexpr uint32_t ones() { return sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u; }
+
+// max of |values| of a stored vector, two bf16 values at a time (NaN ignored).
+template <typename T>
+__device__ __forceinline__ void absmax_vector(uint32_t& top, const uint4& q) {
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 2)
+      asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.bf16x2 %0, %0, t;\n\t}" : "+r"(top) : "r"(u[j]));
+    else
+      top = __float_as_uint(absmax_acc(__uint_as_float(top), __uint_as_float(u[j])));
+  }
+}
+template <typename T>
+__device__ __forceinline__ float absmax_value(uint32_t top) {
+  if constexpr (sizeof(T) == 2) return fmaxf(bf16_lo(top), bf16_hi(top)); else return __uint_as_float(top);
+}
+
+// The elements of one row tensor of a thread as pairs, from its ring slot or
+// from memory; 0 past the row's end.
+template <typename T, bool VEC, int TPR, int NE>
+__device__ __forceinline__ void take_row(const uint4* slot, int stride, const T* row, int tid, int n, float2 (&f)[NE / 2]) {
+  if constexpr (VEC) {
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int v = 0; v < NE / V; ++v) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (column_of<T, true, TPR>(tid, v * V) < n) q = slot[v * stride];
+      unpack_vector<T>(q, f + v * V / 2);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE; i += 2) {
+      const int c = column_of<T, false, TPR>(tid, i), d = column_of<T, false, TPR>(tid, i + 1);
+      f[i / 2] = make_float2(c < n ? to_f32(row[c]) : 0.f, d < n ? to_f32(row[d]) : 0.f);
+    }
+  }
+}
+
+// f(i, in): for the pairs of a thread, whether their elements lie in the row
+// (a vector's all do or none; a scalar form's pair may be cut).
+template <typename T, bool VEC, int TPR, int NE, typename F>
+__device__ __forceinline__ void each_pair(int tid, int n, F f) {
+  if constexpr (VEC) {
+    constexpr int V = 16 / (int)sizeof(T);
+#pragma unroll
+    for (int v = 0; v < NE / V; ++v)
+      if (column_of<T, true, TPR>(tid, v * V) < n)
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) f(v * V / 2 + j, true, true);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i)
+      f(i, column_of<T, false, TPR>(tid, 2 * i) < n, column_of<T, false, TPR>(tid, 2 * i + 1) < n);
+  }
+}
+
+template <typename T, bool VEC, bool HELD, int TPR, int NE>
+__global__ void __launch_bounds__(RowGroup<TPR>::kBlock) norm_kernel(const NormArgs a, int w_fp32) {
+  constexpr int kBlock = RowGroup<TPR>::kBlock, kGroups = RowGroup<TPR>::kGroups;
+  constexpr int V = 16 / (int)sizeof(T), NV = NE / V;
+  constexpr int kAhead = rows_ahead(NV * 16 * kBlock);
+  extern __shared__ uint4 ring[];  // [kAhead][NV][kBlock]
+  __shared__ alignas(16) float sh[2][1][32];
+  const int tid = threadIdx.x % TPR, n = (int)a.cols;
+  const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
+  const float inv_n = 1.0f / (float)n;
+  // the row whose copy is next: its number and this thread's first vector
+  int64_t ahead = first;
+  const T* ahead_x = static_cast<const T*>(a.x) + first * a.ldx + tid * V;
+  const int64_t x_step = step * a.ldx;
+  auto copy = [&](int slot) {
+    if constexpr (VEC) {
+      if (ahead < a.rows) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (column_of<T, true, TPR>(tid, v * V) < n)
+            cp_async16(&ring[(slot * NV + v) * kBlock + threadIdx.x], ahead_x + v * TPR * V);
+      }
+      ahead += step;
+      ahead_x += x_step;
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) copy(s);
+  constexpr bool kHeld = VEC && HELD;
+  const Params<T, TPR, VEC ? NE : V, kHeld> weight(a.weight, w_fp32, tid, n, ones<T>()), bias(a.bias, w_fp32, tid, n, 0u);
+  uint32_t top = 0;
+  float top_scalar = 0.f;
+  int slot = 0;
+  T* y = static_cast<T*>(a.out) + first * a.ldo;
+  const int64_t y_step = step * a.ldo;
+  for (int64_t r = first; r < a.rows; r += step, y += y_step) {
+    float2 x[NE / 2];
+    if constexpr (VEC) cp_async_wait<kAhead - 1>();
+    take_row<T, VEC, TPR, NE>(&ring[slot * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.x) + r * a.ldx, tid, n, x);
+    float2 s2 = pair_of(0.f);
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) s2 = __fadd2_rn(s2, x[i]);
+    float s[1] = {s2.x + s2.y};
+    group_sum<TPR, 1>(s, sh[0]);
+    copy(slot);
+    slot = (slot + 1) % kAhead;
+    const float mean = s[0] * inv_n;
+    s2 = pair_of(0.f);
+    each_pair<T, VEC, TPR, NE>(tid, n, [&](int i, bool in0, bool in1) {
+      x[i] = __fadd2_rn(x[i], pair_of(-mean));
+      if constexpr (!VEC) x[i] = make_float2(in0 ? x[i].x : 0.f, in1 ? x[i].y : 0.f);
+      s2 = __ffma2_rn(x[i], x[i], s2);
+    });
+    s[0] = s2.x + s2.y;
+    group_sum<TPR, 1>(s, sh[1]);
+    const float rstd = 1.0f / sqrtf(s[0] * inv_n + a.eps);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        if (c < n) {
+          float2 w[V / 2], b[V / 2], o[V / 2];
+          weight.get(v, c, w, 1.0f);
+          bias.get(v, c, b, 0.0f);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) o[j] = __ffma2_rn(__fmul2_rn(x[v * V / 2 + j], pair_of(rstd)), w[j], b[j]);
+          const uint4 q = pack_vector<T>(o);
+          *reinterpret_cast<uint4*>(y + c) = q;
+          if (a.amax) absmax_vector<T>(top, q);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = column_of<T, false, TPR>(tid, i);
+        if (c < n) {
+          float o = (i & 1 ? x[i / 2].y : x[i / 2].x) * rstd;
+          if (a.weight) o *= load_param(a.weight, w_fp32, c);
+          if (a.bias) o += load_param(a.bias, w_fp32, c);
+          const T q = from_f32<T>(o);
+          y[c] = q;
+          top_scalar = absmax_acc(top_scalar, to_f32(q));
+        }
+      }
+    }
+    if (tid == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+  if constexpr (VEC) cp_async_wait<0>();
+  if (a.amax) store_amax(a.amax, VEC ? absmax_value<T>(top) : top_scalar);
+}
+
+// dx of each row; the parameter gradients' sums over this CTA's rows go to its
+// part (a.parts [CTA][dweight, dbias][cols]), which norm_join_kernel adds up.
+template <typename T, bool VEC, bool HELD, int TPR, int NE>
+__global__ void __launch_bounds__(RowGroup<TPR>::kBlock) norm_backward_kernel(const NormArgs a, int w_fp32) {
+  constexpr int kBlock = RowGroup<TPR>::kBlock, kGroups = RowGroup<TPR>::kGroups;
+  constexpr int V = 16 / (int)sizeof(T), NV = NE / V;
+  constexpr int kAhead = rows_ahead(2 * NV * 16 * kBlock);
+  extern __shared__ uint4 ring[];  // [kAhead][x, dy][NV][kBlock]
+  __shared__ alignas(16) float sh[2][2][32];
+  const int tid = threadIdx.x % TPR, n = (int)a.cols;
+  const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
+  const float inv_n = 1.0f / (float)n;
+  // the row whose copy is next: its number and this thread's first vectors
+  int64_t ahead = first;
+  const T* ahead_x = static_cast<const T*>(a.x) + first * a.ldx + tid * V;
+  const T* ahead_dy = static_cast<const T*>(a.dy) + first * a.lddy + tid * V;
+  const int64_t x_step = step * a.ldx, dy_step = step * a.lddy;
+  auto copy = [&](int slot) {
+    if constexpr (VEC) {
+      if (ahead < a.rows) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (column_of<T, true, TPR>(tid, v * V) < n) {
+            cp_async16(&ring[(slot * 2 * NV + v) * kBlock + threadIdx.x], ahead_x + v * TPR * V);
+            cp_async16(&ring[((slot * 2 + 1) * NV + v) * kBlock + threadIdx.x], ahead_dy + v * TPR * V);
+          }
+      }
+      ahead += step;
+      ahead_x += x_step;
+      ahead_dy += dy_step;
+      cp_async_commit();
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kAhead; ++s) copy(s);
+  float2 dw[NE / 2], db[NE / 2];
+#pragma unroll
+  for (int i = 0; i < NE / 2; ++i) dw[i] = db[i] = pair_of(0.f);
+  constexpr bool kHeld = VEC && HELD;
+  const Params<T, TPR, VEC ? NE : V, kHeld> weight(a.weight, w_fp32, tid, n, ones<T>());
+  int slot = 0, turn = 0;
+  float mean = first < a.rows ? a.mean_in[first] : 0.f, rstd = first < a.rows ? a.rstd_in[first] : 0.f;
+  T* dx = static_cast<T*>(a.out) + first * a.ldo;
+  const int64_t dx_step = step * a.ldo;
+  for (int64_t r = first; r < a.rows; r += step, dx += dx_step) {
+    // the next row's statistics are on their way while this row is worked on
+    const int64_t rn = r + step < a.rows ? r + step : r;
+    const float next_mean = a.mean_in[rn], next_rstd = a.rstd_in[rn];
+    float2 x[NE / 2], g[NE / 2];
+    if constexpr (VEC) cp_async_wait<kAhead - 1>();
+    take_row<T, VEC, TPR, NE>(&ring[slot * 2 * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.x) + r * a.ldx, tid, n, x);
+    take_row<T, VEC, TPR, NE>(&ring[(slot * 2 + 1) * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.dy) + r * a.lddy, tid, n, g);
+    // (past the row's end g is 0, and with it everything that x enters)
+#pragma unroll
+    for (int i = 0; i < NE / 2; ++i) {
+      x[i] = __fmul2_rn(__fadd2_rn(x[i], pair_of(-mean)), pair_of(rstd));
+      if constexpr (!VEC)
+        x[i] = make_float2(column_of<T, false, TPR>(tid, 2 * i) < n ? x[i].x : 0.f,
+                           column_of<T, false, TPR>(tid, 2 * i + 1) < n ? x[i].y : 0.f);
+      dw[i] = __ffma2_rn(g[i], x[i], dw[i]);
+      db[i] = __fadd2_rn(db[i], g[i]);
+    }
+    float2 s0 = pair_of(0.f), s1 = pair_of(0.f);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        if (c < n) {
+          float2 w[V / 2];
+          weight.get(v, c, w, 1.0f);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) g[v * V / 2 + j] = __fmul2_rn(g[v * V / 2 + j], w[j]);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            s0 = __fadd2_rn(s0, g[v * V / 2 + j]);
+            s1 = __ffma2_rn(g[v * V / 2 + j], x[v * V / 2 + j], s1);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE / 2; ++i) {
+        if (a.weight) {
+          const int c = column_of<T, false, TPR>(tid, 2 * i), d = column_of<T, false, TPR>(tid, 2 * i + 1);
+          if (c < n) g[i].x *= load_param(a.weight, w_fp32, c);
+          if (d < n) g[i].y *= load_param(a.weight, w_fp32, d);
+        }
+        s0 = __fadd2_rn(s0, g[i]);
+        s1 = __ffma2_rn(g[i], x[i], s1);
+      }
+    }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
+    group_sum<TPR, 2>(s, sh[turn]);
+    turn ^= 1;
+    copy(slot);
+    slot = (slot + 1) % kAhead;
+    const float2 m1 = pair_of(-s[0] * inv_n), m2 = pair_of(-s[1] * inv_n);
+    if constexpr (VEC) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        if (c < n) {
+          float2 o[V / 2];
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j)
+            o[j] = __fmul2_rn(__ffma2_rn(x[v * V / 2 + j], m2, __fadd2_rn(g[v * V / 2 + j], m1)), pair_of(rstd));
+          *reinterpret_cast<uint4*>(dx + c) = pack_vector<T>(o);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = column_of<T, false, TPR>(tid, i);
+        const float gi = i & 1 ? g[i / 2].y : g[i / 2].x, xi = i & 1 ? x[i / 2].y : x[i / 2].x;
+        if (c < n) dx[c] = from_f32<T>(rstd * __fmaf_rn(xi, m2.x, gi + m1.x));
+      }
+    }
+    mean = next_mean;
+    rstd = next_rstd;
+  }
+  if constexpr (VEC) cp_async_wait<0>();
+  if (!a.parts) return;
+  float* part = a.parts + (int64_t)blockIdx.x * 2 * n;
+  // the CTA's row groups in order, through the ring's memory
+  float* all = reinterpret_cast<float*>(ring);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const float2 v = which ? db[i / 2] : dw[i / 2];
+      all[(threadIdx.x / TPR) * TPR * NE + column_of<T, VEC, TPR>(tid, i)] = i & 1 ? v.y : v.x;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += kBlock) {
+      float s = 0.f;
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) s += all[q * TPR * NE + c];
+      part[(int64_t)which * n + c] = s;
+    }
+  }
+}
+
+// Whether rows can be read and written 16 bytes at a time.
+bool vector_rows(const NormArgs& a, size_t elem, bool backward) {
+  auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+  const int64_t per = (int64_t)(16 / elem);
+  if (a.cols % per || a.ldx % per || a.ldo % per || !ok(a.x) || !ok(a.out) || !ok(a.weight) || !ok(a.bias)) return false;
+  return !backward || (ok(a.dy) && a.lddy % per == 0);
+}
+
+lpq_status clear_amax(const NormArgs& a, int grid, cudaStream_t s) {
+  if (!a.amax || grid == 1) return LPQ_OK;
+  return cuda_check(cudaMemsetAsync(a.amax, 0, sizeof(float), s), "cudaMemsetAsync(amax)");
+}
+
+template <typename T, bool VEC, bool HELD, int TPR, int NE>
+lpq_status run_forward(const NormArgs& a, int w_fp32, cudaStream_t s) {
+  constexpr int kBlock = RowGroup<TPR>::kBlock, kGroups = RowGroup<TPR>::kGroups;
+  constexpr int kStage = NE * (int)sizeof(T) * kBlock, kSmem = VEC ? rows_ahead(kStage) * kStage : 0;
+  const void* kernel = reinterpret_cast<const void*>(norm_kernel<T, VEC, HELD, TPR, NE>);
+  lpq_status st = set_smem_attr(kernel, kSmem);
+  if (st != LPQ_OK) return st;
+  const int64_t most = (int64_t)device_sms() * resident_ctas(kernel, kBlock, kSmem);
+  const int grid = (int)std::min<int64_t>((a.rows + kGroups - 1) / kGroups, most);
+  if ((st = clear_amax(a, grid, s)) != LPQ_OK) return st;
+  norm_kernel<T, VEC, HELD, TPR, NE><<<grid, kBlock, kSmem, s>>>(a, w_fp32);
   return cuda_check(cudaGetLastError(), "layer norm launch");
 }
 
-template <typename T, typename W>
-lpq_status backward_t(const NormArgs& a, cudaStream_t s) {
+template <typename T, bool VEC, bool HELD, int TPR, int NE>
+lpq_status run_backward(const NormArgs& a, int w_fp32, int& parts, cudaStream_t s) {
+  constexpr int kBlock = RowGroup<TPR>::kBlock, kGroups = RowGroup<TPR>::kGroups;
+  constexpr int kStage = 2 * NE * (int)sizeof(T) * kBlock, kRing = VEC ? rows_ahead(kStage) * kStage : 0;
+  constexpr int kJoin = kBlock * NE * 4;
+  constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+  lpq_status st = set_smem_attr(reinterpret_cast<const void*>(norm_backward_kernel<T, VEC, HELD, TPR, NE>), kSmem);
+  if (st != LPQ_OK) return st;
+  parts = (int)std::min<int64_t>((a.rows + kGroups - 1) / kGroups, norm_parts(a.rows, a.cols));
+  norm_backward_kernel<T, VEC, HELD, TPR, NE><<<parts, kBlock, kSmem, s>>>(a, w_fp32);
+  return cuda_check(cudaGetLastError(), "layer norm backward launch");
+}
+
+// Threads per row and elements per thread by width; beyond 16384 columns the
+// rows are read from memory again.
+template <typename F>
+lpq_status by_width(int64_t cols, F f) {
+  if (cols <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
+  if (cols <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+  if (cols <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 16>{});
+  if (cols <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 16>{});
+  return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 32>{});
+}
+
+template <typename T>
+lpq_status forward_t(const NormArgs& a, int w_fp32, cudaStream_t s) {
+  if (a.cols <= 16384) {
+    const bool vec = vector_rows(a, sizeof(T), false), held = (sizeof(T) == 4) == (w_fp32 != 0);
+    return by_width(a.cols, [&](auto tpr, auto ne) {
+      return !vec ? run_forward<T, false, false, tpr, ne>(a, w_fp32, s)
+             : held ? run_forward<T, true, true, tpr, ne>(a, w_fp32, s) : run_forward<T, true, false, tpr, ne>(a, w_fp32, s);
+    });
+  }
   const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
-  norm_dx_row_kernel<T, W><<<grid, kRowThreads, 0, s>>>(a);
-  lpq_status st = cuda_check(cudaGetLastError(), "layer norm backward launch");
-  if (st != LPQ_OK || (!a.dweight && !a.dbias)) return st;
-  const int parts = (int)norm_parts(a.rows, a.cols);
-  norm_parts_kernel<T><<<dim3((unsigned)((a.cols + kRowThreads - 1) / kRowThreads), parts), kRowThreads, 0, s>>>(a, parts);
-  if ((st = cuda_check(cudaGetLastError(), "layer norm parts launch")) != LPQ_OK) return st;
-  norm_join_kernel<<<dim3((unsigned)((a.cols + 31) / 32), 2), 256, 0, s>>>(a.parts, parts, a.cols, a.dweight, a.dbias);
+  lpq_status st = clear_amax(a, grid, s);
+  if (st != LPQ_OK) return st;
+  norm_row_kernel<T><<<grid, kRowThreads, 0, s>>>(a, w_fp32);
+  return cuda_check(cudaGetLastError(), "layer norm launch");
+}
+
+template <typename T>
+lpq_status backward_t(NormArgs a, int w_fp32, cudaStream_t s) {
+  int parts = 0;
+  lpq_status st;
+  if (!a.dweight && !a.dbias) a.parts = nullptr;
+  if (a.cols <= 16384) {
+    const bool vec = vector_rows(a, sizeof(T), true), held = (sizeof(T) == 4) == (w_fp32 != 0);
+    st = by_width(a.cols, [&](auto tpr, auto ne) {
+      return !vec ? run_backward<T, false, false, tpr, ne>(a, w_fp32, parts, s)
+             : held ? run_backward<T, true, true, tpr, ne>(a, w_fp32, parts, s)
+                    : run_backward<T, true, false, tpr, ne>(a, w_fp32, parts, s);
+    });
+    if (st != LPQ_OK || !a.parts) return st;
+  } else {
+    const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
+    norm_dx_row_kernel<T><<<grid, kRowThreads, 0, s>>>(a, w_fp32);
+    st = cuda_check(cudaGetLastError(), "layer norm backward launch");
+    if (st != LPQ_OK || !a.parts) return st;
+    parts = (int)norm_parts(a.rows, a.cols);
+    norm_parts_kernel<T><<<dim3((unsigned)((a.cols + kRowThreads - 1) / kRowThreads), parts), kRowThreads, 0, s>>>(a, parts);
+    if ((st = cuda_check(cudaGetLastError(), "layer norm parts launch")) != LPQ_OK) return st;
+  }
+  norm_join_kernel<<<dim3((unsigned)((a.cols + 31) / 32), 2), 32 * kJoinWarps, 0, s>>>(a.parts, parts, a.cols, a.dweight, a.dbias);
   return cuda_check(cudaGetLastError(), "layer norm join launch");
 }
 
@@ -174,14 +711,9 @@ int64_t norm_parts(int64_t rows, int64_t cols) {
 }
 
 lpq_status launch_norm(const NormArgs& a, int32_t x_type, int32_t w_type, cudaStream_t s) {
-  if (a.amax) {
-    lpq_status st = cuda_check(cudaMemsetAsync(a.amax, 0, sizeof(float), s), "cudaMemsetAsync(amax)");
-    if (st != LPQ_OK) return st;
-  }
-  if (a.rows == 0) return LPQ_OK;
-  if (x_type == LPQ_TYPE_BF16)
-    return w_type == LPQ_TYPE_BF16 ? forward_t<__nv_bfloat16, __nv_bfloat16>(a, s) : forward_t<__nv_bfloat16, float>(a, s);
-  return w_type == LPQ_TYPE_BF16 ? forward_t<float, __nv_bfloat16>(a, s) : forward_t<float, float>(a, s);
+  if (a.rows == 0) return clear_amax(a, 0, s);
+  const int w_fp32 = w_type == LPQ_TYPE_FP32;
+  return x_type == LPQ_TYPE_BF16 ? forward_t<__nv_bfloat16>(a, w_fp32, s) : forward_t<float>(a, w_fp32, s);
 }
 
 lpq_status launch_norm_backward(const NormArgs& a, int32_t x_type, int32_t w_type, cudaStream_t s) {
@@ -192,10 +724,8 @@ lpq_status launch_norm_backward(const NormArgs& a, int32_t x_type, int32_t w_typ
         return st;
     return LPQ_OK;
   }
-  if (x_type == LPQ_TYPE_BF16)
-    return w_type == LPQ_TYPE_BF16 ? backward_t<__nv_bfloat16, __nv_bfloat16>(a, s)
-                                   : backward_t<__nv_bfloat16, float>(a, s);
-  return w_type == LPQ_TYPE_BF16 ? backward_t<float, __nv_bfloat16>(a, s) : backward_t<float, float>(a, s);
+  const int w_fp32 = w_type == LPQ_TYPE_FP32;
+  return x_type == LPQ_TYPE_BF16 ? backward_t<__nv_bfloat16>(a, w_fp32, s) : backward_t<float>(a, w_fp32, s);
 }
 
 }  // namespace lpq

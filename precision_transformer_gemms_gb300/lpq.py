@@ -107,7 +107,7 @@ def lib():
                                   ctypes.POINTER(GemmOpts), P]
         SZ, PSZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
         L.lpq_layer_norm.argtypes = [P, I64, I32, P, P, I32, I64, I64, F, P, I64, P, P, P, P]
-        L.lpq_layer_norm_workspace.argtypes = [I64, I64, PSZ]
+        L.lpq_layer_norm_workspace.argtypes = [I64, I64, PSZ]  # a c_size_t passes by reference
         L.lpq_layer_norm_backward.argtypes = [P, I64, P, I64, I32, P, P, P, I32, I64, I64, P, I64, P, P, P, SZ, P]
         L.lpq_linear_ce_workspace.argtypes = [I64, I64, I64, I32, I64, PSZ]
         L.lpq_linear_ce.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, SZ, P]
@@ -294,136 +294,133 @@ def gemm(layout, a, b, c=None, out_fp32=False, stream=None, path=None):
 
 # ----------------------------------------------------------------- around the linear layers
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
+_BF16, _FP32 = torch.bfloat16, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _new(stream, shape, dtype, device):
+def _new(like, stream, shape, dtype):
     """A device buffer the call writes: on a stream other than the current one
     its memory is not reused before that stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _rows(x, name):
-    """Checks a [rows, cols] matrix with contiguous rows and returns its leading dimension."""
-    assert x.is_cuda and x.dim() == 2, f"{name} must be a CUDA matrix"
-    assert x.shape[1] <= 1 or x.stride(1) == 1, f"{name} must have contiguous rows"
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]  # the library refuses rows that overlap
+def _stream_of(t, stream):
+    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
 
 
-def _vector(v, n, name, dtype=None):
-    assert v.is_cuda and v.is_contiguous() and v.numel() == n, f"{name} must be a contiguous CUDA vector of {n}"
-    assert dtype is None or v.dtype == dtype, f"{name} must be {dtype}"
+def _ld(x, rows, cols):
+    """Leading dimension of a CUDA matrix with contiguous rows (the library
+    refuses rows that overlap)."""
+    assert x.is_cuda and (cols <= 1 or x.stride(1) == 1), "a CUDA matrix with contiguous rows is needed"
+    return x.stride(0) if rows > 1 else cols
 
 
-def _norm_params(x, weight, bias):
-    assert x.dtype in _TYPES, "layer norm runs on bf16 and fp32"
-    w_type = TYPE_FP32
-    for name, v in (("weight", weight), ("bias", bias)):
-        if v is not None:
-            _vector(v, x.shape[1], name)
-            assert v.dtype in _TYPES, f"{name} must be bf16 or fp32"
-            w_type = _TYPES[v.dtype]
-    assert weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias must have one type"
-    return w_type
+def _is_vector(v, n, dtype):
+    return v.dtype is dtype and v.is_cuda and v.numel() == n and v.is_contiguous()
+
+
+def _check_params(cols, weight, bias):
+    """lpq_type of the parameters."""
+    for v in (weight, bias):
+        assert v is None or (v.dtype in _TYPES and _is_vector(v, cols, v.dtype)), \
+            f"weight and bias must be contiguous bf16 or fp32 CUDA vectors of {cols}"
+    assert weight is None or bias is None or weight.dtype is bias.dtype, "weight and bias must have one type"
+    return _TYPES[weight.dtype] if weight is not None else _TYPES[bias.dtype] if bias is not None else TYPE_FP32
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, amax=None, out=None, stream=None):
     """lpq_layer_norm on a bf16 or fp32 CUDA tensor x [rows, cols]: returns
     (y, mean, rstd).  `amax` (one FP32, optional) receives max |y|, ready for
     quantize(..., lpq.GIVEN_AMAX)."""
-    ldx = _rows(x, "x")
-    w_type = _norm_params(x, weight, bias)
     rows, cols = x.shape
+    dtype = x.dtype
+    assert dtype in _TYPES, "layer norm runs on bf16 and fp32"
+    w_type = _check_params(cols, weight, bias)
+    assert amax is None or _is_vector(amax, 1, _FP32), "amax must be one fp32"
     if out is None:
-        out = _new(stream, (rows, cols), x.dtype, x.device)
-    assert out.dtype == x.dtype and out.shape == x.shape
-    if amax is not None:
-        _vector(amax, 1, "amax", torch.float32)
-    stats = _new(stream, (2, rows), torch.float32, x.device)
-    mean, rstd = stats[0], stats[1]
-    _check(lib().lpq_layer_norm(x.data_ptr(), ldx, _TYPES[x.dtype], _ptr(weight), _ptr(bias), w_type, rows, cols, eps,
-                                out.data_ptr(), _rows(out, "out"), mean.data_ptr(), rstd.data_ptr(), _ptr(amax),
-                                _stream(stream)))
+        out, ldo = _new(x, stream, (rows, cols), dtype), cols
+    else:
+        assert out.dtype is dtype and out.shape == x.shape, "out must be like x"
+        ldo = _ld(out, rows, cols)
+    mean, rstd = _new(x, stream, (2, rows), _FP32).unbind(0)
+    _check(lib().lpq_layer_norm(x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype], _ptr(weight), _ptr(bias), w_type,
+                                rows, cols, eps, out.data_ptr(), ldo, mean.data_ptr(), rstd.data_ptr(), _ptr(amax),
+                                _stream_of(x, stream)))
     return out, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, param_grads=True, stream=None):
     """lpq_layer_norm_backward: returns (dx, dweight, dbias); the parameter
     gradients are FP32 (None, None without `param_grads`)."""
-    assert dy.shape == x.shape and dy.dtype == x.dtype, "dy must be like x"
-    lddy, ldx = _rows(dy, "dy"), _rows(x, "x")
-    w_type = _norm_params(x, weight, None)
     rows, cols = x.shape
-    _vector(mean, rows, "mean", torch.float32)
-    _vector(rstd, rows, "rstd", torch.float32)
-    dx = _new(stream, (rows, cols), x.dtype, x.device)
+    dtype = x.dtype
+    assert dtype in _TYPES, "layer norm runs on bf16 and fp32"
+    assert dy.dtype is dtype and dy.shape == x.shape, "dy must be like x"
+    w_type = _check_params(cols, weight, None)
+    assert _is_vector(mean, rows, _FP32) and _is_vector(rstd, rows, _FP32), f"mean and rstd must be fp32 vectors of {rows}"
+    L = lib()
+    dx = _new(x, stream, (rows, cols), dtype)
     dweight = dbias = ws = None
-    need = 0
+    need = ctypes.c_size_t(0)
     if param_grads:
-        n = ctypes.c_size_t()
-        _check(lib().lpq_layer_norm_workspace(rows, cols, ctypes.byref(n)))
-        need = n.value
-        dweight, dbias = _new(stream, (2, cols), torch.float32, x.device).unbind(0)
-        ws = _new(stream, need, torch.uint8, x.device)
-    _check(lib().lpq_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, _TYPES[x.dtype], mean.data_ptr(),
-                                         rstd.data_ptr(), _ptr(weight), w_type, rows, cols, dx.data_ptr(), cols,
-                                         _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream(stream)))
+        _check(L.lpq_layer_norm_workspace(rows, cols, need))
+        dweight, dbias = _new(x, stream, (2, cols), _FP32).unbind(0)
+        ws = _new(x, stream, need.value, torch.uint8)
+    _check(L.lpq_layer_norm_backward(dy.data_ptr(), _ld(dy, rows, cols), x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype],
+                                     mean.data_ptr(), rstd.data_ptr(), _ptr(weight), w_type, rows, cols, dx.data_ptr(),
+                                     cols, _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream_of(x, stream)))
     return dx, dweight, dbias
 
 
 def _ce_args(h, w, labels):
-    assert h.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, "h and w must be bf16"
-    ldh, ldw = _rows(h, "h"), _rows(w, "w")
-    assert h.shape[1] == w.shape[1], "h and w must have the same number of columns"
-    _vector(labels, h.shape[0], "labels", torch.int64)
-    return ldh, ldw
-
-
-def _ce_workspace(t, v, d, backward, piece, stream, device):
-    n = ctypes.c_size_t()
-    _check(lib().lpq_linear_ce_workspace(t, v, d, backward, piece, ctypes.byref(n)))
-    return _new(stream, n.value, torch.uint8, device), n.value
+    (t, d), (v, dw) = h.shape, w.shape
+    assert h.dtype is _BF16 and w.dtype is _BF16 and d == dw, "h and w must be bf16 with the same number of columns"
+    assert _is_vector(labels, t, torch.int64), f"labels must be {t} int64"
+    return t, d, v, _ld(h, t, d), _ld(w, v, d)
 
 
 def linear_cross_entropy(h, w, labels, stream=None):
     """lpq_linear_ce: the softmax cross entropy of the logits h w^T for hidden
     states h [t, d] and vocabulary weights w [v, d] (bf16) against labels [t]
     (int64; outside 0 .. v - 1: no target, loss 0).  Returns (loss, lse) [t] FP32."""
-    ldh, ldw = _ce_args(h, w, labels)
-    (t, d), v = h.shape, w.shape[0]
-    loss, lse = _new(stream, (2, t), torch.float32, h.device).unbind(0)
-    ws, need = _ce_workspace(t, v, d, 0, 0, stream, h.device)
-    _check(lib().lpq_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), t, v, d, loss.data_ptr(),
-                               lse.data_ptr(), ws.data_ptr(), need, _stream(stream)))
+    t, d, v, ldh, ldw = _ce_args(h, w, labels)
+    L = lib()
+    need = ctypes.c_size_t()
+    _check(L.lpq_linear_ce_workspace(t, v, d, 0, 0, need))
+    loss, lse = _new(h, stream, (2, t), _FP32).unbind(0)
+    ws = _new(h, stream, need.value, torch.uint8)
+    _check(L.lpq_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), t, v, d, loss.data_ptr(),
+                           lse.data_ptr(), ws.data_ptr(), need, _stream_of(h, stream)))
     return loss, lse
 
 
 def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, vocab_piece=0, stream=None):
     """lpq_linear_ce_backward: the gradients (dh [t, d], dw [v, d]) of
     sum(dloss * loss) for dloss [t] FP32 and the forward's lse."""
-    ldh, ldw = _ce_args(h, w, labels)
-    (t, d), v = h.shape, w.shape[0]
-    _vector(lse, t, "lse", torch.float32)
-    _vector(dloss, t, "dloss", torch.float32)
-    dtype = torch.float32 if out_fp32 else torch.bfloat16
-    dh, dw = _new(stream, (t, d), dtype, h.device), _new(stream, (v, d), dtype, h.device)
-    ws, need = _ce_workspace(t, v, d, 1, vocab_piece, stream, h.device)
-    _check(lib().lpq_linear_ce_backward(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
-                                        dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32),
-                                        vocab_piece, ws.data_ptr(), need, _stream(stream)))
+    t, d, v, ldh, ldw = _ce_args(h, w, labels)
+    assert _is_vector(lse, t, _FP32) and _is_vector(dloss, t, _FP32), f"lse and dloss must be {t} fp32"
+    L = lib()
+    need = ctypes.c_size_t()
+    _check(L.lpq_linear_ce_workspace(t, v, d, 1, vocab_piece, need))
+    dtype = _FP32 if out_fp32 else _BF16
+    dh, dw = _new(h, stream, (t, d), dtype), _new(h, stream, (v, d), dtype)
+    ws = _new(h, stream, need.value, torch.uint8)
+    _check(L.lpq_linear_ce_backward(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
+                                    dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32), vocab_piece,
+                                    ws.data_ptr(), need, _stream_of(h, stream)))
     return dh, dw
 
 
 def matvec(x, w, out_fp32=False, stream=None):
     """lpq_matvec: x [m, k] bf16 (a few tokens, not quantized) times the 4-bit
     weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n]."""
-    ldx = _rows(x, "x")
-    assert x.dtype == torch.bfloat16 and x.shape[1] == w.cols, "x must be bf16 [m, k]"
-    m = x.shape[0]
-    y = _new(stream, (m, w.rows), torch.float32 if out_fp32 else torch.bfloat16, x.device)
-    _check(lib().lpq_matvec(ctypes.byref(w.view()), x.data_ptr(), ldx, m, y.data_ptr(), int(out_fp32), _stream(stream)))
+    m, k = x.shape
+    assert x.dtype is _BF16 and k == w.cols, "x must be bf16 [m, k]"
+    y = _new(x, stream, (m, w.rows), _FP32 if out_fp32 else _BF16)
+    _check(lib().lpq_matvec(w.view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _stream_of(x, stream)))
     return y
 
 
