@@ -363,8 +363,9 @@ lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t back
  * aligned), x [m, k] is bf16 and not quantized (rows ldx elements apart, ldx
  * a multiple of 8, 16-byte aligned), y [m, n] contiguous bf16 or FP32.  Codes
  * times scales are exact, products are summed in FP32 and the tensor scale is
- * applied to the sum.  k must be a multiple of 32, at most 2^19; m and n are arbitrary
- * (>= 0), but m is meant to be small: the weights are read once per 16 tokens. */
+ * applied to the sum.  k must be a multiple of 32, at most 2^19 (2^16 with
+ * LPQ_SF_PLAIN scales); m and n are arbitrary
+ * (>= 0), but m is meant to be small: the weights are read once per 8 tokens. */
 lpq_status lpq_matvec(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,
                       lpq_stream_t stream);
 

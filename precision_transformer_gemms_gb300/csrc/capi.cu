@@ -489,7 +489,8 @@ lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m,
   if (m < 0 || w->rows < 0 || w->cols < 0) return set_error(LPQ_ERR_SHAPE, "negative dimension");
   if (w->cols % 32) return set_error(LPQ_ERR_SHAPE, "k %lld not a multiple of 32", (long long)w->cols);
   if (w->rows > (int64_t)1 << 30 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "dimension beyond 2^30");
-  if (w->cols > (int64_t)1 << 19) return set_error(LPQ_ERR_SHAPE, "k %lld beyond 2^19", (long long)w->cols);
+  const int64_t most_k = (int64_t)1 << (w->sf_layout == LPQ_SF_PLAIN ? 16 : 19);
+  if (w->cols > most_k) return set_error(LPQ_ERR_SHAPE, "k %lld beyond %lld", (long long)w->cols, (long long)most_k);
   if (m > 0 && w->cols > 0 && (ldx < w->cols || ldx % 8))
     return set_error(LPQ_ERR_SHAPE, "ldx %lld must be a multiple of 8, at least k = %lld", (long long)ldx, (long long)w->cols);
   if (m > 0 && w->rows > 0) {

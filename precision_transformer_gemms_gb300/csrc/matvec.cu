@@ -2,15 +2,16 @@
 // y[i, n] = sum_k x[i, k] w[n, k], w = code * scale (* tensor scale).
 //
 // The weights are read once and are all the traffic there is, so the kernel is
-// built around their stream: a lane keeps three 16-byte loads (32 codes each)
-// of two weight rows in flight while it works on a fourth.  What bounds the
-// work is instruction issue: at HBM's rate an SM has to take in 40 weights per
-// cycle.  A byte of two E2M1 codes becomes an f16 pair in one conversion and
-// is multiplied with its group scale (exact: 2 significant bits times 4); the
-// products with x run on mma.m16n8k16 (weights as the 16 rows, tokens as the 8
-// columns) with FP32 sums, 1.4 instructions per weight and lane in all.
-// tcgen05 would need the decoded weights written to shared memory first, for a
-// product whose tensor work is small.
+// built around their stream: every lane copies its own 16 bytes (32 codes) of
+// two weight rows, and their scales, some chunks ahead into a ring of its own
+// in shared memory with cp.async (no registers, no barriers: a lane reads back
+// only what it copied).  What bounds the work is instruction issue: at HBM's
+// rate an SM has to take in 40 weights per cycle.  A byte of two E2M1 codes
+// becomes an f16 pair in one conversion and is multiplied with its group scale
+// (exact: 2 significant bits times 4); the products with x run on mma.m16n8k16
+// (weights as the 16 rows, tokens as the 8 columns) with FP32 sums.  tcgen05
+// would need the decoded weights written to shared memory first, for a product
+// whose tensor work is small.
 //
 // x enters as f16 too: a token's values times a power of two that brings its
 // largest one to [2^14, 2^15).  A bf16 value has 8 significant bits, so this
@@ -29,14 +30,14 @@
 namespace lpq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kGroup = 128;         // rows of a group of the tensor-core scale layout: 8 tiles
 constexpr int kChunk = 128;         // codes of a row per warp load: 4 lanes x 32
-constexpr int kBufs = 4;            // loads per row in registers
-constexpr int kStep = kBufs * kChunk;
+constexpr int kRing = 4;            // chunks in a warp's ring
+constexpr int kStep = kRing * kChunk;  // segments of K are whole steps
 constexpr int kSegments = 8;        // most parts of K (and CTAs of a cluster)
-constexpr int kXBytes = 160 * 1024; // most shared memory for x
+constexpr int kTokens = 8;          // most tokens of a pass: the columns of an MMA
+constexpr int kXBytes = 128 * 1024; // most shared memory for x
+constexpr int kSlot = 32 * 40;      // a chunk in a warp's ring: 2 x 16 bytes of codes, 2 x 4 of scales per lane
 
 struct MatvecArgs {
   const uint8_t* codes;
@@ -53,7 +54,7 @@ struct MatvecArgs {
   int y_fp32;
   int steps, segments;  // K in steps, and in parts that are summed by themselves
   int cluster;          // 1, or a CTA per segment
-  int items;            // work items of 8 tiles (cluster > 1) or 8 / segments tiles
+  int items;            // work items of W tiles (cluster > 1) or W / segments tiles
   int x_words;          // 16-byte words of x that a CTA has room for, per token
 };
 
@@ -136,10 +137,14 @@ __device__ __forceinline__ void scale_pairs(uint32_t s, uint32_t (&o)[2]) {
 __device__ __forceinline__ uint32_t mx_rest(uint32_t s) {  // 2^(e - 1) where e > 1, else 1; NaN for 255
   return s == 255u ? 0x7FC07FC0u : (max(s, 128u) - 1u) * 0x00800080u;
 }
-// Whether 2^e times some code of c leaves f16: e outside [-23, 13] with a code
-// that is not zero, or the scale that is no number.
-__device__ __forceinline__ bool mx_outside(uint32_t s, const uint4& c) {
-  return (s - 104u > 36u && ((c.x | c.y | c.z | c.w) & 0x77777777u)) || s == 255u;
+// Whether some group of a warp's chunk leaves f16: its scale 2^e outside e in
+// [-23, 13] and a code of it not zero, or the scale that is no number.
+__device__ __forceinline__ bool mx_far(const Load& l) {
+  if (!__any_sync(0xFFFFFFFFu, l.slo - 104u > 36u || l.shi - 104u > 36u)) return false;
+  auto outside = [](uint32_t s, const uint4& c) {
+    return s - 104u > 36u && (s == 255u || ((c.x | c.y | c.z | c.w) & 0x77777777u));
+  };
+  return __any_sync(0xFFFFFFFFu, outside(l.slo, l.lo) || outside(l.shi, l.hi));
 }
 __device__ __forceinline__ float e2m1_value(uint32_t code) {
   uint32_t h2;
@@ -147,10 +152,10 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
   return __low2float(*reinterpret_cast<const __half2*>(&h2));
 }
 
-// The chunk's products.  e: the lane's x entries per column block (16 bytes per
-// word, words 4 * mm entries apart).
-template <bool MX, bool F16, int NT>
-__device__ __forceinline__ void chunk_products(const Load& l, const uint4* const (&e)[NT], int mm, float (&acc)[NT][4]) {
+// The chunk's products.  e: the lane's x entries (16 bytes per word, words 4 *
+// MP entries apart).
+template <bool MX, bool F16, int MP>
+__device__ __forceinline__ void chunk_products(const Load& l, const uint4* e, float (&acc)[4]) {
   uint32_t sl[2], sh[2], xl = 0, xh = 0;
   scale_pairs<MX, F16>(l.slo, sl);
   scale_pairs<MX, F16>(l.shi, sh);
@@ -181,20 +186,17 @@ __device__ __forceinline__ void chunk_products(const Load& l, const uint4* const
         }
       }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const uint4 b = e[n][w * 4 * mm];
-      mma<F16>(acc[n], pl[0], ph[0], pl[1], ph[1], b.x, b.y);
-      mma<F16>(acc[n], pl[2], ph[2], pl[3], ph[3], b.z, b.w);
-    }
+    const uint4 b = e[w * 4 * MP];
+    mma<F16>(acc, pl[0], ph[0], pl[1], ph[1], b.x, b.y);
+    mma<F16>(acc, pl[2], ph[2], pl[3], ph[3], b.z, b.w);
   }
 }
 
 // A chunk with MXFP4 groups that f16 cannot hold: plain FP32 dot products of
 // the lane's 32 codes with each token, joined over the 4 lanes of a row and
-// added to the warp's sums in shared memory ([token][row], x's own scale).
+// added to the warp's sums in shared memory ([token][row], in x's own scale).
 // back: per token 2^-shift of the entries at e.
-__device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_t shi, const uint4* e, int mm,
+__device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_t shi, const uint4* e, int mp, int mm,
                                        const float* back, float* sums) {
   const int lane = threadIdx.x & 31, t = lane & 3, gid = lane >> 2;
   const float fl = slo == 255u ? __int_as_float(0x7FC00000) : pow2_exact((int)slo - 127);
@@ -205,7 +207,7 @@ __device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_
     float dl = 0.f, dh = 0.f;
 #pragma unroll 1
     for (int w = 0; w < 4; ++w) {
-      const uint4 b = e[w * 4 * mm + token];
+      const uint4 b = e[(w * mp + token) * 4];
       const uint32_t u[4] = {b.x, b.y, b.z, b.w};
       const uint32_t cl = w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w;
       const uint32_t ch = w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w;
@@ -245,285 +247,326 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
 // per CTA, and joins the sums through distributed shared memory.  The segments'
 // sums are added in the same order either way: a row's result does not depend
 // on the number of rows.
-template <bool MX, bool SFG, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 && !MX ? 2 : 2) matvec_kernel(const MatvecArgs g) {
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool there) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+template <bool MX>
+__device__ __forceinline__ uint32_t ld_shared_scale(uint32_t addr) {
+  if constexpr (MX) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+  } else {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+  }
+}
+
+// MP: tokens that x's place in shared memory is laid out for (g.m or more).
+// W warps per CTA: 8, four CTAs on an SM while x is small, else 24 that share x.
+template <bool MX, bool SFG, int MP, int W>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const MatvecArgs g) {
+  constexpr int kThreads = 32 * W;
   extern __shared__ uint4 sx[];
-  constexpr int kCols = 8 * NT;
-  __shared__ uint32_t top_sh[kSegments * kCols], least_sh[kSegments * kCols];
-  __shared__ float back_sh[kSegments * kCols];  // 2^-shift
-  __shared__ int f16_sh[kSegments];
+  __shared__ float back_sh[kSegments * kTokens];  // 2^-shift of a segment's x
+  __shared__ int fits_sh[kSegments * kTokens];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, t = lane & 3;
   const bool shared_k = g.cluster > 1;  // the cluster's CTAs share K
   const int rank = shared_k ? (int)cluster_ctarank() : 0;
   const int first_item = blockIdx.x / g.cluster, item_step = gridDim.x / g.cluster;
-  const int seg = shared_k ? rank : warp % g.segments;                     // this warp's segment,
-  const int slot = shared_k ? warp : warp / g.segments;                    // its tile among the item's,
-  const int slots = shared_k ? kWarps : kWarps / g.segments;               // and how many those are
+  const int seg = shared_k ? rank : warp % g.segments;      // this warp's segment,
+  const int slot = shared_k ? warp : warp / g.segments;     // its tile among the item's,
+  const int slots = shared_k ? W : W / g.segments;          // and how many those are
   const int64_t m0 = (int64_t)blockIdx.y * g.m;
-  const int mm = g.m;
+  const int mm = g.m;  // tokens of this pass
   // segments [seg0, seg1) of this CTA; segment i is steps [i * steps / segments, (i + 1) * steps / segments)
   const int seg0 = shared_k ? rank : 0, seg1 = shared_k ? rank + 1 : g.segments;
   auto seg_begin = [&](int i) { return i * g.steps / g.segments; };
   const int step0 = seg_begin(seg0);
   const int lo = seg_begin(seg), hi = seg_begin(seg + 1);  // this warp's steps
-  constexpr int kSums = kCols * 16 * (MX ? 2 : 1);  // a warp's sums: [token][row], then those of far_chunk
-  float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * mm);  // two buffers of all warps'
+  constexpr int kSums = kTokens * 16;  // a warp's sums: [token][row]
+  float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // two buffers of all warps'
+  const uint32_t ring = smem_u32(sums + 2 * W * kSums) + warp * (kRing * kSlot);
+  const uint32_t codes_sh = ring + lane * 16, scales_sh = ring + 1024 + lane * 4;  // the lane's places in a slot
 
-  // ---- the weight stream
+  // ---- the weight stream: the lane's place in the step that is copied next
   constexpr int kChunkS = SFG ? (MX ? 512 : 1024) : (MX ? 4 : 8);  // scale bytes per chunk
-  const int lane_s = MX ? t : SFG ? (t >> 1) * 512 + (t & 1) * 2 : t * 2;
-  const uint8_t* pc = nullptr;  // the lane's first row: codes and scales
-  const uint8_t* ps = nullptr;
-  int64_t hi_c = 0, hi_s = 0;  // its second row lies 2 rows on
+  const int n_rows = (int)g.n;
   auto row_of = [&](int item, int sl, int r) {  // row r of 16 of an item's tile
-    const int64_t tile = (int64_t)item * slots + sl;
+    const int tile = item * slots + sl;
     return (tile >> 3) * kGroup + 32 * (r & 3) + 4 * (tile & 7) + (r >> 2);
   };
-  auto set_item = [&](int item) {
-    int64_t row = row_of(item, slot, gid);
+  const uint8_t *pc = nullptr, *pc2 = nullptr;  // codes of the lane's two rows
+  const uint8_t *ps = nullptr, *ps2 = nullptr;  // their scales: a 4-byte word (plain layout: the lane's own bytes)
+  int a_item = first_item, a_step = lo;
+  enum { kNone, kWhole, kPartial };  // what of the step there is: nothing (no work left), all of it, up to K's end
+  int a_kind = kNone;
+  auto kind_of = [&]() { return (a_step + 1) * kStep <= g.k ? kWhole : kPartial; };
+  auto set_item = [&]() {
+    int row = row_of(a_item, slot, gid);
     // rows beyond the matrix read its last row; their results are not stored
-    const bool two = row + 2 < g.n;
-    row = min(row, g.n - 1);
-    pc = g.codes + row * (g.k >> 1);
-    ps = g.scales + (SFG ? sf_gemm_offset(row, 0, g.kt) : row * g.row_scales);
-    hi_c = two ? g.k : 0;
-    hi_s = two ? (SFG ? 32 : 2 * g.row_scales) : 0;
+    const bool two = row + 2 < n_rows;
+    row = min(row, n_rows - 1);
+    pc = g.codes + (int64_t)row * (g.k >> 1) + (int64_t)lo * (kStep / 2) + t * 16;
+    ps = g.scales + (int64_t)lo * (kRing * kChunkS) +
+         (SFG ? sf_gemm_offset(row, 0, g.kt) + (MX ? 0 : (t >> 1) * 512) : row * g.row_scales + (MX ? t : 2 * t));
+    pc2 = pc + (two ? g.k : 0);
+    ps2 = ps + (two ? (SFG ? 32 : 2 * g.row_scales) : 0);
   };
-  auto fetch = [&](const uint8_t* c, const uint8_t* s, Load& l) {
-    l.lo = __ldcs(reinterpret_cast<const uint4*>(c));
-    l.hi = __ldcs(reinterpret_cast<const uint4*>(c + hi_c));
-    if constexpr (MX) {
-      l.slo = *s;
-      l.shi = s[hi_s];
-    } else {
-      l.slo = *reinterpret_cast<const uint16_t*>(s);
-      l.shi = *reinterpret_cast<const uint16_t*>(s + hi_s);
-    }
-  };
-  // Chunk h of a step whose first chunk's codes and scales are at c and s.
-  auto load = [&](const uint8_t* c, const uint8_t* s, int step, int h, Load& l) {
-    if ((step + 1) * kStep <= g.k || step * kStep + h * kChunk + t * 32 < g.k) {
-      fetch(c + h * (kChunk / 2), s + h * kChunkS, l);
-    } else {  // past the end of K: the row's first block again, with scale 0 (and x 0)
-      fetch(pc, ps, l);
-      l.slo = l.shi = 0;
-    }
-  };
-  auto codes_at = [&](int step) { return pc + (int64_t)step * (kStep / 2) + t * 16; };
-  auto scales_at = [&](int step) { return ps + (int64_t)step * (kBufs * kChunkS) + lane_s; };
-  Load buf[kBufs];
-  set_item(first_item);
-#pragma unroll
-  for (int h = 0; h < kBufs; ++h) load(codes_at(lo), scales_at(lo), lo, h, buf[h]);
-
-  // ---- x as operand entries of 16 bytes, ordered by chunk, word, lane, token
-  // (a warp's reads are contiguous): first as it is with its range, then converted
-  for (int i = threadIdx.x; i < kSegments * kCols; i += kThreads) {
-    top_sh[i] = 0;
-    least_sh[i] = 0xFFFFu;
-  }
-  const int words = (seg_begin(seg1) - step0) * (kStep / 8);  // 16-byte words per token, a multiple of 64
-  auto segment_of = [&](int i) {  // of word i; a warp's 32 words lie in one token and one segment
-    return shared_k ? rank : ((i / (kStep / 8) + 1) * g.segments - 1) / g.steps;
-  };
-  auto place = [&](int token, int i) { return (((i >> 4) * 4 + (i & 3)) * 4 + ((i >> 2) & 3)) * mm + token; };
-  auto advance = [&](int& token, int& i) {
-    i += kThreads;
-    while (i >= words) {
-      i -= words;
-      ++token;
-    }
-  };
-  __syncthreads();
-  constexpr int kAhead = 8;  // loads in flight per thread
-  for (int token = threadIdx.x / words, i = threadIdx.x % words; token < mm;) {
-    uint4 v[kAhead];
-    int tk = token, at = i;
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      v[a] = make_uint4(0, 0, 0, 0);
-      const int k = step0 * kStep + at * 8;
-      if (tk < mm && k < g.k) v[a] = *reinterpret_cast<const uint4*>(g.x + (m0 + tk) * g.ldx + k);
-      advance(tk, at);
-    }
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (token < mm) {
-        const uint32_t u[4] = {v[a].x, v[a].y, v[a].z, v[a].w};
-        uint32_t top = 0, least = 0xFFFFFFFFu;  // pairs of 16-bit maxima of |x| and minima of |x| - 1 (0 wraps to the top)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t m = u[j] & 0x7FFF7FFFu;
-          top = __vmaxu2(top, m);
-          least = __vminu2(least, __vsub2(m, 0x00010001u));
-        }
-        top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
-        least = __reduce_min_sync(0xFFFFFFFFu, min(least >> 16, least & 0xFFFFu));
-        if (lane == 0) {
-          const int to = segment_of(i) * kCols + token;
-          atomicMax(&top_sh[to], top);
-          atomicMin(&least_sh[to], least);
-        }
-        sx[place(token, i)] = v[a];
+  auto copy = [&](int h) {  // chunk h of the step
+    const uint32_t c = codes_sh + h * kSlot, sc = scales_sh + h * kSlot;
+    if (a_kind == kWhole) {
+      cp_async<16>(c, pc + h * (kChunk / 2));
+      cp_async<16>(c + 512, pc2 + h * (kChunk / 2));
+      if constexpr (SFG) {
+        cp_async<4>(sc, ps + h * kChunkS);
+        cp_async<4>(sc + 128, ps2 + h * kChunkS);
       }
-      advance(token, i);
+    } else if (a_kind == kPartial) {
+      const bool in = a_step * kStep + h * kChunk + t * 32 < g.k;
+      cp_async_or_zero<16>(c, in ? pc + h * (kChunk / 2) : g.codes, in);
+      cp_async_or_zero<16>(c + 512, in ? pc2 + h * (kChunk / 2) : g.codes, in);
+      if constexpr (SFG) {
+        cp_async_or_zero<4>(sc, in ? ps + h * kChunkS : g.scales, in);
+        cp_async_or_zero<4>(sc + 128, in ? ps2 + h * kChunkS : g.scales, in);
+      }
     }
-  }
-  __syncthreads();
-  // x * 2^shift: the largest value's exponent field becomes 14 + 127 (at most
-  // 126 steps up).  f16 holds a bf16 value exactly down to the field 110 (a
-  // subnormal's leading bit lies up to 7 below field 1).
-  if (threadIdx.x < kSegments) f16_sh[threadIdx.x] = 1;
-  __syncthreads();
-  if (threadIdx.x < kSegments * kCols) {
-    const uint32_t top = top_sh[threadIdx.x], least = least_sh[threadIdx.x] + 1u;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto next_step = [&]() {
+    if (a_kind == kNone) return;
+    pc += kStep / 2;
+    pc2 += kStep / 2;
+    ps += kRing * kChunkS;
+    ps2 += kRing * kChunkS;
+    if (++a_step == hi) {
+      a_step = lo;
+      a_item += item_step;
+      if (a_item >= g.items) {
+        a_kind = kNone;
+        return;
+      }
+      set_item();
+    }
+    a_kind = kind_of();
+  };
+  set_item();
+  a_kind = kind_of();
+#pragma unroll
+  for (int h = 0; h < kRing; ++h) copy(h);
+  // plain layout: the scales are loaded when the step begins
+  const uint8_t *os = ps, *os2 = ps2;
+  int o_step = lo;
+  next_step();
+
+  // ---- x as operand entries of 16 bytes, ordered by chunk, word, token, lane of
+  // four (a warp's reads are contiguous in lane order)
+  auto word = [&](int token, int i) {
+    const int k = step0 * kStep + i * 8;
+    return k < g.k ? __ldg(reinterpret_cast<const uint4*>(g.x + (m0 + token) * g.ldx + k)) : make_uint4(0, 0, 0, 0);
+  };
+  auto place = [&](int token, int i) { return (((i >> 4) * 4 + (i & 3)) * MP + token) * 4 + ((i >> 2) & 3); };
+  // A token's part of a segment takes a warp, or several while there are more
+  // warps than parts: each finds the part's range, then converts its share.
+  const int parts = (seg1 - seg0) * mm, share = max(1, W / parts);
+  for (int p = warp / share; p < parts; p += W / share) {
+    const int sg = seg0 + p / mm, token = p % mm;
+    const int w0 = (seg_begin(sg) - step0) * (kStep / 8), w1 = (seg_begin(sg + 1) - step0) * (kStep / 8);
+    uint32_t top = 0, least = 0xFFFFFFFFu;  // pairs of 16-bit maxima of |x| and minima of |x| - 1 (0 wraps to the top)
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint4 v = word(token, i);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t m = u[j] & 0x7FFF7FFFu;
+        top = __vmaxu2(top, m);
+        least = __vminu2(least, __vsub2(m, 0x00010001u));
+      }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, max(top >> 16, top & 0xFFFFu));
+    least = __reduce_min_sync(0xFFFFFFFFu, min(least >> 16, least & 0xFFFFu)) + 1u;
+    // x * 2^shift: the largest value's exponent field becomes 14 + 127 (at most
+    // 126 steps up).  f16 holds a bf16 value exactly down to the field 110 (a
+    // subnormal's leading bit lies up to 7 below field 1).
     const int shift = top ? min(141 - (int)max(top >> 7, 1u), 126) : 0;
-    if (top >= 0x7F80u || (least <= 0xFFFFu && (least >> 7 ? (int)(least >> 7) : -6) + shift < 110))
-      f16_sh[threadIdx.x / kCols] = 0;
-    back_sh[threadIdx.x] = __uint_as_float((uint32_t)(127 - shift) << 23);
-  }
-  __syncthreads();
-  if (threadIdx.x < kSegments * kCols && !f16_sh[threadIdx.x / kCols]) back_sh[threadIdx.x] = 1.0f;
-  __syncthreads();
-  for (int token = threadIdx.x / words, i = threadIdx.x % words; token < mm; advance(token, i)) {
-    const int sg = segment_of(i);
-    uint4& e = sx[place(token, i)];
-    const uint32_t u[4] = {e.x, e.y, e.z, e.w};
-    if (f16_sh[sg]) {
-      const float f = __uint_as_float(0x7F000000u - __float_as_uint(back_sh[sg * kCols + token]));  // 2^shift
+    if (lane == 0) {
+      back_sh[sg * kTokens + token] = __uint_as_float((uint32_t)(127 - shift) << 23);
+      fits_sh[sg * kTokens + token] = top < 0x7F80u && (least > 0xFFFFu || (least >> 7 ? (int)(least >> 7) : -6) + shift >= 110);
+    }
+    const float f = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll 1
+    for (int i = w0 + lane + 32 * (warp % share); i < w1; i += 32 * share) {
+      const uint4 v = word(token, i);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
       uint32_t r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * f, bf16_hi(u[j]) * f);
         r[j] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      e = make_uint4(r[0], r[1], r[2], r[3]);
-    } else {
-      e = make_uint4(__byte_perm(u[0], u[2], 0x5410), __byte_perm(u[0], u[2], 0x7632),
-                     __byte_perm(u[1], u[3], 0x5410), __byte_perm(u[1], u[3], 0x7632));
+      sx[place(token, i)] = make_uint4(r[0], r[1], r[2], r[3]);
     }
   }
   __syncthreads();
+  auto fits = [&](int sg) {
+    bool all = true;
+    for (int token = 0; token < mm; ++token) all = all && fits_sh[sg * kTokens + token];
+    return all;
+  };
+  bool again = false;  // the same in all threads
+  for (int sg = seg0; sg < seg1; ++sg) {
+    if (fits(sg)) continue;
+    again = true;  // x as bf16 pairs instead
+    const int w0 = (seg_begin(sg) - step0) * (kStep / 8), w1 = (seg_begin(sg + 1) - step0) * (kStep / 8);
+    for (int token = 0; token < mm; ++token)
+      for (int i = w0 + threadIdx.x; i < w1; i += kThreads) {
+        const uint4 v = word(token, i);
+        sx[place(token, i)] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+      }
+  }
+  if (again) __syncthreads();
 
   const float tensor = MX ? 1.0f : *g.tensor_scale;
-  auto put = [&](int64_t row, int token, float v) {
-    if (row >= g.n || token >= mm) return;
+  auto put = [&](int row, int token, float v) {
+    if (row >= n_rows || token >= mm) return;
     const int64_t at = (m0 + token) * g.n + row;
     if (g.y_fp32) static_cast<float*>(g.y)[at] = v * tensor;
     else static_cast<__nv_bfloat16*>(g.y)[at] = __float2bfloat16_rn(v * tensor);
   };
-  // columns beyond the tokens repeat the last one: their sums are not stored
-  int col[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) col[n] = t * mm + min(gid + 8 * n, mm - 1);
-
-  const bool f16 = f16_sh[seg];
+  // operand columns beyond the tokens hold anything: their sums are not stored
+  const int col = min(gid, MP - 1) * 4 + t;
+  const bool f16 = fits(seg);
   int jbuf = 0;
   for (int item = first_item; item < g.items; item += item_step, jbuf ^= 1) {
-    float* mine = sums + (jbuf * kWarps + warp) * kSums;
-    float acc[NT][4];
+    float* mine = sums + (jbuf * W + warp) * kSums;
+    float acc[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[n][i] = 0.f;
-        if constexpr (MX) mine[kCols * 16 + (8 * n + 2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = 0.f;
-      }
+    for (int i = 0; i < 4; ++i) {
+      acc[i] = 0.f;
+      if constexpr (MX) mine[(2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = 0.f;  // far_chunk adds to it
+    }
     auto steps = [&](auto f16_path) {
       constexpr bool F16 = decltype(f16_path)::value;
-      for (int s = lo; s < hi; ++s) {
-        // the step whose loads go out now (at the very end the last item's first again)
-        int ns = s + 1;
-        if (ns == hi) {
-          ns = lo;
-          if (item + item_step < g.items) set_item(item + item_step);
-        }
-        const uint8_t* c = codes_at(ns);
-        const uint8_t* sc = scales_at(ns);
-        const uint4* e = sx + (size_t)((s - step0) * (kStep / 8)) * mm;
+      const uint4* e = sx + (size_t)(lo - step0) * (kStep / 8) * MP;
+#pragma unroll 1
+      for (int s = lo; s < hi; ++s, e += (kStep / 8) * MP) {
 #pragma unroll
-        for (int h = 0; h < kBufs; ++h) {
-          const uint4* cols[NT];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) cols[n] = e + h * 16 * mm + col[n];
-          if (MX && F16 &&
-              __any_sync(0xFFFFFFFFu, mx_outside(buf[h].slo, buf[h].lo) || mx_outside(buf[h].shi, buf[h].hi)))
-            far_chunk(buf[h].lo, buf[h].hi, buf[h].slo, buf[h].shi, e + h * 16 * mm + t * mm, mm,
-                      back_sh + seg * kCols, mine + kCols * 16);
+        for (int h = 0; h < kRing; ++h) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+          Load l;
+          l.lo = ld_shared_16(codes_sh + h * kSlot);
+          l.hi = ld_shared_16(codes_sh + h * kSlot + 512);
+          if constexpr (SFG) {  // the lane's bytes of its word: NVFP4 (t & 1) * 2 on, MXFP4 t on
+            const uint32_t at = scales_sh + h * kSlot + (MX ? t : (t & 1) * 2);
+            l.slo = ld_shared_scale<MX>(at);
+            l.shi = ld_shared_scale<MX>(at + 128);
+          } else {
+            l.slo = l.shi = 0;
+            if (o_step * kStep + h * kChunk + t * 32 < g.k) {
+              l.slo = MX ? os[h * kChunkS] : *reinterpret_cast<const uint16_t*>(os + h * kChunkS);
+              l.shi = MX ? os2[h * kChunkS] : *reinterpret_cast<const uint16_t*>(os2 + h * kChunkS);
+            }
+          }
+          const uint4* eh = e + h * (kChunk / 8) * MP;
+          if (MX && F16 && mx_far(l))
+            far_chunk(l.lo, l.hi, l.slo, l.shi, eh + t, MP, mm, back_sh + seg * kTokens, mine);
           else
-            chunk_products<MX, F16, NT>(buf[h], cols, mm, acc);
-          load(c, sc, ns, h, buf[h]);
+            chunk_products<MX, F16, MP>(l, eh + col, acc);
+          copy(h);  // into the slot whose values have just been used
         }
+        if constexpr (!SFG) {  // (the step whose copies have just gone out is the next one)
+          os = ps;
+          os2 = ps2;
+          o_step = a_step;
+        }
+        next_step();
       }
     };
     if (f16) steps(std::true_type{}); else steps(std::false_type{});
     // back to x's own scale (bf16 NVFP4 sums lie 2^-8 down)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int token = 8 * n + 2 * t + (i & 1);
-        acc[n][i] *= back_sh[seg * kCols + min(token, mm - 1)] * (f16 || MX ? 1.0f : 256.0f);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int token = 2 * t + (i & 1);
+      acc[i] *= f16 ? back_sh[seg * kTokens + min(token, mm - 1)] : MX ? 1.0f : 256.0f;
+      if constexpr (MX) acc[i] += mine[token * 16 + gid + (i >> 1) * 8];
+    }
     if (g.segments == 1) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int token = 8 * n + 2 * t + (i & 1), r = gid + (i >> 1) * 8;
-          put(row_of(item, slot, r), token, acc[n][i] + (MX ? mine[kCols * 16 + token * 16 + r] : 0.f));
-        }
+      for (int i = 0; i < 4; ++i) put(row_of(item, slot, gid + (i >> 1) * 8), 2 * t + (i & 1), acc[i]);
       continue;
     }
     // The segments' sums meet in shared memory (two buffers: one barrier per
     // item) and are added in order; in a cluster each CTA adds its share.
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mine[(8 * n + 2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = acc[n][i];
+    for (int i = 0; i < 4; ++i) mine[(2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = acc[i];
     __syncwarp();
     if (shared_k) cluster_sync_all(); else __syncthreads();
-    const int per = shared_k ? kGroup / g.cluster : 16 * slots;  // (tile, row) places of this CTA, per token
-    for (int e = threadIdx.x; e < per * mm; e += kThreads) {
-      const int token = e / per, r = rank * per + e % per;
+    const int per = shared_k ? 16 * W / g.cluster : 16 * slots;  // (tile, row) places of this CTA, per token
+    for (int e = threadIdx.x; e < per * MP; e += kThreads) {
+      const int token = e % MP, r = rank * per + e / MP;
+      if (token >= mm) continue;
       const int sl = r >> 4, at = token * 16 + (r & 15);
-      float v = 0.f, f = 0.f;
+      float v = 0.f;
       if (shared_k) {
-        const uint32_t here = smem_u32(sums + (jbuf * kWarps + sl) * kSums + at);
-        for (int c = 0; c < g.segments; ++c) {
-          const uint32_t from = mapa_shared(here, (uint32_t)c);
-          v += ld_shared_cluster(from);
-          if constexpr (MX) f += ld_shared_cluster(from + kCols * 16 * 4);
-        }
+        const uint32_t here = smem_u32(sums + (jbuf * W + sl) * kSums + at);
+        for (int c = 0; c < g.segments; ++c) v += ld_shared_cluster(mapa_shared(here, (uint32_t)c));
       } else {
-        const float* from = sums + (jbuf * kWarps + sl * g.segments) * kSums + at;
-        for (int c = 0; c < g.segments; ++c) {
-          v += from[c * kSums];
-          if constexpr (MX) f += from[c * kSums + kCols * 16];
-        }
+        const float* from = sums + (jbuf * W + sl * g.segments) * kSums + at;
+        for (int c = 0; c < g.segments; ++c) v += from[c * kSums];
       }
-      put(row_of(item, sl, r & 15), token, v + f);
+      put(row_of(item, sl, r & 15), token, v);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
   if (shared_k) cluster_sync_all();  // no CTA leaves while another may still read its sums
 }
 
-template <bool MX, bool SFG, int NT>
+constexpr int kLayouts[] = {1, 2, kTokens};  // MP
+int layout_for(int tokens) {
+  for (int mp : kLayouts)
+    if (tokens <= mp) return mp;
+  return kTokens;
+}
+
+template <bool MX, bool SFG, int MP, int W>
 lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
-  constexpr int kSumBytes = 2 * kWarps * NT * 128 * 4 * (MX ? 2 : 1);
+  constexpr int kSumBytes = 2 * W * kTokens * 16 * 4;
   const int seg_steps = (g.steps + g.segments - 1) / g.segments;
   g.x_words = (g.cluster > 1 ? seg_steps : g.steps) * (kStep / 8);
-  const int smem = g.x_words * 16 * g.m + (MX || g.segments > 1 ? kSumBytes : 0);
-  lpq_status st = set_smem_attr(reinterpret_cast<const void*>(matvec_kernel<MX, SFG, NT>), kXBytes + kSumBytes);
+  const int smem = g.x_words * 16 * MP + kSumBytes + W * kRing * kSlot;
+  const void* kernel = reinterpret_cast<const void*>(matvec_kernel<MX, SFG, MP, W>);
+  lpq_status st = set_smem_attr(kernel, 222 * 1024);
   if (st != LPQ_OK) return st;
-  const int resident = NT == 1 && !MX ? 2 : 2;
-  const int64_t tiles = (g.n + kGroup - 1) / kGroup * 8, per = g.cluster > 1 ? kWarps : kWarps / g.segments;
+  const int64_t tiles = (g.n + kGroup - 1) / kGroup * 8, per = g.cluster > 1 ? W : W / g.segments;
   g.items = (int)((tiles + per - 1) / per);
+  const int resident = std::max(1, std::min(W == 8 ? 4 : 1, 226 * 1024 / (smem + 2048)));
   const int most = std::max(1, resident * device_sms() / g.cluster);
+  const dim3 grid((unsigned)(std::min(g.items, most) * g.cluster), (unsigned)passes);
+  if (g.cluster == 1) {
+    matvec_kernel<MX, SFG, MP, W><<<grid, 32 * W, smem, s>>>(g);
+    return cuda_check(cudaGetLastError(), "matvec launch");
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(std::min(g.items, most) * g.cluster), (unsigned)passes);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -533,7 +576,15 @@ lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, matvec_kernel<MX, SFG, NT>, g), "matvec launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, matvec_kernel<MX, SFG, MP, W>, g), "matvec launch");
+}
+
+template <bool MX>
+lpq_status run_tokens(const MatvecArgs& g, int passes, bool plain, bool wide_cta, cudaStream_t s) {
+  if (plain) return run_matvec<MX, false, kTokens, 8>(g, passes, s);
+  if (wide_cta) return g.m > 2 ? run_matvec<MX, true, kTokens, 24>(g, passes, s) : run_matvec<MX, true, 2, 24>(g, passes, s);
+  return g.m > 2 ? run_matvec<MX, true, kTokens, 8>(g, passes, s)
+         : g.m == 2 ? run_matvec<MX, true, 2, 8>(g, passes, s) : run_matvec<MX, true, 1, 8>(g, passes, s);
 }
 
 }  // namespace
@@ -557,27 +608,29 @@ lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t
   g.steps = (g.k + kStep - 1) / kStep;
   g.segments = 1;
   while (g.segments < kSegments && 4 * g.segments <= g.steps) g.segments *= 2;
-  // Tokens per pass: 16 or fewer, what fits a CTA's shared memory when a
+  // Tokens per pass: 8 or fewer, what fits a CTA's shared memory when a
   // cluster shares K.
+  const bool plain = w->sf_layout == LPQ_SF_PLAIN;
   const int seg_bytes = (g.steps + g.segments - 1) / g.segments * kStep * 2;  // of one token's x
-  const int most = std::min(16, kXBytes / seg_bytes);
+  int most = 1;
+  for (int mp : kLayouts)
+    if (mp * seg_bytes <= kXBytes) most = mp;
   for (int64_t m0 = 0; m0 < m;) {
     // Passes of equal width share a launch; the rest has one of its own.
     const int64_t left = m - m0;
     g.m = (int)std::min<int64_t>(left, most);
     const int64_t passes = std::min<int64_t>(left / g.m, 65535);
     // Clusters while a group's CTAs all run at once, or when x of all segments
-    // takes more than a third of an SM's shared memory.
+    // is more than a CTA has room for.  Else 8 warps while four CTAs' x fit on
+    // an SM, or 24 that share it.
     const int64_t groups = (g.n + kGroup - 1) / kGroup;
-    g.cluster = groups * g.segments <= 3 * device_sms() || g.steps * kStep * 2 * g.m > 60 * 1024 ? g.segments : 1;
+    const int mp = layout_for(g.m), token_bytes = g.steps * kStep * 2;
+    const bool wide_cta = !plain && token_bytes * mp > 12 * 1024;
+    const int x_bytes = token_bytes * (wide_cta ? std::max(mp, 2) : plain ? kTokens : mp);
+    g.cluster = groups * g.segments <= 4 * device_sms() || x_bytes > (wide_cta ? 64 : 24) * 1024 ? g.segments : 1;
     g.x = static_cast<const __nv_bfloat16*>(x) + m0 * ldx;
     g.y = static_cast<uint8_t*>(y) + (size_t)m0 * (size_t)g.n * (y_is_fp32 ? 4 : 2);
-    const bool plain = w->sf_layout == LPQ_SF_PLAIN, wide = g.m > 8;
-    auto run = mx ? (plain ? (wide ? run_matvec<true, false, 2> : run_matvec<true, false, 1>)
-                           : (wide ? run_matvec<true, true, 2> : run_matvec<true, true, 1>))
-                  : (plain ? (wide ? run_matvec<false, false, 2> : run_matvec<false, false, 1>)
-                           : (wide ? run_matvec<false, true, 2> : run_matvec<false, true, 1>));
-    lpq_status st = run(g, (int)passes, s);
+    lpq_status st = (mx ? run_tokens<true> : run_tokens<false>)(g, (int)passes, plain, wide_cta && g.cluster == 1, s);
     if (st != LPQ_OK) return st;
     m0 += passes * g.m;
   }

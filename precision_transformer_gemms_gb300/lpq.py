@@ -6,6 +6,7 @@ pointers and the current CUDA stream.  If the shared library cannot be built or
 loaded, every call raises: there is no CPU or PyTorch fallback.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -107,7 +108,7 @@ def lib():
                                   ctypes.POINTER(GemmOpts), P]
         SZ, PSZ = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
         L.lpq_layer_norm.argtypes = [P, I64, I32, P, P, I32, I64, I64, F, P, I64, P, P, P, P]
-        L.lpq_layer_norm_workspace.argtypes = [I64, I64, PSZ]  # a c_size_t passes by reference
+        L.lpq_layer_norm_workspace.argtypes = [I64, I64, PSZ]
         L.lpq_layer_norm_backward.argtypes = [P, I64, P, I64, I32, P, P, P, I32, I64, I64, P, I64, P, P, P, SZ, P]
         L.lpq_linear_ce_workspace.argtypes = [I64, I64, I64, I32, I64, PSZ]
         L.lpq_linear_ce.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, SZ, P]
@@ -301,7 +302,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 def _new(like, stream, shape, dtype):
     """A device buffer the call writes: on a stream other than the current one
     its memory is not reused before that stream is done with it."""
-    t = like.new_empty(shape, dtype=dtype)
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t
@@ -320,6 +321,20 @@ def _ld(x, rows, cols):
 
 def _is_vector(v, n, dtype):
     return v.dtype is dtype and v.is_cuda and v.numel() == n and v.is_contiguous()
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(rows, cols):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_layer_norm_workspace(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=256)
+def _ce_workspace(t, v, d, backward, vocab_piece):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_linear_ce_workspace(t, v, d, backward, vocab_piece, ctypes.byref(n)))
+    return n.value
 
 
 def _check_params(cols, weight, bias):
@@ -345,7 +360,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, amax=None, out=None, stream=
     else:
         assert out.dtype is dtype and out.shape == x.shape, "out must be like x"
         ldo = _ld(out, rows, cols)
-    mean, rstd = _new(x, stream, (2, rows), _FP32).unbind(0)
+    mean, rstd = _new(x, stream, rows, _FP32), _new(x, stream, rows, _FP32)
     _check(lib().lpq_layer_norm(x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype], _ptr(weight), _ptr(bias), w_type,
                                 rows, cols, eps, out.data_ptr(), ldo, mean.data_ptr(), rstd.data_ptr(), _ptr(amax),
                                 _stream_of(x, stream)))
@@ -364,11 +379,11 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, param_grads=True, stream
     L = lib()
     dx = _new(x, stream, (rows, cols), dtype)
     dweight = dbias = ws = None
-    need = ctypes.c_size_t(0)
+    need = 0
     if param_grads:
-        _check(L.lpq_layer_norm_workspace(rows, cols, need))
-        dweight, dbias = _new(x, stream, (2, cols), _FP32).unbind(0)
-        ws = _new(x, stream, need.value, torch.uint8)
+        need = _norm_workspace(rows, cols)
+        dweight, dbias = _new(x, stream, cols, _FP32), _new(x, stream, cols, _FP32)
+        ws = _new(x, stream, need, torch.uint8)
     _check(L.lpq_layer_norm_backward(dy.data_ptr(), _ld(dy, rows, cols), x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype],
                                      mean.data_ptr(), rstd.data_ptr(), _ptr(weight), w_type, rows, cols, dx.data_ptr(),
                                      cols, _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream_of(x, stream)))
@@ -388,10 +403,9 @@ def linear_cross_entropy(h, w, labels, stream=None):
     (int64; outside 0 .. v - 1: no target, loss 0).  Returns (loss, lse) [t] FP32."""
     t, d, v, ldh, ldw = _ce_args(h, w, labels)
     L = lib()
-    need = ctypes.c_size_t()
-    _check(L.lpq_linear_ce_workspace(t, v, d, 0, 0, need))
-    loss, lse = _new(h, stream, (2, t), _FP32).unbind(0)
-    ws = _new(h, stream, need.value, torch.uint8)
+    need = _ce_workspace(t, v, d, 0, 0)
+    loss, lse = _new(h, stream, t, _FP32), _new(h, stream, t, _FP32)
+    ws = _new(h, stream, need, torch.uint8)
     _check(L.lpq_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), t, v, d, loss.data_ptr(),
                            lse.data_ptr(), ws.data_ptr(), need, _stream_of(h, stream)))
     return loss, lse
@@ -403,11 +417,10 @@ def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, voca
     t, d, v, ldh, ldw = _ce_args(h, w, labels)
     assert _is_vector(lse, t, _FP32) and _is_vector(dloss, t, _FP32), f"lse and dloss must be {t} fp32"
     L = lib()
-    need = ctypes.c_size_t()
-    _check(L.lpq_linear_ce_workspace(t, v, d, 1, vocab_piece, need))
+    need = _ce_workspace(t, v, d, 1, vocab_piece)
     dtype = _FP32 if out_fp32 else _BF16
     dh, dw = _new(h, stream, (t, d), dtype), _new(h, stream, (v, d), dtype)
-    ws = _new(h, stream, need.value, torch.uint8)
+    ws = _new(h, stream, need, torch.uint8)
     _check(L.lpq_linear_ce_backward(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
                                     dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32), vocab_piece,
                                     ws.data_ptr(), need, _stream_of(h, stream)))
