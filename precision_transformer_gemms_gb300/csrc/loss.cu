@@ -172,6 +172,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     *abort_flag = 1;
   }
   const bool run = *peer_base == tmem_base;
+  let_dependents_start();
+  wait_for_stream();
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
 
@@ -435,6 +437,8 @@ __device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s
 __global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64_t cols, const float* at_label,
                                                       const int64_t* labels, int64_t t, int64_t v, float* loss,
                                                       float* lse) {
+  let_dependents_start();
+  wait_for_stream();
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= t) return;
   const int lane = threadIdx.x & 31;
@@ -461,6 +465,8 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64
 __global__ void __launch_bounds__(1024) ce_scale_kernel(const float* dloss, const int64_t* labels, int64_t t, int64_t v,
                                                         float* scale) {
   __shared__ float sh[32];
+  let_dependents_start();
+  wait_for_stream();
   float m = 0.f;
   for (int64_t i = threadIdx.x; i < t; i += 1024)
     if (labels[i] >= 0 && labels[i] < v) m = absmax_acc(m, dloss[i]);
@@ -476,6 +482,8 @@ __global__ void __launch_bounds__(1024) ce_scale_kernel(const float* dloss, cons
 // dh from its partial sums: the splits in order, times the scale.
 __global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int64_t n4, int splits, const float* scale,
                                                         void* out, int fp32) {
+  let_dependents_start();
+  wait_for_stream();
   const float s = *scale;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
     float4 a = acc[i];
@@ -552,8 +560,8 @@ lpq_status run_pair(CeTile g, Operand a, Operand b, int64_t K, void* c, int64_t 
   if ((st = device_error_word(&g.err)) != LPQ_OK) return st;
   if ((st = set_smem_attr(reinterpret_cast<const void*>(ce_pair_kernel<EPI, A_MN, B_MN>), kSmem)) != LPQ_OK) return st;
   const int pairs = (int)std::min<int64_t>(tm * tn * splits, std::max(1, device_sms() / 2));
-  ce_pair_kernel<EPI, A_MN, B_MN><<<2 * pairs, kThreads, kSmem, s>>>(ta, tb, tc, g);
-  return cuda_check(cudaGetLastError(), "cross entropy launch");
+  return cuda_check(launch_dependent(ce_pair_kernel<EPI, A_MN, B_MN>, 2 * pairs, kThreads, kSmem, s, ta, tb, tc, g),
+                    "cross entropy launch");
 }
 
 // Workspace of the backward pass: scale, dl, partial sums of dh.
@@ -594,9 +602,9 @@ lpq_status launch_ce(const CeArgs& a, cudaStream_t s) {
   g.stat_cols = cdiv(a.v, kHalf);
   lpq_status st = run_pair<kStats, false, false>(g, {a.h, a.ldh}, {a.w, a.ldw}, a.d, nullptr, 0, 1, s);
   if (st != LPQ_OK) return st;
-  ce_join_kernel<<<(unsigned)cdiv(a.t, 8), 256, 0, s>>>(g.stats, g.stat_cols, g.at_label, a.labels, a.t, a.v, a.loss,
-                                                       a.lse_out);
-  return cuda_check(cudaGetLastError(), "cross entropy join launch");
+  return cuda_check(launch_dependent(ce_join_kernel, (unsigned)cdiv(a.t, 8), 256, 0, s, g.stats, g.stat_cols, g.at_label,
+                                     a.labels, a.t, a.v, a.loss, a.lse_out),
+                    "cross entropy join launch");
 }
 
 lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
@@ -613,8 +621,8 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   g.scale = scale;
   g.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   g.out_fp32 = a.grads_fp32;
-  ce_scale_kernel<<<1, 1024, 0, s>>>(a.dloss, a.labels, a.t, a.v, scale);
-  lpq_status st = cuda_check(cudaGetLastError(), "cross entropy scale launch");
+  lpq_status st = cuda_check(launch_dependent(ce_scale_kernel, 1, 1024, 0, s, a.dloss, a.labels, a.t, a.v, scale),
+                             "cross entropy scale launch");
   if (st != LPQ_OK) return st;
   for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
     const int64_t width = std::min(plan.piece, a.v - v0);
@@ -639,9 +647,10 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   }
   if (plan.direct) return LPQ_OK;
   const int64_t n4 = a.t * a.d / 4;
-  ce_finish_kernel<<<(unsigned)std::min<int64_t>(cdiv(n4, 256), (int64_t)device_sms() * 8), 256, 0, s>>>(
-      reinterpret_cast<const float4*>(g.acc), n4, plan.splits, scale, a.dh, a.grads_fp32);
-  return cuda_check(cudaGetLastError(), "cross entropy finish launch");
+  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(n4, 256), (int64_t)device_sms() * 8);
+  return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(g.acc), n4,
+                                     plan.splits, scale, a.dh, a.grads_fp32),
+                    "cross entropy finish launch");
 }
 
 }  // namespace lpq

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float*
   const int which = blockIdx.y;  // 0: dweight, 1: dbias
   float* out = which ? dbias : dweight;
   if (!out) return;
+  wait_for_stream();
   float s = 0.f;
   if (c < cols) {
     const float* p = parts + which * cols + c;
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kBlock) norm_backward_kernel(co
   const int tid = threadIdx.x % TPR, n = (int)a.cols;
   const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
   const float inv_n = 1.0f / (float)n;
+  let_dependents_start();  // (norm_join_kernel waits for the parts)
   // the row whose copy is next: its number and this thread's first vectors
   int64_t ahead = first;
   const T* ahead_x = static_cast<const T*>(a.x) + first * a.ldx + tid * V;
@@ -700,8 +702,9 @@ lpq_status backward_t(NormArgs a, int w_fp32, cudaStream_t s) {
     norm_parts_kernel<T><<<dim3((unsigned)((a.cols + kRowThreads - 1) / kRowThreads), parts), kRowThreads, 0, s>>>(a, parts);
     if ((st = cuda_check(cudaGetLastError(), "layer norm parts launch")) != LPQ_OK) return st;
   }
-  norm_join_kernel<<<dim3((unsigned)((a.cols + 31) / 32), 2), 32 * kJoinWarps, 0, s>>>(a.parts, parts, a.cols, a.dweight, a.dbias);
-  return cuda_check(cudaGetLastError(), "layer norm join launch");
+  return cuda_check(launch_dependent(norm_join_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 32 * kJoinWarps, 0, s,
+                                     a.parts, parts, a.cols, a.dweight, a.dbias),
+                    "layer norm join launch");
 }
 
 }  // namespace
