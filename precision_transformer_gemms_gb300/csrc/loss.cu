@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lpq_device.cuh"
 
@@ -52,18 +53,32 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // the gradients' sums carry dl's bf16 rounding, far above that drift.
 constexpr int kChunk = 16;
 
-// What the epilogue makes of a tile.
+// What a kernel's epilogue makes of a tile.
 //   kStats    row maxima and sums of exponentials of the logits
 //   kDlogits  dl in bf16
-//   kPart     FP32 partial sums of dh (one slab per split of K), added to across pieces
-//   kOut      a finished gradient: times the scale, bf16 or FP32
-enum { kStats, kDlogits, kPart, kOut };
+//   kGrads    of two products: FP32 partial sums of dh (one slab per split of K,
+//             added to across pieces), or a finished gradient: times the scale,
+//             bf16 or FP32
+enum { kStats, kDlogits, kGrads };
 
-struct CeTile {
+// One product C [M, N] = A B^T of a launch.
+struct Product {
   int64_t M, N;
   int num_k;  // steps of kStepK along K
   int tiles_m, tiles_n, splits;
-  uint32_t idesc;
+  int items;  // tiles * splits
+  int a_mn;   // A lies with K along its rows
+  int part;  // partial sums into acc instead of out
+  void* out;
+};
+
+struct alignas(64) CeMaps {
+  CUtensorMap a[2], b[2], c[2];
+};
+
+struct CeTile {
+  Product prod[2];  // the second with no items where there is one product
+  int extra;        // items of the second for the pairs with fewer of the first, before all share the rest
   int* err;
   const int64_t* labels;
   int64_t vocab;
@@ -76,9 +91,14 @@ struct CeTile {
   const float* scale;
   float* acc;  // [splits][M][N]
   int add;     // 1: add to acc
-  void* out;
   int out_fp32;
 };
+
+// Instruction descriptor: F32 accumulator, BF16 x BF16, MN-major flags, N = 256, M = 256.
+constexpr uint32_t instruction_desc(bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -92,22 +112,41 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The i-th work item of a pair: product and item, false after the last.  The
+// first product's items go round the pairs; the pairs that get one fewer take
+// `extra` of the second's, then the rest goes round all pairs.
+__device__ __forceinline__ bool item_at(int i, int pair, int npairs, const CeTile& g, int& which, int& w) {
+  const int n0 = g.prod[0].items, left_over = n0 % npairs;
+  const int mine = n0 / npairs + (pair < left_over ? 1 : 0);
+  which = 0;
+  w = pair + i * npairs;
+  if (i < mine) return true;
+  which = 1;
+  i -= mine;
+  if (pair >= left_over) {
+    w = i * (npairs - left_over) + pair - left_over;
+    if (i < g.extra) return true;
+    i -= g.extra;
+  }
+  w = g.extra * (npairs - left_over) + i * npairs + pair;
+  return w < g.prod[1].items;
+}
 // Work item w -> tile and split; consecutive tiles walk down a band of kGroupM
 // m-tiles, all splits of a tile run together.
-__device__ __forceinline__ void item_coords(int w, const CeTile& g, int& mt, int& nt, int& split) {
-  split = w % g.splits;
-  const int t = w / g.splits;
-  const int per_group = kGroupM * g.tiles_n;
+__device__ __forceinline__ void item_coords(int w, const Product& p, int& mt, int& nt, int& split) {
+  split = w % p.splits;
+  const int t = w / p.splits;
+  const int per_group = kGroupM * p.tiles_n;
   const int group = t / per_group;
   const int first = group * kGroupM;
-  const int size = min(kGroupM, g.tiles_m - first);
+  const int size = min(kGroupM, p.tiles_m - first);
   const int r = t - group * per_group;
   mt = first + r % size;
   nt = r / size;
 }
-__device__ __forceinline__ void split_range(int split, const CeTile& g, int& k0, int& k1) {
-  k0 = (int)((int64_t)g.num_k * split / g.splits);
-  k1 = (int)((int64_t)g.num_k * (split + 1) / g.splits);
+__device__ __forceinline__ void split_range(int split, const Product& p, int& k0, int& k1) {
+  k0 = (int)((int64_t)p.num_k * split / p.splits);
+  k1 = (int)((int64_t)p.num_k * (split + 1) / p.splits);
 }
 
 // After an abort: wait (bounded) for the loads of ring uses [from, to).
@@ -120,12 +159,12 @@ __device__ __forceinline__ void drain(uint64_t* bars, uint32_t from, uint32_t to
 // streams the operands into a ring of shared-memory stages, warp 1 of the even
 // CTA (one lane) issues the pair MMAs, eight epilogue warps per CTA (two per
 // TMEM lane quarter, 128 columns each) finish the tile.
-// MN-major operands (A_MN, B_MN): the matrix lies with K along its rows; a
-// stage holds two 64 x 64 blocks (64 k-rows of 128 bytes each).
-template <int EPI, bool A_MN, bool B_MN>
+// MN-major operands (A where a_mn, B of kGrads): the matrix lies with K along
+// its rows; a stage holds two 64 x 64 blocks (64 k-rows of 128 bytes each).
+template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
-    ce_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const CeTile g) {
+    ce_pair_kernel(const __grid_constant__ CeMaps maps, const __grid_constant__ CeTile g) {
+  constexpr bool B_MN = EPI == kGrads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
@@ -143,7 +182,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-  const int total = g.tiles_m * g.tiles_n * g.splits;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -156,8 +194,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     }
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+    prefetch_tmap(&maps.a[0]);
+    prefetch_tmap(&maps.b[0]);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
   tc_fence_before();
@@ -181,32 +219,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     if (lane == 0) {
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
-      for (int w = pair; w < total && ok; w += npairs) {
+      int which, w;
+      for (int i = 0; ok && item_at(i, pair, npairs, g, which, w); ++i) {
+        const Product& p = g.prod[which];
+        const CUtensorMap *tmA = &maps.a[which], *tmB = &maps.b[which];
         int mt, nt, split, k0, k1;
-        item_coords(w, g, mt, nt, split);
-        split_range(split, g, k0, k1);
+        item_coords(w, p, mt, nt, split);
+        split_range(split, p, k0, k1);
         const int32_t arow = mt * kTile + (int32_t)rank * kHalf, brow = nt * kTile + (int32_t)rank * kHalf;
-        for (int kt = k0; kt < k1; ++kt) {
-          if (!(ok = mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, g.err))) break;
-          if (leader) mbar_arrive_expect_tx(&full[s], 4 * kOperand);
-          const uint32_t fb = full_leader + 8 * s;
-          uint8_t* da = sA + s * kOperand;
-          uint8_t* db = sB + s * kOperand;
-          if constexpr (A_MN) {
-            tma_load_2d_pair(da, &tmA, arow, kt * kStepK, fb);
-            tma_load_2d_pair(da + kOperand / 2, &tmA, arow + 64, kt * kStepK, fb);
-          } else {
-            tma_load_2d_pair(da, &tmA, kt * kStepK, arow, fb);
+        auto loads = [&](auto a_is_mn) {
+          constexpr bool A_MN = decltype(a_is_mn)::value;
+          for (int kt = k0; kt < k1; ++kt) {
+            if (!(ok = mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, g.err))) break;
+            if (leader) mbar_arrive_expect_tx(&full[s], 4 * kOperand);
+            const uint32_t fb = full_leader + 8 * s;
+            uint8_t* da = sA + s * kOperand;
+            uint8_t* db = sB + s * kOperand;
+            if constexpr (A_MN) {
+              tma_load_2d_pair(da, tmA, arow, kt * kStepK, fb);
+              tma_load_2d_pair(da + kOperand / 2, tmA, arow + 64, kt * kStepK, fb);
+            } else {
+              tma_load_2d_pair(da, tmA, kt * kStepK, arow, fb);
+            }
+            if constexpr (B_MN) {
+              tma_load_2d_pair(db, tmB, brow, kt * kStepK, fb);
+              tma_load_2d_pair(db + kOperand / 2, tmB, brow + 64, kt * kStepK, fb);
+            } else {
+              tma_load_2d_pair(db, tmB, kt * kStepK, brow, fb);
+            }
+            ++it;
+            if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
           }
-          if constexpr (B_MN) {
-            tma_load_2d_pair(db, &tmB, brow, kt * kStepK, fb);
-            tma_load_2d_pair(db + kOperand / 2, &tmB, brow + 64, kt * kStepK, fb);
-          } else {
-            tma_load_2d_pair(db, &tmB, kt * kStepK, brow, fb);
-          }
-          ++it;
-          if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
-        }
+        };
+        if (EPI == kGrads && p.a_mn) loads(std::true_type{}); else loads(std::false_type{});
       }
       // After an abort, the even CTA lets the pair's loads in flight land
       // (they all signal its full barriers) before either CTA exits.
@@ -217,14 +262,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       // K-major: 8-row groups of 1024 bytes, 16 values along K = 32 bytes on.
       // MN-major: 64-value blocks kOperand / 2 bytes apart, 8-row groups of K of
       // 1024 bytes, 16 rows along K = 2048 bytes on.
-      const uint64_t ad0 = smem_desc(smem_u32(sA), A_MN ? kOperand / 2 : 16, 1024, 2);
+      const uint64_t ad_k = smem_desc(smem_u32(sA), 16, 1024, 2), ad_mn = smem_desc(smem_u32(sA), kOperand / 2, 1024, 2);
       const uint64_t bd0 = smem_desc(smem_u32(sB), B_MN ? kOperand / 2 : 16, 1024, 2);
       uint32_t s = 0, ph = 0, lt = 0;
       bool ok = true;
-      for (int w = pair; w < total && ok; w += npairs) {
-        int mt, nt, split, k0, k1;
-        item_coords(w, g, mt, nt, split);
-        split_range(split, g, k0, k1);
+      // the products of one item; a_mn as a constant
+      auto item_products = [&](auto a_is_mn, int k0, int k1) {
+        constexpr bool A_MN = decltype(a_is_mn)::value;
+        constexpr uint32_t idesc = instruction_desc(A_MN, B_MN);
         int kt = k0;
         do {  // one accumulator per chunk of the sum (a split without steps still hands one over)
           const int kend = EPI == kStats ? min(k1, kt + kChunk) : k1;
@@ -236,31 +281,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           for (const int first = kt; kt < kend; ++kt) {
             if (!(ok = mbar_wait_bounded(&full[s], ph, abort_flag, g.err))) break;
             tc_fence_after();
-            const uint64_t ad = ad0 + (uint64_t)(s * (kOperand >> 4)), bd = bd0 + (uint64_t)(s * (kOperand >> 4));
+            const uint64_t ad = (A_MN ? ad_mn : ad_k) + (uint64_t)(s * (kOperand >> 4)), bd = bd0 + (uint64_t)(s * (kOperand >> 4));
 #pragma unroll
             for (int j = 0; j < kStepK / 16; ++j)
-              mma_pair<kKindF16>(tmem_d, ad + (uint64_t)(j * (A_MN ? 128 : 2)), bd + (uint64_t)(j * (B_MN ? 128 : 2)),
-                                 g.idesc, (kt > first || j > 0) ? 1u : 0u);
+              mma_pair<kKindF16>(tmem_d, ad + (uint64_t)(j * (A_MN ? 128 : 2)), bd + (uint64_t)(j * (B_MN ? 128 : 2)), idesc,
+                                 (kt > first || j > 0) ? 1u : 0u);
             tc_commit_pair(&empty[s], 0x3);
             if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
           }
           if (ok) tc_commit_pair(&acc_full[a], 0x3);
         } while (ok && kt < k1);
+      };
+      int which, w;
+      for (int i = 0; ok && item_at(i, pair, npairs, g, which, w); ++i) {
+        const Product& p = g.prod[which];
+        int k0, k1;
+        split_range(w % p.splits, p, k0, k1);
+        if (EPI == kGrads && p.a_mn) item_products(std::true_type{}, k0, k1);
+        else item_products(std::false_type{}, k0, k1);
       }
     }
   } else if (run && warp >= 2) {
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = stage_c + (warp - 2) * kStgWarp;
     float scale = 1.f;
-    if constexpr (EPI == kDlogits || EPI == kOut) scale = *g.scale;
+    if constexpr (EPI != kStats) scale = *g.scale;
     uint32_t lt = 0;
-    for (int w = pair; w < total; w += npairs) {
+    int which, w;
+    for (int item = 0; item_at(item, pair, npairs, g, which, w); ++item) {
+      const Product& p = g.prod[which];
       int mt, nt, split;
-      item_coords(w, g, mt, nt, split);
+      item_coords(w, p, mt, nt, split);
       const int64_t row = (int64_t)mt * kTile + rank * kHalf + q * 32 + lane;
       const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
-      const bool live = row < g.M;
-      const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, g.N - c0));  // columns of this warp inside the matrix
+      const bool live = row < p.M;
+      const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, p.N - c0));  // columns of this warp inside the matrix
       // what the row needs is fetched before the accumulator is waited for
       int label = -1;  // its column among this warp's 128, -1: not here
       float lse2 = 0.f, gs = 0.f;
@@ -298,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       if constexpr (EPI == kStats) {
         float l[kHalf];
         bool ok = true;
-        for (int kt = 0; kt < g.num_k && ok; kt += kChunk) {
+        for (int kt = 0; kt < p.num_k && ok; kt += kChunk) {
           if (!(ok = take())) break;
 #pragma unroll
           for (int cc = 0; cc < kHalf / 32; ++cc) {
@@ -333,9 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         continue;
       }
       bool some = true;
-      if constexpr (EPI == kPart) {  // a ragged last piece can leave a split without steps: nothing to add
+      const bool part = EPI == kGrads && p.part;
+      if (part) {  // a ragged last piece can leave a split without steps: nothing to add
         int k0, k1;
-        split_range(split, g, k0, k1);
+        split_range(split, p, k0, k1);
         some = k0 < k1;
       }
       if (!take()) break;
@@ -345,28 +401,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         __syncwarp();
         tmem_ld32(tbase + (uint32_t)(cc * 32), v);
         if (cc == kHalf / 32 - 1) give();
-        if constexpr (EPI == kPart) {
+        if (part) {
           if (live && some && cc * 32 < ncols) {
-            float* p = g.acc + ((int64_t)split * g.M + row) * g.N + c0 + cc * 32;
+            float* to = g.acc + ((int64_t)split * p.M + row) * p.N + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (cc * 32 + 4 * i >= ncols) break;
               float4 o = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                                      __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
               if (g.add) {
-                const float4 b = reinterpret_cast<const float4*>(p)[i];
+                const float4 b = reinterpret_cast<const float4*>(to)[i];
                 o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
               }
-              reinterpret_cast<float4*>(p)[i] = o;
+              reinterpret_cast<float4*>(to)[i] = o;
             }
           }
-        } else if (EPI == kOut && g.out_fp32) {
+        } else if (EPI == kGrads && g.out_fp32) {
           if (live && cc * 32 < ncols) {
-            float* p = static_cast<float*>(g.out) + row * g.N + c0 + cc * 32;
+            float* to = static_cast<float*>(p.out) + row * p.N + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (cc * 32 + 4 * i >= ncols) break;
-              reinterpret_cast<float4*>(p)[i] =
+              reinterpret_cast<float4*>(to)[i] =
                   make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
                               __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale);
             }
@@ -406,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&tmC, stg, (int32_t)(c0 + (cc - 1) * 32), mt * kTile + (int32_t)rank * kHalf + q * 32);
+              tma_store_2d(&maps.c[which], stg, (int32_t)(c0 + (cc - 1) * 32), mt * kTile + (int32_t)rank * kHalf + q * 32);
               bulk_commit_group();
             }
           }
@@ -511,18 +567,32 @@ int64_t piece_of(int64_t t, int64_t v, int64_t piece) {
   return std::min(piece, round_up(v, 64));
 }
 
+constexpr double kItemStart = 3;  // a tile's start and end, in steps (it also stores its result over the port that feeds it)
+
+// What a pair with one item fewer of the first product (n0 of c0 steps) takes
+// of the second (n1 of c1 steps) instead.
+int extra_items(int64_t n0, double c0, int64_t n1, double c1, int pairs) {
+  const int64_t fewer = pairs - n0 % pairs;
+  return fewer == pairs ? 0 : (int)std::min<int64_t>((int64_t)(c0 / c1 + 0.5), n1 / fewer);
+}
+
 // Splits of dh's sum over a piece's words.  dh has few tiles when t is small
-// and its sum is long, so the sum is split until the pairs are busy; each
-// split costs its slab of FP32 partial sums written and read once.  The
-// estimate: a step of a pair tile takes 0.33 us, a tile's start and end 1 us,
-// memory 6.5 TB/s.
+// and its sum is long: the split makes items that spread over the pairs beside
+// dw's (t steps each), and costs its slab of FP32 partial sums written and read
+// once.  The estimate: the longest pair at 0.33 us a step, memory at 6.5 TB/s.
 int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
   const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK);
+  const int64_t n1 = cdiv(width, kTile) * cdiv(d, kTile);
+  const double c1 = (double)cdiv(t, kStepK) + kItemStart;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 64 && s <= steps; ++s) {
-    const double us = (double)cdiv(tiles * s, pairs) * ((double)cdiv(steps, s) * 0.33 + 1.0) +
-                      (s > 1 ? (double)s * (double)t * (double)d * 8.0 / 6.5e6 : 0.0);
+    const int64_t n0 = tiles * s;
+    const double c0 = (double)cdiv(steps, s) + kItemStart;
+    const int64_t fewer = pairs - n0 % pairs, extra = extra_items(n0, c0, n1, c1, pairs);
+    const double shared = (double)cdiv(n1 - extra * fewer, pairs) * c1;
+    const double longest = std::max((double)cdiv(n0, pairs) * c0, (double)(n0 / pairs) * c0 + (double)extra * c1) + shared;
+    const double us = longest * 0.33 + (s > 1 ? (double)s * (double)t * (double)d * 8.0 / 6.5e6 : 0.0);
     if (s == 1 || us < least) {
       least = us;
       best = s;
@@ -536,32 +606,41 @@ struct Operand {
   int64_t ld;  // elements
 };
 
-// Launches one product: A [M, K] (K-major) or [K, M] (A_MN), B likewise; C the
-// bf16 output of the kinds that store one.
-template <int EPI, bool A_MN, bool B_MN>
-lpq_status run_pair(CeTile g, Operand a, Operand b, int64_t K, void* c, int64_t ldc, int splits, cudaStream_t s) {
-  CUtensorMap ta, tb, tc;
+// Describes product i of a launch: A [M, K] (K-major) or [K, M] (a_mn), B [N, K]
+// or (b_mn) [K, N]; C the bf16 output of the kinds that store one by TMA.
+lpq_status set_product(CeTile& g, CeMaps& maps, int i, int64_t M, int64_t N, int64_t K, Operand a, bool a_mn, Operand b,
+                       bool b_mn, void* c, int64_t ldc, int splits) {
   lpq_status st;
-  if ((st = A_MN ? make_map(&ta, a.p, true, g.M, K, a.ld * 2, 64, kStepK)
-                 : make_map(&ta, a.p, true, K, g.M, a.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
-  if ((st = B_MN ? make_map(&tb, b.p, true, g.N, K, b.ld * 2, 64, kStepK)
-                 : make_map(&tb, b.p, true, K, g.N, b.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
-  tc = ta;
-  if (c && (st = make_map(&tc, c, true, g.N, g.M, ldc * 2, 64, 32)) != LPQ_OK) return st;
-  const int64_t tm = cdiv(g.M, kTile), tn = cdiv(g.N, kTile);
+  if ((st = a_mn ? make_map(&maps.a[i], a.p, true, M, K, a.ld * 2, 64, kStepK)
+                 : make_map(&maps.a[i], a.p, true, K, M, a.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+  if ((st = b_mn ? make_map(&maps.b[i], b.p, true, N, K, b.ld * 2, 64, kStepK)
+                 : make_map(&maps.b[i], b.p, true, K, N, b.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+  if (c && (st = make_map(&maps.c[i], c, true, N, M, ldc * 2, 64, 32)) != LPQ_OK) return st;
+  const int64_t tm = cdiv(M, kTile), tn = cdiv(N, kTile);
   if (tm * tn * splits > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "too many output tiles");
-  g.num_k = (int)cdiv(K, kStepK);
-  g.tiles_m = (int)tm;
-  g.tiles_n = (int)tn;
-  g.splits = splits;
-  // F32 accumulator, BF16 x BF16, MN-major flags, N = 256, M = 256
-  g.idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) |
-            ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-  if ((st = device_error_word(&g.err)) != LPQ_OK) return st;
-  if ((st = set_smem_attr(reinterpret_cast<const void*>(ce_pair_kernel<EPI, A_MN, B_MN>), kSmem)) != LPQ_OK) return st;
-  const int pairs = (int)std::min<int64_t>(tm * tn * splits, std::max(1, device_sms() / 2));
-  return cuda_check(launch_dependent(ce_pair_kernel<EPI, A_MN, B_MN>, 2 * pairs, kThreads, kSmem, s, ta, tb, tc, g),
-                    "cross entropy launch");
+  Product& p = g.prod[i];
+  p.M = M;
+  p.N = N;
+  p.num_k = (int)cdiv(K, kStepK);
+  p.tiles_m = (int)tm;
+  p.tiles_n = (int)tn;
+  p.splits = splits;
+  p.items = (int)(tm * tn * splits);
+  p.a_mn = a_mn;
+  return LPQ_OK;
+}
+
+template <int EPI>
+lpq_status run_pair(CeTile& g, const CeMaps& maps, cudaStream_t s) {
+  lpq_status st = device_error_word(&g.err);
+  if (st != LPQ_OK) return st;
+  if ((st = set_smem_attr(reinterpret_cast<const void*>(ce_pair_kernel<EPI>), kSmem)) != LPQ_OK) return st;
+  const int64_t items = (int64_t)g.prod[0].items + g.prod[1].items;
+  const int pairs = (int)std::min<int64_t>(items, std::max(1, device_sms() / 2));
+  if (g.prod[1].items > 0)
+    g.extra = extra_items(g.prod[0].items, (double)cdiv(g.prod[0].num_k, g.prod[0].splits) + kItemStart, g.prod[1].items,
+                          (double)g.prod[1].num_k + kItemStart, pairs);
+  return cuda_check(launch_dependent(ce_pair_kernel<EPI>, 2 * pairs, kThreads, kSmem, s, maps, g), "cross entropy launch");
 }
 
 // Workspace of the backward pass: scale, dl, partial sums of dh.
@@ -593,15 +672,15 @@ size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piec
 lpq_status launch_ce(const CeArgs& a, cudaStream_t s) {
   if (a.t == 0) return LPQ_OK;
   CeTile g{};
-  g.M = a.t;
-  g.N = a.v;
+  CeMaps maps{};
   g.labels = a.labels;
   g.vocab = a.v;
   g.at_label = reinterpret_cast<float*>(a.workspace);
   g.stats = reinterpret_cast<float2*>(a.workspace + round_up(a.t * 4, 256));
   g.stat_cols = cdiv(a.v, kHalf);
-  lpq_status st = run_pair<kStats, false, false>(g, {a.h, a.ldh}, {a.w, a.ldw}, a.d, nullptr, 0, 1, s);
+  lpq_status st = set_product(g, maps, 0, a.t, a.v, a.d, {a.h, a.ldh}, false, {a.w, a.ldw}, false, nullptr, 0, 1);
   if (st != LPQ_OK) return st;
+  if ((st = run_pair<kStats>(g, maps, s)) != LPQ_OK) return st;
   return cuda_check(launch_dependent(ce_join_kernel, (unsigned)cdiv(a.t, 8), 256, 0, s, g.stats, g.stat_cols, g.at_label,
                                      a.labels, a.t, a.v, a.loss, a.lse_out),
                     "cross entropy join launch");
@@ -613,42 +692,53 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   const BackwardPlan plan(a.t, a.v, a.d, a.piece);
   float* scale = reinterpret_cast<float*>(a.workspace);
   void* dl = a.workspace + plan.dl_at;
-  CeTile g{};
-  g.labels = a.labels;
-  g.vocab = a.v;
-  g.lse = a.lse;
-  g.dloss = a.dloss;
-  g.scale = scale;
-  g.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
-  g.out_fp32 = a.grads_fp32;
+  CeTile base{};
+  base.labels = a.labels;
+  base.vocab = a.v;
+  base.lse = a.lse;
+  base.dloss = a.dloss;
+  base.scale = scale;
+  base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
+  base.out_fp32 = a.grads_fp32;
   lpq_status st = cuda_check(launch_dependent(ce_scale_kernel, 1, 1024, 0, s, a.dloss, a.labels, a.t, a.v, scale),
                              "cross entropy scale launch");
   if (st != LPQ_OK) return st;
+  const Operand h{a.h, a.ldh}, l{dl, plan.dl_ld};
   for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
     const int64_t width = std::min(plan.piece, a.v - v0);
     const Operand w{static_cast<const uint8_t*>(a.w) + (size_t)v0 * (size_t)a.ldw * 2, a.ldw};
-    const Operand h{a.h, a.ldh}, l{dl, plan.dl_ld};
+    CeMaps maps{};
     // dl = (exp(h w^T - lse) - onehot) dloss / s
-    g.M = a.t; g.N = width; g.col0 = v0;
-    if ((st = run_pair<kDlogits, false, false>(g, h, w, a.d, dl, plan.dl_ld, 1, s)) != LPQ_OK) return st;
-    // dh (+)= dl w
-    g.M = a.t; g.N = a.d; g.add = v0 > 0;
-    if (plan.direct) {
-      g.out = a.dh;
-      st = run_pair<kOut, false, true>(g, l, w, width, a.grads_fp32 ? nullptr : a.dh, a.d, 1, s);
-    } else {
-      st = run_pair<kPart, false, true>(g, l, w, width, nullptr, 0, plan.splits, s);
+    CeTile g = base;
+    g.col0 = v0;
+    if ((st = set_product(g, maps, 0, a.t, width, a.d, h, false, w, false, dl, plan.dl_ld, 1)) != LPQ_OK) return st;
+    if ((st = run_pair<kDlogits>(g, maps, s)) != LPQ_OK) return st;
+    // dh (+)= dl w and dw = dl^T h
+    g = base;
+    g.add = v0 > 0;
+    void* dw = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
+    if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, a.grads_fp32 || !plan.direct ? nullptr : a.dh, a.d,
+                          plan.splits)) != LPQ_OK) return st;
+    g.prod[0].part = !plan.direct;
+    g.prod[0].out = a.dh;
+    // in one launch where dh's last round would leave over a tenth of the
+    // pairs' time for it idle, which dw's items then fill (1001 x 1024 x 50001:
+    // 238 -> 233 us in all); else one after the other, each with the L2 to
+    // itself (7936 x 4096 x 32000: 3680 us, 3765 us in one)
+    const int64_t P = std::max(1, device_sms() / 2), n0 = g.prod[0].items, rounds = cdiv(n0, P) * P;
+    const int at = 10 * (rounds - n0) > rounds ? 1 : 0;
+    if (at == 0) {
+      if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
+      g = base;
     }
-    if (st != LPQ_OK) return st;
-    // dw = dl^T h
-    g.M = width; g.N = a.d;
-    g.out = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
-    if ((st = run_pair<kOut, true, true>(g, l, h, a.t, a.grads_fp32 ? nullptr : g.out, a.d, 1, s)) != LPQ_OK) return st;
+    if ((st = set_product(g, maps, at, width, a.d, a.t, l, true, h, true, a.grads_fp32 ? nullptr : dw, a.d, 1)) != LPQ_OK) return st;
+    g.prod[at].out = dw;
+    if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
   }
   if (plan.direct) return LPQ_OK;
   const int64_t n4 = a.t * a.d / 4;
   const unsigned grid = (unsigned)std::min<int64_t>(cdiv(n4, 256), (int64_t)device_sms() * 8);
-  return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(g.acc), n4,
+  return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc), n4,
                                      plan.splits, scale, a.dh, a.grads_fp32),
                     "cross entropy finish launch");
 }
