@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(const float*
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   const int which = blockIdx.y;  // 0: dweight, 1: dbias
   float* out = which ? dbias : dweight;
-  if (!out) return;
+  let_dependents_start();
   wait_for_stream();
+  if (!out) return;
   float s = 0.f;
   if (c < cols) {
     const float* p = parts + which * cols + c;
@@ -384,6 +385,8 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kBlock) norm_kernel(const NormA
   const int tid = threadIdx.x % TPR, n = (int)a.cols;
   const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
   const float inv_n = 1.0f / (float)n;
+  let_dependents_start();
+  wait_for_stream();
   // the row whose copy is next: its number and this thread's first vector
   int64_t ahead = first;
   const T* ahead_x = static_cast<const T*>(a.x) + first * a.ldx + tid * V;
@@ -481,7 +484,8 @@ __global__ void __launch_bounds__(RowGroup<TPR>::kBlock) norm_backward_kernel(co
   const int tid = threadIdx.x % TPR, n = (int)a.cols;
   const int64_t first = (int64_t)blockIdx.x * kGroups + threadIdx.x / TPR, step = (int64_t)gridDim.x * kGroups;
   const float inv_n = 1.0f / (float)n;
-  let_dependents_start();  // (norm_join_kernel waits for the parts)
+  let_dependents_start();
+  wait_for_stream();
   // the row whose copy is next: its number and this thread's first vectors
   int64_t ahead = first;
   const T* ahead_x = static_cast<const T*>(a.x) + first * a.ldx + tid * V;
@@ -636,8 +640,7 @@ lpq_status run_forward(const NormArgs& a, int w_fp32, cudaStream_t s) {
   const int64_t most = (int64_t)device_sms() * resident_ctas(kernel, kBlock, kSmem);
   const int grid = (int)std::min<int64_t>((a.rows + kGroups - 1) / kGroups, most);
   if ((st = clear_amax(a, grid, s)) != LPQ_OK) return st;
-  norm_kernel<T, VEC, HELD, TPR, NE><<<grid, kBlock, kSmem, s>>>(a, w_fp32);
-  return cuda_check(cudaGetLastError(), "layer norm launch");
+  return cuda_check(launch_dependent(norm_kernel<T, VEC, HELD, TPR, NE>, grid, kBlock, kSmem, s, a, w_fp32), "layer norm launch");
 }
 
 template <typename T, bool VEC, bool HELD, int TPR, int NE>
@@ -649,8 +652,8 @@ lpq_status run_backward(const NormArgs& a, int w_fp32, int& parts, cudaStream_t 
   lpq_status st = set_smem_attr(reinterpret_cast<const void*>(norm_backward_kernel<T, VEC, HELD, TPR, NE>), kSmem);
   if (st != LPQ_OK) return st;
   parts = (int)std::min<int64_t>((a.rows + kGroups - 1) / kGroups, norm_parts(a.rows, a.cols));
-  norm_backward_kernel<T, VEC, HELD, TPR, NE><<<parts, kBlock, kSmem, s>>>(a, w_fp32);
-  return cuda_check(cudaGetLastError(), "layer norm backward launch");
+  return cuda_check(launch_dependent(norm_backward_kernel<T, VEC, HELD, TPR, NE>, parts, kBlock, kSmem, s, a, w_fp32),
+                    "layer norm backward launch");
 }
 
 // Threads per row and elements per thread by width; beyond 16384 columns the
