@@ -188,12 +188,13 @@ struct RowGroup {
   static constexpr int kGroups = kBlock / TPR;
 };
 
-// Rows in flight for a ring stage of this many bytes: two CTAs fit an SM in the
-// forward pass, one in the backward pass.
+// Rows in flight for a ring stage of this many bytes.  Forward, with several
+// CTAs per SM: two or three (four are slower: 182 us instead of 174 at 63488 x
+// 4096 bf16).  Backward, one CTA per SM: four while they fit.
 template <bool BACKWARD>
 constexpr int rows_ahead(int stage) {
-  constexpr int most = BACKWARD ? 196608 : 98304;
-  return 4 * stage <= most ? 4 : 3 * stage <= most ? 3 : 2 * stage <= 200000 ? 2 : 1;
+  constexpr int most = BACKWARD ? 196608 : 24576;
+  return BACKWARD && 4 * stage <= most ? 4 : 3 * stage <= most ? 3 : 2 * stage <= 200000 ? 2 : 1;
 }
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
   constexpr int kBlock = RowGroup<TPR, true>::kBlock, kGroups = RowGroup<TPR, true>::kGroups;
   constexpr int V = 16 / (int)sizeof(T), NV = NE / V;
   constexpr int kAhead = rows_ahead<true>(2 * NV * 16 * kBlock);
+  constexpr bool kAgain = VEC && NE > 16;
   extern __shared__ uint4 ring[];  // [kAhead][x, dy][NV][kBlock]
   __shared__ alignas(16) float sh[2][2][32];
   const int tid = threadIdx.x % TPR, n = (int)a.cols;
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
   float2 dw[NE / 2], db[NE / 2];
 #pragma unroll
   for (int i = 0; i < NE / 2; ++i) dw[i] = db[i] = pair_of(0.f);
-  constexpr bool kHeld = VEC && HELD;
+  constexpr bool kHeld = VEC && HELD && !kAgain;
   const Params<T, TPR, VEC ? NE : V, kHeld> weight(a.weight, w_fp32, tid, n, ones<T>());
   int slot = 0, turn = 0;
   float mean = first < a.rows ? a.mean_in[first] : 0.f, rstd = first < a.rows ? a.rstd_in[first] : 0.f;
@@ -530,6 +532,55 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
     const float next_mean = a.mean_in[rn], next_rstd = a.rstd_in[rn];
     float2 x[NE / 2], g[NE / 2];
     if constexpr (VEC) cp_async_wait<kAhead - 1>();
+    if constexpr (kAgain) {
+      // 32 elements of x, dy and both gradients are more than a thread can
+      // hold: the row's sums first, then its vectors once more from the ring
+      float2 s0 = pair_of(0.f), s1 = pair_of(0.f);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        if (c < n) {
+          float2 xv[V / 2], gv[V / 2], w[V / 2];
+          unpack_vector<T>(ring[(slot * 2 * NV + v) * kBlock + threadIdx.x], xv);
+          unpack_vector<T>(ring[((slot * 2 + 1) * NV + v) * kBlock + threadIdx.x], gv);
+          weight.get(v, c, w, 1.0f);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            xv[j] = __fmul2_rn(__fadd2_rn(xv[j], pair_of(-mean)), pair_of(rstd));
+            dw[v * V / 2 + j] = __ffma2_rn(gv[j], xv[j], dw[v * V / 2 + j]);
+            db[v * V / 2 + j] = __fadd2_rn(db[v * V / 2 + j], gv[j]);
+            gv[j] = __fmul2_rn(gv[j], w[j]);
+            s0 = __fadd2_rn(s0, gv[j]);
+            s1 = __ffma2_rn(gv[j], xv[j], s1);
+          }
+        }
+      }
+      float s[2] = {s0.x + s0.y, s1.x + s1.y};
+      group_sum<TPR, 2>(s, sh[turn]);
+      turn ^= 1;
+      const float2 m1 = pair_of(-s[0] * inv_n), m2 = pair_of(-s[1] * inv_n);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = column_of<T, true, TPR>(tid, v * V);
+        if (c < n) {
+          float2 xv[V / 2], gv[V / 2], w[V / 2];
+          unpack_vector<T>(ring[(slot * 2 * NV + v) * kBlock + threadIdx.x], xv);
+          unpack_vector<T>(ring[((slot * 2 + 1) * NV + v) * kBlock + threadIdx.x], gv);
+          weight.get(v, c, w, 1.0f);
+#pragma unroll
+          for (int j = 0; j < V / 2; ++j) {
+            xv[j] = __fmul2_rn(__fadd2_rn(xv[j], pair_of(-mean)), pair_of(rstd));
+            gv[j] = __fmul2_rn(__ffma2_rn(xv[j], m2, __ffma2_rn(gv[j], w[j], m1)), pair_of(rstd));
+          }
+          *reinterpret_cast<uint4*>(dx + c) = pack_vector<T>(gv);
+        }
+      }
+      copy(slot);
+      slot = (slot + 1) % kAhead;
+      mean = next_mean;
+      rstd = next_rstd;
+      continue;
+    }
     take_row<T, VEC, TPR, NE>(&ring[slot * 2 * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.x) + r * a.ldx, tid, n, x);
     take_row<T, VEC, TPR, NE>(&ring[(slot * 2 + 1) * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.dy) + r * a.lddy, tid, n, g);
     // (past the row's end g is 0, and with it everything that x enters)
@@ -631,9 +682,16 @@ bool vector_rows(const NormArgs& a, size_t elem, bool backward) {
   return !backward || (ok(a.dy) && a.lddy % per == 0);
 }
 
+// amax = 0 before the CTAs of a launch raise it.  A kernel, and not a memset: the
+// norm's kernel starts under it.
+__global__ void clear_amax_kernel(float* amax) {
+  let_dependents_start();
+  wait_for_stream();
+  *amax = 0.f;
+}
 lpq_status clear_amax(const NormArgs& a, int grid, cudaStream_t s) {
   if (!a.amax || grid == 1) return LPQ_OK;
-  return cuda_check(cudaMemsetAsync(a.amax, 0, sizeof(float), s), "cudaMemsetAsync(amax)");
+  return cuda_check(launch_dependent(clear_amax_kernel, 1, 1, 0, s, a.amax), "layer norm amax launch");
 }
 
 template <typename T, bool VEC, bool HELD, int TPR, int NE>
@@ -666,11 +724,14 @@ lpq_status run_backward(const NormArgs& a, int w_fp32, int& parts, cudaStream_t 
 // rows are read from memory again.
 template <typename F>
 lpq_status by_width(int64_t cols, F f) {
-  if (cols <= 256) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 8>{});
-  if (cols <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
-  if (cols <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 16>{});
-  if (cols <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 16>{});
-  return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 32>{});
+  using std::integral_constant;
+  if (cols <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+  if (cols <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  if (cols <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+  if (cols <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 16>{});
+  if (cols <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 16>{});
+  if (cols <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 16>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, 32>{});
 }
 
 template <typename T>
