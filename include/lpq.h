@@ -339,7 +339,8 @@ lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw,
 
 /* Gradients of sum_i dloss[i] * loss[i]: with the forward's lse and
  *   dl[i, j] = dloss[i] * (exp(l[i, j] - lse[i]) - (j == labels[i]))
- * (0 in rows without target, whatever their dloss and lse hold)
+ * (0 in rows without target, whatever their h, dloss and lse hold; such rows are
+ * left out of the work)
  *   dh [t, d] = dl w,   dw [v, d] = dl^T h,
  * contiguous, bf16 (grads_fp32 = 0) or FP32.  The logits are computed again,
  * vocab_piece words at a time (0: the library's choice; else a positive

@@ -13,6 +13,11 @@
 // TMEM.  The operand that a product sums along its rows (w in dl w; dl and h
 // in dl^T h) is read as it lies, as an MN-major operand: no transposed copies.
 //
+// The backward pass works on the rows that have a target alone: they are
+// counted and listed on the device, their hidden states copied together where
+// there are others, and the kernels take their sizes from the count.  What the
+// other rows hold reaches nothing, and costs nothing.
+//
 // dl is divided by s = max |dloss| before its rounding to bf16 (what the
 // tensor cores read) and s multiplies the FP32 sums: with equal dloss, the
 // mean over the tokens say, the entry p - 1 of a label is then rounded as it
@@ -68,18 +73,24 @@ struct Product {
   int tiles_m, tiles_n, splits;
   int items;  // tiles * splits
   int a_mn;   // A lies with K along its rows
-  int part;  // partial sums into acc instead of out
+  int m_rows, k_rows;  // M, or K, is the number of rows with a target (known on the device)
+  int scatter;         // rows of the result go to the places of their list
+  int part;            // partial sums into acc instead of out
   void* out;
 };
 
 struct alignas(64) CeMaps {
   CUtensorMap a[2], b[2], c[2];
+  CUtensorMap alt;  // of the copied rows of h: A of kDlogits, B of dw
 };
 
 struct CeTile {
   Product prod[2];  // the second with no items where there is one product
   int extra;        // items of the second for the pairs with fewer of the first, before all share the rest
   int* err;
+  int64_t t;        // rows of h
+  const int* rows;  // how many of them have a target (backward)
+  const int* list;  // which
   const int64_t* labels;
   int64_t vocab;
   int64_t col0;     // first word of the piece
@@ -115,8 +126,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // The i-th work item of a pair: product and item, false after the last.  The
 // first product's items go round the pairs; the pairs that get one fewer take
 // `extra` of the second's, then the rest goes round all pairs.
-__device__ __forceinline__ bool item_at(int i, int pair, int npairs, const CeTile& g, int& which, int& w) {
-  const int n0 = g.prod[0].items, left_over = n0 % npairs;
+__device__ __forceinline__ bool item_at(int i, int pair, int npairs, const Product* prod, int extra, int& which, int& w) {
+  const int n0 = prod[0].items, left_over = n0 % npairs;
   const int mine = n0 / npairs + (pair < left_over ? 1 : 0);
   which = 0;
   w = pair + i * npairs;
@@ -125,11 +136,11 @@ __device__ __forceinline__ bool item_at(int i, int pair, int npairs, const CeTil
   i -= mine;
   if (pair >= left_over) {
     w = i * (npairs - left_over) + pair - left_over;
-    if (i < g.extra) return true;
-    i -= g.extra;
+    if (i < extra) return true;
+    i -= extra;
   }
-  w = g.extra * (npairs - left_over) + i * npairs + pair;
-  return w < g.prod[1].items;
+  w = extra * (npairs - left_over) + i * npairs + pair;
+  return w < prod[1].items;
 }
 // Work item w -> tile and split; consecutive tiles walk down a band of kGroupM
 // m-tiles, all splits of a tile run together.
@@ -212,6 +223,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   const bool run = *peer_base == tmem_base;
   let_dependents_start();
   wait_for_stream();
+  // the products at their sizes on the device
+  __shared__ Product prod[2];
+  __shared__ int extra_sh;
+  const int rows = EPI == kStats ? 0 : *g.rows;
+  const bool some_rows = EPI != kStats && rows < g.t;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      Product p = g.prod[i];
+      if (p.m_rows) {
+        p.M = rows;
+        p.tiles_m = (rows + kTile - 1) / kTile;
+        p.items = p.tiles_m * p.tiles_n * p.splits;
+      }
+      if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK;
+      prod[i] = p;
+    }
+    const int left_over = prod[0].items % npairs;
+    extra_sh = left_over ? min(g.extra, prod[1].items / (npairs - left_over)) : 0;
+  }
+  __syncthreads();
+  const int extra = extra_sh;
   const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
 
@@ -220,9 +252,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       uint32_t s = 0, ph = 0, it = 0;
       bool ok = true;
       int which, w;
-      for (int i = 0; ok && item_at(i, pair, npairs, g, which, w); ++i) {
-        const Product& p = g.prod[which];
-        const CUtensorMap *tmA = &maps.a[which], *tmB = &maps.b[which];
+      for (int i = 0; ok && item_at(i, pair, npairs, prod, extra, which, w); ++i) {
+        const Product& p = prod[which];
+        const CUtensorMap* tmA = EPI == kDlogits && some_rows ? &maps.alt : &maps.a[which];
+        const CUtensorMap* tmB = EPI == kGrads && p.k_rows && some_rows ? &maps.alt : &maps.b[which];
         int mt, nt, split, k0, k1;
         item_coords(w, p, mt, nt, split);
         split_range(split, p, k0, k1);
@@ -293,8 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         } while (ok && kt < k1);
       };
       int which, w;
-      for (int i = 0; ok && item_at(i, pair, npairs, g, which, w); ++i) {
-        const Product& p = g.prod[which];
+      for (int i = 0; ok && item_at(i, pair, npairs, prod, extra, which, w); ++i) {
+        const Product& p = prod[which];
         int k0, k1;
         split_range(w % p.splits, p, k0, k1);
         if (EPI == kGrads && p.a_mn) item_products(std::true_type{}, k0, k1);
@@ -308,8 +341,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     if constexpr (EPI != kStats) scale = *g.scale;
     uint32_t lt = 0;
     int which, w;
-    for (int item = 0; item_at(item, pair, npairs, g, which, w); ++item) {
-      const Product& p = g.prod[which];
+    for (int item = 0; item_at(item, pair, npairs, prod, extra, which, w); ++item) {
+      const Product& p = prod[which];
       int mt, nt, split;
       item_coords(w, p, mt, nt, split);
       const int64_t row = (int64_t)mt * kTile + rank * kHalf + q * 32 + lane;
@@ -317,19 +350,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       const bool live = row < p.M;
       const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, p.N - c0));  // columns of this warp inside the matrix
       // what the row needs is fetched before the accumulator is waited for
+      int64_t from = row;  // the row of h
+      if (EPI == kGrads && p.scatter && live) from = g.list[row];
       int label = -1;  // its column among this warp's 128, -1: not here
       float lse2 = 0.f, gs = 0.f;
       bool target = false;
       if constexpr (EPI == kStats || EPI == kDlogits) {
-        const int64_t word = live ? g.labels[row] : -1;
+        if (EPI == kDlogits && live) from = g.list[row];
+        const int64_t word = live ? g.labels[from] : -1;
         target = word >= 0 && word < g.vocab;
         const int64_t col = word - (g.col0 + c0);
         if (target && col >= 0 && col < kHalf) label = (int)col;
       }
       if constexpr (EPI == kDlogits) {
         if (target) {
-          lse2 = g.lse[row] * kLog2e;
-          gs = g.dloss[row] / scale;
+          lse2 = g.lse[from] * kLog2e;
+          gs = g.dloss[from] / scale;
         }
       }
       // Waits for the next accumulator; hands it back once its values are in registers.
@@ -389,7 +425,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       }
       bool some = true;
       const bool part = EPI == kGrads && p.part;
-      if (part) {  // a ragged last piece can leave a split without steps: nothing to add
+      if constexpr (EPI == kGrads) {
+        // no steps: a split of a ragged last piece (nothing to add), or dw without rows (zeros)
         int k0, k1;
         split_range(split, p, k0, k1);
         some = k0 < k1;
@@ -418,13 +455,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           }
         } else if (EPI == kGrads && g.out_fp32) {
           if (live && cc * 32 < ncols) {
-            float* to = static_cast<float*>(p.out) + row * p.N + c0 + cc * 32;
+            float* to = static_cast<float*>(p.out) + from * p.N + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (cc * 32 + 4 * i >= ncols) break;
               reinterpret_cast<float4*>(to)[i] =
-                  make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
-                              __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale);
+                  some ? make_float4(__uint_as_float(v[4 * i]) * scale, __uint_as_float(v[4 * i + 1]) * scale,
+                                     __uint_as_float(v[4 * i + 2]) * scale, __uint_as_float(v[4 * i + 3]) * scale)
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
             }
           }
         } else {
@@ -441,23 +479,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
                 if (label == cc * 32 + i) v[i] = __float_as_uint(__uint_as_float(v[i]) - gs);
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * scale);
+            for (int i = 0; i < 32; ++i) v[i] = some ? __float_as_uint(__uint_as_float(v[i]) * scale) : 0u;
+          }
+          uint4 pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
+              u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            pk[i] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+          if (EPI == kGrads && p.scatter) {  // (d is a multiple of 8: whole vectors)
+            if (live) {
+              uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + from * p.N + c0 + cc * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (cc * 32 + 8 * i < ncols) to[i] = pk[i];
+            }
+            continue;
           }
           if ((cc & 1) == 0) {
             if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
             __syncwarp();
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-              pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            const int chunk = (cc & 1) * 4 + i;
-            *reinterpret_cast<uint4*>(stg + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<uint4*>(stg + lane * 128 + ((((cc & 1) * 4 + i) ^ (lane & 7)) << 4)) = pk[i];
           if (cc & 1) {
             fence_proxy_async_smem();
             __syncwarp();
@@ -517,41 +567,108 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64
   }
 }
 
-// s = max |dloss| over the rows with a target; 1 where that is 0 or not finite.
-__global__ void __launch_bounds__(1024) ce_scale_kernel(const float* dloss, const int64_t* labels, int64_t t, int64_t v,
-                                                        float* scale) {
-  __shared__ float sh[32];
+// The rows with a target in order, their number, and s = max |dloss| over them
+// (1 where that is 0 or not finite).  Where there are other rows, the listed
+// rows of h are copied together (and zeros up to a whole step of K behind them)
+// and the others' rows of dh are set to zero.  Every CTA takes a run of rows and
+// counts the labels ahead of it by itself, 8 bytes a row from the L2: one launch.
+__global__ void __launch_bounds__(256) ce_rows_kernel(const float* dloss, const int64_t* labels, int64_t t, int64_t v,
+                                                      const uint4* h, int64_t ldh8, int d8, uint4* copied, uint4* dh,
+                                                      int dh16, float* scale, int* rows_p, int* list) {
+  __shared__ float top_sh[8];
+  __shared__ int before_sh[8], total_sh[8], count_sh[8], place_sh[256];
   let_dependents_start();
   wait_for_stream();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t per = (t + gridDim.x - 1) / gridDim.x, r0 = min(t, blockIdx.x * per), r1 = min(t, r0 + per);
   float m = 0.f;
-  for (int64_t i = threadIdx.x; i < t; i += 1024)
-    if (labels[i] >= 0 && labels[i] < v) m = absmax_acc(m, dloss[i]);
+  int before = 0, total = 0;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < t; i += 256) {
+    const int64_t label = labels[i];
+    const bool target = label >= 0 && label < v;
+    total += target;
+    before += target && i < r0;
+    if (blockIdx.x == 0 && target) m = absmax_acc(m, dloss[i]);
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
   m = warp_max_xor(m, 32);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  if (lane == 0) {
+    before_sh[warp] = before;
+    total_sh[warp] = total;
+    top_sh[warp] = m;
+  }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    m = warp_max_xor(sh[threadIdx.x], 32);
-    if (threadIdx.x == 0) *scale = finite_pos(m) ? m : 1.f;
+  before = total = 0;
+  for (int i = 0; i < 8; ++i) {
+    before += before_sh[i];
+    total += total_sh[i];
+    m = fmaxf(m, top_sh[i]);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *scale = finite_pos(m) ? m : 1.f;
+    *rows_p = total;
+  }
+  const bool all = total == t;
+  for (int64_t b = r0; b < r1; b += 256) {
+    const int64_t i = b + threadIdx.x;
+    const int64_t label = i < r1 ? labels[i] : -1;
+    const bool target = label >= 0 && label < v;
+    const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, target);
+    __syncthreads();  // the last run's places are used
+    if (lane == 0) count_sh[warp] = __popc(ballot);
+    __syncthreads();
+    int place = before + __popc(ballot & ((1u << lane) - 1u));
+    for (int j = 0; j < 8; ++j) {
+      if (j < warp) place += count_sh[j];
+      before += count_sh[j];
+    }
+    place_sh[threadIdx.x] = target ? place : -1;
+    if (target) list[place] = (int)i;
+    if (all) continue;
+    __syncthreads();
+    for (int64_t r = b + warp; r < min(r1, b + 256); r += 8) {  // one warp per row
+      const int to = place_sh[r - b];
+      if (to >= 0) {
+#pragma unroll 8
+        for (int j = lane; j < d8; j += 32) copied[(int64_t)to * d8 + j] = h[r * ldh8 + j];
+      } else {
+        for (int j = lane; j < dh16; j += 32) dh[r * dh16 + j] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  if (!all && blockIdx.x == gridDim.x - 1) {
+    const int64_t padded = min(t, ((int64_t)total + kStepK - 1) / kStepK * kStepK);
+    for (int64_t i = (int64_t)total * d8 + threadIdx.x; i < padded * d8; i += 256) copied[i] = make_uint4(0, 0, 0, 0);
   }
 }
 
-// dh from its partial sums: the splits in order, times the scale.
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int64_t n4, int splits, const float* scale,
-                                                        void* out, int fp32) {
+// dh from its partial sums: the splits in order, times the scale, to the listed
+// rows.  A warp takes 32 vectors of a row.
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int d4, int splits, const float* scale,
+                                                        const int* rows_p, const int* list, void* out, int fp32) {
   let_dependents_start();
   wait_for_stream();
   const float s = *scale;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    float4 a = acc[i];
+  const int rows = *rows_p, lane = threadIdx.x & 31, runs = (d4 + 31) / 32;
+  const int64_t slab = (int64_t)rows * d4, items = (int64_t)rows * runs;
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < items; w += (int64_t)gridDim.x * 8) {
+    const int64_t r = w / runs;
+    const int i = (int)(w - r * runs) * 32 + lane;
+    if (i >= d4) continue;
+    const int64_t at = (int64_t)list[r] * d4 + i;
+    float4 a = acc[r * d4 + i];
+#pragma unroll 4
     for (int k = 1; k < splits; ++k) {
-      const float4 b = acc[k * n4 + i];
+      const float4 b = acc[k * slab + r * d4 + i];
       a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
     if (fp32) {
-      static_cast<float4*>(out)[i] = make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
+      static_cast<float4*>(out)[at] = make_float4(a.x * s, a.y * s, a.z * s, a.w * s);
     } else {
       const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x * s, a.y * s), hi = __floats2bfloat162_rn(a.z * s, a.w * s);
-      static_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      static_cast<uint2*>(out)[at] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
 }
@@ -643,19 +760,22 @@ lpq_status run_pair(CeTile& g, const CeMaps& maps, cudaStream_t s) {
   return cuda_check(launch_dependent(ce_pair_kernel<EPI>, 2 * pairs, kThreads, kSmem, s, maps, g), "cross entropy launch");
 }
 
-// Workspace of the backward pass: scale, dl, partial sums of dh.
+// Workspace of the backward pass: scale and count, list, copied rows of h, dl,
+// partial sums of dh.
 struct BackwardPlan {
   int64_t piece, dl_ld;
   int splits;
   bool direct;  // one piece, one split: dh is stored by its product
-  size_t dl_at, acc_at, bytes;
+  size_t list_at, h_at, dl_at, acc_at, bytes;
   BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked) {
     piece = piece_of(t, v, asked);
     dl_ld = std::min(piece, round_up(v, 8));
     // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
     splits = dh_splits(t, d, std::min(piece, v), 76);
     direct = splits == 1 && piece >= v;
-    dl_at = 256;
+    list_at = 256;
+    h_at = list_at + (size_t)round_up(t * 4, 256);
+    dl_at = h_at + (size_t)round_up(t * d * 2, 256);
     acc_at = dl_at + (size_t)round_up(t * dl_ld * 2, 256);
     bytes = acc_at + (direct ? 0 : (size_t)splits * (size_t)t * (size_t)d * 4);
   }
@@ -691,8 +811,13 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   if (a.t == 0) return cuda_check(cudaMemsetAsync(a.dw, 0, (size_t)a.v * (size_t)a.d * elem, s), "cudaMemsetAsync(dw)");
   const BackwardPlan plan(a.t, a.v, a.d, a.piece);
   float* scale = reinterpret_cast<float*>(a.workspace);
+  int* rows = reinterpret_cast<int*>(a.workspace + 4);
+  int* list = reinterpret_cast<int*>(a.workspace + plan.list_at);
   void* dl = a.workspace + plan.dl_at;
   CeTile base{};
+  base.t = a.t;
+  base.rows = rows;
+  base.list = list;
   base.labels = a.labels;
   base.vocab = a.v;
   base.lse = a.lse;
@@ -700,10 +825,14 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   base.scale = scale;
   base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   base.out_fp32 = a.grads_fp32;
-  lpq_status st = cuda_check(launch_dependent(ce_scale_kernel, 1, 1024, 0, s, a.dloss, a.labels, a.t, a.v, scale),
-                             "cross entropy scale launch");
+  const Operand h{a.h, a.ldh}, copied{a.workspace + plan.h_at, a.d}, l{dl, plan.dl_ld};
+  lpq_status st = cuda_check(
+      launch_dependent(ce_rows_kernel, (unsigned)std::min<int64_t>(cdiv(a.t, 8), (int64_t)device_sms() * 8), 256, 0, s, a.dloss,
+                       a.labels, a.t, a.v, static_cast<const uint4*>(a.h), a.ldh / 8, (int)(a.d / 8),
+                       reinterpret_cast<uint4*>(a.workspace + plan.h_at), static_cast<uint4*>(a.dh),
+                       (int)(a.d * (int64_t)elem / 16), scale, rows, list),
+      "cross entropy rows launch");
   if (st != LPQ_OK) return st;
-  const Operand h{a.h, a.ldh}, l{dl, plan.dl_ld};
   for (int64_t v0 = 0; v0 < a.v; v0 += plan.piece) {
     const int64_t width = std::min(plan.piece, a.v - v0);
     const Operand w{static_cast<const uint8_t*>(a.w) + (size_t)v0 * (size_t)a.ldw * 2, a.ldw};
@@ -712,13 +841,17 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     CeTile g = base;
     g.col0 = v0;
     if ((st = set_product(g, maps, 0, a.t, width, a.d, h, false, w, false, dl, plan.dl_ld, 1)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+    g.prod[0].m_rows = 1;
     if ((st = run_pair<kDlogits>(g, maps, s)) != LPQ_OK) return st;
     // dh (+)= dl w and dw = dl^T h
     g = base;
     g.add = v0 > 0;
     void* dw = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
-    if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, a.grads_fp32 || !plan.direct ? nullptr : a.dh, a.d,
-                          plan.splits)) != LPQ_OK) return st;
+    if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, nullptr, 0, plan.splits)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, 64, kStepK)) != LPQ_OK) return st;
+    g.prod[0].m_rows = 1;
+    g.prod[0].scatter = plan.direct;
     g.prod[0].part = !plan.direct;
     g.prod[0].out = a.dh;
     // in one launch where dh's last round would leave over a tenth of the
@@ -732,14 +865,14 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
       g = base;
     }
     if ((st = set_product(g, maps, at, width, a.d, a.t, l, true, h, true, a.grads_fp32 ? nullptr : dw, a.d, 1)) != LPQ_OK) return st;
+    g.prod[at].k_rows = 1;
     g.prod[at].out = dw;
     if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
   }
   if (plan.direct) return LPQ_OK;
-  const int64_t n4 = a.t * a.d / 4;
-  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(n4, 256), (int64_t)device_sms() * 8);
-  return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc), n4,
-                                     plan.splits, scale, a.dh, a.grads_fp32),
+  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(a.t * cdiv(a.d, 128), 8), (int64_t)device_sms() * 8);
+  return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc),
+                                     (int)(a.d / 4), plan.splits, scale, rows, list, a.dh, a.grads_fp32),
                     "cross entropy finish launch");
 }
 
