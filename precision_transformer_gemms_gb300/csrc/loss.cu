@@ -13,6 +13,14 @@
 // TMEM.  The operand that a product sums along its rows (w in dl w; dl and h
 // in dl^T h) is read as it lies, as an MN-major operand: no transposed copies.
 //
+// The tensor cores bound it: 2 t v d operations forward, 6 t v d backward (the
+// logits again).  Measured: 4096 x 4096 x 19456 forward 343 us and dl 336 us, dh
+// and dw 700 us together, the tensor pipe 89 to 96% active, 1.87 to 1.94
+// PFLOP/s at full clocks (cuBLAS 1.91 burst, 1.71 sustained under the power
+// cap); in a loop, 7936 x 4096 x 32000 forward 1.22 ms (1.70 PFLOP/s) and
+// backward 3.65 ms (1.71).  With d = 1024 a tile's result weighs on the port
+// that feeds it: 1001 x 1024 x 50001 backward 236 us (1.30).
+//
 // The backward pass works on the rows that have a target alone: they are
 // counted and listed on the device, their hidden states copied together where
 // there are others, and the kernels take their sizes from the count.  What the
@@ -856,8 +864,8 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     g.prod[0].out = a.dh;
     // in one launch where dh's last round would leave over a tenth of the
     // pairs' time for it idle, which dw's items then fill (1001 x 1024 x 50001:
-    // 238 -> 233 us in all); else one after the other, each with the L2 to
-    // itself (7936 x 4096 x 32000: 3680 us, 3765 us in one)
+    // dh and dw 139 us one after the other, 125 us in one); else one after the
+    // other, each with the L2 to itself (7936 x 4096 x 32000: 2182 us, in one 2250)
     const int64_t P = std::max(1, device_sms() / 2), n0 = g.prod[0].items, rounds = cdiv(n0, P) * P;
     const int at = 10 * (rounds - n0) > rounds ? 1 : 0;
     if (at == 0) {

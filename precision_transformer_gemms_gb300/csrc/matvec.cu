@@ -13,6 +13,12 @@
 // would need the decoded weights written to shared memory first, for a product
 // whose tensor work is small.
 //
+// Measured, weights and scales against the copy bandwidth of 6787 GB/s, NVFP4 at
+// k = 4096 unless said: 524288 rows 192 us for one token (93%), 214 us for seven
+// (83%); 131073 rows 53 us (83%) and 64 us (70%); 65536 rows 30 us (75%); 12288
+// rows 11.4 us and 4096 rows 7 us, of which about 6 us are launch, the
+// conversion of x and the join of the segments; MXFP4 4096 x 16384 14.4 us.
+//
 // x enters as f16 too: a token's values times a power of two that brings its
 // largest one to [2^14, 2^15).  A bf16 value has 8 significant bits, so this
 // is exact down to 2^-31 of the largest.  Where a nonzero x is smaller than

@@ -6,6 +6,15 @@
 //
 // All sums are FP32; the variance is taken from the centred values (a second
 // pass over the row), so a row's offset does not cancel its digits.
+//
+// HBM bounds both: one read and one write of the rows forward, two reads and one
+// write backward.  Measured against the copy bandwidth of 6787 GB/s, bf16:
+//   forward   15872 x 4096 42.4 us (90%), 65536 x 1024 46.6 us (85%), 8192 x 16384 82.4 us (96%)
+//   backward  15872 x 4096 66.5 us (86%), 63488 x 4096 231 us (99%), 65536 x 1024 70 us (85%),
+//             8192 x 16384 196 us (60%: two passes over the ring, one CTA per SM)
+// What is left at 15872 x 4096 is the start and the end of a 40 us kernel, and
+// backward the join of its 152 parts (5 us).  Unaligned rows go element by
+// element (15872 x 4095 142 us forward, 246 us backward).
 #include <cuda_bf16.h>
 
 #include <algorithm>
