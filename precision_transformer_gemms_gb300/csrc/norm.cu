@@ -14,7 +14,9 @@
 //             8192 x 16384 196 us (60%: two passes over the ring, one CTA per SM)
 // What is left at 15872 x 4096 is the start and the end of a 40 us kernel, and
 // backward the join of its 152 parts (5 us).  Unaligned rows go element by
-// element (15872 x 4095 142 us forward, 246 us backward).
+// element, the next row loaded to registers while this one is worked on: 15872 x 4095
+// bf16 73 us forward (52%), 116 us backward (50%), bound by the count of 2-byte loads;
+// 15872 x 2047 FP32 45 us (84%) and 78 us (74%).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -331,6 +333,26 @@ struct Params {
     }
   }
 };
+// The same for the scalar form, in FP32.
+template <int TPR, int NE, bool HELD>
+struct ScalarParams {
+  float held[HELD ? NE : 1];
+  const void* p;
+  int w_fp32;
+  float none;
+  __device__ __forceinline__ ScalarParams(const void* param, int fp32, int tid, int n, float fill) : p(param), w_fp32(fp32), none(fill) {
+    if constexpr (HELD)
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = i * TPR + tid;
+        held[i] = p && c < n ? load_param(p, w_fp32, c) : none;
+      }
+  }
+  __device__ __forceinline__ float get(int i, int c) const {
+    if constexpr (HELD) return held[i];
+    return p ? load_param(p, w_fp32, c) : none;
+  }
+};
 // 1.0 in every element of a register of T.
 template <typename T>
 constexpr uint32_t ones() { return sizeof(T) == 2 ? 0x3F803F80u : 0x3F800000u; }
@@ -352,26 +374,35 @@ __device__ __forceinline__ float absmax_value(uint32_t top) {
   if constexpr (sizeof(T) == 2) return fmaxf(bf16_lo(top), bf16_hi(top)); else return __uint_as_float(top);
 }
 
-// The elements of one row tensor of a thread as pairs, from its ring slot or
-// from memory; 0 past the row's end.
-template <typename T, bool VEC, int TPR, int NE>
-__device__ __forceinline__ void take_row(const uint4* slot, int stride, const T* row, int tid, int n, float2 (&f)[NE / 2]) {
-  if constexpr (VEC) {
-    constexpr int V = 16 / (int)sizeof(T);
+// The elements of one row tensor of a thread as pairs, from its ring slot; 0
+// past the row's end.
+template <typename T, int TPR, int NE>
+__device__ __forceinline__ void take_row(const uint4* slot, int stride, int tid, int n, float2 (&f)[NE / 2]) {
+  constexpr int V = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int v = 0; v < NE / V; ++v) {
-      uint4 q = make_uint4(0, 0, 0, 0);
-      if (column_of<T, true, TPR>(tid, v * V) < n) q = slot[v * stride];
-      unpack_vector<T>(q, f + v * V / 2);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NE; i += 2) {
-      const int c = column_of<T, false, TPR>(tid, i), d = column_of<T, false, TPR>(tid, i + 1);
-      f[i / 2] = make_float2(c < n ? to_f32(row[c]) : 0.f, d < n ? to_f32(row[d]) : 0.f);
-    }
+  for (int v = 0; v < NE / V; ++v) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (column_of<T, true, TPR>(tid, v * V) < n) q = slot[v * stride];
+    unpack_vector<T>(q, f + v * V / 2);
   }
 }
+// Scalar form: the next row's elements, loaded while the row before is worked on.
+template <typename T, bool VEC, int TPR, int NE>
+struct NextRow {
+  T raw[VEC ? 1 : NE];
+  __device__ __forceinline__ void load(const T* row, bool there, int tid, int n) {
+    if constexpr (!VEC)
+#pragma unroll
+      for (int i = 0; i < NE; ++i) {
+        const int c = i * TPR + tid;
+        raw[i] = there && c < n ? row[c] : from_f32<T>(0.f);
+      }
+  }
+  __device__ __forceinline__ void take(float2 (&f)[NE / 2]) const {
+#pragma unroll
+    for (int i = 0; i < NE; i += 2) f[i / 2] = make_float2(to_f32(raw[i]), to_f32(raw[i + 1]));
+  }
+};
 
 // f(i, in): for the pairs of a thread, whether their elements lie in the row
 // (a vector's all do or none; a scalar form's pair may be cut).
@@ -424,15 +455,24 @@ __global__ void __launch_bounds__(RowGroup<TPR, false>::kBlock) norm_kernel(cons
   for (int s = 0; s < kAhead; ++s) copy(s);
   constexpr bool kHeld = VEC && HELD;
   const Params<T, TPR, VEC ? NE : V, kHeld> weight(a.weight, w_fp32, tid, n, ones<T>()), bias(a.bias, w_fp32, tid, n, 0u);
+  using Scalars = ScalarParams<TPR, VEC ? 1 : NE, (NE <= 16)>;
+  const Scalars weight1(a.weight, w_fp32, tid, n, 1.0f), bias1(a.bias, w_fp32, tid, n, 0.0f);
   uint32_t top = 0;
   float top_scalar = 0.f;
   int slot = 0;
+  NextRow<T, VEC, TPR, NE> next_x;
+  next_x.load(static_cast<const T*>(a.x) + first * a.ldx, first < a.rows, tid, n);
   T* y = static_cast<T*>(a.out) + first * a.ldo;
   const int64_t y_step = step * a.ldo;
   for (int64_t r = first; r < a.rows; r += step, y += y_step) {
     float2 x[NE / 2];
     if constexpr (VEC) cp_async_wait<kAhead - 1>();
-    take_row<T, VEC, TPR, NE>(&ring[slot * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.x) + r * a.ldx, tid, n, x);
+    if constexpr (VEC) {
+      take_row<T, TPR, NE>(&ring[slot * NV * kBlock + threadIdx.x], kBlock, tid, n, x);
+    } else {
+      next_x.take(x);
+      next_x.load(static_cast<const T*>(a.x) + (r + step) * a.ldx, r + step < a.rows, tid, n);
+    }
     float2 s2 = pair_of(0.f);
 #pragma unroll
     for (int i = 0; i < NE / 2; ++i) s2 = __fadd2_rn(s2, x[i]);
@@ -470,10 +510,7 @@ __global__ void __launch_bounds__(RowGroup<TPR, false>::kBlock) norm_kernel(cons
       for (int i = 0; i < NE; ++i) {
         const int c = column_of<T, false, TPR>(tid, i);
         if (c < n) {
-          float o = (i & 1 ? x[i / 2].y : x[i / 2].x) * rstd;
-          if (a.weight) o *= load_param(a.weight, w_fp32, c);
-          if (a.bias) o += load_param(a.bias, w_fp32, c);
-          const T q = from_f32<T>(o);
+          const T q = from_f32<T>(__fmaf_rn((i & 1 ? x[i / 2].y : x[i / 2].x) * rstd, weight1.get(i, c), bias1.get(i, c)));
           y[c] = q;
           top_scalar = absmax_acc(top_scalar, to_f32(q));
         }
@@ -533,6 +570,11 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
   const Params<T, TPR, VEC ? NE : V, kHeld> weight(a.weight, w_fp32, tid, n, ones<T>());
   int slot = 0, turn = 0;
   float mean = first < a.rows ? a.mean_in[first] : 0.f, rstd = first < a.rows ? a.rstd_in[first] : 0.f;
+  const ScalarParams<TPR, VEC ? 1 : NE, (NE <= 8)> weight1(a.weight, w_fp32, tid, n, 1.0f);
+  constexpr bool kNext = !VEC && NE <= 8;  // (wider threads have no registers for the next row)
+  NextRow<T, !kNext, TPR, NE> next_x, next_dy;
+  next_x.load(static_cast<const T*>(a.x) + first * a.ldx, first < a.rows, tid, n);
+  next_dy.load(static_cast<const T*>(a.dy) + first * a.lddy, first < a.rows, tid, n);
   T* dx = static_cast<T*>(a.out) + first * a.ldo;
   const int64_t dx_step = step * a.ldo;
   for (int64_t r = first; r < a.rows; r += step, dx += dx_step) {
@@ -590,8 +632,21 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
       rstd = next_rstd;
       continue;
     }
-    take_row<T, VEC, TPR, NE>(&ring[slot * 2 * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.x) + r * a.ldx, tid, n, x);
-    take_row<T, VEC, TPR, NE>(&ring[(slot * 2 + 1) * NV * kBlock + threadIdx.x], kBlock, static_cast<const T*>(a.dy) + r * a.lddy, tid, n, g);
+    if constexpr (VEC) {
+      take_row<T, TPR, NE>(&ring[slot * 2 * NV * kBlock + threadIdx.x], kBlock, tid, n, x);
+      take_row<T, TPR, NE>(&ring[(slot * 2 + 1) * NV * kBlock + threadIdx.x], kBlock, tid, n, g);
+    } else if constexpr (kNext) {
+      next_x.take(x);
+      next_dy.take(g);
+      next_x.load(static_cast<const T*>(a.x) + rn * a.ldx, rn > r, tid, n);
+      next_dy.load(static_cast<const T*>(a.dy) + rn * a.lddy, rn > r, tid, n);
+    } else {
+      NextRow<T, false, TPR, NE> row;
+      row.load(static_cast<const T*>(a.x) + r * a.ldx, true, tid, n);
+      row.take(x);
+      row.load(static_cast<const T*>(a.dy) + r * a.lddy, true, tid, n);
+      row.take(g);
+    }
     // (past the row's end g is 0, and with it everything that x enters)
 #pragma unroll
     for (int i = 0; i < NE / 2; ++i) {
@@ -622,11 +677,9 @@ __global__ void __launch_bounds__(RowGroup<TPR, true>::kBlock, 1) norm_backward_
     } else {
 #pragma unroll
       for (int i = 0; i < NE / 2; ++i) {
-        if (a.weight) {
-          const int c = column_of<T, false, TPR>(tid, 2 * i), d = column_of<T, false, TPR>(tid, 2 * i + 1);
-          if (c < n) g[i].x *= load_param(a.weight, w_fp32, c);
-          if (d < n) g[i].y *= load_param(a.weight, w_fp32, d);
-        }
+        const int c = column_of<T, false, TPR>(tid, 2 * i), d = column_of<T, false, TPR>(tid, 2 * i + 1);
+        if (c < n) g[i].x *= weight1.get(2 * i, c);
+        if (d < n) g[i].y *= weight1.get(2 * i + 1, d);
         s0 = __fadd2_rn(s0, g[i]);
         s1 = __ffma2_rn(g[i], x[i], s1);
       }
@@ -731,17 +784,21 @@ lpq_status run_backward(const NormArgs& a, int w_fp32, int& parts, cudaStream_t 
 
 // Threads per row and elements per thread by width; beyond 16384 columns the
 // rows are read from memory again.
-// FEWER: half the threads, with 32 elements each, for 4097 to 8192 columns (bf16
-// forward, where two CTAs then fit an SM: 15872 x 8192 104 -> 86 us).
-template <bool FEWER, typename F>
+// kFewer: half the threads, with 32 elements each, for 4097 to 8192 columns (bf16
+// forward, where two CTAs then fit an SM: 15872 x 8192 104 -> 86 us).  kNarrow:
+// 8 elements a thread up to 4096 columns (scalar backward, which then has
+// registers for the next row: 15872 x 4095 248 -> 116 us).
+enum { kUsual, kFewer, kNarrow };
+template <int HOW, typename F>
 lpq_status by_width(int64_t cols, F f) {
   using std::integral_constant;
+  constexpr int K = HOW == kNarrow ? 2 : 1;
   if (cols <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
   if (cols <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-  if (cols <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
-  if (cols <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 16>{});
-  if (cols <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 16>{});
-  if (cols <= 8192) return f(integral_constant<int, FEWER ? 256 : 512>{}, integral_constant<int, FEWER ? 32 : 16>{});
+  if (cols <= 1024) return f(integral_constant<int, 64 * K>{}, integral_constant<int, 16 / K>{});
+  if (cols <= 2048) return f(integral_constant<int, 128 * K>{}, integral_constant<int, 16 / K>{});
+  if (cols <= 4096) return f(integral_constant<int, 256 * K>{}, integral_constant<int, 16 / K>{});
+  if (cols <= 8192) return f(integral_constant<int, HOW == kFewer ? 256 : 512>{}, integral_constant<int, HOW == kFewer ? 32 : 16>{});
   return f(integral_constant<int, 512>{}, integral_constant<int, 32>{});
 }
 
@@ -749,7 +806,7 @@ template <typename T>
 lpq_status forward_t(const NormArgs& a, int w_fp32, cudaStream_t s) {
   if (a.cols <= 16384) {
     const bool vec = vector_rows(a, sizeof(T), false), held = (sizeof(T) == 4) == (w_fp32 != 0);
-    return by_width<sizeof(T) == 2>(a.cols, [&](auto tpr, auto ne) {
+    return by_width<sizeof(T) == 2 ? kFewer : kUsual>(a.cols, [&](auto tpr, auto ne) {
       return !vec ? run_forward<T, false, false, tpr, ne>(a, w_fp32, s)
              : held ? run_forward<T, true, true, tpr, ne>(a, w_fp32, s) : run_forward<T, true, false, tpr, ne>(a, w_fp32, s);
     });
@@ -768,11 +825,13 @@ lpq_status backward_t(NormArgs a, int w_fp32, cudaStream_t s) {
   if (!a.dweight && !a.dbias) a.parts = nullptr;
   if (a.cols <= 16384) {
     const bool vec = vector_rows(a, sizeof(T), true), held = (sizeof(T) == 4) == (w_fp32 != 0);
-    st = by_width<false>(a.cols, [&](auto tpr, auto ne) {
-      return !vec ? run_backward<T, false, false, tpr, ne>(a, w_fp32, parts, s)
-             : held ? run_backward<T, true, true, tpr, ne>(a, w_fp32, parts, s)
+    if (vec)
+      st = by_width<kUsual>(a.cols, [&](auto tpr, auto ne) {
+        return held ? run_backward<T, true, true, tpr, ne>(a, w_fp32, parts, s)
                     : run_backward<T, true, false, tpr, ne>(a, w_fp32, parts, s);
-    });
+      });
+    else
+      st = by_width<kNarrow>(a.cols, [&](auto tpr, auto ne) { return run_backward<T, false, false, tpr, ne>(a, w_fp32, parts, s); });
     if (st != LPQ_OK || !a.parts) return st;
   } else {
     const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
