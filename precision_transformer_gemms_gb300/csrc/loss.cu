@@ -29,11 +29,14 @@
 // dl is divided by s = max |dloss| before its rounding to bf16 (what the
 // tensor cores read) and s multiplies the FP32 sums: with equal dloss, the
 // mean over the tokens say, the entry p - 1 of a label is then rounded as it
-// is instead of after a product with 1 / t.
+// is instead of after a product with 1 / t.  Over many tokens the roundings
+// average out below those of bf16 gradients; a few tokens' would show, so up to
+// 128 rows dl is held as the sum of two bf16 terms (16 bits).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "lpq_device.cuh"
@@ -66,6 +69,16 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // the gradients' sums carry dl's bf16 rounding, far above that drift.
 constexpr int kChunk = 16;
 
+// Up to kFew rows dl is stored as two terms, the value in bf16 and in bf16 what
+// that leaves out, t rows each.  In dh = dl w they are the rows of the two CTAs
+// (one of which had none), whose sums are added in the end; in dw = dl^T h they
+// follow one another along K, against the same h.  Reading w and storing dw
+// bound the pass up to there, so the terms cost little: 32000 x 4096, 33 or 128
+// rows, 198 and 192 us either way; at worst (one row) 209 -> 219 us.  Error of
+// bf16 gradients of up to 128 rows against 64 bits: 0.0020 to 0.0025 with one
+// term, 0.0017 with two, which is their own rounding.
+constexpr int kFew = kHalf;
+
 // What a kernel's epilogue makes of a tile.
 //   kStats    row maxima and sums of exponentials of the logits
 //   kDlogits  dl in bf16
@@ -85,10 +98,12 @@ struct Product {
   int scatter;         // rows of the result go to the places of their list
   int part;            // partial sums into acc instead of out
   void* out;
+  int64_t ld;          // of the second terms of dl
 };
 
 struct alignas(64) CeMaps {
   CUtensorMap a[2], b[2], c[2];
+  CUtensorMap a2[2];  // of the second terms of dl
   CUtensorMap alt;  // of the copied rows of h: A of kDlogits, B of dw
 };
 
@@ -110,6 +125,7 @@ struct CeTile {
   const float* scale;
   float* acc;  // [splits][M][N]
   int add;     // 1: add to acc
+  int two;     // dl in two terms
   int out_fp32;
 };
 
@@ -244,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         p.tiles_m = (rows + kTile - 1) / kTile;
         p.items = p.tiles_m * p.tiles_n * p.splits;
       }
-      if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK;
+      if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK * (g.two ? 2 : 1);
       prod[i] = p;
     }
     const int left_over = prod[0].items % npairs;
@@ -263,11 +279,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       for (int i = 0; ok && item_at(i, pair, npairs, prod, extra, which, w); ++i) {
         const Product& p = prod[which];
         const CUtensorMap* tmA = EPI == kDlogits && some_rows ? &maps.alt : &maps.a[which];
+        const CUtensorMap* tmA2 = EPI == kGrads && g.two ? &maps.a2[which] : tmA;
         const CUtensorMap* tmB = EPI == kGrads && p.k_rows && some_rows ? &maps.alt : &maps.b[which];
         int mt, nt, split, k0, k1;
         item_coords(w, p, mt, nt, split);
         split_range(split, p, k0, k1);
-        const int32_t arow = mt * kTile + (int32_t)rank * kHalf, brow = nt * kTile + (int32_t)rank * kHalf;
+        const bool terms = EPI == kGrads && g.two && p.m_rows;  // the CTAs take a term each
+        const int32_t arow = mt * kTile + (terms ? 0 : (int32_t)rank * kHalf), brow = nt * kTile + (int32_t)rank * kHalf;
+        // the first step with the second terms
+        const int second = terms ? (rank ? 0 : INT_MAX) : EPI == kGrads && g.two ? p.num_k / 2 : INT_MAX;
         auto loads = [&](auto a_is_mn) {
           constexpr bool A_MN = decltype(a_is_mn)::value;
           for (int kt = k0; kt < k1; ++kt) {
@@ -276,17 +296,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             const uint32_t fb = full_leader + 8 * s;
             uint8_t* da = sA + s * kOperand;
             uint8_t* db = sB + s * kOperand;
+            const CUtensorMap* ta = kt < second ? tmA : tmA2;
+            const int32_t k = (kt < second ? kt : kt - second) * kStepK;
             if constexpr (A_MN) {
-              tma_load_2d_pair(da, tmA, arow, kt * kStepK, fb);
-              tma_load_2d_pair(da + kOperand / 2, tmA, arow + 64, kt * kStepK, fb);
+              tma_load_2d_pair(da, ta, arow, k, fb);
+              tma_load_2d_pair(da + kOperand / 2, ta, arow + 64, k, fb);
             } else {
-              tma_load_2d_pair(da, tmA, kt * kStepK, arow, fb);
+              tma_load_2d_pair(da, ta, k, arow, fb);
             }
             if constexpr (B_MN) {
-              tma_load_2d_pair(db, tmB, brow, kt * kStepK, fb);
-              tma_load_2d_pair(db + kOperand / 2, tmB, brow + 64, kt * kStepK, fb);
+              tma_load_2d_pair(db, tmB, brow, k, fb);
+              tma_load_2d_pair(db + kOperand / 2, tmB, brow + 64, k, fb);
             } else {
-              tma_load_2d_pair(db, tmB, kt * kStepK, brow, fb);
+              tma_load_2d_pair(db, tmB, k, brow, fb);
             }
             ++it;
             if (++s == (uint32_t)kStages) { s = 0; ph ^= 1u; }
@@ -353,7 +375,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       const Product& p = prod[which];
       int mt, nt, split;
       item_coords(w, p, mt, nt, split);
-      const int64_t row = (int64_t)mt * kTile + rank * kHalf + q * 32 + lane;
+      const bool terms = EPI != kStats && g.two && p.m_rows;  // (dl or dh: one tile down)
+      const int64_t row = (int64_t)mt * kTile + (EPI == kGrads && terms ? 0 : rank * kHalf) + q * 32 + lane;
       const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
       const bool live = row < p.M;
       const int ncols = (int)max((int64_t)0, min((int64_t)kHalf, p.N - c0));  // columns of this warp inside the matrix
@@ -448,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         if (cc == kHalf / 32 - 1) give();
         if (part) {
           if (live && some && cc * 32 < ncols) {
-            float* to = g.acc + ((int64_t)split * p.M + row) * p.N + c0 + cc * 32;
+            float* to = g.acc + ((terms ? split * 2 + (int)rank : split) * p.M + row) * p.N + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (cc * 32 + 4 * i >= ncols) break;
@@ -508,6 +531,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
                 if (cc * 32 + 8 * i < ncols) to[i] = pk[i];
             }
             continue;
+          }
+          if (EPI == kDlogits && terms) {
+            if (rank) continue;  // (rows of this CTA: none)
+            uint16_t* to = static_cast<uint16_t*>(p.out) + row * p.ld + c0 + cc * 32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t u[4];
+              const uint32_t top[4] = {pk[i].x, pk[i].y, pk[i].z, pk[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float a0 = __uint_as_float(top[j] << 16), a1 = __uint_as_float(top[j] & 0xFFFF0000u);
+                // (nothing is left out of an infinity)
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(
+                    fabsf(a0) < -kNegInf ? __uint_as_float(v[8 * i + 2 * j]) - a0 : 0.f,
+                    fabsf(a1) < -kNegInf ? __uint_as_float(v[8 * i + 2 * j + 1]) - a1 : 0.f);
+                u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              if (row < g.t && cc * 32 + 8 * i < ncols) reinterpret_cast<uint4*>(to)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
           }
           if ((cc & 1) == 0) {
             if (lane == 0) bulk_wait_group_read0();  // the previous store has read the buffer
@@ -708,7 +750,8 @@ int extra_items(int64_t n0, double c0, int64_t n1, double c1, int pairs) {
 int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
   const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK);
   const int64_t n1 = cdiv(width, kTile) * cdiv(d, kTile);
-  const double c1 = (double)cdiv(t, kStepK) + kItemStart;
+  const int terms = t <= kFew ? 2 : 1;
+  const double c1 = (double)(terms * cdiv(t, kStepK)) + kItemStart;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 64 && s <= steps; ++s) {
@@ -717,7 +760,7 @@ int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
     const int64_t fewer = pairs - n0 % pairs, extra = extra_items(n0, c0, n1, c1, pairs);
     const double shared = (double)cdiv(n1 - extra * fewer, pairs) * c1;
     const double longest = std::max((double)cdiv(n0, pairs) * c0, (double)(n0 / pairs) * c0 + (double)extra * c1) + shared;
-    const double us = longest * 0.33 + (s > 1 ? (double)s * (double)t * (double)d * 8.0 / 6.5e6 : 0.0);
+    const double us = longest * 0.33 + (s > 1 ? (double)(s * terms) * (double)t * (double)d * 8.0 / 6.5e6 : 0.0);
     if (s == 1 || us < least) {
       least = us;
       best = s;
@@ -773,6 +816,7 @@ lpq_status run_pair(CeTile& g, const CeMaps& maps, cudaStream_t s) {
 struct BackwardPlan {
   int64_t piece, dl_ld;
   int splits;
+  bool two;     // dl in two terms
   bool direct;  // one piece, one split: dh is stored by its product
   size_t list_at, h_at, dl_at, acc_at, bytes;
   BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked) {
@@ -780,12 +824,13 @@ struct BackwardPlan {
     dl_ld = std::min(piece, round_up(v, 8));
     // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
     splits = dh_splits(t, d, std::min(piece, v), 76);
-    direct = splits == 1 && piece >= v;
+    two = t <= kFew;
+    direct = splits == 1 && piece >= v && !two;
     list_at = 256;
     h_at = list_at + (size_t)round_up(t * 4, 256);
     dl_at = h_at + (size_t)round_up(t * d * 2, 256);
-    acc_at = dl_at + (size_t)round_up(t * dl_ld * 2, 256);
-    bytes = acc_at + (direct ? 0 : (size_t)splits * (size_t)t * (size_t)d * 4);
+    acc_at = dl_at + (size_t)round_up((two ? 2 * t : t) * dl_ld * 2, 256);
+    bytes = acc_at + (direct ? 0 : (size_t)(two ? 2 * splits : splits) * (size_t)t * (size_t)d * 4);
   }
 };
 
@@ -833,6 +878,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   base.scale = scale;
   base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   base.out_fp32 = a.grads_fp32;
+  base.two = plan.two;
   const Operand h{a.h, a.ldh}, copied{a.workspace + plan.h_at, a.d}, l{dl, plan.dl_ld};
   lpq_status st = cuda_check(
       launch_dependent(ce_rows_kernel, (unsigned)std::min<int64_t>(cdiv(a.t, 8), (int64_t)device_sms() * 8), 256, 0, s, a.dloss,
@@ -851,12 +897,16 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     if ((st = set_product(g, maps, 0, a.t, width, a.d, h, false, w, false, dl, plan.dl_ld, 1)) != LPQ_OK) return st;
     if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
+    const Operand l2{static_cast<uint8_t*>(dl) + (plan.two ? (size_t)a.t * (size_t)plan.dl_ld * 2 : 0), plan.dl_ld};
+    g.prod[0].out = const_cast<void*>(l2.p);
+    g.prod[0].ld = plan.dl_ld;
     if ((st = run_pair<kDlogits>(g, maps, s)) != LPQ_OK) return st;
     // dh (+)= dl w and dw = dl^T h
     g = base;
     g.add = v0 > 0;
     void* dw = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
     if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, nullptr, 0, plan.splits)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.a2[0], l2.p, true, width, a.t, l2.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
     if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, 64, kStepK)) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
     g.prod[0].scatter = plan.direct;
@@ -873,6 +923,8 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
       g = base;
     }
     if ((st = set_product(g, maps, at, width, a.d, a.t, l, true, h, true, a.grads_fp32 ? nullptr : dw, a.d, 1)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.a2[at], l2.p, true, width, a.t, l2.ld * 2, 64, kStepK)) != LPQ_OK) return st;
+    if (plan.two) g.prod[at].num_k *= 2;
     g.prod[at].k_rows = 1;
     g.prod[at].out = dw;
     if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
@@ -880,7 +932,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   if (plan.direct) return LPQ_OK;
   const unsigned grid = (unsigned)std::min<int64_t>(cdiv(a.t * cdiv(a.d, 128), 8), (int64_t)device_sms() * 8);
   return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc),
-                                     (int)(a.d / 4), plan.splits, scale, rows, list, a.dh, a.grads_fp32),
+                                     (int)(a.d / 4), plan.two ? 2 * plan.splits : plan.splits, scale, rows, list, a.dh, a.grads_fp32),
                     "cross entropy finish launch");
 }
 
