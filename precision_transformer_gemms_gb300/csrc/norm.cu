@@ -16,7 +16,9 @@
 // backward the join of its 152 parts (5 us).  Unaligned rows go element by
 // element, the next row loaded to registers while this one is worked on: 15872 x 4095
 // bf16 73 us forward (52%), 116 us backward (50%), bound by the count of 2-byte loads;
-// 15872 x 2047 FP32 45 us (84%) and 78 us (74%).
+// 15872 x 2047 FP32 45 us (84%) and 78 us (74%).  Rows beyond 16384 columns are
+// read again from the L2: 4096 x 32768 125 us forward (63%), 273 us backward (43%:
+// the parameter gradients are a launch of their own).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -61,7 +63,7 @@ __device__ __forceinline__ void store_amax(float* amax, float top) {
   }
 }
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
 
 // Sum over the CTA, the same value in every thread.
 __device__ __forceinline__ float block_sum(float v, float* sh) {
@@ -74,82 +76,6 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
 #pragma unroll
   for (int i = 0; i < kRowThreads / 32; ++i) s += sh[i];
   return s;
-}
-
-// ------------------------------------------------------------------ rows beyond 16384 columns
-// One CTA per row, element by element: any size, stride and alignment.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a, int w_fp32) {
-  __shared__ float sh[kRowThreads / 32];
-  const int n = (int)a.cols;
-  float top = 0.f;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    T* y = static_cast<T*>(a.out) + r * a.ldo;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) s += to_f32(x[i]);
-    const float mean = block_sum(s, sh) / (float)n;
-    s = 0.f;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float c = to_f32(x[i]) - mean;
-      s += c * c;
-    }
-    const float rstd = 1.0f / sqrtf(block_sum(s, sh) / (float)n + a.eps);
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float c = (to_f32(x[i]) - mean) * rstd;
-      const T o = from_f32<T>(c * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f) + (a.bias ? load_param(a.bias, w_fp32, i) : 0.0f));
-      y[i] = o;
-      top = absmax_acc(top, to_f32(o));
-    }
-    if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
-    }
-  }
-  if (a.amax) store_amax(a.amax, top);
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) norm_dx_row_kernel(const NormArgs a, int w_fp32) {
-  __shared__ float sh[kRowThreads / 32];
-  const int n = (int)a.cols;
-  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
-    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
-    T* dx = static_cast<T*>(a.out) + r * a.ldo;
-    const float mean = a.mean_in[r], rstd = a.rstd_in[r];
-    float s1 = 0.f, s2 = 0.f;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float g = to_f32(dy[i]) * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f);
-      s1 += g;
-      s2 += g * ((to_f32(x[i]) - mean) * rstd);
-    }
-    const float m1 = block_sum(s1, sh) / (float)n;
-    const float m2 = block_sum(s2, sh) / (float)n;
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      const float g = to_f32(dy[i]) * (a.weight ? load_param(a.weight, w_fp32, i) : 1.0f);
-      const float xh = (to_f32(x[i]) - mean) * rstd;
-      dx[i] = from_f32<T>(rstd * (g - m1 - xh * m2));
-    }
-  }
-}
-
-// Part p of the parameter gradients: the rows p, p + parts, ...; one thread per column.
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) norm_parts_kernel(const NormArgs a, int parts) {
-  const int64_t c = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  if (c >= a.cols) return;
-  for (int p = blockIdx.y; p < parts; p += gridDim.y) {
-    float dw = 0.f, db = 0.f;
-    for (int64_t r = p; r < a.rows; r += parts) {
-      const float dy = to_f32(static_cast<const T*>(a.dy)[r * a.lddy + c]);
-      const float xh = (to_f32(static_cast<const T*>(a.x)[r * a.ldx + c]) - a.mean_in[r]) * a.rstd_in[r];
-      dw += dy * xh;
-      db += dy;
-    }
-    a.parts[(int64_t)p * 2 * a.cols + c] = dw;
-    a.parts[((int64_t)p * 2 + 1) * a.cols + c] = db;
-  }
 }
 
 // Joins the parts: 32 columns per CTA, its 16 warps each summing every 16th
@@ -301,6 +227,167 @@ __device__ __forceinline__ void load_params(const void* p, int w_fp32, int c, fl
     f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
     f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
   }
+}
+
+// ------------------------------------------------------------------ rows beyond 16384 columns
+// One CTA per row, in passes over it: the first from memory, the others mostly
+// from the L2 (two CTAs an SM: 304 rows).  VEC: 16 bytes at a time.
+template <typename T, bool VEC>
+struct RowSpan {
+  static constexpr int V = VEC ? 16 / (int)sizeof(T) : 1, NP = VEC ? V / 2 : 1;  // elements, pairs (scalar: y = 0)
+  static __device__ __forceinline__ void load(const T* p, int c, float2 (&f)[NP]) {
+    if constexpr (VEC) unpack_vector<T>(*reinterpret_cast<const uint4*>(p + c), f);
+    else f[0] = make_float2(to_f32(p[c]), 0.f);
+  }
+  static __device__ __forceinline__ void param(const void* p, int w_fp32, int c, float2 (&f)[NP], float none) {
+    if (!p) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) f[j] = pair_of(none);
+    } else if constexpr (VEC) {
+      load_params<NP>(p, w_fp32, c, f);
+    } else {
+      f[0] = make_float2(load_param(p, w_fp32, c), 0.f);
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int c, const float2 (&f)[NP]) {
+    if constexpr (VEC) *reinterpret_cast<uint4*>(p + c) = pack_vector<T>(f);
+    else p[c] = from_f32<T>(f[0].x);
+  }
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) norm_row_kernel(const NormArgs a, int w_fp32) {
+  using R = RowSpan<T, VEC>;
+  __shared__ float sh[kRowThreads / 32];
+  const int n = (int)a.cols;
+  float top = 0.f;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    T* y = static_cast<T*>(a.out) + r * a.ldo;
+    float s = 0.f;
+#pragma unroll 4
+    for (int c = threadIdx.x * R::V; c < n; c += kRowThreads * R::V) {
+      float2 f[R::NP];
+      R::load(x, c, f);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) s += f[j].x + f[j].y;
+    }
+    const float mean = block_sum(s, sh) / (float)n;
+    s = 0.f;
+#pragma unroll 4
+    for (int c = threadIdx.x * R::V; c < n; c += kRowThreads * R::V) {
+      float2 f[R::NP];
+      R::load(x, c, f);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) {
+        const float dx = f[j].x - mean, dy = VEC ? f[j].y - mean : 0.f;
+        s += dx * dx + dy * dy;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(s, sh) / (float)n + a.eps);
+#pragma unroll 2
+    for (int c = threadIdx.x * R::V; c < n; c += kRowThreads * R::V) {
+      float2 f[R::NP], w[R::NP], b[R::NP];
+      R::load(x, c, f);
+      R::param(a.weight, w_fp32, c, w, 1.0f);
+      R::param(a.bias, w_fp32, c, b, 0.0f);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) {
+        f[j] = make_float2((f[j].x - mean) * rstd * w[j].x + b[j].x, VEC ? (f[j].y - mean) * rstd * w[j].y + b[j].y : 0.f);
+        top = absmax_acc(absmax_acc(top, to_f32(from_f32<T>(f[j].x))), to_f32(from_f32<T>(f[j].y)));
+      }
+      R::store(y, c, f);
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+  if (a.amax) store_amax(a.amax, top);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kRowThreads) norm_dx_row_kernel(const NormArgs a, int w_fp32) {
+  using R = RowSpan<T, VEC>;
+  __shared__ float sh[kRowThreads / 32];
+  const int n = (int)a.cols;
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + r * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + r * a.lddy;
+    T* dx = static_cast<T*>(a.out) + r * a.ldo;
+    const float mean = a.mean_in[r], rstd = a.rstd_in[r];
+    float s1 = 0.f, s2 = 0.f;
+    // xhat and g = dy w
+    auto take = [&](int c, float2 (&xh)[R::NP], float2 (&g)[R::NP]) {
+      float2 w[R::NP];
+      R::load(x, c, xh);
+      R::load(dy, c, g);
+      R::param(a.weight, w_fp32, c, w, 1.0f);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) {
+        xh[j] = make_float2((xh[j].x - mean) * rstd, VEC ? (xh[j].y - mean) * rstd : 0.f);
+        g[j] = make_float2(g[j].x * w[j].x, VEC ? g[j].y * w[j].y : 0.f);
+      }
+    };
+#pragma unroll 2
+    for (int c = threadIdx.x * R::V; c < n; c += kRowThreads * R::V) {
+      float2 xh[R::NP], g[R::NP];
+      take(c, xh, g);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) {
+        s1 += g[j].x + g[j].y;
+        s2 += g[j].x * xh[j].x + g[j].y * xh[j].y;
+      }
+    }
+    const float m1 = block_sum(s1, sh) / (float)n;
+    const float m2 = block_sum(s2, sh) / (float)n;
+#pragma unroll 2
+    for (int c = threadIdx.x * R::V; c < n; c += kRowThreads * R::V) {
+      float2 xh[R::NP], g[R::NP];
+      take(c, xh, g);
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j)
+        g[j] = make_float2(rstd * (g[j].x - m1 - xh[j].x * m2), rstd * (g[j].y - m1 - xh[j].y * m2));
+      R::store(dx, c, g);
+    }
+  }
+}
+
+// Part p of the parameter gradients: the rows p, p + parts, ...; a thread per
+// column or 16 bytes of columns.
+constexpr int kPartThreads = 128;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kPartThreads) norm_parts_kernel(const NormArgs a, int parts) {
+  using R = RowSpan<T, VEC>;
+  const int64_t c = ((int64_t)blockIdx.x * kPartThreads + threadIdx.x) * R::V;
+  if (c >= a.cols) return;
+  const int p = blockIdx.y;
+  float2 dw[R::NP] = {}, db[R::NP] = {};
+#pragma unroll 4
+  for (int64_t r = p; r < a.rows; r += parts) {
+    float2 x[R::NP], dy[R::NP];
+    R::load(static_cast<const T*>(a.x) + r * a.ldx, (int)c, x);
+    R::load(static_cast<const T*>(a.dy) + r * a.lddy, (int)c, dy);
+    const float mean = a.mean_in[r], rstd = a.rstd_in[r];
+#pragma unroll
+    for (int j = 0; j < R::NP; ++j) {
+      dw[j].x += dy[j].x * ((x[j].x - mean) * rstd);
+      dw[j].y += dy[j].y * ((x[j].y - mean) * rstd);
+      db[j].x += dy[j].x;
+      db[j].y += dy[j].y;
+    }
+  }
+  float* to = a.parts + (int64_t)p * 2 * a.cols + c;
+  auto put = [&](float* q, const float2 (&f)[R::NP]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < R::NP; ++j) *reinterpret_cast<float2*>(q + 2 * j) = f[j];
+    } else {
+      q[0] = f[0].x;
+    }
+  };
+  put(to, dw);
+  put(to + a.cols, db);
 }
 
 // The parameters of a thread's vectors.  HELD (parameters of the rows' own
@@ -811,10 +898,10 @@ lpq_status forward_t(const NormArgs& a, int w_fp32, cudaStream_t s) {
              : held ? run_forward<T, true, true, tpr, ne>(a, w_fp32, s) : run_forward<T, true, false, tpr, ne>(a, w_fp32, s);
     });
   }
-  const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
+  const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 2);
   lpq_status st = clear_amax(a, grid, s);
   if (st != LPQ_OK) return st;
-  norm_row_kernel<T><<<grid, kRowThreads, 0, s>>>(a, w_fp32);
+  (vector_rows(a, sizeof(T), false) ? norm_row_kernel<T, true> : norm_row_kernel<T, false>)<<<grid, kRowThreads, 0, s>>>(a, w_fp32);
   return cuda_check(cudaGetLastError(), "layer norm launch");
 }
 
@@ -834,12 +921,15 @@ lpq_status backward_t(NormArgs a, int w_fp32, cudaStream_t s) {
       st = by_width<kNarrow>(a.cols, [&](auto tpr, auto ne) { return run_backward<T, false, false, tpr, ne>(a, w_fp32, parts, s); });
     if (st != LPQ_OK || !a.parts) return st;
   } else {
-    const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 8);
-    norm_dx_row_kernel<T><<<grid, kRowThreads, 0, s>>>(a, w_fp32);
+    const bool vec = vector_rows(a, sizeof(T), true);
+    const int grid = (int)std::min<int64_t>(a.rows, (int64_t)device_sms() * 2);
+    (vec ? norm_dx_row_kernel<T, true> : norm_dx_row_kernel<T, false>)<<<grid, kRowThreads, 0, s>>>(a, w_fp32);
     st = cuda_check(cudaGetLastError(), "layer norm backward launch");
     if (st != LPQ_OK || !a.parts) return st;
     parts = (int)norm_parts(a.rows, a.cols);
-    norm_parts_kernel<T><<<dim3((unsigned)((a.cols + kRowThreads - 1) / kRowThreads), parts), kRowThreads, 0, s>>>(a, parts);
+    const int64_t threads = a.cols / (vec ? 16 / (int)sizeof(T) : 1);
+    const dim3 blocks((unsigned)((threads + kPartThreads - 1) / kPartThreads), (unsigned)parts);
+    (vec ? norm_parts_kernel<T, true> : norm_parts_kernel<T, false>)<<<blocks, kPartThreads, 0, s>>>(a, parts);
     if ((st = cuda_check(cudaGetLastError(), "layer norm parts launch")) != LPQ_OK) return st;
   }
   return cuda_check(launch_dependent(norm_join_kernel, dim3((unsigned)((a.cols + 31) / 32), 2), 32 * kJoinWarps, 0, s,
