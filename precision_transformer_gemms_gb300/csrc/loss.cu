@@ -99,6 +99,7 @@ struct Product {
   int part;            // partial sums into acc instead of out
   void* out;
   int64_t ld;          // of the second terms of dl
+  int a_box;           // rows of A that a load takes: kHalf, or fewer that are all of them
 };
 
 struct alignas(64) CeMaps {
@@ -288,11 +289,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         const int32_t arow = mt * kTile + (terms ? 0 : (int32_t)rank * kHalf), brow = nt * kTile + (int32_t)rank * kHalf;
         // the first step with the second terms
         const int second = terms ? (rank ? 0 : INT_MAX) : EPI == kGrads && g.two ? p.num_k / 2 : INT_MAX;
+        const bool has_a = p.a_box == kHalf || terms || leader;
+        const uint32_t bytes = 2 * kOperand + (p.a_box == kHalf || terms ? 2 : 1) * p.a_box * (kStepK * 2);
         auto loads = [&](auto a_is_mn) {
           constexpr bool A_MN = decltype(a_is_mn)::value;
           for (int kt = k0; kt < k1; ++kt) {
             if (!(ok = mbar_wait_bounded(&empty[s], ph ^ 1u, abort_flag, g.err))) break;
-            if (leader) mbar_arrive_expect_tx(&full[s], 4 * kOperand);
+            if (leader) mbar_arrive_expect_tx(&full[s], bytes);
             const uint32_t fb = full_leader + 8 * s;
             uint8_t* da = sA + s * kOperand;
             uint8_t* db = sB + s * kOperand;
@@ -301,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             if constexpr (A_MN) {
               tma_load_2d_pair(da, ta, arow, k, fb);
               tma_load_2d_pair(da + kOperand / 2, ta, arow + 64, k, fb);
-            } else {
+            } else if (has_a) {
               tma_load_2d_pair(da, ta, k, arow, fb);
             }
             if constexpr (B_MN) {
@@ -769,6 +772,13 @@ int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
   return best;
 }
 
+// Rows of A in a load.  A K-major A of up to kFew rows takes those alone, in the
+// even CTA (or a term in each): a load of rows that are not there costs more
+// than one of rows that are.  What the rest of the stage holds enters rows that
+// are not stored.  Forward, one row: 32000 x 4096 90 -> 55 us, 131072 x 1024
+// 80 -> 53 us; from 64 rows on no difference.
+int a_box(bool a_mn, int64_t M) { return !a_mn && M <= kFew ? (int)round_up(M, 8) : kHalf; }
+
 struct Operand {
   const void* p;
   int64_t ld;  // elements
@@ -780,7 +790,7 @@ lpq_status set_product(CeTile& g, CeMaps& maps, int i, int64_t M, int64_t N, int
                        bool b_mn, void* c, int64_t ldc, int splits) {
   lpq_status st;
   if ((st = a_mn ? make_map(&maps.a[i], a.p, true, M, K, a.ld * 2, 64, kStepK)
-                 : make_map(&maps.a[i], a.p, true, K, M, a.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+                 : make_map(&maps.a[i], a.p, true, K, M, a.ld * 2, kStepK, a_box(a_mn, M))) != LPQ_OK) return st;
   if ((st = b_mn ? make_map(&maps.b[i], b.p, true, N, K, b.ld * 2, 64, kStepK)
                  : make_map(&maps.b[i], b.p, true, K, N, b.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
   if (c && (st = make_map(&maps.c[i], c, true, N, M, ldc * 2, 64, 32)) != LPQ_OK) return st;
@@ -795,6 +805,7 @@ lpq_status set_product(CeTile& g, CeMaps& maps, int i, int64_t M, int64_t N, int
   p.splits = splits;
   p.items = (int)(tm * tn * splits);
   p.a_mn = a_mn;
+  p.a_box = a_box(a_mn, M);
   return LPQ_OK;
 }
 
@@ -895,7 +906,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     CeTile g = base;
     g.col0 = v0;
     if ((st = set_product(g, maps, 0, a.t, width, a.d, h, false, w, false, dl, plan.dl_ld, 1)) != LPQ_OK) return st;
-    if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, kStepK, a_box(false, a.t))) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
     const Operand l2{static_cast<uint8_t*>(dl) + (plan.two ? (size_t)a.t * (size_t)plan.dl_ld * 2 : 0), plan.dl_ld};
     g.prod[0].out = const_cast<void*>(l2.p);
@@ -906,7 +917,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     g.add = v0 > 0;
     void* dw = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
     if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, nullptr, 0, plan.splits)) != LPQ_OK) return st;
-    if ((st = make_map(&maps.a2[0], l2.p, true, width, a.t, l2.ld * 2, kStepK, kHalf)) != LPQ_OK) return st;
+    if ((st = make_map(&maps.a2[0], l2.p, true, width, a.t, l2.ld * 2, kStepK, a_box(false, a.t))) != LPQ_OK) return st;
     if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, 64, kStepK)) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
     g.prod[0].scatter = plan.direct;
