@@ -141,6 +141,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// exp(x - y).  The difference comes first: a product of x alone with log2 e
+// would be rounded at x's size, and exp(0) would not be 1.
+__device__ __forceinline__ float exp_of_difference(float x, float y) { return ex2((x - y) * kLog2e); }
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -387,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       int64_t from = row;  // the row of h
       if (EPI == kGrads && p.scatter && live) from = g.list[row];
       int label = -1;  // its column among this warp's 128, -1: not here
-      float lse2 = 0.f, gs = 0.f;
+      float lse = 0.f, gs = 0.f;
       bool target = false;
       if constexpr (EPI == kStats || EPI == kDlogits) {
         if (EPI == kDlogits && live) from = g.list[row];
@@ -398,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       }
       if constexpr (EPI == kDlogits) {
         if (target) {
-          lse2 = g.lse[from] * kLog2e;
+          lse = g.lse[from];
           gs = g.dloss[from] / scale;
         }
       }
@@ -446,14 +449,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             if (label == i) at = l[i];
           g.at_label[row] = at;
         }
-        float m = kNegInf, sum = 0.f;
+        float m = kNegInf;
 #pragma unroll
         for (int i = 0; i < kHalf; ++i) m = max_nan(m, l[i]);
-        // all -inf: the exponents are taken against 0, and each term is exp(-inf) = 0
-        const float base = m == kNegInf ? 0.f : m * kLog2e;
+        // all -inf: the differences are taken from 0, and each term is exp(-inf) = 0
+        const float base = m == kNegInf ? 0.f : m;
+        const float2 minus = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+        float2 e[kHalf / 2];
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) sum += ex2(__fmaf_rn(l[i], kLog2e, -base));
-        if (live && ncols > 0) g.stats[row * g.stat_cols + nt * 2 + half] = make_float2(m, sum);
+        for (int i = 0; i < kHalf / 2; ++i) {  // exp_of_difference, two at a time
+          const float2 d = __fmul2_rn(__fadd2_rn(make_float2(l[2 * i], l[2 * i + 1]), minus), log2e);
+          e[i] = make_float2(ex2(d.x), ex2(d.y));
+        }
+        // in pairs: one after the other, 127 small terms would lose their last
+        // bits to a running sum of about 1 (a confident token's)
+#pragma unroll
+        for (int w = kHalf / 4; w > 0; w >>= 1)
+#pragma unroll
+          for (int i = 0; i < w; ++i) e[i] = __fadd2_rn(e[i], e[i + w]);
+        if (live && ncols > 0) g.stats[row * g.stat_cols + nt * 2 + half] = make_float2(m, e[0].x + e[0].y);
         __syncwarp();
         continue;
       }
@@ -506,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           if constexpr (EPI == kDlogits) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              v[i] = __float_as_uint(target ? ex2(__fmaf_rn(__uint_as_float(v[i]), kLog2e, -lse2)) * gs : 0.f);
+              v[i] = __float_as_uint(target ? exp_of_difference(__uint_as_float(v[i]), lse) * gs : 0.f);
             if (label >= cc * 32 && label < cc * 32 + 32)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
@@ -584,12 +598,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
 }
 
 // Joins (m, s) pairs: the sum of s exp(m - M) under the common maximum M.  A
-// maximum that is NaN, +inf or -inf is the result by itself.
-__device__ __forceinline__ void join_stats(float& m, float& s, float m2, float s2) {
-  const float top = max_nan(m, m2);
-  const float base = top == kNegInf ? 0.f : top * kLog2e;
-  s = s * ex2(__fmaf_rn(m, kLog2e, -base)) + s2 * ex2(__fmaf_rn(m2, kLog2e, -base));
-  m = top;
+// maximum that is NaN, +inf or -inf is the result by itself.  c holds what the
+// additions' roundings left out of s (exactly, where neither factor rounds).
+struct Stats {
+  float m, s, c;
+};
+__device__ __forceinline__ void join_stats(Stats& a, const Stats& b) {
+  const float top = max_nan(a.m, b.m);
+  const float base = top == kNegInf ? 0.f : top;
+  const float fa = exp_of_difference(a.m, base), fb = exp_of_difference(b.m, base);
+  const float x = __fmul_rn(a.s, fa), y = __fmul_rn(b.s, fb);
+  const float sum = __fadd_rn(x, y), part = __fsub_rn(sum, x);
+  const float left = __fadd_rn(__fsub_rn(x, __fsub_rn(sum, part)), __fsub_rn(y, part));
+  a.c = a.c * fa + b.c * fb + left;
+  a.s = sum;
+  a.m = top;
 }
 
 // lse and loss of a row from its column blocks' maxima and sums; one warp per row.
@@ -601,22 +624,23 @@ __global__ void __launch_bounds__(256) ce_join_kernel(const float2* stats, int64
   const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= t) return;
   const int lane = threadIdx.x & 31;
-  float m = kNegInf, s = 0.f;
+  Stats a{kNegInf, 0.f, 0.f};
 #pragma unroll 4
   for (int64_t i = lane; i < cols; i += 32) {
     const float2 x = stats[row * cols + i];
-    join_stats(m, s, x.x, x.y);
+    join_stats(a, {x.x, x.y, 0.f});
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    join_stats(m, s, m2, s2);
-  }
+  for (int o = 16; o > 0; o >>= 1)
+    join_stats(a, {__shfl_xor_sync(0xFFFFFFFFu, a.m, o), __shfl_xor_sync(0xFFFFFFFFu, a.s, o), __shfl_xor_sync(0xFFFFFFFFu, a.c, o)});
   if (lane == 0) {
-    const float l = (m == m && fabsf(m) != -kNegInf) ? m + logf(s) : m;
+    const float m = a.m, s = a.s + a.c;
+    // the loss is taken from the maximum, not from lse: a confident token's is
+    // far smaller than lse's last bit (and, with s >= 1, never negative)
+    const float rest = (m == m && fabsf(m) != -kNegInf) ? logf(s) : 0.f;
     const int64_t label = labels[row];
-    lse[row] = l;
-    loss[row] = label >= 0 && label < v ? l - at_label[row] : 0.f;
+    lse[row] = m + rest;
+    loss[row] = label >= 0 && label < v ? (m - at_label[row]) + rest : 0.f;
   }
 }
 
