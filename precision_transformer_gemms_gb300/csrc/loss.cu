@@ -63,10 +63,12 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 
 // The tensor core cuts (does not round) the FP32 sum at every 16 products, so
 // a long sum drifts towards zero: measured 2.5e-6 of the loss over d = 4096.
-// The logits of the forward pass are therefore summed in TMEM over kChunk
-// steps (1024 values) at a time and across chunks in the epilogue's registers:
-// 2% of the time at 7936 x 4096 x 32000, a fifth to an eighth of the drift;
-// the gradients' sums carry dl's bf16 rounding, far above that drift.
+// The logits are therefore summed in TMEM over kChunk steps (1024 values) at a
+// time and across chunks in the epilogue's registers: 2% of the time at 7936 x
+// 4096 x 32000, a fifth to an eighth of the drift.  Both passes do so: exp(l -
+// lse) takes the bits that lse was made of, and where p is near 1 its p - 1 is
+// not the difference of two drifts.  The gradients' sums are cut in full, below
+// dl's bf16 rounding.
 constexpr int kChunk = 16;
 
 // Up to kFew rows dl is stored as two terms, the value in bf16 and in bf16 what
@@ -144,6 +146,11 @@ __device__ __forceinline__ float ex2(float x) {
 // exp(x - y).  The difference comes first: a product of x alone with log2 e
 // would be rounded at x's size, and exp(0) would not be 1.
 __device__ __forceinline__ float exp_of_difference(float x, float y) { return ex2((x - y) * kLog2e); }
+// The same of two x at a time, y given as -y.
+__device__ __forceinline__ float2 exp_of_differences(float2 x, float2 minus_y) {
+  const float2 d = __fmul2_rn(__fadd2_rn(x, minus_y), make_float2(kLog2e, kLog2e));
+  return make_float2(ex2(d.x), ex2(d.y));
+}
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -341,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         constexpr uint32_t idesc = instruction_desc(A_MN, B_MN);
         int kt = k0;
         do {  // one accumulator per chunk of the sum (a split without steps still hands one over)
-          const int kend = EPI == kStats ? min(k1, kt + kChunk) : k1;
+          const int kend = EPI != kGrads ? min(k1, kt + kChunk) : k1;
           const uint32_t a = lt % kNacc, aph = (lt / kNacc) & 1u;
           ++lt;
           if (!(ok = mbar_wait_bounded(&acc_empty[a], aph ^ 1u, abort_flag, g.err))) break;
@@ -423,21 +430,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           if (leader) mbar_arrive(&acc_empty[a]); else mbar_arrive_remote_relaxed(acc_empty_leader + 8 * a);
         }
       };
-      if constexpr (EPI == kStats) {
-        float l[kHalf];
+      float l[EPI != kGrads ? kHalf : 1];  // logits
+      if constexpr (EPI != kGrads) {
         bool ok = true;
         for (int kt = 0; kt < p.num_k && ok; kt += kChunk) {
           if (!(ok = take())) break;
 #pragma unroll
-          for (int cc = 0; cc < kHalf / 32; ++cc) {
-            uint32_t v[32];
-            tmem_ld32(tbase + (uint32_t)(cc * 32), v);
+          for (int cc = 0; cc < kHalf / 16; ++cc) {
+            uint32_t v[16];
+            tmem_ld16(tbase + (uint32_t)(cc * 16), v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) l[cc * 32 + i] = (kt ? l[cc * 32 + i] : 0.f) + __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) l[cc * 16 + i] = (kt ? l[cc * 16 + i] : 0.f) + __uint_as_float(v[i]);
           }
           give();
         }
         if (!ok) break;
+      }
+      if constexpr (EPI == kStats) {
         if (ncols < kHalf)
 #pragma unroll
           for (int i = 0; i < kHalf; ++i)
@@ -454,13 +463,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         for (int i = 0; i < kHalf; ++i) m = max_nan(m, l[i]);
         // all -inf: the differences are taken from 0, and each term is exp(-inf) = 0
         const float base = m == kNegInf ? 0.f : m;
-        const float2 minus = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+        const float2 minus = make_float2(-base, -base);
         float2 e[kHalf / 2];
 #pragma unroll
-        for (int i = 0; i < kHalf / 2; ++i) {  // exp_of_difference, two at a time
-          const float2 d = __fmul2_rn(__fadd2_rn(make_float2(l[2 * i], l[2 * i + 1]), minus), log2e);
-          e[i] = make_float2(ex2(d.x), ex2(d.y));
-        }
+        for (int i = 0; i < kHalf / 2; ++i) e[i] = exp_of_differences(make_float2(l[2 * i], l[2 * i + 1]), minus);
         // in pairs: one after the other, 127 small terms would lose their last
         // bits to a running sum of about 1 (a confident token's)
 #pragma unroll
@@ -471,6 +477,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         __syncwarp();
         continue;
       }
+      if constexpr (EPI == kDlogits) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) l[i] = target ? exp_of_difference(l[i], lse) * gs : 0.f;
+        if (label >= 0)
+#pragma unroll
+          for (int i = 0; i < kHalf; ++i)
+            if (label == i) l[i] -= gs;
+        // in place of each pair: its bf16 values and, with two terms, in bf16 what
+        // those leave out (nothing of an infinity)
+        if (terms) {
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 2) {
+            const __nv_bfloat162 top = __floats2bfloat162_rn(l[i], l[i + 1]);
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(&top);
+            const float a0 = bf16_lo(u), a1 = bf16_hi(u);
+            const __nv_bfloat162 rest = __floats2bfloat162_rn(fabsf(a0) < -kNegInf ? l[i] - a0 : 0.f,
+                                                              fabsf(a1) < -kNegInf ? l[i + 1] - a1 : 0.f);
+            l[i] = __uint_as_float(u);
+            l[i + 1] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&rest));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kHalf; i += 2) {
+            const __nv_bfloat162 top = __floats2bfloat162_rn(l[i], l[i + 1]);
+            l[i] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&top));
+          }
+        }
+      }
       bool some = true;
       const bool part = EPI == kGrads && p.part;
       if constexpr (EPI == kGrads) {
@@ -479,13 +513,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         split_range(split, p, k0, k1);
         some = k0 < k1;
       }
-      if (!take()) break;
-#pragma unroll 1
-      for (int cc = 0; cc < kHalf / 32; ++cc) {
+      if (EPI == kGrads && !take()) break;
+      // 32 columns: the last of kGrads hands the accumulator back once it is read
+      auto block = [&](int cc) {
         uint32_t v[32];
         __syncwarp();
-        tmem_ld32(tbase + (uint32_t)(cc * 32), v);
-        if (cc == kHalf / 32 - 1) give();
+        if constexpr (EPI == kGrads) {
+          tmem_ld32(tbase + (uint32_t)(cc * 32), v);
+          if (cc == kHalf / 32 - 1) give();
+        }
         if (part) {
           if (live && some && cc * 32 < ncols) {
             float* to = g.acc + ((terms ? split * 2 + (int)rank : split) * p.M + row) * p.N + c0 + cc * 32;
@@ -517,28 +553,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
           // bf16 tile: 32 rows x 64 columns staged (128-byte swizzle: 16-byte
           // chunk i of row r at chunk i ^ (r & 7)) and stored by TMA, which
           // clips at the matrix's edges
+          uint4 pk[4];
           if constexpr (EPI == kDlogits) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              v[i] = __float_as_uint(target ? exp_of_difference(__uint_as_float(v[i]), lse) * gs : 0.f);
-            if (label >= cc * 32 && label < cc * 32 + 32)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (label == cc * 32 + i) v[i] = __float_as_uint(__uint_as_float(v[i]) - gs);
+            for (int i = 0; i < 4; ++i) {
+              const float* f = l + cc * 32 + 8 * i;
+              pk[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[2]), __float_as_uint(f[4]), __float_as_uint(f[6]));
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = some ? __float_as_uint(__uint_as_float(v[i]) * scale) : 0u;
-          }
-          uint4 pk[4];
+            for (int i = 0; i < 4; ++i) {
+              uint32_t u[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(v[8 * i + 2 * j]), __uint_as_float(v[8 * i + 2 * j + 1]));
-              u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+              for (int j = 0; j < 4; ++j) {
+                const float lo = __uint_as_float(v[8 * i + 2 * j]) * scale, hi = __uint_as_float(v[8 * i + 2 * j + 1]) * scale;
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(some ? lo : 0.f, some ? hi : 0.f);
+                u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              pk[i] = make_uint4(u[0], u[1], u[2], u[3]);
             }
-            pk[i] = make_uint4(u[0], u[1], u[2], u[3]);
           }
           if (EPI == kGrads && p.scatter) {  // (d is a multiple of 8: whole vectors)
             if (live) {
@@ -547,25 +580,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
               for (int i = 0; i < 4; ++i)
                 if (cc * 32 + 8 * i < ncols) to[i] = pk[i];
             }
-            continue;
+            return;
           }
           if (EPI == kDlogits && terms) {
-            if (rank) continue;  // (rows of this CTA: none)
+            if (rank) return;  // (rows of this CTA: none)
             uint16_t* to = static_cast<uint16_t*>(p.out) + row * p.ld + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t u[4];
-              const uint32_t top[4] = {pk[i].x, pk[i].y, pk[i].z, pk[i].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float a0 = __uint_as_float(top[j] << 16), a1 = __uint_as_float(top[j] & 0xFFFF0000u);
-                // (nothing is left out of an infinity)
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(
-                    fabsf(a0) < -kNegInf ? __uint_as_float(v[8 * i + 2 * j]) - a0 : 0.f,
-                    fabsf(a1) < -kNegInf ? __uint_as_float(v[8 * i + 2 * j + 1]) - a1 : 0.f);
-                u[j] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              if (row < g.t && cc * 32 + 8 * i < ncols) reinterpret_cast<uint4*>(to)[i] = make_uint4(u[0], u[1], u[2], u[3]);
+              const float* f = l + cc * 32 + 8 * i;
+              if (row < g.t && cc * 32 + 8 * i < ncols)
+                reinterpret_cast<uint4*>(to)[i] =
+                    make_uint4(__float_as_uint(f[1]), __float_as_uint(f[3]), __float_as_uint(f[5]), __float_as_uint(f[7]));
             }
           }
           if ((cc & 1) == 0) {
@@ -584,6 +609,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             }
           }
         }
+      };
+      if constexpr (EPI == kGrads) {
+#pragma unroll 1
+        for (int cc = 0; cc < kHalf / 32; ++cc) block(cc);
+      } else {
+#pragma unroll
+        for (int cc = 0; cc < kHalf / 32; ++cc) block(cc);
       }
     }
     if (lane == 0) bulk_wait_group0();  // this warp's TMA stores complete before the CTA exits
