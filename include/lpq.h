@@ -346,8 +346,9 @@ lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw,
  * vocab_piece words at a time (0: the library's choice; else a positive
  * multiple of 64), so that only t * vocab_piece values of dl exist at once.
  * They are divided by max |dloss| and rounded to bf16, which the tensor cores
- * read (up to 128 rows: held as the sum of two bf16 terms); all sums are FP32 and the factor is put back before the final
- * rounding.  The same inputs give the same bits.  0 rows give dw = 0. */
+ * read (where up to 128 rows have a target: held as the sum of two bf16 terms);
+ * all sums are FP32 and the factor is put back before the final rounding.  The
+ * same inputs give the same bits.  0 rows give dw = 0. */
 lpq_status lpq_linear_ce_backward(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels,
                                   const float *lse, const float *dloss, int64_t t, int64_t v, int64_t d, void *dh,
                                   void *dw, int32_t grads_fp32, int64_t vocab_piece, void *workspace,

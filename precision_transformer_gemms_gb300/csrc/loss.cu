@@ -30,8 +30,8 @@
 // tensor cores read) and s multiplies the FP32 sums: with equal dloss, the
 // mean over the tokens say, the entry p - 1 of a label is then rounded as it
 // is instead of after a product with 1 / t.  Over many tokens the roundings
-// average out below those of bf16 gradients; a few tokens' would show, so up to
-// 128 rows dl is held as the sum of two bf16 terms (16 bits).
+// average out below those of bf16 gradients; a few tokens' would show, so where
+// up to 128 rows have a target dl is held as the sum of two bf16 terms (16 bits).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -71,14 +71,15 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // dl's bf16 rounding.
 constexpr int kChunk = 16;
 
-// Up to kFew rows dl is stored as two terms, the value in bf16 and in bf16 what
-// that leaves out, t rows each.  In dh = dl w they are the rows of the two CTAs
-// (one of which had none), whose sums are added in the end; in dw = dl^T h they
-// follow one another along K, against the same h.  Reading w and storing dw
-// bound the pass up to there, so the terms cost little: 32000 x 4096, 33 or 128
-// rows, 198 and 192 us either way; at worst (one row) 209 -> 219 us.  Error of
-// bf16 gradients of up to 128 rows against 64 bits: 0.0020 to 0.0025 with one
-// term, 0.0017 with two, which is their own rounding.
+// Where up to kFew rows have a target (counted on the device) dl is stored as two
+// terms, the value in bf16 and in bf16 what that leaves out.  In dw = dl^T h they
+// follow one another along K, against the same h; in dh = dl w too, unless t
+// itself is up to kFew: then they are the rows of the two CTAs (one of which had
+// none), whose sums are added in the end.  Reading w and storing dw bound the pass
+// up to there, so the terms cost little: 32000 x 4096, 33 or 128 rows, 198 and 192
+// us either way; at worst (one row) 209 -> 219 us.  Error of bf16 gradients of up
+// to 128 rows against 64 bits: 0.0020 to 0.0025 with one term, 0.0017 with two,
+// which is their own rounding.
 constexpr int kFew = kHalf;
 
 // What a kernel's epilogue makes of a tile.
@@ -128,7 +129,8 @@ struct CeTile {
   const float* scale;
   float* acc;  // [splits][M][N]
   int add;     // 1: add to acc
-  int two;     // dl in two terms
+  int few;     // t is up to kFew: a CTA of the pair takes a term of dl
+  int64_t rest_rows;  // rows that there is room for in dl's second terms
   int out_fp32;
 };
 
@@ -263,6 +265,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   __shared__ int extra_sh;
   const int rows = EPI == kStats ? 0 : *g.rows;
   const bool some_rows = EPI != kStats && rows < g.t;
+  const bool two = EPI != kStats && rows <= kFew;  // dl in two terms
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       Product p = g.prod[i];
@@ -271,7 +274,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         p.tiles_m = (rows + kTile - 1) / kTile;
         p.items = p.tiles_m * p.tiles_n * p.splits;
       }
-      if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK * (g.two ? 2 : 1);
+      if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK;
+      if (EPI == kGrads && two && !(p.m_rows && g.few)) p.num_k *= 2;  // a term after the other
       prod[i] = p;
     }
     const int left_over = prod[0].items % npairs;
@@ -290,15 +294,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       for (int i = 0; ok && item_at(i, pair, npairs, prod, extra, which, w); ++i) {
         const Product& p = prod[which];
         const CUtensorMap* tmA = EPI == kDlogits && some_rows ? &maps.alt : &maps.a[which];
-        const CUtensorMap* tmA2 = EPI == kGrads && g.two ? &maps.a2[which] : tmA;
+        const CUtensorMap* tmA2 = EPI == kGrads && two ? &maps.a2[which] : tmA;
         const CUtensorMap* tmB = EPI == kGrads && p.k_rows && some_rows ? &maps.alt : &maps.b[which];
         int mt, nt, split, k0, k1;
         item_coords(w, p, mt, nt, split);
         split_range(split, p, k0, k1);
-        const bool terms = EPI == kGrads && g.two && p.m_rows;  // the CTAs take a term each
+        const bool terms = EPI == kGrads && g.few && p.m_rows;  // the CTAs take a term each
         const int32_t arow = mt * kTile + (terms ? 0 : (int32_t)rank * kHalf), brow = nt * kTile + (int32_t)rank * kHalf;
         // the first step with the second terms
-        const int second = terms ? (rank ? 0 : INT_MAX) : EPI == kGrads && g.two ? p.num_k / 2 : INT_MAX;
+        const int second = terms ? (rank ? 0 : INT_MAX) : EPI == kGrads && two ? p.num_k / 2 : INT_MAX;
         const bool has_a = p.a_box == kHalf || terms || leader;
         const uint32_t bytes = 2 * kOperand + (p.a_box == kHalf || terms ? 2 : 1) * p.a_box * (kStepK * 2);
         auto loads = [&](auto a_is_mn) {
@@ -388,7 +392,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       const Product& p = prod[which];
       int mt, nt, split;
       item_coords(w, p, mt, nt, split);
-      const bool terms = EPI != kStats && g.two && p.m_rows;  // (dl or dh: one tile down)
+      const bool terms = EPI != kStats && g.few && p.m_rows;  // (dl or dh: one tile down)
       const int64_t row = (int64_t)mt * kTile + (EPI == kGrads && terms ? 0 : rank * kHalf) + q * 32 + lane;
       const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
       const bool live = row < p.M;
@@ -486,7 +490,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             if (label == i) l[i] -= gs;
         // in place of each pair: its bf16 values and, with two terms, in bf16 what
         // those leave out (nothing of an infinity)
-        if (terms) {
+        if (two) {
 #pragma unroll
           for (int i = 0; i < kHalf; i += 2) {
             const __nv_bfloat162 top = __floats2bfloat162_rn(l[i], l[i + 1]);
@@ -582,13 +586,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             }
             return;
           }
-          if (EPI == kDlogits && terms) {
-            if (rank) return;  // (rows of this CTA: none)
+          if (EPI == kDlogits && terms && rank) return;  // (rows of this CTA: none)
+          if (EPI == kDlogits && two) {
             uint16_t* to = static_cast<uint16_t*>(p.out) + row * p.ld + c0 + cc * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float* f = l + cc * 32 + 8 * i;
-              if (row < g.t && cc * 32 + 8 * i < ncols)
+              if (row < g.rest_rows && cc * 32 + 8 * i < ncols)
                 reinterpret_cast<uint4*>(to)[i] =
                     make_uint4(__float_as_uint(f[1]), __float_as_uint(f[3]), __float_as_uint(f[5]), __float_as_uint(f[7]));
             }
@@ -883,21 +887,23 @@ lpq_status run_pair(CeTile& g, const CeMaps& maps, cudaStream_t s) {
 struct BackwardPlan {
   int64_t piece, dl_ld;
   int splits;
-  bool two;     // dl in two terms
+  bool few;     // t is up to kFew
   bool direct;  // one piece, one split: dh is stored by its product
+  int64_t rest_rows;  // of dl's second terms
   size_t list_at, h_at, dl_at, acc_at, bytes;
   BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked) {
     piece = piece_of(t, v, asked);
     dl_ld = std::min(piece, round_up(v, 8));
     // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
     splits = dh_splits(t, d, std::min(piece, v), 76);
-    two = t <= kFew;
-    direct = splits == 1 && piece >= v && !two;
+    few = t <= kFew;
+    direct = splits == 1 && piece >= v && !few;
+    rest_rows = std::min<int64_t>(t, kFew);
     list_at = 256;
     h_at = list_at + (size_t)round_up(t * 4, 256);
     dl_at = h_at + (size_t)round_up(t * d * 2, 256);
-    acc_at = dl_at + (size_t)round_up((two ? 2 * t : t) * dl_ld * 2, 256);
-    bytes = acc_at + (direct ? 0 : (size_t)(two ? 2 * splits : splits) * (size_t)t * (size_t)d * 4);
+    acc_at = dl_at + (size_t)round_up((t + rest_rows) * dl_ld * 2, 256);
+    bytes = acc_at + (direct ? 0 : (size_t)(few ? 2 * splits : splits) * (size_t)t * (size_t)d * 4);
   }
 };
 
@@ -945,7 +951,8 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   base.scale = scale;
   base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   base.out_fp32 = a.grads_fp32;
-  base.two = plan.two;
+  base.few = plan.few;
+  base.rest_rows = plan.rest_rows;
   const Operand h{a.h, a.ldh}, copied{a.workspace + plan.h_at, a.d}, l{dl, plan.dl_ld};
   lpq_status st = cuda_check(
       launch_dependent(ce_rows_kernel, (unsigned)std::min<int64_t>(cdiv(a.t, 8), (int64_t)device_sms() * 8), 256, 0, s, a.dloss,
@@ -964,7 +971,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     if ((st = set_product(g, maps, 0, a.t, width, a.d, h, false, w, false, dl, plan.dl_ld, 1)) != LPQ_OK) return st;
     if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, kStepK, a_box(false, a.t))) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
-    const Operand l2{static_cast<uint8_t*>(dl) + (plan.two ? (size_t)a.t * (size_t)plan.dl_ld * 2 : 0), plan.dl_ld};
+    const Operand l2{static_cast<uint8_t*>(dl) + (size_t)a.t * (size_t)plan.dl_ld * 2, plan.dl_ld};
     g.prod[0].out = const_cast<void*>(l2.p);
     g.prod[0].ld = plan.dl_ld;
     if ((st = run_pair<kDlogits>(g, maps, s)) != LPQ_OK) return st;
@@ -973,7 +980,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     g.add = v0 > 0;
     void* dw = static_cast<uint8_t*>(a.dw) + (size_t)v0 * (size_t)a.d * elem;
     if ((st = set_product(g, maps, 0, a.t, a.d, width, l, false, w, true, nullptr, 0, plan.splits)) != LPQ_OK) return st;
-    if ((st = make_map(&maps.a2[0], l2.p, true, width, a.t, l2.ld * 2, kStepK, a_box(false, a.t))) != LPQ_OK) return st;
+    if ((st = make_map(&maps.a2[0], l2.p, true, width, plan.rest_rows, l2.ld * 2, kStepK, a_box(false, a.t))) != LPQ_OK) return st;
     if ((st = make_map(&maps.alt, copied.p, true, a.d, a.t, copied.ld * 2, 64, kStepK)) != LPQ_OK) return st;
     g.prod[0].m_rows = 1;
     g.prod[0].scatter = plan.direct;
@@ -990,8 +997,8 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
       g = base;
     }
     if ((st = set_product(g, maps, at, width, a.d, a.t, l, true, h, true, a.grads_fp32 ? nullptr : dw, a.d, 1)) != LPQ_OK) return st;
-    if ((st = make_map(&maps.a2[at], l2.p, true, width, a.t, l2.ld * 2, 64, kStepK)) != LPQ_OK) return st;
-    if (plan.two) g.prod[at].num_k *= 2;
+    if ((st = make_map(&maps.a2[at], l2.p, true, width, plan.rest_rows, l2.ld * 2, 64, kStepK)) != LPQ_OK) return st;
+    if (plan.few) g.prod[at].num_k *= 2;
     g.prod[at].k_rows = 1;
     g.prod[at].out = dw;
     if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
@@ -999,7 +1006,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   if (plan.direct) return LPQ_OK;
   const unsigned grid = (unsigned)std::min<int64_t>(cdiv(a.t * cdiv(a.d, 128), 8), (int64_t)device_sms() * 8);
   return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc),
-                                     (int)(a.d / 4), plan.two ? 2 * plan.splits : plan.splits, scale, rows, list, a.dh, a.grads_fp32),
+                                     (int)(a.d / 4), plan.few ? 2 * plan.splits : plan.splits, scale, rows, list, a.dh, a.grads_fp32),
                     "cross entropy finish launch");
 }
 
