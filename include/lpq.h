@@ -346,16 +346,34 @@ lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw,
  * vocab_piece words at a time (0: the library's choice; else a positive
  * multiple of 64), so that only t * vocab_piece values of dl exist at once.
  * They are divided by max |dloss| and rounded to bf16, which the tensor cores
- * read (where up to 128 rows have a target: held as the sum of two bf16 terms);
- * all sums are FP32 and the factor is put back before the final rounding.  The
+ * read (where up to 128 rows have a target: held as the sum of two bf16 terms;
+ * beyond, FP32 gradients too carry that rounding, 2^-9 of each value, unless two
+ * terms are asked for by lpq_linear_ce_backward_ex); all sums are FP32 and the factor is put back before the final rounding.  The
  * same inputs give the same bits.  0 rows give dw = 0. */
 lpq_status lpq_linear_ce_backward(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels,
                                   const float *lse, const float *dloss, int64_t t, int64_t v, int64_t d, void *dh,
                                   void *dw, int32_t grads_fp32, int64_t vocab_piece, void *workspace,
                                   size_t workspace_bytes, lpq_stream_t stream);
 
+/* Options of lpq_linear_ce_backward_ex (all zero: lpq_linear_ce_backward).
+ *   two_terms   1: each value of dl as the sum of two bf16 terms (16 bits) for
+ *               any number of rows, at 10 t v d operations instead of 6 beyond
+ *               128 rows; 0: up to 128 rows with a target alone.
+ *   reserved    must be 0. */
+typedef struct {
+  int32_t two_terms;
+  int32_t reserved[3];
+} lpq_ce_opts;
+
+/* lpq_linear_ce_backward with explicit options (NULL = all defaults). */
+lpq_status lpq_linear_ce_backward_ex(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels,
+                                     const float *lse, const float *dloss, int64_t t, int64_t v, int64_t d, void *dh,
+                                     void *dw, int32_t grads_fp32, int64_t vocab_piece, void *workspace,
+                                     size_t workspace_bytes, const lpq_ce_opts *opts, lpq_stream_t stream);
+
 /* Workspace bytes of lpq_linear_ce (backward = 0) and lpq_linear_ce_backward
- * (backward = 1, with the same vocab_piece).  Host-only. */
+ * (backward = 1, or 2 with the option two_terms; with the same vocab_piece).
+ * Host-only. */
 lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t backward, int64_t vocab_piece,
                                    size_t *bytes);
 

@@ -438,7 +438,7 @@ lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t back
   lpq_status st = check_ce_shape(t, v, d);
   if (st != LPQ_OK) return st;
   if ((st = check_piece(vocab_piece)) != LPQ_OK) return st;
-  *bytes = ce_workspace(t, v, d, backward != 0, vocab_piece);
+  *bytes = ce_workspace(t, v, d, backward != 0, vocab_piece, backward == 2);
   return LPQ_OK;
 }
 
@@ -449,7 +449,7 @@ lpq_status lpq_linear_ce(const void* h, int64_t ldh, const void* w, int64_t ldw,
   if (st != LPQ_OK) return st;
   if (t > 0 && (!loss || !lse)) return set_error(LPQ_ERR_INVALID_ARG, "loss or lse is NULL");
   if (!aligned_to(loss, 4) || !aligned_to(lse, 4)) return set_error(LPQ_ERR_ALIGN, "loss or lse not 4-byte aligned");
-  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, false, 0))) != LPQ_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, false, 0, false))) != LPQ_OK) return st;
   if ((st = check_arch()) != LPQ_OK) return st;
   CeArgs a{};
   a.h = h; a.w = w; a.labels = labels; a.ldh = ldh; a.ldw = ldw; a.t = t; a.v = v; a.d = d;
@@ -461,18 +461,33 @@ lpq_status lpq_linear_ce_backward(const void* h, int64_t ldh, const void* w, int
                                   const float* lse, const float* dloss, int64_t t, int64_t v, int64_t d, void* dh,
                                   void* dw, int32_t grads_fp32, int64_t vocab_piece, void* workspace,
                                   size_t workspace_bytes, lpq_stream_t stream) {
+  return lpq_linear_ce_backward_ex(h, ldh, w, ldw, labels, lse, dloss, t, v, d, dh, dw, grads_fp32, vocab_piece, workspace,
+                                   workspace_bytes, nullptr, stream);
+}
+
+lpq_status lpq_linear_ce_backward_ex(const void* h, int64_t ldh, const void* w, int64_t ldw, const int64_t* labels,
+                                     const float* lse, const float* dloss, int64_t t, int64_t v, int64_t d, void* dh,
+                                     void* dw, int32_t grads_fp32, int64_t vocab_piece, void* workspace,
+                                     size_t workspace_bytes, const lpq_ce_opts* opts, lpq_stream_t stream) {
+  const lpq_ce_opts none{};
+  if (!opts) opts = &none;
   lpq_status st = check_ce(h, ldh, w, ldw, labels, t, v, d);
   if (st != LPQ_OK) return st;
+  if (opts->two_terms < 0 || opts->two_terms > 1) return set_error(LPQ_ERR_INVALID_ARG, "two_terms %d", opts->two_terms);
+  for (int32_t r : opts->reserved)
+    if (r) return set_error(LPQ_ERR_INVALID_ARG, "reserved option %d", r);
   if ((st = check_piece(vocab_piece)) != LPQ_OK) return st;
   if (grads_fp32 < 0 || grads_fp32 > 1) return set_error(LPQ_ERR_INVALID_ARG, "grads_fp32 %d", grads_fp32);
   if ((t > 0 && (!lse || !dloss || !dh)) || !dw) return set_error(LPQ_ERR_INVALID_ARG, "lse, dloss, dh or dw is NULL");
   if (!aligned_to(lse, 4) || !aligned_to(dloss, 4)) return set_error(LPQ_ERR_ALIGN, "lse or dloss not 4-byte aligned");
   if (!aligned16(dh) || !aligned16(dw)) return set_error(LPQ_ERR_ALIGN, "dh or dw not 16-byte aligned");
-  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, true, vocab_piece))) != LPQ_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, ce_workspace(t, v, d, true, vocab_piece, opts->two_terms))) != LPQ_OK)
+    return st;
   if ((st = check_arch()) != LPQ_OK) return st;
   CeArgs a{};
   a.h = h; a.w = w; a.labels = labels; a.ldh = ldh; a.ldw = ldw; a.t = t; a.v = v; a.d = d;
   a.lse = lse; a.dloss = dloss; a.dh = dh; a.dw = dw; a.grads_fp32 = grads_fp32; a.piece = vocab_piece;
+  a.two_terms = opts->two_terms;
   a.workspace = static_cast<uint8_t*>(workspace);
   return launch_ce_backward(a, reinterpret_cast<cudaStream_t>(stream));
 }

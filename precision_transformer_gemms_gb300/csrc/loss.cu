@@ -31,7 +31,8 @@
 // mean over the tokens say, the entry p - 1 of a label is then rounded as it
 // is instead of after a product with 1 / t.  Over many tokens the roundings
 // average out below those of bf16 gradients; a few tokens' would show, so where
-// up to 128 rows have a target dl is held as the sum of two bf16 terms (16 bits).
+// up to 128 rows have a target, or the caller asks for it, dl is held as the sum
+// of two bf16 terms (16 bits).
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -71,8 +72,9 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // dl's bf16 rounding.
 constexpr int kChunk = 16;
 
-// Where up to kFew rows have a target (counted on the device) dl is stored as two
-// terms, the value in bf16 and in bf16 what that leaves out.  In dw = dl^T h they
+// Where up to kFew rows have a target (counted on the device), or any number when
+// the caller asks for it, dl is stored as two terms, the value in bf16 and in bf16
+// what that leaves out.  In dw = dl^T h they
 // follow one another along K, against the same h; in dh = dl w too, unless t
 // itself is up to kFew: then they are the rows of the two CTAs (one of which had
 // none), whose sums are added in the end.  Reading w and storing dw bound the pass
@@ -130,6 +132,7 @@ struct CeTile {
   float* acc;  // [splits][M][N]
   int add;     // 1: add to acc
   int few;     // t is up to kFew: a CTA of the pair takes a term of dl
+  int two_to;  // rows with a target up to which dl is in two terms
   int64_t rest_rows;  // rows that there is room for in dl's second terms
   int out_fp32;
 };
@@ -265,7 +268,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   __shared__ int extra_sh;
   const int rows = EPI == kStats ? 0 : *g.rows;
   const bool some_rows = EPI != kStats && rows < g.t;
-  const bool two = EPI != kStats && rows <= kFew;  // dl in two terms
+  const bool two = EPI != kStats && rows <= g.two_to;  // dl in two terms
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       Product p = g.prod[i];
@@ -792,8 +795,8 @@ int64_t cdiv(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // Words per piece of the backward pass: dl takes at most 2^28 values (512 MiB)
 // unless 64 words of it are more.
-int64_t piece_of(int64_t t, int64_t v, int64_t piece) {
-  if (piece == 0) piece = std::max<int64_t>(64, (((int64_t)1 << 28) / std::max<int64_t>(t, 1)) / 64 * 64);
+int64_t piece_of(int64_t rows, int64_t v, int64_t piece) {
+  if (piece == 0) piece = std::max<int64_t>(64, (((int64_t)1 << 28) / std::max<int64_t>(rows, 1)) / 64 * 64);
   return std::min(piece, round_up(v, 64));
 }
 
@@ -810,11 +813,12 @@ int extra_items(int64_t n0, double c0, int64_t n1, double c1, int pairs) {
 // and its sum is long: the split makes items that spread over the pairs beside
 // dw's (t steps each), and costs its slab of FP32 partial sums written and read
 // once.  The estimate: the longest pair at 0.33 us a step, memory at 6.5 TB/s.
-int dh_splits(int64_t t, int64_t d, int64_t width, int pairs) {
-  const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK);
+int dh_splits(int64_t t, int64_t d, int64_t width, bool two_terms, int pairs) {
+  const bool few = t <= kFew;
+  const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK) * (two_terms && !few ? 2 : 1);
   const int64_t n1 = cdiv(width, kTile) * cdiv(d, kTile);
-  const int terms = t <= kFew ? 2 : 1;
-  const double c1 = (double)(terms * cdiv(t, kStepK)) + kItemStart;
+  const int terms = few ? 2 : 1;  // slabs of dh's sums
+  const double c1 = (double)((two_terms || few ? 2 : 1) * cdiv(t, kStepK)) + kItemStart;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= 64 && s <= steps; ++s) {
@@ -889,16 +893,18 @@ struct BackwardPlan {
   int splits;
   bool few;     // t is up to kFew
   bool direct;  // one piece, one split: dh is stored by its product
+  int two_to;   // rows with a target up to which dl is in two terms
   int64_t rest_rows;  // of dl's second terms
   size_t list_at, h_at, dl_at, acc_at, bytes;
-  BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked) {
-    piece = piece_of(t, v, asked);
+  BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked, bool two_terms) {
+    few = t <= kFew;
+    two_to = two_terms ? INT_MAX : kFew;
+    rest_rows = std::min<int64_t>(t, two_to);
+    piece = piece_of(two_terms && !few ? 2 * t : t, v, asked);
     dl_ld = std::min(piece, round_up(v, 8));
     // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
-    splits = dh_splits(t, d, std::min(piece, v), 76);
-    few = t <= kFew;
+    splits = dh_splits(t, d, std::min(piece, v), two_terms, 76);
     direct = splits == 1 && piece >= v && !few;
-    rest_rows = std::min<int64_t>(t, kFew);
     list_at = 256;
     h_at = list_at + (size_t)round_up(t * 4, 256);
     dl_at = h_at + (size_t)round_up(t * d * 2, 256);
@@ -909,10 +915,10 @@ struct BackwardPlan {
 
 }  // namespace
 
-size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece) {
+size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece, bool two_terms) {
   if (t == 0) return 0;
   if (!backward) return (size_t)round_up(t * 4, 256) + (size_t)cdiv(v, kHalf) * (size_t)t * sizeof(float2);
-  return BackwardPlan(t, v, d, piece).bytes;
+  return BackwardPlan(t, v, d, piece, two_terms).bytes;
 }
 
 lpq_status launch_ce(const CeArgs& a, cudaStream_t s) {
@@ -935,7 +941,7 @@ lpq_status launch_ce(const CeArgs& a, cudaStream_t s) {
 lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   const size_t elem = a.grads_fp32 ? 4 : 2;
   if (a.t == 0) return cuda_check(cudaMemsetAsync(a.dw, 0, (size_t)a.v * (size_t)a.d * elem, s), "cudaMemsetAsync(dw)");
-  const BackwardPlan plan(a.t, a.v, a.d, a.piece);
+  const BackwardPlan plan(a.t, a.v, a.d, a.piece, a.two_terms);
   float* scale = reinterpret_cast<float*>(a.workspace);
   int* rows = reinterpret_cast<int*>(a.workspace + 4);
   int* list = reinterpret_cast<int*>(a.workspace + plan.list_at);
@@ -952,6 +958,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   base.out_fp32 = a.grads_fp32;
   base.few = plan.few;
+  base.two_to = plan.two_to;
   base.rest_rows = plan.rest_rows;
   const Operand h{a.h, a.ldh}, copied{a.workspace + plan.h_at, a.d}, l{dl, plan.dl_ld};
   lpq_status st = cuda_check(

@@ -93,9 +93,10 @@ struct CeArgs {
   void* dw;
   int32_t grads_fp32;
   int64_t piece;  // backward: words per piece, 0 = choose
+  bool two_terms;  // backward: dl in two terms for any number of rows
   uint8_t* workspace;
 };
-size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece);
+size_t ce_workspace(int64_t t, int64_t v, int64_t d, bool backward, int64_t piece, bool two_terms);
 lpq_status launch_ce(const CeArgs& a, cudaStream_t stream);
 lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t stream);
 

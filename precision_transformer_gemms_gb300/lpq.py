@@ -60,6 +60,11 @@ class GemmOpts(ctypes.Structure):
                 ("direct_store", ctypes.c_int32), ("whole_tiles", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
 
 
+class CeOpts(ctypes.Structure):
+    """Options of lpq_linear_ce_backward_ex (all zero: lpq_linear_ce_backward)."""
+    _fields_ = [("two_terms", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
+
+
 # Named kernel paths of the GEMM (every one computes the same result).
 GEMM_PATHS = {
     "default": GemmOpts(),
@@ -113,6 +118,7 @@ def lib():
         L.lpq_linear_ce_workspace.argtypes = [I64, I64, I64, I32, I64, PSZ]
         L.lpq_linear_ce.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, SZ, P]
         L.lpq_linear_ce_backward.argtypes = [P, I64, P, I64, P, P, P, I64, I64, I64, P, P, I32, I64, P, SZ, P]
+        L.lpq_linear_ce_backward_ex.argtypes = L.lpq_linear_ce_backward.argtypes[:-1] + [ctypes.POINTER(CeOpts), P]
         L.lpq_matvec.argtypes = [ctypes.POINTER(QView), P, I64, I64, P, I32, P]
         L.lpq_layer_shapes.argtypes = [ctypes.POINTER(TransformerCfg), ctypes.POINTER(GemmShape),
                                        ctypes.POINTER(I32)]
@@ -125,7 +131,7 @@ def lib():
         for name in ("lpq_copy_bytes", "lpq_quantize", "lpq_scale_update", "lpq_gemm", "lpq_gemm_ex", "lpq_amax", "lpq_layer_shapes",
                      "lpq_device_status", "lpq_selftest_wait", "lpq_mma_peak", "lpq_selftest_arith", "lpq_layer_norm",
                      "lpq_layer_norm_workspace", "lpq_layer_norm_backward", "lpq_linear_ce_workspace", "lpq_linear_ce",
-                     "lpq_linear_ce_backward", "lpq_matvec"):
+                     "lpq_linear_ce_backward", "lpq_linear_ce_backward_ex", "lpq_matvec"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -297,6 +303,7 @@ def gemm(layout, a, b, c=None, out_fp32=False, stream=None, path=None):
 _TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_FP32}
 _BF16, _FP32 = torch.bfloat16, torch.float32
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_TWO_TERMS = ctypes.byref(CeOpts(two_terms=1))
 
 
 def _new(like, stream, shape, dtype):
@@ -411,19 +418,21 @@ def linear_cross_entropy(h, w, labels, stream=None):
     return loss, lse
 
 
-def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, vocab_piece=0, stream=None):
+def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, vocab_piece=0, stream=None, two_terms=False):
     """lpq_linear_ce_backward: the gradients (dh [t, d], dw [v, d]) of
-    sum(dloss * loss) for dloss [t] FP32 and the forward's lse."""
+    sum(dloss * loss) for dloss [t] FP32 and the forward's lse.  Where over 128
+    rows have a target, the gradient of the logits is rounded to bf16, of FP32
+    results too, unless `two_terms` asks for 16 bits of it."""
     t, d, v, ldh, ldw = _ce_args(h, w, labels)
     assert _is_vector(lse, t, _FP32) and _is_vector(dloss, t, _FP32), f"lse and dloss must be {t} fp32"
     L = lib()
-    need = _ce_workspace(t, v, d, 1, vocab_piece)
+    need = _ce_workspace(t, v, d, 2 if two_terms else 1, vocab_piece)
     dtype = _FP32 if out_fp32 else _BF16
     dh, dw = _new(h, stream, (t, d), dtype), _new(h, stream, (v, d), dtype)
     ws = _new(h, stream, need, torch.uint8)
-    _check(L.lpq_linear_ce_backward(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
-                                    dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32), vocab_piece,
-                                    ws.data_ptr(), need, _stream_of(h, stream)))
+    _check(L.lpq_linear_ce_backward_ex(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
+                                       dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32), vocab_piece,
+                                       ws.data_ptr(), need, _TWO_TERMS if two_terms else None, _stream_of(h, stream)))
     return dh, dw
 
 
