@@ -113,13 +113,14 @@ struct Load {
 
 // The two group scales of a lane's 32 codes as operand pairs.  NVFP4: f16 the
 // scale, bf16 the scale * 2^118 (the decoded values lie 2^-126 down, the sums
-// come out 2^-8 down).  MXFP4, scale 2^e: f16 2^e (callers see to the range);
-// bf16 2^(min(e, 1) + 126) and, where e > 1, the rest by mx_rest.
+// come out 2^-8 down).  MXFP4, scale 2^e: f16 2^min(e, 13) (beyond that callers
+// leave groups of zero codes alone, which any finite scale gives: infinity would
+// make them NaN); bf16 2^(min(e, 1) + 126) and, where e > 1, the rest by mx_rest.
 template <bool MX, bool F16>
 __device__ __forceinline__ void scale_pairs(uint32_t s, uint32_t (&o)[2]) {
   if constexpr (MX) {
     if constexpr (F16) {
-      const float f = __uint_as_float(s << 23);
+      const float f = __uint_as_float(min(s, 140u) << 23);
       const __half2 h = __floats2half2_rn(f, f);
       o[0] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
