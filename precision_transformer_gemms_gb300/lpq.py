@@ -8,6 +8,7 @@ loaded, every call raises: there is no CPU or PyTorch fallback.
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -175,6 +176,18 @@ def layer_shapes(hidden, intermediate, micro_batch, seq, heads=32, layers=1):
 
 
 # ----------------------------------------------------------------- device buffers
+_TENSOR_SCALED = (FP8_E4M3, FP8_E5M2, NVFP4, NVFP4_2D)  # formats with a factor per tensor
+_pack_view = struct.Struct("@PPPPqqiiii").pack  # QView's fields
+
+
+@functools.lru_cache(maxsize=256)
+def _copy_spec(fmt, rows, cols, sf_layout):
+    """What of_parts asks of a copy: types and bytes of codes and scales, whether it has a tensor scale."""
+    code_bytes, scale_bytes = copy_bytes(fmt, rows, cols, sf_layout)
+    return (torch.bfloat16 if fmt == BF16 else torch.uint8, code_bytes,
+            torch.float32 if fmt in (FP8_BLOCK_1x128, FP8_BLOCK_128x128) else torch.uint8, scale_bytes, fmt in _TENSOR_SCALED)
+
+
 class Copy:
     """One quantized copy: torch-owned device buffers plus its C view."""
 
@@ -192,7 +205,7 @@ class Copy:
         else:
             self.scales = None
         # per-tensor factor and amax only where the format has them
-        scalar = fmt in (FP8_E4M3, FP8_E5M2, NVFP4, NVFP4_2D)
+        scalar = fmt in _TENSOR_SCALED
         self.tensor_scale = torch.ones(1, dtype=torch.float32, device=device) if scalar else None
         self.amax = torch.zeros(1, dtype=torch.float32, device=device) if scalar else None
 
@@ -206,15 +219,37 @@ class Copy:
 
     @classmethod
     def of_parts(cls, fmt, rows, cols, codes, scales, tensor_scale=None, sf_layout=SF_GEMM, colwise=False):
-        """Wraps existing codes (uint8), block scales and tensor scale as a copy, e.g. from a checkpoint."""
+        """Wraps existing codes, block scales and tensor scale as a copy, e.g. from a checkpoint.
+
+        Each is a contiguous CUDA tensor, all on one device: `codes` uint8 (bf16 for
+        BF16) and `scales` uint8 (FP32 for the FP8 block formats, None where the format
+        has none) of at least copy_bytes(fmt, rows, cols, sf_layout) bytes,
+        `tensor_scale` one FP32 where the format has one.  SF_GEMM scales are padded to
+        128 rows and 256 columns; scales as [rows, blocks] are SF_PLAIN."""
+        code_type, code_bytes, scale_type, scale_bytes, scaled = _copy_spec(fmt, rows, cols, sf_layout)
+        assert codes is not None and codes.dtype is code_type and codes.nbytes >= code_bytes and codes.is_contiguous(), \
+            f"codes must be a contiguous {code_type} tensor of at least {code_bytes} bytes"
+        device = codes.get_device()
+        there = device >= 0
+        if scale_bytes:
+            assert scales is not None and scales.dtype is scale_type and scales.nbytes >= scale_bytes and scales.is_contiguous(), \
+                f"scales must be a contiguous {scale_type} tensor of at least {scale_bytes} bytes"
+            there = there and scales.get_device() == device
+        if scaled:
+            assert tensor_scale is not None and tensor_scale.dtype is torch.float32 and tensor_scale.numel() == 1, \
+                "tensor_scale must be one fp32"
+            there = there and tensor_scale.get_device() == device
+        assert there, "the parts of a copy must lie on one CUDA device"
         c = cls.__new__(cls)
         c.fmt, c.rows, c.cols, c.colwise, c.sf_layout = fmt, rows, cols, int(colwise), sf_layout
         c.codes, c.scales, c.tensor_scale, c.amax = codes, scales, tensor_scale, None
         return c
 
     def view(self):
-        return QView(_ptr(self.codes), _ptr(self.scales), _ptr(self.tensor_scale), _ptr(self.amax), self.rows,
-                     self.cols, self.fmt, self.sf_layout, self.colwise, 0)
+        scales, scale, amax = self.scales, self.tensor_scale, self.amax
+        return QView.from_buffer_copy(_pack_view(
+            self.codes.data_ptr(), 0 if scales is None else scales.data_ptr(), 0 if scale is None else scale.data_ptr(),
+            0 if amax is None else amax.data_ptr(), self.rows, self.cols, self.fmt, self.sf_layout, self.colwise, 0))
 
     def codes_matrix(self):
         """Codes as a [rows, bytes per row] uint8 tensor (packed for NVFP4 and MXFP4)."""
@@ -441,6 +476,7 @@ def matvec(x, w, out_fp32=False, stream=None):
     weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n]."""
     m, k = x.shape
     assert x.dtype is _BF16 and k == w.cols, "x must be bf16 [m, k]"
+    assert x.get_device() == w.codes.get_device(), "x must lie where the weights do"
     y = _new(x, stream, (m, w.rows), _FP32 if out_fp32 else _BF16)
     _check(lib().lpq_matvec(w.view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _stream_of(x, stream)))
     return y
