@@ -4,6 +4,11 @@ Every step of the quantize / GEMM path runs in liblpq's CUDA kernels.  This
 module only allocates output buffers with torch, builds the C views and passes
 pointers and the current CUDA stream.  If the shared library cannot be built or
 loaded, every call raises: there is no CPU or PyTorch fallback.
+
+A call with ``stream=s`` runs on s and takes the memory of its results and
+workspaces there.  The caller sees to it that s waits for the work that makes the
+inputs, that these live until s is done with them, and that other streams wait
+for s before they use the results.
 """
 import ctypes
 import functools
@@ -278,6 +283,33 @@ class DelayedState:
                              self.hist.numel())
 
 
+def _tensors(obj):
+    if isinstance(obj, torch.Tensor):
+        yield obj
+    elif isinstance(obj, QTensor):
+        yield from _tensors((obj.row, obj.col))
+    elif isinstance(obj, Copy):
+        yield from _tensors((obj.codes, obj.scales, obj.tensor_scale, obj.amax))
+    elif isinstance(obj, (tuple, list)):
+        for o in obj:
+            yield from _tensors(o)
+    elif isinstance(obj, dict):
+        yield from _tensors(tuple(obj.values()))
+
+
+def on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with its kernels and its memory on `stream`.  Memory of the
+    current stream would not do: a block that it has given back, with work on it
+    still to come, could be written at once.  What comes back may be dropped by the
+    caller's stream too: its memory is kept until that stream is done with it."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in _tensors(out):
+        t.record_stream(caller)
+    return out
+
+
 def alloc(fmt, rows, cols, flags, sf_layout=SF_GEMM, device="cuda"):
     return QTensor(Copy(fmt, rows, cols, False, sf_layout, device) if flags & ROWWISE else None,
                    Copy(fmt, cols, rows, True, sf_layout, device) if flags & COLWISE else None)
@@ -286,6 +318,8 @@ def alloc(fmt, rows, cols, flags, sf_layout=SF_GEMM, device="cuda"):
 def quantize(x, fmt, flags, scaling=SCALING_CURRENT, seed=0, counter_offset=0, rht_seed=0, state=None,
              sf_layout=SF_GEMM, out=None, stream=None):
     """lpq_quantize on a bf16 CUDA tensor x [rows, cols]; returns a QTensor."""
+    if stream is not None:
+        return on_stream(stream, quantize, x, fmt, flags, scaling, seed, counter_offset, rht_seed, state, sf_layout, out)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.is_contiguous()
     rows, cols = x.shape
     if out is None:
@@ -294,7 +328,7 @@ def quantize(x, fmt, flags, scaling=SCALING_CURRENT, seed=0, counter_offset=0, r
                   out.col.view() if out.col is not None else QView())
     st = ctypes.byref(state.c()) if state is not None else None
     _check(lib().lpq_quantize(_ptr(x), rows, cols, fmt, scaling, flags, seed, counter_offset, rht_seed, st,
-                              ctypes.byref(qt), _stream(stream)))
+                              ctypes.byref(qt), _stream()))
     return out
 
 
@@ -302,13 +336,15 @@ def amax(x, rht=False, rht_seed=0, out=None, rht_out=None, stream=None):
     """lpq_amax on a bf16 CUDA tensor x [rows, cols]: max |x| into `out` (and,
     with rht, the column-wise RHT amax into `rht_out`); returns (out, rht_out)
     as 1-element FP32 device tensors."""
+    if stream is not None:
+        return on_stream(stream, amax, x, rht, rht_seed, out, rht_out)
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.is_contiguous()
     if out is None:
         out = torch.empty(1, dtype=torch.float32, device=x.device)
     if rht and rht_out is None:
         rht_out = torch.empty(1, dtype=torch.float32, device=x.device)
     _check(lib().lpq_amax(_ptr(x), x.shape[0], x.shape[1], RHT_COLWISE if rht else 0, rht_seed, _ptr(out),
-                          _ptr(rht_out) if rht else None, _stream(stream)))
+                          _ptr(rht_out) if rht else None, _stream()))
     return out, (rht_out if rht else None)
 
 
@@ -320,17 +356,18 @@ def gemm(layout, a, b, c=None, out_fp32=False, stream=None, path=None):
     """lpq_gemm: C[m, n] = sum_k deq(a)[m, k] deq(b)[n, k]; a, b are Copy objects.
     `path` (a GEMM_PATHS name or a GemmOpts) selects a kernel path through
     lpq_gemm_ex; None is lpq_gemm's default."""
+    if stream is not None:
+        return on_stream(stream, gemm, layout, a, b, c, out_fp32, path=path)
     m, k, n = a.rows, a.cols, b.rows
     if c is None:
         c = torch.empty((m, n), dtype=torch.float32 if out_fp32 else torch.bfloat16, device=a.codes.device)
     va, vb = a.view(), b.view()
     if path is None:
-        _check(lib().lpq_gemm(layout, ctypes.byref(va), ctypes.byref(vb), _ptr(c), int(out_fp32), m, n, k,
-                              _stream(stream)))
+        _check(lib().lpq_gemm(layout, ctypes.byref(va), ctypes.byref(vb), _ptr(c), int(out_fp32), m, n, k, _stream()))
     else:
         opts = GEMM_PATHS[path] if isinstance(path, str) else path
         _check(lib().lpq_gemm_ex(layout, ctypes.byref(va), ctypes.byref(vb), _ptr(c), int(out_fp32), m, n, k,
-                                 ctypes.byref(opts), _stream(stream)))
+                                 ctypes.byref(opts), _stream()))
     return c
 
 
@@ -341,17 +378,13 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _TWO_TERMS = ctypes.byref(CeOpts(two_terms=1))
 
 
-def _new(like, stream, shape, dtype):
-    """A device buffer the call writes: on a stream other than the current one
-    its memory is not reused before that stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+def _new(like, shape, dtype):
+    """A device buffer the call writes, in the current stream's memory."""
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _stream_of(t, stream):
-    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
+def _stream_of(t):
+    return _raw_stream(t.get_device())
 
 
 def _ld(x, rows, cols):
@@ -392,26 +425,30 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, amax=None, out=None, stream=
     """lpq_layer_norm on a bf16 or fp32 CUDA tensor x [rows, cols]: returns
     (y, mean, rstd).  `amax` (one FP32, optional) receives max |y|, ready for
     quantize(..., lpq.GIVEN_AMAX)."""
+    if stream is not None:
+        return on_stream(stream, layer_norm, x, weight, bias, eps, amax, out)
     rows, cols = x.shape
     dtype = x.dtype
     assert dtype in _TYPES, "layer norm runs on bf16 and fp32"
     w_type = _check_params(cols, weight, bias)
     assert amax is None or _is_vector(amax, 1, _FP32), "amax must be one fp32"
     if out is None:
-        out, ldo = _new(x, stream, (rows, cols), dtype), cols
+        out, ldo = _new(x, (rows, cols), dtype), cols
     else:
         assert out.dtype is dtype and out.shape == x.shape, "out must be like x"
         ldo = _ld(out, rows, cols)
-    mean, rstd = _new(x, stream, rows, _FP32), _new(x, stream, rows, _FP32)
+    mean, rstd = _new(x, rows, _FP32), _new(x, rows, _FP32)
     _check(lib().lpq_layer_norm(x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype], _ptr(weight), _ptr(bias), w_type,
                                 rows, cols, eps, out.data_ptr(), ldo, mean.data_ptr(), rstd.data_ptr(), _ptr(amax),
-                                _stream_of(x, stream)))
+                                _stream_of(x)))
     return out, mean, rstd
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, param_grads=True, stream=None):
     """lpq_layer_norm_backward: returns (dx, dweight, dbias); the parameter
     gradients are FP32 (None, None without `param_grads`)."""
+    if stream is not None:
+        return on_stream(stream, layer_norm_backward, dy, x, mean, rstd, weight, param_grads)
     rows, cols = x.shape
     dtype = x.dtype
     assert dtype in _TYPES, "layer norm runs on bf16 and fp32"
@@ -419,16 +456,16 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, param_grads=True, stream
     w_type = _check_params(cols, weight, None)
     assert _is_vector(mean, rows, _FP32) and _is_vector(rstd, rows, _FP32), f"mean and rstd must be fp32 vectors of {rows}"
     L = lib()
-    dx = _new(x, stream, (rows, cols), dtype)
+    dx = _new(x, (rows, cols), dtype)
     dweight = dbias = ws = None
     need = 0
     if param_grads:
         need = _norm_workspace(rows, cols)
-        dweight, dbias = _new(x, stream, cols, _FP32), _new(x, stream, cols, _FP32)
-        ws = _new(x, stream, need, torch.uint8)
+        dweight, dbias = _new(x, cols, _FP32), _new(x, cols, _FP32)
+        ws = _new(x, need, torch.uint8)
     _check(L.lpq_layer_norm_backward(dy.data_ptr(), _ld(dy, rows, cols), x.data_ptr(), _ld(x, rows, cols), _TYPES[dtype],
                                      mean.data_ptr(), rstd.data_ptr(), _ptr(weight), w_type, rows, cols, dx.data_ptr(),
-                                     cols, _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream_of(x, stream)))
+                                     cols, _ptr(dweight), _ptr(dbias), _ptr(ws), need, _stream_of(x)))
     return dx, dweight, dbias
 
 
@@ -443,13 +480,15 @@ def linear_cross_entropy(h, w, labels, stream=None):
     """lpq_linear_ce: the softmax cross entropy of the logits h w^T for hidden
     states h [t, d] and vocabulary weights w [v, d] (bf16) against labels [t]
     (int64; outside 0 .. v - 1: no target, loss 0).  Returns (loss, lse) [t] FP32."""
+    if stream is not None:
+        return on_stream(stream, linear_cross_entropy, h, w, labels)
     t, d, v, ldh, ldw = _ce_args(h, w, labels)
     L = lib()
     need = _ce_workspace(t, v, d, 0, 0)
-    loss, lse = _new(h, stream, t, _FP32), _new(h, stream, t, _FP32)
-    ws = _new(h, stream, need, torch.uint8)
+    loss, lse = _new(h, t, _FP32), _new(h, t, _FP32)
+    ws = _new(h, need, torch.uint8)
     _check(L.lpq_linear_ce(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), t, v, d, loss.data_ptr(),
-                           lse.data_ptr(), ws.data_ptr(), need, _stream_of(h, stream)))
+                           lse.data_ptr(), ws.data_ptr(), need, _stream_of(h)))
     return loss, lse
 
 
@@ -458,27 +497,31 @@ def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, voca
     sum(dloss * loss) for dloss [t] FP32 and the forward's lse.  Where over 128
     rows have a target, the gradient of the logits is rounded to bf16, of FP32
     results too, unless `two_terms` asks for 16 bits of it."""
+    if stream is not None:
+        return on_stream(stream, linear_cross_entropy_backward, h, w, labels, lse, dloss, out_fp32, vocab_piece, two_terms=two_terms)
     t, d, v, ldh, ldw = _ce_args(h, w, labels)
     assert _is_vector(lse, t, _FP32) and _is_vector(dloss, t, _FP32), f"lse and dloss must be {t} fp32"
     L = lib()
     need = _ce_workspace(t, v, d, 2 if two_terms else 1, vocab_piece)
     dtype = _FP32 if out_fp32 else _BF16
-    dh, dw = _new(h, stream, (t, d), dtype), _new(h, stream, (v, d), dtype)
-    ws = _new(h, stream, need, torch.uint8)
+    dh, dw = _new(h, (t, d), dtype), _new(h, (v, d), dtype)
+    ws = _new(h, need, torch.uint8)
     _check(L.lpq_linear_ce_backward_ex(h.data_ptr(), ldh, w.data_ptr(), ldw, labels.data_ptr(), lse.data_ptr(),
                                        dloss.data_ptr(), t, v, d, dh.data_ptr(), dw.data_ptr(), int(out_fp32), vocab_piece,
-                                       ws.data_ptr(), need, _TWO_TERMS if two_terms else None, _stream_of(h, stream)))
+                                       ws.data_ptr(), need, _TWO_TERMS if two_terms else None, _stream_of(h)))
     return dh, dw
 
 
 def matvec(x, w, out_fp32=False, stream=None):
     """lpq_matvec: x [m, k] bf16 (a few tokens, not quantized) times the 4-bit
     weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n]."""
+    if stream is not None:
+        return on_stream(stream, matvec, x, w, out_fp32)
     m, k = x.shape
     assert x.dtype is _BF16 and k == w.cols, "x must be bf16 [m, k]"
     assert x.get_device() == w.codes.get_device(), "x must lie where the weights do"
-    y = _new(x, stream, (m, w.rows), _FP32 if out_fp32 else _BF16)
-    _check(lib().lpq_matvec(w.view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _stream_of(x, stream)))
+    y = _new(x, (m, w.rows), _FP32 if out_fp32 else _BF16)
+    _check(lib().lpq_matvec(w.view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _stream_of(x)))
     return y
 
 
