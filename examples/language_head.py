@@ -27,7 +27,7 @@ def batch(g, directions, tokens, noise=0.7):
 
 def train_and_decode(steps=60, fmt=lpq.NVFP4, d=256, v=1000, tokens=2048, seed=0, say=print):
     """Returns (first loss, last loss, share of words decoded right one by one,
-    the same through the prompt's GEMM or None)."""
+    the same through the prompt's GEMM)."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
     directions = torch.randn(v, d, generator=g, device="cuda")
@@ -50,10 +50,8 @@ def train_and_decode(steps=60, fmt=lpq.NVFP4, d=256, v=1000, tokens=2048, seed=0
     picked = torch.cat([head.logits(x[i:i + 1]).argmax(1) for i in range(x.shape[0])])
     right = (picked == words).float().mean().item()
     say(f"{lpq.FORMAT_NAMES[fmt]} weights, one token at a time: {100 * right:.1f}% of the next words")
-    prompt = None
-    if fmt == lpq.NVFP4:
-        prompt = (head.prompt_logits(x).argmax(1) == words).float().mean().item()
-        say(f"the same states as one prompt (NVFP4 activations): {100 * prompt:.1f}%")
+    prompt = (head.prompt_logits(x).argmax(1) == words).float().mean().item()
+    say(f"the same states as one prompt (activations in 4 bits too): {100 * prompt:.1f}%")
     return losses[0], losses[-1], right, prompt
 
 

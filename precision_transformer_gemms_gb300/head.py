@@ -47,7 +47,7 @@ class LanguageHead:
         return {"x": dx, "weight": dweight, "bias": dbias, "w": dw}
 
     def freeze(self, fmt=lpq.NVFP4, stream=None):
-        """Quantizes the vocabulary weights for decoding (NVFP4 or MXFP4)."""
+        """Quantizes the vocabulary weights for decoding (NVFP4, NVFP4_2D or MXFP4)."""
         freeze = lambda: lpq.quantize(self.w.contiguous(), fmt, lpq.ROWWISE).row
         self.frozen = freeze() if stream is None else lpq.on_stream(stream, freeze)
         return self
@@ -62,13 +62,15 @@ class LanguageHead:
         return lpq.matvec(h, self.frozen, out_fp32=True)
 
     def prompt_logits(self, x, stream=None):
-        """FP32 logits of many hidden states on the frozen NVFP4 weights through
-        the block-scaled GEMM: the norm's amax scales the quantizer, which then
-        runs without an amax pass of its own."""
+        """FP32 logits of many hidden states on the frozen weights through the
+        block-scaled GEMM, the states in NVFP4 (MXFP4 on MXFP4 weights).  The norm's
+        amax scales the NVFP4 quantizer, which then runs without an amax pass of its
+        own."""
         if stream is not None:
             return lpq.on_stream(stream, self.prompt_logits, x)
-        assert self.frozen is not None and self.frozen.fmt == lpq.NVFP4, "freeze() the head in NVFP4 first"
-        q = lpq.alloc(lpq.NVFP4, x.shape[0], x.shape[1], lpq.ROWWISE, device=x.device)
-        h, _, _ = lpq.layer_norm(x, self.weight, self.bias, eps=self.eps, amax=q.row.amax)
-        lpq.quantize(h, lpq.NVFP4, lpq.ROWWISE | lpq.GIVEN_AMAX, out=q)
+        assert self.frozen is not None, "freeze() the head first"
+        fmt, flags = (lpq.MXFP4, lpq.ROWWISE) if self.frozen.fmt == lpq.MXFP4 else (lpq.NVFP4, lpq.ROWWISE | lpq.GIVEN_AMAX)
+        q = lpq.alloc(fmt, x.shape[0], x.shape[1], lpq.ROWWISE, device=x.device)
+        h, _, _ = lpq.layer_norm(x, self.weight, self.bias, eps=self.eps, amax=q.row.amax)  # (MXFP4 has none)
+        lpq.quantize(h, fmt, flags, out=q)
         return lpq.gemm(lpq.FPROP, q.row, self.frozen, out_fp32=True)
