@@ -72,16 +72,15 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // dl's bf16 rounding.
 constexpr int kChunk = 16;
 
-// Where up to kFew rows have a target (counted on the device), or any number when
-// the caller asks for it, dl is stored as two terms, the value in bf16 and in bf16
-// what that leaves out.  In dw = dl^T h they
-// follow one another along K, against the same h; in dh = dl w too, unless t
-// itself is up to kFew: then they are the rows of the two CTAs (one of which had
-// none), whose sums are added in the end.  Reading w and storing dw bound the pass
-// up to there, so the terms cost little: 32000 x 4096, 33 or 128 rows, 198 and 192
-// us either way; at worst (one row) 209 -> 219 us.  Error of bf16 gradients of up
-// to 128 rows against 64 bits: 0.0020 to 0.0025 with one term, 0.0017 with two,
-// which is their own rounding.
+// Where up to kFew rows have a target (counted on the device) dl is stored as two
+// terms, the value in bf16 and in bf16 what that leaves out.  In dh = dl w they are
+// the rows of the two CTAs (one of which had none), whose sums are added in the
+// end; in dw = dl^T h they follow one another along K, against the same h.  Reading
+// w and storing dw bound the pass up to there, so the terms cost little: 32000 x
+// 4096, 33 or 128 rows, 198 and 192 us either way; at worst (one row) 209 -> 219
+// us.  Error of bf16 gradients of up to 128 rows against 64 bits: 0.0020 to 0.0025
+// with one term, 0.0017 with two, which is their own rounding.  A caller can ask
+// for two terms of any number of rows: they then follow one another in dh too.
 constexpr int kFew = kHalf;
 
 // What a kernel's epilogue makes of a tile.
@@ -131,8 +130,7 @@ struct CeTile {
   const float* scale;
   float* acc;  // [splits][M][N]
   int add;     // 1: add to acc
-  int few;     // t is up to kFew: a CTA of the pair takes a term of dl
-  int two_to;  // rows with a target up to which dl is in two terms
+  int two_terms;      // dl in two terms however many rows have a target
   int64_t rest_rows;  // rows that there is room for in dl's second terms
   int out_fp32;
 };
@@ -268,7 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
   __shared__ int extra_sh;
   const int rows = EPI == kStats ? 0 : *g.rows;
   const bool some_rows = EPI != kStats && rows < g.t;
-  const bool two = EPI != kStats && rows <= g.two_to;  // dl in two terms
+  const bool few = EPI != kStats && rows <= kFew;  // dl in two terms, in dh one for each CTA of a pair
+  const bool two = few || (EPI != kStats && g.two_terms);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       Product p = g.prod[i];
@@ -278,7 +277,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         p.items = p.tiles_m * p.tiles_n * p.splits;
       }
       if (p.k_rows) p.num_k = (rows + kStepK - 1) / kStepK;
-      if (EPI == kGrads && two && !(p.m_rows && g.few)) p.num_k *= 2;  // a term after the other
+      if (EPI == kGrads && few && p.m_rows) {
+        p.part = 1;
+        p.scatter = 0;
+      } else if (EPI == kGrads && two) {
+        p.num_k *= 2;  // a term after the other
+      }
       prod[i] = p;
     }
     const int left_over = prod[0].items % npairs;
@@ -302,7 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         int mt, nt, split, k0, k1;
         item_coords(w, p, mt, nt, split);
         split_range(split, p, k0, k1);
-        const bool terms = EPI == kGrads && g.few && p.m_rows;  // the CTAs take a term each
+        const bool terms = EPI == kGrads && few && p.m_rows;  // the CTAs take a term each
         const int32_t arow = mt * kTile + (terms ? 0 : (int32_t)rank * kHalf), brow = nt * kTile + (int32_t)rank * kHalf;
         // the first step with the second terms
         const int second = terms ? (rank ? 0 : INT_MAX) : EPI == kGrads && two ? p.num_k / 2 : INT_MAX;
@@ -395,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
       const Product& p = prod[which];
       int mt, nt, split;
       item_coords(w, p, mt, nt, split);
-      const bool terms = EPI != kStats && g.few && p.m_rows;  // (dl or dh: one tile down)
+      const bool terms = few && p.m_rows;  // (dl or dh: one tile down)
       const int64_t row = (int64_t)mt * kTile + (EPI == kGrads && terms ? 0 : rank * kHalf) + q * 32 + lane;
       const int64_t c0 = (int64_t)nt * kTile + half * kHalf;
       const bool live = row < p.M;
@@ -760,14 +764,17 @@ __global__ void __launch_bounds__(256) ce_rows_kernel(const float* dloss, const 
   }
 }
 
-// dh from its partial sums: the splits in order, times the scale, to the listed
-// rows.  A warp takes 32 vectors of a row.
-__global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int d4, int splits, const float* scale,
-                                                        const int* rows_p, const int* list, void* out, int fp32) {
+// dh from its partial sums: the splits in order (and of few rows both terms of
+// each), times the scale, to the listed rows.  A warp takes 32 vectors of a row.
+__global__ void __launch_bounds__(256) ce_finish_kernel(const float4* acc, int d4, int splits, int direct,
+                                                        const float* scale, const int* rows_p, const int* list, void* out,
+                                                        int fp32) {
   let_dependents_start();
   wait_for_stream();
   const float s = *scale;
   const int rows = *rows_p, lane = threadIdx.x & 31, runs = (d4 + 31) / 32;
+  if (rows <= kFew) splits *= 2;
+  else if (direct) return;
   const int64_t slab = (int64_t)rows * d4, items = (int64_t)rows * runs;
   for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < items; w += (int64_t)gridDim.x * 8) {
     const int64_t r = w / runs;
@@ -815,7 +822,8 @@ int extra_items(int64_t n0, double c0, int64_t n1, double c1, int pairs) {
 // once.  The estimate: the longest pair at 0.33 us a step, memory at 6.5 TB/s.
 int dh_splits(int64_t t, int64_t d, int64_t width, bool two_terms, int pairs) {
   const bool few = t <= kFew;
-  const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK) * (two_terms && !few ? 2 : 1);
+  const int64_t tiles = cdiv(t, kTile) * cdiv(d, kTile), steps = cdiv(width, kStepK);
+  const int64_t along = two_terms && !few ? 2 * steps : steps;  // (of few rows with a target: `steps` all the same)
   const int64_t n1 = cdiv(width, kTile) * cdiv(d, kTile);
   const int terms = few ? 2 : 1;  // slabs of dh's sums
   const double c1 = (double)((two_terms || few ? 2 : 1) * cdiv(t, kStepK)) + kItemStart;
@@ -823,7 +831,7 @@ int dh_splits(int64_t t, int64_t d, int64_t width, bool two_terms, int pairs) {
   double least = 0;
   for (int s = 1; s <= 64 && s <= steps; ++s) {
     const int64_t n0 = tiles * s;
-    const double c0 = (double)cdiv(steps, s) + kItemStart;
+    const double c0 = (double)cdiv(along, s) + kItemStart;
     const int64_t fewer = pairs - n0 % pairs, extra = extra_items(n0, c0, n1, c1, pairs);
     const double shared = (double)cdiv(n1 - extra * fewer, pairs) * c1;
     const double longest = std::max((double)cdiv(n0, pairs) * c0, (double)(n0 / pairs) * c0 + (double)extra * c1) + shared;
@@ -891,25 +899,23 @@ lpq_status run_pair(CeTile& g, const CeMaps& maps, cudaStream_t s) {
 struct BackwardPlan {
   int64_t piece, dl_ld;
   int splits;
-  bool few;     // t is up to kFew
-  bool direct;  // one piece, one split: dh is stored by its product
-  int two_to;   // rows with a target up to which dl is in two terms
+  bool direct;  // one piece, one split: dh is stored by its product (if over kFew rows have a target)
   int64_t rest_rows;  // of dl's second terms
   size_t list_at, h_at, dl_at, acc_at, bytes;
   BackwardPlan(int64_t t, int64_t v, int64_t d, int64_t asked, bool two_terms) {
-    few = t <= kFew;
-    two_to = two_terms ? INT_MAX : kFew;
-    rest_rows = std::min<int64_t>(t, two_to);
-    piece = piece_of(two_terms && !few ? 2 * t : t, v, asked);
+    const int64_t few = std::min<int64_t>(t, kFew);
+    rest_rows = two_terms ? t : few;
+    piece = piece_of(two_terms && t > kFew ? 2 * t : t, v, asked);
     dl_ld = std::min(piece, round_up(v, 8));
     // 76 pairs whatever the device has: the workspace and the results depend on the sizes alone
     splits = dh_splits(t, d, std::min(piece, v), two_terms, 76);
-    direct = splits == 1 && piece >= v && !few;
+    direct = splits == 1 && piece >= v && t > kFew;
     list_at = 256;
     h_at = list_at + (size_t)round_up(t * 4, 256);
     dl_at = h_at + (size_t)round_up(t * d * 2, 256);
     acc_at = dl_at + (size_t)round_up((t + rest_rows) * dl_ld * 2, 256);
-    bytes = acc_at + (direct ? 0 : (size_t)(few ? 2 * splits : splits) * (size_t)t * (size_t)d * 4);
+    // partial sums of all rows, and two of each of a few
+    bytes = acc_at + (size_t)std::max(direct ? 0 : t, 2 * few) * (size_t)splits * (size_t)d * 4;
   }
 };
 
@@ -957,8 +963,7 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
   base.scale = scale;
   base.acc = reinterpret_cast<float*>(a.workspace + plan.acc_at);
   base.out_fp32 = a.grads_fp32;
-  base.few = plan.few;
-  base.two_to = plan.two_to;
+  base.two_terms = a.two_terms;
   base.rest_rows = plan.rest_rows;
   const Operand h{a.h, a.ldh}, copied{a.workspace + plan.h_at, a.d}, l{dl, plan.dl_ld};
   lpq_status st = cuda_check(
@@ -1005,15 +1010,15 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t s) {
     }
     if ((st = set_product(g, maps, at, width, a.d, a.t, l, true, h, true, a.grads_fp32 ? nullptr : dw, a.d, 1)) != LPQ_OK) return st;
     if ((st = make_map(&maps.a2[at], l2.p, true, width, plan.rest_rows, l2.ld * 2, 64, kStepK)) != LPQ_OK) return st;
-    if (plan.few) g.prod[at].num_k *= 2;
+    if (a.t <= kFew) g.prod[at].num_k *= 2;
     g.prod[at].k_rows = 1;
     g.prod[at].out = dw;
     if ((st = run_pair<kGrads>(g, maps, s)) != LPQ_OK) return st;
   }
-  if (plan.direct) return LPQ_OK;
-  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(a.t * cdiv(a.d, 128), 8), (int64_t)device_sms() * 8);
+  const int64_t most = plan.direct ? kFew : a.t;  // rows to join
+  const unsigned grid = (unsigned)std::min<int64_t>(cdiv(most * cdiv(a.d, 128), 8), (int64_t)device_sms() * 8);
   return cuda_check(launch_dependent(ce_finish_kernel, grid, 256, 0, s, reinterpret_cast<const float4*>(base.acc),
-                                     (int)(a.d / 4), plan.few ? 2 * plan.splits : plan.splits, scale, rows, list, a.dh, a.grads_fp32),
+                                     (int)(a.d / 4), plan.splits, (int)plan.direct, scale, rows, list, a.dh, a.grads_fp32),
                     "cross entropy finish launch");
 }
 
