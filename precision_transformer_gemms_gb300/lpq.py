@@ -125,7 +125,7 @@ def lib():
         L.lpq_linear_ce.argtypes = [P, I64, P, I64, P, I64, I64, I64, P, P, P, SZ, P]
         L.lpq_linear_ce_backward.argtypes = [P, I64, P, I64, P, P, P, I64, I64, I64, P, P, I32, I64, P, SZ, P]
         L.lpq_linear_ce_backward_ex.argtypes = L.lpq_linear_ce_backward.argtypes[:-1] + [ctypes.POINTER(CeOpts), P]
-        L.lpq_matvec.argtypes = [ctypes.POINTER(QView), P, I64, I64, P, I32, P]
+        L.lpq_matvec.argtypes = [P, P, I64, I64, P, I32, P]  # (the view as a pointer or as its bytes)
         L.lpq_layer_shapes.argtypes = [ctypes.POINTER(TransformerCfg), ctypes.POINTER(GemmShape),
                                        ctypes.POINTER(I32)]
         L.lpq_last_error.restype = ctypes.c_char_p
@@ -250,11 +250,15 @@ class Copy:
         c.codes, c.scales, c.tensor_scale, c.amax = codes, scales, tensor_scale, None
         return c
 
-    def view(self):
+    def packed_view(self):
+        """The bytes of view()."""
         scales, scale, amax = self.scales, self.tensor_scale, self.amax
-        return QView.from_buffer_copy(_pack_view(
+        return _pack_view(
             self.codes.data_ptr(), 0 if scales is None else scales.data_ptr(), 0 if scale is None else scale.data_ptr(),
-            0 if amax is None else amax.data_ptr(), self.rows, self.cols, self.fmt, self.sf_layout, self.colwise, 0))
+            0 if amax is None else amax.data_ptr(), self.rows, self.cols, self.fmt, self.sf_layout, self.colwise, 0)
+
+    def view(self):
+        return QView.from_buffer_copy(self.packed_view())
 
     def codes_matrix(self):
         """Codes as a [rows, bytes per row] uint8 tensor (packed for NVFP4 and MXFP4)."""
@@ -519,9 +523,10 @@ def matvec(x, w, out_fp32=False, stream=None):
         return on_stream(stream, matvec, x, w, out_fp32)
     m, k = x.shape
     assert x.dtype is _BF16 and k == w.cols, "x must be bf16 [m, k]"
-    assert x.get_device() == w.codes.get_device(), "x must lie where the weights do"
-    y = _new(x, (m, w.rows), _FP32 if out_fp32 else _BF16)
-    _check(lib().lpq_matvec(w.view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _stream_of(x)))
+    device = x.get_device()
+    assert device == w.codes.get_device(), "x must lie where the weights do"
+    y = torch.empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device)
+    _check(lib().lpq_matvec(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _raw_stream(device)))
     return y
 
 
