@@ -332,7 +332,10 @@ lpq_status lpq_layer_norm_backward(const void *dy, int64_t lddy, const void *x, 
  * without target: its loss is 0 and its gradients vanish, its lse is computed.
  * Any t >= 0, v >= 1; d >= 8 a multiple of 8; ldh and ldw >= d multiples of 8;
  * h, w and the workspace 16-byte aligned.  A row whose logits hold a NaN has
- * lse NaN; one with a +infinity has lse +infinity. */
+ * lse NaN; one with a +infinity has lse +infinity.  The exponentials are taken of
+ * differences from the row's largest logit, the loss too: it is as near for a
+ * confident token (2^-21 of 1 + loss, beside the logits' own error) as for others,
+ * and never negative. */
 lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels, int64_t t,
                          int64_t v, int64_t d, float *loss, float *lse, void *workspace, size_t workspace_bytes,
                          lpq_stream_t stream);
@@ -348,8 +351,9 @@ lpq_status lpq_linear_ce(const void *h, int64_t ldh, const void *w, int64_t ldw,
  * They are divided by max |dloss| and rounded to bf16, which the tensor cores
  * read (where up to 128 rows have a target: held as the sum of two bf16 terms;
  * beyond, FP32 gradients too carry that rounding, 2^-9 of each value, unless two
- * terms are asked for by lpq_linear_ce_backward_ex); all sums are FP32 and the factor is put back before the final rounding.  The
- * same inputs give the same bits.  0 rows give dw = 0. */
+ * terms are asked for by lpq_linear_ce_backward_ex); all sums are FP32 and the
+ * factor is put back before the final rounding.  The same inputs give the same
+ * bits.  0 rows give dw = 0.  dh and dw must be 16-byte aligned. */
 lpq_status lpq_linear_ce_backward(const void *h, int64_t ldh, const void *w, int64_t ldw, const int64_t *labels,
                                   const float *lse, const float *dloss, int64_t t, int64_t v, int64_t d, void *dh,
                                   void *dw, int32_t grads_fp32, int64_t vocab_piece, void *workspace,
@@ -381,9 +385,9 @@ lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t back
  * w is a row-wise copy [n, k] of NVFP4, NVFP4_2D or MXFP4 as lpq_quantize
  * writes it (either scale layout; codes 16-byte aligned, scales 4-byte
  * aligned), x [m, k] is bf16 and not quantized (rows ldx elements apart, ldx
- * a multiple of 8, 16-byte aligned), y [m, n] contiguous bf16 or FP32.  Codes
- * times scales are exact, products are summed in FP32 and the tensor scale is
- * applied to the sum.  k must be a multiple of 32, at most 2^19 (2^16 with
+ * a multiple of 8, 16-byte aligned), y [m, n] contiguous bf16 or FP32, 16-byte
+ * aligned.  Codes times scales are exact (a code of zero is 0 beside any finite
+ * scale), products are summed in FP32 and the tensor scale is applied to the sum.  k must be a multiple of 32, at most 2^19 (2^16 with
  * LPQ_SF_PLAIN scales); m and n are arbitrary
  * (>= 0), but m is meant to be small: the weights are read once per 8 tokens. */
 lpq_status lpq_matvec(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,

@@ -14,12 +14,12 @@
 // in dl^T h) is read as it lies, as an MN-major operand: no transposed copies.
 //
 // The tensor cores bound it: 2 t v d operations forward, 6 t v d backward (the
-// logits again).  Measured: 4096 x 4096 x 19456 forward 343 us and dl 336 us, dh
-// and dw 700 us together, the tensor pipe 89 to 96% active, 1.87 to 1.94
+// logits again).  Measured: 4096 x 4096 x 19456 forward 327 us and dl 343 us, dh
+// and dw 670 us together, the tensor pipe 86 to 95% active, 1.90 to 2.00
 // PFLOP/s at full clocks (cuBLAS 1.91 burst, 1.71 sustained under the power
-// cap); in a loop, 7936 x 4096 x 32000 forward 1.22 ms (1.70 PFLOP/s) and
+// cap); in a loop, 7936 x 4096 x 32000 forward 1.19 ms (1.75 PFLOP/s) and
 // backward 3.65 ms (1.71).  With d = 1024 a tile's result weighs on the port
-// that feeds it: 1001 x 1024 x 50001 backward 236 us (1.30).
+// that feeds it: 1001 x 1024 x 50001 backward 235 us (1.31).
 //
 // The backward pass works on the rows that have a target alone: they are
 // counted and listed on the device, their hidden states copied together where
@@ -66,7 +66,8 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // a long sum drifts towards zero: measured 2.5e-6 of the loss over d = 4096.
 // The logits are therefore summed in TMEM over kChunk steps (1024 values) at a
 // time and across chunks in the epilogue's registers: 2% of the time at 7936 x
-// 4096 x 32000, a fifth to an eighth of the drift.  Both passes do so: exp(l -
+// 4096 x 32000 (3% backward at 1001 x 1024 x 50001), a fifth to an eighth of the
+// drift.  Both passes do so: exp(l -
 // lse) takes the bits that lse was made of, and where p is near 1 its p - 1 is
 // not the difference of two drifts.  The gradients' sums are cut in full, below
 // dl's bf16 rounding.
@@ -77,10 +78,11 @@ constexpr int kChunk = 16;
 // the rows of the two CTAs (one of which had none), whose sums are added in the
 // end; in dw = dl^T h they follow one another along K, against the same h.  Reading
 // w and storing dw bound the pass up to there, so the terms cost little: 32000 x
-// 4096, 33 or 128 rows, 198 and 192 us either way; at worst (one row) 209 -> 219
-// us.  Error of bf16 gradients of up to 128 rows against 64 bits: 0.0020 to 0.0025
-// with one term, 0.0017 with two, which is their own rounding.  A caller can ask
-// for two terms of any number of rows: they then follow one another in dh too.
+// 4096, 1, 33 or 128 rows 196, 200 and 193 us; 20 of 512 rows 235 us (224 with one
+// term).  Error of bf16 gradients of up to 128 rows against 64 bits: 0.0020 to
+// 0.0025 with one term, 0.0017 with two, which is their own rounding.  A caller can
+// ask for two terms of any number of rows: they then follow one another in dh too
+// (7936 x 4096 x 32000 3.6 -> 6.3 ms).
 constexpr int kFew = kHalf;
 
 // What a kernel's epilogue makes of a tile.
@@ -847,7 +849,7 @@ int dh_splits(int64_t t, int64_t d, int64_t width, bool two_terms, int pairs) {
 // Rows of A in a load.  A K-major A of up to kFew rows takes those alone, in the
 // even CTA (or a term in each): a load of rows that are not there costs more
 // than one of rows that are.  What the rest of the stage holds enters rows that
-// are not stored.  Forward, one row: 32000 x 4096 90 -> 55 us, 131072 x 1024
+// are not stored.  Forward, one row: 32000 x 4096 90 -> 54 us, 131072 x 1024
 // 80 -> 53 us; from 64 rows on no difference.
 int a_box(bool a_mn, int64_t M) { return !a_mn && M <= kFew ? (int)round_up(M, 8) : kHalf; }
 

@@ -13,12 +13,21 @@
 //   backward  15872 x 4096 66.5 us (86%), 63488 x 4096 231 us (99%), 65536 x 1024 70 us (85%),
 //             8192 x 16384 196 us (60%: two passes over the ring, one CTA per SM)
 // What is left at 15872 x 4096 is the start and the end of a 40 us kernel, and
-// backward the join of its 152 parts (5 us).  Unaligned rows go element by
-// element, the next row loaded to registers while this one is worked on: 15872 x 4095
-// bf16 73 us forward (52%), 116 us backward (50%), bound by the count of 2-byte loads;
-// 15872 x 2047 FP32 45 us (84%) and 78 us (74%).  Rows beyond 16384 columns are
-// read again from the L2: 4096 x 32768 125 us forward (63%), 273 us backward (43%:
-// the parameter gradients are a launch of their own).
+// backward the join of its 152 parts (5 us).  FP32 rows of 8193 to 16384 columns
+// leave the backward ring room for one row, so that loads and work take turns:
+// 4000 x 16384 90 us forward (86%), 164 us backward (71%).
+//
+// Unaligned rows go element by element, forward and up to 4096 columns backward
+// with the next row loaded to registers while this one is worked on: 15872 x 4095
+// bf16 79 us forward (49%), 115 us backward (50%), bound by the count of 2-byte
+// loads; 15872 x 2047 FP32 45 us (85%) and 78 us (74%).  Wider ones are loaded
+// backward when their turn comes, and beyond 8192 columns spill: 4000 x 8191 bf16
+// 80 and 124 us (24%, 23%), FP32 51 and 214 (75%, 27%); 4000 x 16383 bf16 157 and
+// 355 us (25%, 16%), FP32 236 and 498 (33%, 23%).
+//
+// Rows beyond 16384 columns are read again from the L2: 4096 x 32768 137 us
+// forward (58%), 277 us backward (43%: the parameter gradients are a launch of
+// their own).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -127,7 +136,8 @@ struct RowGroup {
 
 // Rows in flight for a ring stage of this many bytes.  Forward, with several
 // CTAs per SM: two or three (four are slower: 182 us instead of 174 at 63488 x
-// 4096 bf16).  Backward, one CTA per SM: four while they fit.
+// 4096 bf16).  Backward, one CTA per SM: four while they fit, down to one of FP32
+// rows beyond 8192 columns.
 template <bool BACKWARD>
 constexpr int rows_ahead(int stage) {
   constexpr int most = BACKWARD ? 196608 : 24576;
