@@ -67,10 +67,9 @@ static_assert(kStages == 6 && kNacc * kTile <= 512, "shared memory and TMEM budg
 // The logits are therefore summed in TMEM over kChunk steps (1024 values) at a
 // time and across chunks in the epilogue's registers: 2% of the time at 7936 x
 // 4096 x 32000 (3% backward at 1001 x 1024 x 50001), a fifth to an eighth of the
-// drift.  Both passes do so: exp(l -
-// lse) takes the bits that lse was made of, and where p is near 1 its p - 1 is
-// not the difference of two drifts.  The gradients' sums are cut in full, below
-// dl's bf16 rounding.
+// drift.  Both passes do so: exp(l - lse) takes the bits that lse was made of, and
+// where p is near 1 its p - 1 is not the difference of two drifts.  The gradients'
+// sums are cut in full, which stays below dl's bf16 rounding.
 constexpr int kChunk = 16;
 
 // Where up to kFew rows have a target (counted on the device) dl is stored as two
