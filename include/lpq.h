@@ -393,6 +393,93 @@ lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t back
 lpq_status lpq_matvec(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,
                       lpq_stream_t stream);
 
+/* RMS norm of every query and key head with the position rotation, behind the
+ * QKV projection.  x [rows, >= (q_heads + k_heads) * head_dim] holds a token's
+ * query heads, then its key heads (rows ldx elements apart; what lies behind the
+ * key heads is not touched).  Of every head, with w the query or key weight:
+ *   n = x * rstd * w,  rstd = 1 / sqrt(sum(x^2) / head_dim + eps),
+ *   pair i < rotary_dim / 2 turned by a = positions[row] * freqs[i]:
+ *     (y1, y2) = (n1 cos a - n2 sin a, n2 cos a + n1 sin a).
+ *   type         of x and y; w_type that of the weights.
+ *   q_weight, k_weight  [head_dim], one for all heads; NULL = 1.
+ *   positions    [rows] int64, device.
+ *   freqs        [rotary_dim / 2] radians per position, HOST memory, read before
+ *                the call returns (base^(-2 i / rotary_dim) by custom); finite.
+ *   interleaved  0: the pairs are values i and i + rotary_dim / 2 of the head;
+ *                1: values 2 i and 2 i + 1.  Values from rotary_dim on are not
+ *                turned.
+ *   y            rows ldy elements apart, same heads; y may be x itself (then
+ *                ldy = ldx), else they must not overlap.
+ * Angles are reduced modulo a turn in 64 bits: off by at most 2^-26 turns (1e-7
+ * radians) and 2^-52 |position freqs[i]|; any int64 position is valid.
+ * Statistics are FP32 and y is rounded once.  head_dim is even, 2 ..
+ * 512; rotary_dim even, 0 .. head_dim; any rows, heads >= 0; eps >= 0.  Heads
+ * and a rotary_dim of a multiple of 16 values, with 16-byte aligned rows, take
+ * 16-byte accesses; others go value by value. */
+lpq_status lpq_qk_norm_rope(const void *x, int64_t ldx, int32_t type, int64_t rows, int64_t q_heads, int64_t k_heads,
+                            int64_t head_dim, const void *q_weight, const void *k_weight, int32_t w_type,
+                            const int64_t *positions, const double *freqs, int64_t rotary_dim, int32_t interleaved,
+                            float eps, void *y, int64_t ldy, lpq_stream_t stream);
+
+/* Bytes of lpq_qk_norm_rope_backward's workspace (16-byte aligned device memory).
+ * Host-only. */
+lpq_status lpq_qk_norm_rope_workspace(int64_t rows, int64_t head_dim, size_t *bytes);
+
+/* Backward pass of lpq_qk_norm_rope from dy and the forward's x.  With g = dy
+ * turned by -a:
+ *   dx = rstd * (g * w - x * rstd^2 * sum(g * w * x) / head_dim),
+ *   dq_weight = sum over rows and query heads of g * x * rstd, dk_weight over the
+ *   key heads (FP32; either may be NULL, no workspace is needed without both).
+ * dx may be dy or x itself (with its leading dimension), else they must not
+ * overlap.  The sums are split into parts by sizes and joined in a fixed order:
+ * the same inputs give the same bits.  0 rows or heads give zero gradients. */
+lpq_status lpq_qk_norm_rope_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t type, int64_t rows,
+                                     int64_t q_heads, int64_t k_heads, int64_t head_dim, const void *q_weight,
+                                     const void *k_weight, int32_t w_type, const int64_t *positions, const double *freqs,
+                                     int64_t rotary_dim, int32_t interleaved, float eps, void *dx, int64_t lddx,
+                                     float *dq_weight, float *dk_weight, void *workspace, size_t workspace_bytes,
+                                     lpq_stream_t stream);
+
+/* What changes the logits of the next words.  Device pointers; any group may be
+ * NULL, which leaves its step out.
+ *   history      [rows, max_len] int64 words of every request's context, rows
+ *                ld_history elements apart: lengths[row] of them (taken within 0 ..
+ *                max_len), of which the first prompt[row] (NULL: 0) are the prompt
+ *                and the others the answer so far.  Words outside 0 .. v - 1 count
+ *                for nothing.  lengths goes with it.
+ *   repetition   [rows]: a word of the context has its logit divided by r where it
+ *                is positive and multiplied by r elsewhere.
+ *   frequency, presence  [rows]: a word that stands c > 0 times in the answer loses
+ *                frequency * c + presence.
+ *   bias_offsets [rows + 1], bias_words [bias_count] int64, bias_values
+ *                [bias_count]: entries bias_offsets[row] .. bias_offsets[row + 1] - 1
+ *                (taken within 0 .. bias_count) are added to their words' logits,
+ *                those of one word in the list's order.
+ *   allowed      [rows, ceil(v / 32)] int32, rows ld_allowed elements apart: bit j %
+ *                32 of element j / 32 says whether word j may follow; the others get
+ *                -infinity, whatever they held (a row without a bit: all of them).
+ * The penalties need a history; the history has no effect without them. */
+typedef struct {
+  const int64_t *history;
+  int64_t ld_history, max_len;
+  const int64_t *lengths, *prompt;
+  const float *repetition, *frequency, *presence;
+  const int64_t *bias_offsets, *bias_words;
+  const float *bias_values;
+  int64_t bias_count;
+  const int32_t *allowed;
+  int64_t ld_allowed;
+} lpq_logit_controls;
+
+/* out = the logits [rows, v] (type lpq_type, rows ld elements apart) under the
+ * controls, in the order repetition, frequency and presence, bias, mask; FP32
+ * arithmetic, rounded once.  out has the logits' type, rows ldo elements apart, and
+ * may be the logits themselves (then ldo = ld), else they must not overlap.  Any
+ * rows and v >= 0, v at most 2^31; rows that begin equally far from a 16-byte
+ * boundary on both sides take 16-byte accesses. */
+lpq_status lpq_adjust_logits(const void *logits, int64_t ld, int32_t type, int64_t rows, int64_t v,
+                             const lpq_logit_controls *controls, void *out, int64_t ldo, lpq_stream_t stream);
+
 /* Transformer configuration ([TE] "model configuration and training input"). */
 typedef struct {
   int64_t hidden, intermediate, heads, layers, micro_batch, seq;

@@ -524,6 +524,126 @@ lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m,
   return launch_matvec(w, x, ldx, m, y, y_is_fp32, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+// What both directions of the head norm check; fills the shared arguments.
+lpq_status check_qk(QkArgs& a, const void* x, int64_t ldx, int32_t type, int64_t rows, int64_t q_heads, int64_t k_heads,
+                    int64_t head_dim, const void* q_weight, const void* k_weight, int32_t w_type, const int64_t* positions,
+                    const double* freqs, int64_t rotary_dim, int32_t interleaved, float eps) {
+  if (!valid_type(type)) return set_error(LPQ_ERR_INVALID_ARG, "type %d", type);
+  if (!valid_type(w_type)) return set_error(LPQ_ERR_INVALID_ARG, "w_type %d", w_type);
+  if (interleaved < 0 || interleaved > 1) return set_error(LPQ_ERR_INVALID_ARG, "interleaved %d", interleaved);
+  if (!(eps >= 0.f)) return set_error(LPQ_ERR_INVALID_ARG, "eps must be at least 0");
+  if (head_dim < 2 || head_dim > kQkMaxDim || head_dim % 2)
+    return set_error(LPQ_ERR_SHAPE, "head_dim %lld must be even, 2 to %d", (long long)head_dim, kQkMaxDim);
+  if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2)
+    return set_error(LPQ_ERR_SHAPE, "rotary_dim %lld must be even, 0 to head_dim", (long long)rotary_dim);
+  const int64_t most = (int64_t)1 << 20;
+  if (rows < 0 || q_heads < 0 || k_heads < 0 || rows > (int64_t)1 << 40 || q_heads > most || k_heads > most)
+    return set_error(LPQ_ERR_SHAPE, "rows %lld, heads %lld and %lld", (long long)rows, (long long)q_heads, (long long)k_heads);
+  const int64_t cols = (q_heads + k_heads) * head_dim;
+  lpq_status st = check_matrix(cols ? x : &a, "x", ldx, rows, cols, type_bytes(type));
+  if (st != LPQ_OK) return st;
+  if (!aligned_to(q_weight, type_bytes(w_type)) || !aligned_to(k_weight, type_bytes(w_type)))
+    return set_error(LPQ_ERR_ALIGN, "q_weight or k_weight not aligned to its elements");
+  if (rows > 0 && cols > 0 && !positions) return set_error(LPQ_ERR_INVALID_ARG, "positions is NULL");
+  if (!aligned_to(positions, 8)) return set_error(LPQ_ERR_ALIGN, "positions not 8-byte aligned");
+  if (rotary_dim > 0 && !freqs) return set_error(LPQ_ERR_INVALID_ARG, "freqs is NULL");
+  for (int64_t i = 0; i < rotary_dim / 2; ++i)
+    if (!(freqs[i] - freqs[i] == 0)) return set_error(LPQ_ERR_INVALID_ARG, "freqs[%lld] is not finite", (long long)i);
+  a.x = x; a.ldx = ldx; a.rows = rows; a.q_heads = (int)q_heads; a.k_heads = (int)k_heads; a.dim = (int)head_dim;
+  a.q_weight = q_weight; a.k_weight = k_weight; a.w_type = w_type; a.positions = positions; a.freqs = freqs;
+  a.rotary = (int)rotary_dim; a.neighbours = interleaved != 0; a.eps = eps;
+  return LPQ_OK;
+}
+}  // namespace
+
+lpq_status lpq_qk_norm_rope(const void* x, int64_t ldx, int32_t type, int64_t rows, int64_t q_heads, int64_t k_heads,
+                            int64_t head_dim, const void* q_weight, const void* k_weight, int32_t w_type,
+                            const int64_t* positions, const double* freqs, int64_t rotary_dim, int32_t interleaved, float eps,
+                            void* y, int64_t ldy, lpq_stream_t stream) {
+  QkArgs a{};
+  lpq_status st = check_qk(a, x, ldx, type, rows, q_heads, k_heads, head_dim, q_weight, k_weight, w_type, positions, freqs,
+                           rotary_dim, interleaved, eps);
+  if (st != LPQ_OK) return st;
+  const int64_t cols = (q_heads + k_heads) * head_dim;
+  if ((st = check_matrix(cols ? y : &a, "y", ldy, rows, cols, type_bytes(type))) != LPQ_OK) return st;
+  if (y == x && ldy != ldx && rows > 1 && cols > 0) return set_error(LPQ_ERR_SHAPE, "y in x's place needs x's leading dimension");
+  if ((st = check_arch()) != LPQ_OK) return st;
+  a.out = y; a.ldo = ldy;
+  return launch_qk_norm(a, type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_qk_norm_rope_workspace(int64_t rows, int64_t head_dim, size_t* bytes) {
+  if (!bytes) return set_error(LPQ_ERR_INVALID_ARG, "NULL output pointer");
+  if (rows < 0 || head_dim < 2 || head_dim > kQkMaxDim)
+    return set_error(LPQ_ERR_SHAPE, "rows %lld, head_dim %lld", (long long)rows, (long long)head_dim);
+  *bytes = qk_norm_workspace(rows, head_dim);
+  return LPQ_OK;
+}
+
+lpq_status lpq_qk_norm_rope_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, int32_t type, int64_t rows,
+                                     int64_t q_heads, int64_t k_heads, int64_t head_dim, const void* q_weight,
+                                     const void* k_weight, int32_t w_type, const int64_t* positions, const double* freqs,
+                                     int64_t rotary_dim, int32_t interleaved, float eps, void* dx, int64_t lddx,
+                                     float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                     lpq_stream_t stream) {
+  QkArgs a{};
+  lpq_status st = check_qk(a, x, ldx, type, rows, q_heads, k_heads, head_dim, q_weight, k_weight, w_type, positions, freqs,
+                           rotary_dim, interleaved, eps);
+  if (st != LPQ_OK) return st;
+  const int64_t cols = (q_heads + k_heads) * head_dim;
+  if ((st = check_matrix(cols ? dy : &a, "dy", lddy, rows, cols, type_bytes(type))) != LPQ_OK) return st;
+  if ((st = check_matrix(cols ? dx : &a, "dx", lddx, rows, cols, type_bytes(type))) != LPQ_OK) return st;
+  if (rows > 1 && cols > 0 && ((dx == x && lddx != ldx) || (dx == dy && lddx != lddy)))
+    return set_error(LPQ_ERR_SHAPE, "dx in another's place needs its leading dimension");
+  if (!aligned_to(dq_weight, 4) || !aligned_to(dk_weight, 4))
+    return set_error(LPQ_ERR_ALIGN, "dq_weight or dk_weight not 4-byte aligned");
+  if (dq_weight || dk_weight)
+    if ((st = check_workspace(workspace, workspace_bytes, qk_norm_workspace(rows, head_dim))) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  a.dy = dy; a.lddy = lddy; a.out = dx; a.ldo = lddx; a.dq_weight = dq_weight; a.dk_weight = dk_weight;
+  a.parts = static_cast<float*>(workspace);
+  return launch_qk_norm_backward(a, type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_adjust_logits(const void* logits, int64_t ld, int32_t type, int64_t rows, int64_t v,
+                             const lpq_logit_controls* controls, void* out, int64_t ldo, lpq_stream_t stream) {
+  if (!controls) return set_error(LPQ_ERR_INVALID_ARG, "controls is NULL");
+  const lpq_logit_controls& c = *controls;
+  if (!valid_type(type)) return set_error(LPQ_ERR_INVALID_ARG, "type %d", type);
+  if (rows < 0 || v < 0 || rows > (int64_t)1 << 30 || v > (int64_t)1 << 31)
+    return set_error(LPQ_ERR_SHAPE, "rows %lld, v %lld", (long long)rows, (long long)v);
+  const bool any = rows > 0 && v > 0;
+  lpq_status st = check_matrix(any ? logits : &c, "logits", ld, rows, v, type_bytes(type));
+  if (st != LPQ_OK) return st;
+  if ((st = check_matrix(any ? out : &c, "out", ldo, rows, v, type_bytes(type))) != LPQ_OK) return st;
+  if (out == logits && rows > 1 && v > 0 && ld != ldo) return set_error(LPQ_ERR_SHAPE, "out in the logits' place needs their leading dimension");
+  if (c.history) {
+    if (c.max_len < 0 || c.ld_history < c.max_len)
+      return set_error(LPQ_ERR_SHAPE, "history of %lld in rows of %lld", (long long)c.max_len, (long long)c.ld_history);
+    if (!c.lengths) return set_error(LPQ_ERR_INVALID_ARG, "lengths is NULL");
+  } else if (c.repetition || c.frequency || c.presence) {
+    return set_error(LPQ_ERR_INVALID_ARG, "penalties without a history");
+  }
+  if (c.bias_words) {
+    if (!c.bias_offsets || !c.bias_values) return set_error(LPQ_ERR_INVALID_ARG, "bias_offsets or bias_values is NULL");
+    if (c.bias_count < 0) return set_error(LPQ_ERR_SHAPE, "bias_count %lld", (long long)c.bias_count);
+  }
+  if (c.allowed && c.ld_allowed < (v + 31) / 32)
+    return set_error(LPQ_ERR_SHAPE, "ld_allowed %lld below %lld", (long long)c.ld_allowed, (long long)((v + 31) / 32));
+  for (const void* p : {(const void*)c.history, (const void*)c.lengths, (const void*)c.prompt, (const void*)c.bias_offsets,
+                        (const void*)c.bias_words})
+    if (!aligned_to(p, 8)) return set_error(LPQ_ERR_ALIGN, "an int64 array is not 8-byte aligned");
+  for (const void* p : {(const void*)c.repetition, (const void*)c.frequency, (const void*)c.presence, (const void*)c.bias_values,
+                        (const void*)c.allowed})
+    if (!aligned_to(p, 4)) return set_error(LPQ_ERR_ALIGN, "a 4-byte array is not 4-byte aligned");
+  if ((st = check_arch()) != LPQ_OK) return st;
+  LogitsArgs a{};
+  a.logits = logits; a.out = out; a.ld = ld; a.ldo = ldo; a.rows = rows; a.v = v; a.c = c;
+  if (!c.repetition && !c.frequency && !c.presence) a.c.history = nullptr;
+  return launch_adjust_logits(a, type, reinterpret_cast<cudaStream_t>(stream));
+}
+
 lpq_status lpq_layer_shapes(const lpq_transformer_cfg* cfg, lpq_gemm_shape out[12], int32_t* count) {
   if (!cfg || !out || !count) return set_error(LPQ_ERR_INVALID_ARG, "NULL argument");
   if (cfg->hidden <= 0 || cfg->intermediate <= 0 || cfg->micro_batch <= 0 || cfg->seq <= 0)

@@ -104,6 +104,41 @@ lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t stream);
 lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
                          cudaStream_t stream);
 
+// Head norm and rotation launchers (qknorm.cu).  Arguments validated.
+constexpr int kQkMaxDim = 512;  // values of a head
+struct QkArgs {
+  const void* x;
+  const void* dy;  // backward only
+  void* out;       // y or dx
+  int64_t ldx, lddy, ldo;
+  int64_t rows;
+  int q_heads, k_heads, dim;
+  const void* q_weight;  // may be NULL
+  const void* k_weight;
+  int32_t w_type;
+  const int64_t* positions;
+  const double* freqs;  // host, [rotary / 2]
+  int rotary;
+  bool neighbours;
+  float eps;
+  float* dq_weight;  // backward; may be NULL
+  float* dk_weight;
+  float* parts;  // backward workspace
+};
+size_t qk_norm_workspace(int64_t rows, int64_t dim);
+lpq_status launch_qk_norm(const QkArgs& a, int32_t type, cudaStream_t stream);
+lpq_status launch_qk_norm_backward(const QkArgs& a, int32_t type, cudaStream_t stream);
+
+// Logit controls launcher (logits.cu).  Arguments validated.
+struct LogitsArgs {
+  const void* logits;
+  void* out;
+  int64_t ld, ldo;
+  int64_t rows, v;
+  lpq_logit_controls c;
+};
+lpq_status launch_adjust_logits(const LogitsArgs& a, int32_t type, cudaStream_t stream);
+
 // Device error word (gemm.cu owns it).
 lpq_status device_error_word(int** word);
 lpq_status read_and_clear_device_error(cudaStream_t stream, int32_t* code);

@@ -52,14 +52,16 @@ class LanguageHead:
         self.frozen = freeze() if stream is None else lpq.on_stream(stream, freeze)
         return self
 
-    def logits(self, x, stream=None):
+    def logits(self, x, stream=None, controls=None):
         """FP32 logits [t, v] of a few hidden states x [t, d] on the frozen
-        weights; the activations stay bf16."""
+        weights; the activations stay bf16.  `controls`: keywords of
+        lpq.adjust_logits (penalties, biases, mask), applied in place."""
         if stream is not None:
-            return lpq.on_stream(stream, self.logits, x)
+            return lpq.on_stream(stream, self.logits, x, controls=controls)
         assert self.frozen is not None, "freeze() the head first"
         h, _, _ = lpq.layer_norm(x, self.weight, self.bias, eps=self.eps)
-        return lpq.matvec(h, self.frozen, out_fp32=True)
+        logits = lpq.matvec(h, self.frozen, out_fp32=True)
+        return logits if controls is None else lpq.adjust_logits(logits, **controls, out=logits)
 
     def prompt_logits(self, x, stream=None):
         """FP32 logits of many hidden states on the frozen weights through the

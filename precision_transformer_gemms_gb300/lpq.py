@@ -85,6 +85,14 @@ GEMM_PATHS = {
 }
 
 
+class LogitControls(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("ld_history", ctypes.c_int64), ("max_len", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("prompt", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p),
+                ("bias_words", ctypes.c_void_p), ("bias_values", ctypes.c_void_p), ("bias_count", ctypes.c_int64),
+                ("allowed", ctypes.c_void_p), ("ld_allowed", ctypes.c_int64)]
+
+
 class TransformerCfg(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int64), ("intermediate", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("layers", ctypes.c_int64), ("micro_batch", ctypes.c_int64), ("seq", ctypes.c_int64)]
@@ -126,6 +134,12 @@ def lib():
         L.lpq_linear_ce_backward.argtypes = [P, I64, P, I64, P, P, P, I64, I64, I64, P, P, I32, I64, P, SZ, P]
         L.lpq_linear_ce_backward_ex.argtypes = L.lpq_linear_ce_backward.argtypes[:-1] + [ctypes.POINTER(CeOpts), P]
         L.lpq_matvec.argtypes = [P, P, I64, I64, P, I32, P]  # (the view as a pointer or as its bytes)
+        PD = ctypes.POINTER(ctypes.c_double)
+        L.lpq_qk_norm_rope.argtypes = [P, I64, I32, I64, I64, I64, I64, P, P, I32, P, PD, I64, I32, F, P, I64, P]
+        L.lpq_qk_norm_rope_workspace.argtypes = [I64, I64, PSZ]
+        L.lpq_qk_norm_rope_backward.argtypes = [P, I64, P, I64, I32, I64, I64, I64, I64, P, P, I32, P, PD, I64, I32, F, P, I64,
+                                                P, P, P, SZ, P]
+        L.lpq_adjust_logits.argtypes = [P, I64, I32, I64, I64, P, P, I64, P]  # (the controls as their bytes)
         L.lpq_layer_shapes.argtypes = [ctypes.POINTER(TransformerCfg), ctypes.POINTER(GemmShape),
                                        ctypes.POINTER(I32)]
         L.lpq_last_error.restype = ctypes.c_char_p
@@ -137,7 +151,8 @@ def lib():
         for name in ("lpq_copy_bytes", "lpq_quantize", "lpq_scale_update", "lpq_gemm", "lpq_gemm_ex", "lpq_amax", "lpq_layer_shapes",
                      "lpq_device_status", "lpq_selftest_wait", "lpq_mma_peak", "lpq_selftest_arith", "lpq_layer_norm",
                      "lpq_layer_norm_workspace", "lpq_layer_norm_backward", "lpq_linear_ce_workspace", "lpq_linear_ce",
-                     "lpq_linear_ce_backward", "lpq_linear_ce_backward_ex", "lpq_matvec"):
+                     "lpq_linear_ce_backward", "lpq_linear_ce_backward_ex", "lpq_matvec", "lpq_qk_norm_rope",
+                     "lpq_qk_norm_rope_workspace", "lpq_qk_norm_rope_backward", "lpq_adjust_logits"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -528,6 +543,160 @@ def matvec(x, w, out_fp32=False, stream=None):
     y = torch.empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device)
     _check(lib().lpq_matvec(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _raw_stream(device)))
     return y
+
+
+# ----------------------------------------------------------------- around attention
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_its_device(call):
+    """The call with the device of its first tensor current, which the library launches on."""
+    @functools.wraps(call)
+    def at(x, *args, stream=None, **kw):
+        if stream is not None:
+            return on_stream(stream, at, x, *args, **kw)
+        assert x.is_cuda, "a CUDA tensor is needed"
+        if x.get_device() == _current_device():
+            return call(x, *args, **kw)
+        with torch.cuda.device(x.device):
+            return call(x, *args, **kw)
+    return at
+
+
+def _beside(x, **tensors):
+    """All tensors lie on x's device."""
+    for name, t in tensors.items():
+        assert t is None or t.get_device() == x.get_device(), f"{name} must lie where the first argument does"
+
+
+@functools.lru_cache(maxsize=64)
+def _freqs(rotary_dim, base, freqs):
+    """Radians per position of every pair, as the library's array."""
+    if freqs is None:
+        freqs = [float(base) ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    assert len(freqs) == rotary_dim // 2, f"freqs must hold {rotary_dim // 2} values"
+    return (ctypes.c_double * max(1, len(freqs)))(*freqs)
+
+
+@functools.lru_cache(maxsize=64)
+def _qk_workspace(rows, head_dim):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_qk_norm_rope_workspace(rows, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs):
+    rows, cols = x.shape
+    used = (q_heads + k_heads) * head_dim
+    assert x.dtype in _TYPES, "the head norm runs on bf16 and fp32"
+    assert 0 <= used <= cols, f"x must hold {q_heads} + {k_heads} heads of {head_dim}"
+    assert _is_vector(positions, rows, torch.int64), f"positions must be {rows} int64"
+    w_type = _check_params(head_dim, q_weight, k_weight)
+    _beside(x, positions=positions, q_weight=q_weight, k_weight=k_weight)
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    return rows, used, w_type, rotary_dim, _freqs(rotary_dim, None if freqs is not None else base, None if freqs is None else tuple(freqs))
+
+
+def _heads_out(out, x, rows, used, name):
+    """The result's tensor and its leading dimension."""
+    if out is None:
+        return _new(x, (rows, used), x.dtype), used
+    assert out.dtype is x.dtype and out.dim() == 2 and out.shape[0] == rows and out.shape[1] >= used, \
+        f"{name} must be of x's type, {rows} rows of at least {used}"
+    _beside(x, out=out)
+    return out, _ld(out, rows, out.shape[1])
+
+
+@_on_its_device
+def qk_norm_rope(x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weight=None, rotary_dim=None, base=10000.0, freqs=None,
+                 interleaved=False, eps=1e-6, out=None):
+    """lpq_qk_norm_rope: the RMS norm of every query and key head of x [t, >= (q_heads
+    + k_heads) * head_dim] (bf16 or fp32: a token's query heads, then its key heads),
+    turned by its position (positions [t] int64).  Pair i of the first `rotary_dim`
+    values turns by freqs[i] (default base^(-2 i / rotary_dim)) radians a position.
+    Returns `out` (a new [t, (q_heads + k_heads) * head_dim]; x itself: in place,
+    and what lies behind the key heads stays).  `stream`: see the module."""
+    rows, used, w_type, rotary_dim, f = _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs)
+    y, ldy = _heads_out(out, x, rows, used, "out")
+    _check(lib().lpq_qk_norm_rope(x.data_ptr(), _ld(x, rows, x.shape[1]), _TYPES[x.dtype], rows, q_heads, k_heads, head_dim, _ptr(q_weight),
+                                  _ptr(k_weight), w_type, positions.data_ptr(), f, rotary_dim, int(interleaved), eps, y.data_ptr(), ldy,
+                                  _stream_of(x)))
+    return y
+
+
+@_on_its_device
+def qk_norm_rope_backward(dy, x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weight=None, rotary_dim=None, base=10000.0,
+                          freqs=None, interleaved=False, eps=1e-6, param_grads=True, out=None):
+    """lpq_qk_norm_rope_backward: returns (dx, dq_weight, dk_weight) from dy [t, >=
+    (q_heads + k_heads) * head_dim] and the forward's x; the weights' gradients are
+    FP32 (None, None without `param_grads`).  dx goes to `out` (dy, x or a wider
+    tensor whose first columns it fills) or a new tensor.  `stream`: see the module."""
+    rows, used, w_type, rotary_dim, f = _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs)
+    assert dy.dtype is x.dtype and dy.dim() == 2 and dy.shape[0] == rows and dy.shape[1] >= used, "dy must be like x"
+    _beside(x, dy=dy)
+    dx, lddx = _heads_out(out, x, rows, used, "out")
+    dq = dk = ws = None
+    need = 0
+    if param_grads:
+        need = _qk_workspace(rows, head_dim)
+        dq, dk, ws = _new(x, head_dim, _FP32), _new(x, head_dim, _FP32), _new(x, need, torch.uint8)
+    _check(lib().lpq_qk_norm_rope_backward(dy.data_ptr(), _ld(dy, rows, dy.shape[1]), x.data_ptr(), _ld(x, rows, x.shape[1]),
+                                           _TYPES[x.dtype], rows, q_heads, k_heads, head_dim, _ptr(q_weight), _ptr(k_weight), w_type,
+                                           positions.data_ptr(), f, rotary_dim, int(interleaved), eps, dx.data_ptr(), lddx, _ptr(dq),
+                                           _ptr(dk), _ptr(ws), need, _stream_of(x)))
+    return dx, dq, dk
+
+
+_pack_controls = struct.Struct("@PqqPPPPPPPPqPq").pack  # LogitControls' fields
+_I64, _I32 = torch.int64, torch.int32
+
+
+@_on_its_device
+def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=None, frequency=None, presence=None, bias=None,
+                  allowed=None, out=None):
+    """lpq_adjust_logits on logits [t, v] (bf16 or fp32): penalties for words that
+    stand in each row's context, biases and a mask; returns `out` (a new tensor;
+    logits itself: in place).
+
+    `history` [t, n] int64 words, `lengths` [t] int64 of them valid, of which the first
+    `prompt` [t] int64 are the prompt (default 0) and the others the answer;
+    `repetition`, `frequency`, `presence` [t] fp32; `bias` (offsets [t + 1] int64, words
+    int64, values fp32); `allowed` [t, ceil(v / 32)] int32, one bit a word.  `stream`:
+    see the module."""
+    rows, v = logits.shape
+    dtype, device = logits.dtype, logits.get_device()
+    assert dtype in _TYPES, "logits must be bf16 or fp32"
+    ld_history = max_len = bias_count = ld_allowed = 0
+    offsets = words = values = None
+    if history is not None:
+        assert history.dtype is _I64 and history.dim() == 2 and history.shape[0] == rows, f"history must be int64 [{rows}, n]"
+        max_len = history.shape[1]
+        ld_history = _ld(history, rows, max_len)
+        assert lengths is not None, "history needs lengths"
+    if bias is not None:
+        offsets, words, values = bias
+        bias_count = words.numel()
+        assert _is_vector(offsets, rows + 1, _I64) and _is_vector(words, bias_count, _I64) and _is_vector(values, bias_count, _FP32), \
+            f"bias must be {rows + 1} int64 offsets, int64 words and as many fp32 values"
+    if allowed is not None:
+        assert allowed.dtype is _I32 and allowed.shape == (rows, (v + 31) // 32), f"allowed must be int32 [{rows}, {(v + 31) // 32}]"
+        ld_allowed = _ld(allowed, rows, allowed.shape[1])
+    for p, kind in ((lengths, _I64), (prompt, _I64), (repetition, _FP32), (frequency, _FP32), (presence, _FP32)):
+        assert p is None or _is_vector(p, rows, kind), f"lengths and prompt must be {rows} int64, the penalties {rows} fp32"
+    for p in (history, lengths, prompt, repetition, frequency, presence, offsets, words, values, allowed, out):
+        assert p is None or p.get_device() == device, "all tensors must lie where the logits do"
+    if out is None:
+        out, ldo = _new(logits, (rows, v), dtype), v
+    else:
+        assert out.dtype is dtype and out.shape == logits.shape, "out must be like the logits"
+        ldo = _ld(out, rows, v)
+    at = lambda t: 0 if t is None else t.data_ptr()
+    # an empty tensor has no address, which would read as one that is not given
+    some = lambda t: 0 if t is None else t.data_ptr() or 8
+    c = _pack_controls(some(history), ld_history, max_len, some(lengths), at(prompt), at(repetition), at(frequency), at(presence), at(offsets),
+                       at(words), at(values), bias_count, at(allowed), ld_allowed)
+    _check(lib().lpq_adjust_logits(logits.data_ptr(), _ld(logits, rows, v), _TYPES[dtype], rows, v, c, out.data_ptr(), ldo, _raw_stream(device)))
+    return out
 
 
 def device_status(stream=None):
