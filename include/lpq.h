@@ -393,6 +393,59 @@ lpq_status lpq_linear_ce_workspace(int64_t t, int64_t v, int64_t d, int32_t back
 lpq_status lpq_matvec(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,
                       lpq_stream_t stream);
 
+/* Low-rank adapters of one linear layer: pair e is a[e] [rank, k] and b[e] [n, rank]
+ * (bf16, contiguous, 16-byte aligned), rank a multiple of 8 up to 256 (smaller ones
+ * are padded with zeros); scale [count] FP32, NULL = 1. */
+typedef struct {
+  const void *a, *b;
+  const float *scale;
+  int64_t count, rank;
+} lpq_adapters;
+
+/* lpq_matvec with an adapter for every token:
+ *   y[i, n] = sum_k x[i, k] * deq(w)[n, k] + scale[e] * sum_r b[e][n, r] * (sum_k
+ *             a[e][r, k] * x[i, k]),   e = index[i]
+ * index [m] int64, device; outside 0 .. count - 1: no adapter.  The inner vector and
+ * all sums are FP32, y is rounded once.  The workspace (16-byte aligned device
+ * memory) is written before it is read. */
+lpq_status lpq_matvec_adapted(const lpq_qview *w, const void *x, int64_t ldx, int64_t m, void *y, int32_t y_is_fp32,
+                              const lpq_adapters *adapters, const int64_t *index, void *workspace, size_t workspace_bytes,
+                              lpq_stream_t stream);
+
+/* Bytes of lpq_matvec_adapted's workspace.  Host-only. */
+lpq_status lpq_matvec_adapted_workspace(int64_t m, int64_t rank, size_t *bytes);
+
+/* A mixture-of-experts layer for a few tokens.  The router: with the logits l = x w^T
+ * (FP32) of x [m, d] and w [experts, d] (bf16, rows ldx and ldw elements apart),
+ *   ids [m, k] int64: the k largest in descending order (equal ones: the lower index
+ *   first; NaN below everything),
+ *   probs [m, k] FP32: the softmax over the chosen (renormalize = 1) or over all
+ *   (renormalize = 0) at those places.
+ * d is a multiple of 8, ldx and ldw too, x and w 16-byte aligned; 1 <= k <= 32, k <=
+ * experts <= 1024; any m >= 0 (the kernel is made for few). */
+lpq_status lpq_moe_route(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t d, int64_t experts,
+                         int64_t k, int32_t renormalize, int64_t *ids, float *probs, lpq_stream_t stream);
+
+/* The experts' products: for token i
+ *   y[i] = sum_j probs[i, j] * W2_e (silu(W1g_e x[i]) * (W1u_e x[i])),   e = ids[i, j]
+ * on 4-bit weights (NVFP4, NVFP4_2D or MXFP4, row-wise copies with LPQ_SF_GEMM scales):
+ *   up    [experts * 2 f, d]: each expert's f gate rows, then its f up rows;
+ *   down  [experts * d, f].
+ * x [m, d] bf16 (rows ldx elements apart, a multiple of 8; 16-byte aligned), not
+ * quantized; ids [m, k] int64 (outside 0 .. experts - 1: the place counts for nothing;
+ * one expert may stand twice), probs [m, k] FP32; y [m, d] bf16, contiguous.  Sums are
+ * FP32; hidden values enter the second product with 11 significant bits of their
+ * vector's range; y is rounded once, its sum taken in the order of j.  d and f are
+ * multiples of 32 up to 65536; 0 <= k <= 32, experts <= 1024; any m >= 0, but m is meant
+ * to be small: an expert's weights are read once for up to 8 of its tokens. */
+lpq_status lpq_moe(const lpq_qview *up, const lpq_qview *down, int64_t experts, const void *x, int64_t ldx, int64_t m,
+                   const int64_t *ids, const float *probs, int64_t k, void *y, void *workspace, size_t workspace_bytes,
+                   lpq_stream_t stream);
+
+/* Bytes of lpq_moe's workspace (16-byte aligned device memory; written before it is
+ * read).  Host-only. */
+lpq_status lpq_moe_workspace(int64_t m, int64_t k, int64_t d, int64_t f, size_t *bytes);
+
 /* RMS norm of every query and key head with the position rotation, behind the
  * QKV projection.  x [rows, >= (q_heads + k_heads) * head_dim] holds a token's
  * query heads, then its key heads (rows ldx elements apart; what lies behind the

@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "liblpq.so")
-SOURCES = ["capi.cu", "quantize.cu", "gemm.cu", "norm.cu", "loss.cu", "matvec.cu", "qknorm.cu", "logits.cu"]
+SOURCES = ["capi.cu", "quantize.cu", "gemm.cu", "norm.cu", "loss.cu", "matvec.cu", "qknorm.cu", "logits.cu", "moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I" + INCLUDE, "-I" + CSRC]

@@ -492,8 +492,8 @@ lpq_status lpq_linear_ce_backward_ex(const void* h, int64_t ldh, const void* w, 
   return launch_ce_backward(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
-lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
-                      lpq_stream_t stream) {
+namespace {
+lpq_status check_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, const void* y, int32_t y_is_fp32) {
   if (!w) return set_error(LPQ_ERR_INVALID_ARG, "w is NULL");
   if (!(is_nvfp4(w->fmt) || w->fmt == LPQ_MXFP4))
     return set_error(LPQ_ERR_UNSUPPORTED, "lpq_matvec reads NVFP4, NVFP4_2D and MXFP4 weights, not format %d", w->fmt);
@@ -519,9 +519,118 @@ lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m,
         return set_error(LPQ_ERR_ALIGN, "w.scales or w.tensor_scale not 4-byte aligned");
     }
   }
+  return LPQ_OK;
+}
+}  // namespace
+
+lpq_status lpq_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
+                      lpq_stream_t stream) {
+  lpq_status st = check_matvec(w, x, ldx, m, y, y_is_fp32);
+  if (st != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  return launch_matvec(w, x, ldx, m, y, y_is_fp32, nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_matvec_adapted_workspace(int64_t m, int64_t rank, size_t* bytes) {
+  if (!bytes) return set_error(LPQ_ERR_INVALID_ARG, "NULL output pointer");
+  if (m < 0 || m > (int64_t)1 << 30 || rank < 8 || rank > 256 || rank % 8)
+    return set_error(LPQ_ERR_SHAPE, "m %lld, rank %lld (a multiple of 8, 8 to 256)", (long long)m, (long long)rank);
+  *bytes = (size_t)m * (size_t)rank * sizeof(float);
+  return LPQ_OK;
+}
+
+lpq_status lpq_matvec_adapted(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
+                              const lpq_adapters* adapters, const int64_t* index, void* workspace, size_t workspace_bytes,
+                              lpq_stream_t stream) {
+  lpq_status st = check_matvec(w, x, ldx, m, y, y_is_fp32);
+  if (st != LPQ_OK) return st;
+  if (!adapters) return set_error(LPQ_ERR_INVALID_ARG, "adapters is NULL");
+  if (adapters->count < 0 || adapters->count > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "adapters.count %lld", (long long)adapters->count);
+  size_t need = 0;
+  if ((st = lpq_matvec_adapted_workspace(m, adapters->rank, &need)) != LPQ_OK) return st;
+  const bool any = m > 0 && w->rows > 0 && w->cols > 0 && adapters->count > 0;
+  if (any && (!adapters->a || !adapters->b || !index)) return set_error(LPQ_ERR_INVALID_ARG, "adapters.a, adapters.b or index is NULL");
+  if (!aligned16(adapters->a) || !aligned16(adapters->b)) return set_error(LPQ_ERR_ALIGN, "adapters.a or adapters.b not 16-byte aligned");
+  if (!aligned_to(adapters->scale, 4)) return set_error(LPQ_ERR_ALIGN, "adapters.scale not 4-byte aligned");
+  if (!aligned_to(index, 8)) return set_error(LPQ_ERR_ALIGN, "index not 8-byte aligned");
+  if (any && (st = check_workspace(workspace, workspace_bytes, need)) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  AdapterArgs a{};
+  a.a = adapters->a; a.b = adapters->b; a.scale = adapters->scale; a.index = index; a.count = adapters->count; a.rank = adapters->rank;
+  a.inner = static_cast<float*>(workspace);
+  return launch_matvec(w, x, ldx, m, y, y_is_fp32, any ? &a : nullptr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lpq_status lpq_moe_route(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t m, int64_t d, int64_t experts, int64_t k,
+                         int32_t renormalize, int64_t* ids, float* probs, lpq_stream_t stream) {
+  if (renormalize < 0 || renormalize > 1) return set_error(LPQ_ERR_INVALID_ARG, "renormalize %d", renormalize);
+  if (m < 0 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "m %lld", (long long)m);
+  if (d < 8 || d % 8 || d > (int64_t)1 << 20) return set_error(LPQ_ERR_SHAPE, "d %lld not a multiple of 8, 8 to 2^20", (long long)d);
+  if (experts < 1 || experts > kMoeMostExperts) return set_error(LPQ_ERR_SHAPE, "experts %lld, at most %d", (long long)experts, kMoeMostExperts);
+  if (k < 1 || k > kMoeMostChoices || k > experts)
+    return set_error(LPQ_ERR_SHAPE, "k %lld of %lld experts, at most %d", (long long)k, (long long)experts, kMoeMostChoices);
+  if (ldx < d || ldx % 8 || ldw < d || ldw % 8)
+    return set_error(LPQ_ERR_SHAPE, "ldx %lld and ldw %lld must be multiples of 8, at least d = %lld", (long long)ldx, (long long)ldw, (long long)d);
+  if (!w || (m > 0 && (!x || !ids || !probs))) return set_error(LPQ_ERR_INVALID_ARG, "x, w, ids or probs is NULL");
+  if (!aligned16(x) || !aligned16(w)) return set_error(LPQ_ERR_ALIGN, "x or w not 16-byte aligned");
+  if (!aligned_to(ids, 8) || !aligned_to(probs, 4)) return set_error(LPQ_ERR_ALIGN, "ids or probs not aligned to its elements");
   lpq_status st = check_arch();
   if (st != LPQ_OK) return st;
-  return launch_matvec(w, x, ldx, m, y, y_is_fp32, reinterpret_cast<cudaStream_t>(stream));
+  RouteArgs a{};
+  a.x = static_cast<const __nv_bfloat16*>(x); a.w = static_cast<const __nv_bfloat16*>(w); a.ldx = ldx; a.ldw = ldw; a.m = m;
+  a.d = (int)d; a.experts = (int)experts; a.k = (int)k; a.renormalize = renormalize != 0; a.ids = ids; a.probs = probs;
+  return launch_moe_route(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+namespace {
+lpq_status check_moe_shape(int64_t m, int64_t k, int64_t d, int64_t f) {
+  const int64_t most = 65536;
+  if (m < 0 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "m %lld", (long long)m);
+  if (k < 0 || k > kMoeMostChoices) return set_error(LPQ_ERR_SHAPE, "k %lld, at most %d", (long long)k, kMoeMostChoices);
+  if (d < 32 || d % 32 || d > most || f < 32 || f % 32 || f > most)
+    return set_error(LPQ_ERR_SHAPE, "d %lld and f %lld must be multiples of 32, 32 to %lld", (long long)d, (long long)f, (long long)most);
+  return LPQ_OK;
+}
+lpq_status check_experts(const lpq_qview* w, const char* name, int64_t rows) {
+  if (!w) return set_error(LPQ_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!(is_nvfp4(w->fmt) || w->fmt == LPQ_MXFP4))
+    return set_error(LPQ_ERR_UNSUPPORTED, "lpq_moe reads NVFP4, NVFP4_2D and MXFP4 weights, not format %d (%s)", w->fmt, name);
+  if (w->sf_layout != LPQ_SF_GEMM) return set_error(LPQ_ERR_UNSUPPORTED, "lpq_moe reads LPQ_SF_GEMM scales (%s)", name);
+  if (rows >= 0 && w->rows != rows)
+    return set_error(LPQ_ERR_SHAPE, "%s has %lld rows, %lld expected", name, (long long)w->rows, (long long)rows);
+  return check_view(w, name, w->fmt, w->rows, w->cols, 0, is_nvfp4(w->fmt), false);
+}
+}  // namespace
+
+lpq_status lpq_moe_workspace(int64_t m, int64_t k, int64_t d, int64_t f, size_t* bytes) {
+  if (!bytes) return set_error(LPQ_ERR_INVALID_ARG, "NULL output pointer");
+  lpq_status st = check_moe_shape(m, k, d, f);
+  if (st != LPQ_OK) return st;
+  *bytes = moe_workspace(m, k, d, f);
+  return LPQ_OK;
+}
+
+lpq_status lpq_moe(const lpq_qview* up, const lpq_qview* down, int64_t experts, const void* x, int64_t ldx, int64_t m,
+                   const int64_t* ids, const float* probs, int64_t k, void* y, void* workspace, size_t workspace_bytes,
+                   lpq_stream_t stream) {
+  if (!up || !down) return set_error(LPQ_ERR_INVALID_ARG, "up or down is NULL");
+  const int64_t d = up->cols, f = down->cols;
+  lpq_status st = check_moe_shape(m, k, d, f);
+  if (st != LPQ_OK) return st;
+  if (experts < 1 || experts > kMoeMostExperts) return set_error(LPQ_ERR_SHAPE, "experts %lld, at most %d", (long long)experts, kMoeMostExperts);
+  if ((st = check_experts(up, "up", experts * 2 * f)) != LPQ_OK) return st;
+  if ((st = check_experts(down, "down", experts * d)) != LPQ_OK) return st;
+  if (ldx < d || ldx % 8) return set_error(LPQ_ERR_SHAPE, "ldx %lld must be a multiple of 8, at least d = %lld", (long long)ldx, (long long)d);
+  if (m > 0 && (!x || !y || (k > 0 && (!ids || !probs)))) return set_error(LPQ_ERR_INVALID_ARG, "x, y, ids or probs is NULL");
+  if (!aligned16(x)) return set_error(LPQ_ERR_ALIGN, "x not 16-byte aligned");
+  if (!aligned_to(y, 2) || !aligned_to(ids, 8) || !aligned_to(probs, 4) || !aligned_to(up->tensor_scale, 4) || !aligned_to(down->tensor_scale, 4))
+    return set_error(LPQ_ERR_ALIGN, "y, ids, probs or a tensor_scale not aligned to its elements");
+  if (m > 0 && (st = check_workspace(workspace, workspace_bytes, moe_workspace(m, k, d, f))) != LPQ_OK) return st;
+  if ((st = check_arch()) != LPQ_OK) return st;
+  MoeArgs a{};
+  a.up = up; a.down = down; a.x = x; a.ldx = ldx; a.m = m; a.experts = experts; a.top = k; a.ids = ids; a.probs = probs; a.y = y;
+  a.workspace = static_cast<uint8_t*>(workspace);
+  return launch_moe(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 namespace {

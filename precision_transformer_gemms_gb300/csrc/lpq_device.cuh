@@ -562,6 +562,11 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 // Relaxed remote arrival, for hand-overs of TMEM whose accesses by the
 // arriving side are already complete (tcgen05.wait::st / wait::ld), with no
 // memory writes to publish.  A release at cluster scope would make the thread

@@ -1,5 +1,6 @@
 // Internal declarations shared by the translation units of liblpq.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -101,8 +102,16 @@ lpq_status launch_ce(const CeArgs& a, cudaStream_t stream);
 lpq_status launch_ce_backward(const CeArgs& a, cudaStream_t stream);
 
 // 4-bit matrix-vector launcher (matvec.cu).  Arguments validated.
+struct AdapterArgs {
+  const void* a;
+  const void* b;
+  const float* scale;  // may be NULL
+  const int64_t* index;
+  int64_t count, rank;
+  float* inner;  // workspace
+};
 lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
-                         cudaStream_t stream);
+                         const AdapterArgs* adapters, cudaStream_t stream);  // adapters may be NULL
 
 // Head norm and rotation launchers (qknorm.cu).  Arguments validated.
 constexpr int kQkMaxDim = 512;  // values of a head
@@ -128,6 +137,32 @@ struct QkArgs {
 size_t qk_norm_workspace(int64_t rows, int64_t dim);
 lpq_status launch_qk_norm(const QkArgs& a, int32_t type, cudaStream_t stream);
 lpq_status launch_qk_norm_backward(const QkArgs& a, int32_t type, cudaStream_t stream);
+
+// Mixture-of-experts launchers (moe.cu).  Arguments validated.
+constexpr int kMoeMostExperts = 1024, kMoeMostChoices = 32;
+struct RouteArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w;
+  int64_t ldx, ldw;
+  int64_t m;
+  int d, experts, k;
+  bool renormalize;
+  int64_t* ids;
+  float* probs;
+};
+lpq_status launch_moe_route(const RouteArgs& a, cudaStream_t stream);
+struct MoeArgs {
+  const lpq_qview* up;
+  const lpq_qview* down;
+  const void* x;
+  int64_t ldx, m, experts, top;
+  const int64_t* ids;
+  const float* probs;
+  void* y;
+  uint8_t* workspace;
+};
+size_t moe_workspace(int64_t m, int64_t top, int64_t hidden, int64_t inter);
+lpq_status launch_moe(const MoeArgs& a, cudaStream_t stream);
 
 // Logit controls launcher (logits.cu).  Arguments validated.
 struct LogitsArgs {

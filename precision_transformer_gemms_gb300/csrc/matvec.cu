@@ -25,25 +25,24 @@
 // that, the CTA takes bf16 operands instead (twice the instructions: bf16 has
 // no conversion from E2M1).  Either way codes, scales and x are exact and only
 // the FP32 sums round.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+//
+// With adapters, y[i, n] gains s B_e (A_e x_i) for the low-rank pair e of token
+// i.  The inner vectors s A_e x_i are a launch of their own in front, of few
+// CTAs, which the weights' stream runs beside: the products' kernel waits for
+// them only where its sums are done, and adds a row's B there in FP32 before the
+// one rounding.
 #include <algorithm>
 #include <type_traits>
 
-#include "lpq_device.cuh"
+#include "fp4_rows.cuh"
 
 namespace lpq {
 namespace {
 
-constexpr int kGroup = 128;         // rows of a group of the tensor-core scale layout: 8 tiles
-constexpr int kChunk = 128;         // codes of a row per warp load: 4 lanes x 32
 constexpr int kRing = 4;            // chunks in a warp's ring
 constexpr int kStep = kRing * kChunk;  // segments of K are whole steps
 constexpr int kSegments = 8;        // most parts of K (and CTAs of a cluster)
-constexpr int kTokens = 8;          // most tokens of a pass: the columns of an MMA
 constexpr int kXBytes = 128 * 1024; // most shared memory for x
-constexpr int kSlot = 32 * 40;      // a chunk in a warp's ring: 2 x 16 bytes of codes, 2 x 4 of scales per lane
 
 struct MatvecArgs {
   const uint8_t* codes;
@@ -62,188 +61,13 @@ struct MatvecArgs {
   int cluster;          // 1, or a CTA per segment
   int items;            // work items of W tiles (cluster > 1) or W / segments tiles
   int x_words;          // 16-byte words of x that a CTA has room for, per token
+  // adapters (ADAPTED kernels alone)
+  const __nv_bfloat16* b;  // [count, n, rank]
+  const float* inner;      // [token, rank]: s A x
+  const int64_t* index;    // the token's adapter; outside 0 .. count - 1: none
+  int64_t count;
+  int rank;
 };
-
-template <bool F16>
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (F16) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Eight E2M1 codes -> four pairs.  f16: the codes 2 i and 2 i + 1, their values.
-// bf16: the codes i and i + 4, their values * 2^-126 (the code's exponent and
-// mantissa bits are the low bits of a bf16 with the same meaning, subnormals
-// included, 126 exponent steps down).
-template <bool F16>
-__device__ __forceinline__ void decode8(uint32_t u, uint32_t (&p)[4]) {
-  if constexpr (F16) {
-    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "mov.b32 {a, b, c, d}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(p[0]), "=r"(p[1]), "=r"(p[2]), "=r"(p[3]) : "r"(u));
-  } else {
-    p[0] = ((u << 12) & 0x80008000u) | ((u << 6) & 0x01C001C0u);
-    p[1] = ((u << 8) & 0x80008000u) | ((u << 2) & 0x01C001C0u);
-    p[2] = ((u << 4) & 0x80008000u) | ((u >> 2) & 0x01C001C0u);
-    p[3] = (u & 0x80008000u) | ((u >> 6) & 0x01C001C0u);
-  }
-}
-
-// A lane's part of a chunk: 32 codes of two rows and their scales (NVFP4 two
-// E4M3 bytes, MXFP4 one E8M0 byte per row).
-struct Load {
-  uint4 lo, hi;
-  uint32_t slo, shi;
-};
-
-// The two group scales of a lane's 32 codes as operand pairs.  NVFP4: f16 the
-// scale, bf16 the scale * 2^118 (the decoded values lie 2^-126 down, the sums
-// come out 2^-8 down).  MXFP4, scale 2^e: f16 2^min(e, 13) (beyond that callers
-// leave groups of zero codes alone, which any finite scale gives: infinity would
-// make them NaN); bf16 2^(min(e, 1) + 126) and, where e > 1, the rest by mx_rest.
-template <bool MX, bool F16>
-__device__ __forceinline__ void scale_pairs(uint32_t s, uint32_t (&o)[2]) {
-  if constexpr (MX) {
-    if constexpr (F16) {
-      const float f = __uint_as_float(min(s, 140u) << 23);
-      const __half2 h = __floats2half2_rn(f, f);
-      o[0] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      o[0] = (min(s, 128u) + 126u) * 0x00800080u;
-    }
-    o[1] = o[0];
-  } else {
-    uint32_t h2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)s));
-    if constexpr (F16) {
-      o[0] = __byte_perm(h2, h2, 0x1010);
-      o[1] = __byte_perm(h2, h2, 0x3232);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-      const uint32_t a = __float_as_uint(f.x * 3.3230700e35f), b = __float_as_uint(f.y * 3.3230700e35f);  // 2^118
-      o[0] = __byte_perm(a, a, 0x3232);
-      o[1] = __byte_perm(b, b, 0x3232);
-    }
-  }
-}
-__device__ __forceinline__ uint32_t mx_rest(uint32_t s) {  // 2^(e - 1) where e > 1, else 1; NaN for 255
-  return s == 255u ? 0x7FC07FC0u : (max(s, 128u) - 1u) * 0x00800080u;
-}
-// Whether some group of a warp's chunk leaves f16: its scale 2^e outside e in
-// [-23, 13] and a code of it not zero, or the scale that is no number.
-__device__ __forceinline__ bool mx_far(const Load& l) {
-  if (!__any_sync(0xFFFFFFFFu, l.slo - 104u > 36u || l.shi - 104u > 36u)) return false;
-  auto outside = [](uint32_t s, const uint4& c) {
-    return s - 104u > 36u && (s == 255u || ((c.x | c.y | c.z | c.w) & 0x77777777u));
-  };
-  return __any_sync(0xFFFFFFFFu, outside(l.slo, l.lo) || outside(l.shi, l.hi));
-}
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  uint32_t h2;
-  asm("{\n\t.reg .b8 a, b;\n\tmov.b16 {a, b}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h2) : "h"((uint16_t)(code & 15u)));
-  return __low2float(*reinterpret_cast<const __half2*>(&h2));
-}
-
-// The chunk's products.  e: the lane's x entries (16 bytes per word, words 4 *
-// MP entries apart).
-template <bool MX, bool F16, int MP>
-__device__ __forceinline__ void chunk_products(const Load& l, const uint4* e, float (&acc)[4]) {
-  uint32_t sl[2], sh[2], xl = 0, xh = 0;
-  scale_pairs<MX, F16>(l.slo, sl);
-  scale_pairs<MX, F16>(l.shi, sh);
-  bool rest = false;
-  if constexpr (MX && !F16) {
-    rest = __any_sync(0xFFFFFFFFu, l.slo > 128u || l.shi > 128u);
-    xl = mx_rest(l.slo);
-    xh = mx_rest(l.shi);
-  }
-  const uint32_t wl[4] = {l.lo.x, l.lo.y, l.lo.z, l.lo.w};
-  const uint32_t wh[4] = {l.hi.x, l.hi.y, l.hi.z, l.hi.w};
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t pl[4], ph[4];
-    decode8<F16>(wl[w], pl);
-    decode8<F16>(wh[w], ph);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pl[i] = mul2<F16>(pl[i], sl[w >> 1]);
-      ph[i] = mul2<F16>(ph[i], sh[w >> 1]);
-    }
-    if constexpr (MX && !F16) {
-      if (rest) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          pl[i] = mul2<F16>(pl[i], xl);
-          ph[i] = mul2<F16>(ph[i], xh);
-        }
-      }
-    }
-    const uint4 b = e[w * 4 * MP];
-    mma<F16>(acc, pl[0], ph[0], pl[1], ph[1], b.x, b.y);
-    mma<F16>(acc, pl[2], ph[2], pl[3], ph[3], b.z, b.w);
-  }
-}
-
-// A chunk with MXFP4 groups that f16 cannot hold: plain FP32 dot products of
-// the lane's 32 codes with each token, joined over the 4 lanes of a row and
-// added to the warp's sums in shared memory ([token][row], in x's own scale).
-// back: per token 2^-shift of the entries at e.
-__device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_t shi, const uint4* e, int mp, int mm,
-                                       const float* back, float* sums) {
-  const int lane = threadIdx.x & 31, t = lane & 3, gid = lane >> 2;
-  const float fl = slo == 255u ? __int_as_float(0x7FC00000) : pow2_exact((int)slo - 127);
-  const float fh = shi == 255u ? __int_as_float(0x7FC00000) : pow2_exact((int)shi - 127);
-#pragma unroll 1
-  for (int token = 0; token < mm; ++token) {
-    const float f = back[token];
-    float dl = 0.f, dh = 0.f;
-#pragma unroll 1
-    for (int w = 0; w < 4; ++w) {
-      const uint4 b = e[(w * mp + token) * 4];
-      const uint32_t u[4] = {b.x, b.y, b.z, b.w};
-      const uint32_t cl = w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w;
-      const uint32_t ch = w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[i >> 1]));
-        const float xv = (i & 1 ? p.y : p.x) * f;
-        dl += e2m1_value(cl >> (4 * i)) * xv;
-        dh += e2m1_value(ch >> (4 * i)) * xv;
-      }
-    }
-    dl *= fl;
-    dh *= fh;
-    dl += __shfl_xor_sync(0xFFFFFFFFu, dl, 1);
-    dh += __shfl_xor_sync(0xFFFFFFFFu, dh, 1);
-    dl += __shfl_xor_sync(0xFFFFFFFFu, dl, 2);
-    dh += __shfl_xor_sync(0xFFFFFFFFu, dh, 2);
-    if (((token & 7) >> 1) == t) {  // the lane that holds this token's column
-      sums[token * 16 + gid] += dl;
-      sums[token * 16 + gid + 8] += dh;
-    }
-  }
-}
-
-__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 
 // A warp's tile is 16 weight rows: 4 runs of 4 neighbours, 32 apart (rows 32 j
 // + i of a 128-row group, i in a run of 4), whose scales of 4 neighbouring
@@ -254,46 +78,84 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
 // per CTA, and joins the sums through distributed shared memory.  The segments'
 // sums are added in the same order either way: a row's result does not depend
 // on the number of rows.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Row `row` of B_e times the token's inner vector.
+__device__ __forceinline__ float adapter_row(const MatvecArgs& g, int64_t token, int row) {
+  const int64_t e = g.index[token];
+  if ((uint64_t)e >= (uint64_t)g.count) return 0.f;
+  const uint4* b = reinterpret_cast<const uint4*>(g.b + (e * g.n + row) * g.rank);
+  const float4* s = reinterpret_cast<const float4*>(g.inner + token * g.rank);
+  float sum = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < g.rank / 8; ++i) {
+    float f[8];
+    unpack8(__ldg(b + i), f);
+    const float4 p = s[2 * i], q = s[2 * i + 1];
+    sum = fmaf(f[0], p.x, sum);
+    sum = fmaf(f[1], p.y, sum);
+    sum = fmaf(f[2], p.z, sum);
+    sum = fmaf(f[3], p.w, sum);
+    sum = fmaf(f[4], q.x, sum);
+    sum = fmaf(f[5], q.y, sum);
+    sum = fmaf(f[6], q.z, sum);
+    sum = fmaf(f[7], q.w, sum);
+  }
+  return sum;
 }
-template <int BYTES>
-__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool there) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-template <bool MX>
-__device__ __forceinline__ uint32_t ld_shared_scale(uint32_t addr) {
-  if constexpr (MX) {
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
-  } else {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-    return v;
+
+// inner[token, r] = s A_e[r] . x: a CTA for four rows of a token.
+constexpr int kInnerRows = 4, kInnerThreads = 256;
+__global__ void __launch_bounds__(kInnerThreads) adapter_inner_kernel(const __nv_bfloat16* a, const float* scale, const int64_t* index,
+                                                                      int64_t count, int rank, const __nv_bfloat16* x, int64_t ldx,
+                                                                      int k, float* inner) {
+  __shared__ float sh[kInnerThreads / 32][kInnerRows];
+  wait_for_stream();
+  let_dependents_start();  // not before: the products' kernel reads x and the weights without a wait of its own
+  const int per = rank / kInnerRows;
+  const int64_t token = blockIdx.x / per;
+  const int r0 = (int)(blockIdx.x - token * per) * kInnerRows;
+  const int64_t e = index[token];
+  if ((uint64_t)e >= (uint64_t)count) return;
+  const __nv_bfloat16* rows = a + (e * rank + r0) * k;
+  const __nv_bfloat16* xr = x + token * ldx;
+  float sum[kInnerRows] = {};
+#pragma unroll 2
+  for (int c = threadIdx.x * 8; c < k; c += kInnerThreads * 8) {
+    float xv[8];
+    unpack8(__ldg(reinterpret_cast<const uint4*>(xr + c)), xv);
+#pragma unroll
+    for (int r = 0; r < kInnerRows; ++r) {
+      float f[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(rows + (int64_t)r * k + c)), f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[r] = fmaf(f[i], xv[i], sum[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kInnerRows; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], o);
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5][r] = sum[r];
+  }
+  __syncthreads();
+  if (threadIdx.x < kInnerRows) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kInnerThreads / 32; ++w) s += sh[w][threadIdx.x];
+    inner[token * rank + r0 + threadIdx.x] = s * (scale ? scale[e] : 1.0f);
   }
 }
 
 // MP: tokens that x's place in shared memory is laid out for (g.m or more).
 // W warps per CTA: 8, four CTAs on an SM while x is small, else 24 that share x.
-template <bool MX, bool SFG, int MP, int W>
+template <bool MX, bool SFG, int MP, int W, bool ADAPTED>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const MatvecArgs g) {
   constexpr int kThreads = 32 * W;
   extern __shared__ uint4 sx[];
   __shared__ float back_sh[kSegments * kTokens];  // 2^-shift of a segment's x
   __shared__ int fits_sh[kSegments * kTokens];
   let_dependents_start();
-  wait_for_stream();
+  // (the inner vectors' kernel has waited for the stream before it let this one start)
+  if constexpr (!ADAPTED) wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, t = lane & 3;
   const bool shared_k = g.cluster > 1;  // the cluster's CTAs share K
@@ -457,8 +319,10 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const Ma
   auto put = [&](int row, int token, float v) {
     if (row >= n_rows || token >= mm) return;
     const int64_t at = (m0 + token) * g.n + row;
-    if (g.y_fp32) static_cast<float*>(g.y)[at] = v * tensor;
-    else static_cast<__nv_bfloat16*>(g.y)[at] = __float2bfloat16_rn(v * tensor);
+    v *= tensor;
+    if constexpr (ADAPTED) v += adapter_row(g, m0 + token, row);
+    if (g.y_fp32) static_cast<float*>(g.y)[at] = v;
+    else static_cast<__nv_bfloat16*>(g.y)[at] = __float2bfloat16_rn(v);
   };
   // operand columns beyond the tokens hold anything: their sums are not stored
   const int col = min(gid, MP - 1) * 4 + t;
@@ -517,6 +381,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const Ma
       acc[i] *= f16 ? back_sh[seg * kTokens + min(token, mm - 1)] : MX ? 1.0f : 256.0f;
       if constexpr (MX) acc[i] += mine[token * 16 + gid + (i >> 1) * 8];
     }
+    if constexpr (ADAPTED) wait_for_stream();  // the inner vectors are there
     if (g.segments == 1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) put(row_of(item, slot, gid + (i >> 1) * 8), 2 * t + (i & 1), acc[i]);
@@ -555,13 +420,13 @@ int layout_for(int tokens) {
   return kTokens;
 }
 
-template <bool MX, bool SFG, int MP, int W>
+template <bool MX, bool SFG, int MP, int W, bool ADAPTED>
 lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
   constexpr int kSumBytes = 2 * W * kTokens * 16 * 4;
   const int seg_steps = (g.steps + g.segments - 1) / g.segments;
   g.x_words = (g.cluster > 1 ? seg_steps : g.steps) * (kStep / 8);
   const int smem = g.x_words * 16 * MP + kSumBytes + W * kRing * kSlot;
-  const void* kernel = reinterpret_cast<const void*>(matvec_kernel<MX, SFG, MP, W>);
+  const void* kernel = reinterpret_cast<const void*>(matvec_kernel<MX, SFG, MP, W, ADAPTED>);
   lpq_status st = set_smem_attr(kernel, 222 * 1024);
   if (st != LPQ_OK) return st;
   const int64_t tiles = (g.n + kGroup - 1) / kGroup * 8, per = g.cluster > 1 ? W : W / g.segments;
@@ -570,7 +435,7 @@ lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
   const int most = std::max(1, resident * device_sms() / g.cluster);
   const dim3 grid((unsigned)(std::min(g.items, most) * g.cluster), (unsigned)passes);
   if (g.cluster == 1)
-    return cuda_check(launch_dependent(matvec_kernel<MX, SFG, MP, W>, grid, 32 * W, smem, s, g), "matvec launch");
+    return cuda_check(launch_dependent(matvec_kernel<MX, SFG, MP, W, ADAPTED>, grid, 32 * W, smem, s, g), "matvec launch");
   // Clusters start when the stream is done: an early start would place them
   // around the kernel ahead and leave the SMs unevenly loaded (16384 -> 4096:
   // 19.9 us, 14.7 us so).
@@ -586,21 +451,21 @@ lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, matvec_kernel<MX, SFG, MP, W>, g), "matvec launch");
+  return cuda_check(cudaLaunchKernelEx(&cfg, matvec_kernel<MX, SFG, MP, W, ADAPTED>, g), "matvec launch");
 }
 
-template <bool MX>
+template <bool MX, bool ADAPTED>
 lpq_status run_tokens(const MatvecArgs& g, int passes, bool plain, bool wide_cta, cudaStream_t s) {
-  if (plain) return run_matvec<MX, false, kTokens, 8>(g, passes, s);
-  if (wide_cta) return g.m > 2 ? run_matvec<MX, true, kTokens, 24>(g, passes, s) : run_matvec<MX, true, 2, 24>(g, passes, s);
-  return g.m > 2 ? run_matvec<MX, true, kTokens, 8>(g, passes, s)
-         : g.m == 2 ? run_matvec<MX, true, 2, 8>(g, passes, s) : run_matvec<MX, true, 1, 8>(g, passes, s);
+  if (plain) return run_matvec<MX, false, kTokens, 8, ADAPTED>(g, passes, s);
+  if (wide_cta) return g.m > 2 ? run_matvec<MX, true, kTokens, 24, ADAPTED>(g, passes, s) : run_matvec<MX, true, 2, 24, ADAPTED>(g, passes, s);
+  return g.m > 2 ? run_matvec<MX, true, kTokens, 8, ADAPTED>(g, passes, s)
+         : g.m == 2 ? run_matvec<MX, true, 2, 8, ADAPTED>(g, passes, s) : run_matvec<MX, true, 1, 8, ADAPTED>(g, passes, s);
 }
 
 }  // namespace
 
 lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t m, void* y, int32_t y_is_fp32,
-                         cudaStream_t s) {
+                         const AdapterArgs* ad, cudaStream_t s) {
   if (m == 0 || w->rows == 0) return LPQ_OK;
   if (w->cols == 0)  // empty reduction: y = 0
     return cuda_check(cudaMemsetAsync(y, 0, (size_t)m * (size_t)w->rows * (y_is_fp32 ? 4 : 2), s), "cudaMemsetAsync(y)");
@@ -618,6 +483,17 @@ lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t
   g.steps = (g.k + kStep - 1) / kStep;
   g.segments = 1;
   while (g.segments < kSegments && 4 * g.segments <= g.steps) g.segments *= 2;
+  if (ad) {
+    g.count = ad->count;
+    g.rank = (int)ad->rank;
+    const int64_t ctas = m * (ad->rank / kInnerRows);
+    if (ctas > 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "adapters: too many tokens");
+    lpq_status st = cuda_check(
+        launch_dependent(adapter_inner_kernel, dim3((unsigned)ctas), dim3(kInnerThreads), 0, s, static_cast<const __nv_bfloat16*>(ad->a),
+                         ad->scale, ad->index, ad->count, g.rank, static_cast<const __nv_bfloat16*>(x), ldx, g.k, ad->inner),
+        "adapter launch");
+    if (st != LPQ_OK) return st;
+  }
   // Tokens per pass: 8 or fewer, what fits a CTA's shared memory when a
   // cluster shares K.
   const bool plain = w->sf_layout == LPQ_SF_PLAIN;
@@ -640,7 +516,13 @@ lpq_status launch_matvec(const lpq_qview* w, const void* x, int64_t ldx, int64_t
     g.cluster = groups * g.segments <= 4 * device_sms() || x_bytes > (wide_cta ? 64 : 24) * 1024 ? g.segments : 1;
     g.x = static_cast<const __nv_bfloat16*>(x) + m0 * ldx;
     g.y = static_cast<uint8_t*>(y) + (size_t)m0 * (size_t)g.n * (y_is_fp32 ? 4 : 2);
-    lpq_status st = (mx ? run_tokens<true> : run_tokens<false>)(g, (int)passes, plain, wide_cta && g.cluster == 1, s);
+    if (ad) {
+      g.b = static_cast<const __nv_bfloat16*>(ad->b);
+      g.index = ad->index + m0;
+      g.inner = ad->inner + m0 * ad->rank;
+    }
+    const auto run = ad ? (mx ? run_tokens<true, true> : run_tokens<false, true>) : (mx ? run_tokens<true, false> : run_tokens<false, false>);
+    lpq_status st = run(g, (int)passes, plain, wide_cta && g.cluster == 1, s);
     if (st != LPQ_OK) return st;
     m0 += passes * g.m;
   }

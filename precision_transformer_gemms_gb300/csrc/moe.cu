@@ -1,0 +1,589 @@
+// A mixture-of-experts layer for a few tokens on 4-bit weights, on sm_103a.
+//
+//   route:  l = x Wr^T;  the k largest (ties: the lower index);  p = softmax over them
+//   layer:  y_i = sum over j of p_ij W2_e (silu(W1g_e x_i) * (W1u_e x_i)),  e = ids_ij
+//
+// The chosen experts' weights, read once, are the traffic there is; their rows
+// stream, decode and multiply as in the plain products of a few tokens.  Two
+// launches.  Up: an item is 64 hidden values of an expert, whose gate and up rows
+// share a warp's 16 MMA rows, so that a lane ends with both and stores silu(g) u;
+// the MMA's columns are the tokens that chose the expert.  Down: an item is 128
+// rows of an expert, whose results lie in a workspace until the last expert of
+// those rows has come: that CTA adds them up per token, in the order of the
+// token's choice.  Which experts there are, and for whom, every CTA reads from
+// the ids by itself.
+//
+// Hidden values enter the second product as f16 times a power of two per vector
+// (the largest in [2^14, 2^15)): 11 significant bits, a thirty-second of y's own
+// bf16 rounding.  Everything else is exact or FP32.
+#include <algorithm>
+#include <type_traits>
+
+#include "fp4_rows.cuh"
+
+namespace lpq {
+namespace {
+
+// ------------------------------------------------------------------ the router
+// A cluster takes up to T tokens: its warps share the experts (and the columns,
+// where there are few experts), the logits meet in shared memory, and CTA i picks
+// token i's experts.
+constexpr int kRouteCtas = 8, kRouteWarps = 16;
+
+// Floats in the order of their values, from 1 (NaN, below -infinity) up; -0 = +0.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return v != v ? 1u : b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+template <int T>
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs g, int split) {
+  extern __shared__ float logits[];  // [split][T][experts of this CTA]; then, in CTA i, all of token i's: [experts]
+  let_dependents_start();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int64_t m0 = (int64_t)(blockIdx.x / kRouteCtas) * T;
+  const int mm = (int)min((int64_t)T, g.m - m0);
+  const int mine = (g.experts + kRouteCtas - 1) / kRouteCtas;  // experts rank, rank + 8, ...
+  for (int task = warp; task < mine * split; task += kRouteWarps) {
+    const int local = task / split, part = task - local * split;
+    const int e = rank + local * kRouteCtas;
+    if (e >= g.experts) continue;
+    const __nv_bfloat16* w = g.w + (int64_t)e * g.ldw;
+    float sum[T] = {};
+#pragma unroll 4
+    for (int c = (part * 32 + lane) * 8; c < g.d; c += split * 256) {
+      float f[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(w + c)), f);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        float x[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(g.x + (m0 + min(t, mm - 1)) * g.ldx + c)), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[t] = fmaf(f[i], x[i], sum[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xFFFFFFFFu, sum[t], o);
+      if (lane == 0) logits[(part * T + t) * mine + local] = sum[t];
+    }
+  }
+  cluster_sync_all();
+  float* row = logits + ((split * T * mine + 1) & ~1);
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(row + ((g.experts + 1) & ~1));
+  if (rank < mm) {
+    for (int e = threadIdx.x; e < g.experts; e += 32 * kRouteWarps) {
+      const uint32_t from = mapa_shared(smem_u32(logits + rank * mine + e / kRouteCtas), (uint32_t)(e % kRouteCtas));
+      float v = 0.f;
+      for (int p = 0; p < split; ++p) v += ld_shared_cluster(from + p * T * mine * 4);
+      row[e] = v;
+      keys[e] = (unsigned long long)ordered(v) << 32 | (0xFFFFFFFFu - (uint32_t)e);
+    }
+  }
+  cluster_sync_all();  // (no CTA leaves while another may still read its logits)
+  if (rank >= mm || warp != 0) return;
+  int pick = 0;
+  float value = 0.f, top = 0.f;  // lane j: the j-th choice
+  for (int j = 0; j < g.k; ++j) {
+    unsigned long long best = 0;
+    for (int e = lane; e < g.experts; e += 32) best = max(best, keys[e]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+    const int e = (int)(0xFFFFFFFFu - (uint32_t)best);
+    if (j == 0) top = row[e];
+    if (lane == j) {
+      pick = e;
+      value = row[e];
+    }
+    __syncwarp();
+    if (lane == 0) keys[e] = 0;
+    __syncwarp();
+  }
+  float sum = 0.f;
+  if (g.renormalize) {
+    if (lane < g.k) sum = expf(value - top);
+  } else {
+    for (int e = lane; e < g.experts; e += 32) sum += expf(row[e] - top);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane < g.k) {
+    const int64_t at = (m0 + rank) * g.k + lane;
+    g.ids[at] = pick;
+    g.probs[at] = __fdiv_rn(expf(value - top), sum);
+  }
+}
+
+template <int T>
+lpq_status route(const RouteArgs& g, cudaStream_t s) {
+  const int mine = (g.experts + kRouteCtas - 1) / kRouteCtas;
+  int split = 1;  // while warps idle and a part keeps two loads a lane
+  while (mine * split < kRouteWarps && split * 1024 <= g.d) split *= 2;
+  const int smem = (((split * T * mine + 1) & ~1) + ((g.experts + 1) & ~1)) * 4 + g.experts * 8;
+  const void* kernel = reinterpret_cast<const void*>(moe_route_kernel<T>);
+  lpq_status st = set_smem_attr(kernel, 96 * 1024);
+  if (st != LPQ_OK) return st;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((g.m + T - 1) / T * kRouteCtas));
+  cfg.blockDim = dim3(32 * kRouteWarps);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kRouteCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_check(cudaLaunchKernelEx(&cfg, moe_route_kernel<T>, g, split), "route launch");
+}
+
+// ------------------------------------------------------------------ the experts
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kRing = 4;          // chunks of a warp on their way
+constexpr int kMostPairs = 512;   // (token, choice) pairs of a launch
+
+struct MoeKernelArgs {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* tensor_scale;
+  int64_t kt;       // scale atoms per 128-row group
+  int k;            // columns of the weights
+  int rows;         // results of an expert: hidden values (up), rows (down)
+  int tiles;        // items of an expert
+  int m, top, experts;
+  const int64_t* ids;    // [m, top]
+  const float* probs;    // down
+  const __nv_bfloat16* x;  // up: [m, k]
+  int64_t ldx;
+  float* hidden;    // [pair, hidden values]
+  float* results;   // [pair, rows], down
+  int* arrived;     // [tiles], down; set to 0 by up
+  int down_tiles;
+  __nv_bfloat16* y;  // [m, rows], down
+  int x_words;      // 16-byte words of a vector in shared memory
+};
+
+// Which experts a launch reads, and the pairs of each, in shared memory.
+struct Plan {
+  int16_t id[kMostPairs];        // of a pair: its expert, or -1
+  uint16_t pair[kMostPairs];     // the pairs, by expert
+  uint16_t expert[kMostPairs];   // entries: up to MP pairs of one expert
+  uint16_t first[kMostPairs];    // of an entry: its place in `pair`
+  uint8_t count[kMostPairs];
+  int entries;
+};
+
+// count and start: room for the experts' numbers.
+template <int MP>
+__device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g, int* count, int* start) {
+  const int pairs = g.m * g.top, tid = threadIdx.x;
+  for (int e = tid; e < g.experts; e += kThreads) count[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int64_t e = g.ids[i];
+    const bool there = (uint64_t)e < (uint64_t)g.experts;
+    p.id[i] = there ? (int16_t)e : -1;
+    if (there) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  if (tid < 32) {  // running sums over the experts
+    int pairs_before = 0, entries_before = 0;
+    for (int e0 = 0; e0 < g.experts; e0 += 32) {
+      const int e = e0 + tid, n = e < g.experts ? count[e] : 0, c = (n + MP - 1) / MP;
+      int np = n, nc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xFFFFFFFFu, np, o), b = __shfl_up_sync(0xFFFFFFFFu, nc, o);
+        if (tid >= o) {
+          np += a;
+          nc += b;
+        }
+      }
+      if (e < g.experts) start[e] = pairs_before + np - n;
+      for (int i = 0; i < c; ++i) {
+        const int at = entries_before + nc - c + i;
+        p.expert[at] = (uint16_t)e;
+        p.first[at] = (uint16_t)(pairs_before + np - n + i * MP);
+        p.count[at] = (uint8_t)min(MP, n - i * MP);
+      }
+      pairs_before += __shfl_sync(0xFFFFFFFFu, np, 31);
+      entries_before += __shfl_sync(0xFFFFFFFFu, nc, 31);
+    }
+    if (tid == 0) p.entries = entries_before;
+  }
+  __syncthreads();
+  // (the order of an expert's pairs is that of the atomics; each has a column of its own)
+  for (int i = tid; i < pairs; i += kThreads)
+    if (p.id[i] >= 0) p.pair[atomicAdd(&start[p.id[i]], 1)] = (uint16_t)i;
+  __syncthreads();
+}
+
+template <bool MX, int MP, bool UP>
+__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g) {
+  extern __shared__ uint4 sx[];
+  __shared__ Plan plan;
+  __shared__ uint32_t red[2][kTokens][kWarps];
+  __shared__ float back_sh[kTokens];
+  __shared__ int last_sh;
+  constexpr int kSums = kTokens * 16;
+  float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int gid = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_u32(sums + kWarps * kSums) + warp * (kRing * kSlot);
+  int* numbers = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sums + kWarps * kSums) + kWarps * kRing * kSlot);
+  if constexpr (UP) {
+    wait_for_stream();
+    let_dependents_start();  // not before: down reads the ids and the weights without a wait of its own
+    if (blockIdx.x == 0)
+      for (int i = tid; i < g.down_tiles; i += kThreads) g.arrived[i] = 0;
+  } else {
+    let_dependents_start();
+  }
+  make_plan<MP>(plan, g, numbers, numbers + g.experts);
+  const int items = plan.entries * g.tiles;
+  const int chunks = (g.k + kChunk - 1) / kChunk;
+
+  // ---- the weight stream
+  const uint32_t codes_sh = ring + lane * 16, scales_sh = ring + 1024 + lane * 4;
+  constexpr int kChunkS = MX ? 512 : 1024;
+  // The tile's rows for this lane: up, a gate and an up row of one hidden value; down, two rows.
+  auto value_of = [&](int tile, int r) {  // place in the expert's results of row r of 16 (up: of 8) of this warp's tile
+    return UP ? (tile >> 1) * 128 + 32 * (r & 3) + 16 * (tile & 1) + 2 * warp + (r >> 2)
+              : tile * 128 + 32 * (r & 3) + 4 * warp + (r >> 2);
+  };
+  const uint8_t *pc = nullptr, *pc2 = nullptr, *ps = nullptr, *ps2 = nullptr;
+  int a_item = blockIdx.x, a_chunk = 0;
+  uint32_t a_slot = 0;
+  auto set_item = [&]() {
+    const int entry = a_item / g.tiles, tile = a_item - entry * g.tiles;
+    const int64_t e = plan.expert[entry];
+    const int last = g.rows - 1;  // rows beyond the expert read its last one; their results are not stored
+    int64_t r1, r2;
+    if constexpr (UP) {
+      r1 = e * 2 * g.rows + min(value_of(tile, gid), last);
+      r2 = r1 + g.rows;
+    } else {
+      r1 = e * g.rows + min(value_of(tile, gid), last);
+      r2 = e * g.rows + min(value_of(tile, gid + 8), last);
+    }
+    pc = g.codes + r1 * (g.k >> 1) + t * 16;
+    pc2 = g.codes + r2 * (g.k >> 1) + t * 16;
+    ps = g.scales + sf_gemm_offset(r1, 0, g.kt) + (MX ? 0 : (t >> 1) * 512);
+    ps2 = g.scales + sf_gemm_offset(r2, 0, g.kt) + (MX ? 0 : (t >> 1) * 512);
+  };
+  auto copy = [&]() {  // the next chunk of the stream
+    if (a_item < items) {
+      const uint32_t c = codes_sh + a_slot, sc = scales_sh + a_slot;
+      const bool in = a_chunk * kChunk + t * 32 < g.k;
+      cp_async_or_zero<16>(c, in ? pc : g.codes, in);
+      cp_async_or_zero<16>(c + 512, in ? pc2 : g.codes, in);
+      cp_async_or_zero<4>(sc, in ? ps : g.scales, in);
+      cp_async_or_zero<4>(sc + 128, in ? ps2 : g.scales, in);
+      pc += kChunk / 2;
+      pc2 += kChunk / 2;
+      ps += kChunkS;
+      ps2 += kChunkS;
+      if (++a_chunk == chunks) {
+        a_chunk = 0;
+        a_item += gridDim.x;
+        if (a_item < items) set_item();
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    a_slot = a_slot == (kRing - 1) * kSlot ? 0 : a_slot + kSlot;
+  };
+  if (a_item < items) set_item();
+#pragma unroll
+  for (int i = 0; i < kRing; ++i) copy();
+  if constexpr (!UP) {
+    wait_for_stream();  // the hidden values are there
+    if (items == 0)     // no token has an expert
+      for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (int64_t)g.m * g.rows; i += (int64_t)gridDim.x * kThreads)
+        g.y[i] = __float2bfloat16_rn(0.f);
+  }
+
+  const float tensor = MX ? 1.0f : *g.tensor_scale;
+  const int words = g.k >> 3, all_words = chunks * (kChunk / 8);
+  auto place = [&](int c, int i) { return (((i >> 4) * 4 + (i & 3)) * MP + c) * 4 + ((i >> 2) & 3); };
+  float* mine = sums + warp * kSums;
+  uint32_t slot = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int entry = item / g.tiles, tile = item - entry * g.tiles;
+    const int n = plan.count[entry];
+    const uint16_t* pair = plan.pair + plan.first[entry];
+    // ---- the entry's vectors as operand entries: their range, then their values
+    const uint4* xs[MP];
+#pragma unroll
+    for (int c = 0; c < MP; ++c)
+      if (c < n)
+        xs[c] = UP ? reinterpret_cast<const uint4*>(g.x + (int64_t)(pair[c] / g.top) * g.ldx)
+                   : reinterpret_cast<const uint4*>(g.hidden + (int64_t)pair[c] * g.k);
+#pragma unroll
+    for (int c = 0; c < MP; ++c) {
+      if (c >= n) break;
+      uint32_t top = 0, least = 0xFFFFFFFFu;
+      for (int i = tid; i < words; i += kThreads) {
+        if constexpr (UP) {
+          const uint4 v = __ldg(xs[c] + i);
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a = u[j] & 0x7FFF7FFFu;
+            top = __vmaxu2(top, a);
+            least = __vminu2(least, __vsub2(a, 0x00010001u));
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = xs[c][2 * i + h];
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a = u[j] & 0x7FFFFFFFu;
+              if (a < 0x7F800000u) top = max(top, a);  // (no number keeps what it is)
+            }
+          }
+        }
+      }
+      if constexpr (UP) {
+        top = max(top >> 16, top & 0xFFFFu);
+        least = min(least >> 16, least & 0xFFFFu);
+      }
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      least = __reduce_min_sync(0xFFFFFFFFu, least);
+      if (lane == 0) {
+        red[0][c][warp] = top;
+        red[1][c][warp] = least;
+      }
+    }
+    __syncthreads();  // (the last item's products are done, too)
+    bool f16 = true;
+    float up_by[MP];
+#pragma unroll
+    for (int c = 0; c < MP; ++c) {
+      if (c >= n) break;
+      uint32_t top = 0, least = 0xFFFFFFFFu;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        top = max(top, red[0][c][w]);
+        least = min(least, red[1][c][w]);
+      }
+      int shift;
+      if constexpr (UP) {  // (bf16 bits; as in the plain products: exact or not in f16)
+        least = (least & 0xFFFFu) + 1u;
+        shift = top ? min(141 - (int)max(top >> 7, 1u), 126) : 0;
+        f16 = f16 && top < 0x7F80u && (least > 0xFFFFu || (least >> 7 ? (int)(least >> 7) : -6) + shift >= 110);
+      } else {
+        shift = top ? min(141 - (int)max(top >> 23, 1u), 126) : 0;
+      }
+      up_by[c] = __uint_as_float((uint32_t)(127 + shift) << 23);
+      if (tid == 0) back_sh[c] = __uint_as_float((uint32_t)(127 - shift) << 23);
+    }
+#pragma unroll
+    for (int c = 0; c < MP; ++c) {
+      if (c >= n) break;
+      for (int i = tid; i < all_words; i += kThreads) {
+        uint32_t r[4] = {0, 0, 0, 0};
+        if (i < words) {
+          if constexpr (UP) {
+            const uint4 v = __ldg(xs[c] + i);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            if (f16) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * up_by[c], bf16_hi(u[j]) * up_by[c]);
+                r[j] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+            } else {
+              r[0] = __byte_perm(v.x, v.z, 0x5410);
+              r[1] = __byte_perm(v.x, v.z, 0x7632);
+              r[2] = __byte_perm(v.y, v.w, 0x5410);
+              r[3] = __byte_perm(v.y, v.w, 0x7632);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 v = xs[c][2 * i + h];
+              const __half2 lo = __floats2half2_rn(__uint_as_float(v.x) * up_by[c], __uint_as_float(v.y) * up_by[c]);
+              const __half2 hi = __floats2half2_rn(__uint_as_float(v.z) * up_by[c], __uint_as_float(v.w) * up_by[c]);
+              r[2 * h] = *reinterpret_cast<const uint32_t*>(&lo);
+              r[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+            }
+          }
+        }
+        sx[place(c, i)] = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+    }
+    __syncthreads();
+
+    // ---- the products
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine[(2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = 0.f;  // far_chunk adds to it
+      __syncwarp();
+    }
+    const int col = min(gid, MP - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
+    auto stream = [&](auto f16_path) {
+      constexpr bool F16 = decltype(f16_path)::value;
+      const uint4* e = sx;
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c, e += (kChunk / 8) * MP) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        Load l;
+        l.lo = ld_shared_16(codes_sh + slot);
+        l.hi = ld_shared_16(codes_sh + slot + 512);
+        const uint32_t at = scales_sh + slot + (MX ? t : (t & 1) * 2);
+        l.slo = ld_shared_scale<MX>(at);
+        l.shi = ld_shared_scale<MX>(at + 128);
+        if (MX && F16 && mx_far(l))
+          far_chunk(l.lo, l.hi, l.slo, l.shi, e + t, MP, n, back_sh, mine);
+        else
+          chunk_products<MX, F16, MP>(l, e + col, acc);
+        copy();  // into the slot whose values have just been used
+        slot = slot == (kRing - 1) * kSlot ? 0 : slot + kSlot;
+      }
+    };
+    if (!UP || f16) stream(std::true_type{}); else stream(std::false_type{});
+    if constexpr (MX) __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = 2 * t + (i & 1);
+      acc[i] *= !UP || f16 ? back_sh[min(c, n - 1)] : MX ? 1.0f : 256.0f;
+      if constexpr (MX) acc[i] += mine[c * 16 + gid + (i >> 1) * 8];
+      acc[i] *= tensor;
+    }
+    if constexpr (UP) {
+      const int v = value_of(tile, gid);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = 2 * t + i;
+        const float gate = acc[i], lin = acc[2 + i];
+        if (c < n && v < g.rows) g.hidden[(int64_t)pair[c] * g.rows + v] = __fdiv_rn(gate, 1.0f + expf(-gate)) * lin;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = 2 * t + (i & 1), v = value_of(tile, gid + (i >> 1) * 8);
+        if (c < n && v < g.rows) g.results[(int64_t)pair[c] * g.rows + v] = acc[i];
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) last_sh = atomicAdd(&g.arrived[tile], 1) == plan.entries - 1;
+      __syncthreads();
+      if (last_sh) {  // all experts' results of these rows are there
+        __threadfence();
+        const int v = tile * 128 + (tid & 127);
+        if (v < g.rows)
+          for (int i = tid >> 7; i < g.m; i += kThreads / 128) {
+            float sum = 0.f;
+#pragma unroll 4
+            for (int j = i * g.top; j < (i + 1) * g.top; ++j)
+              if (plan.id[j] >= 0) sum = fmaf(__ldcg(g.probs + j), __ldcg(g.results + (int64_t)j * g.rows + v), sum);
+            g.y[(int64_t)i * g.rows + v] = __float2bfloat16_rn(sum);
+          }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+int smem_bytes(int k, int mp, int experts) {
+  const int chunks = (k + kChunk - 1) / kChunk;
+  return chunks * (kChunk / 8) * 16 * mp + kWarps * kTokens * 16 * 4 + kWarps * kRing * kSlot + 2 * experts * 4;
+}
+
+template <bool MX, int MP, bool UP>
+lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
+  const void* kernel = reinterpret_cast<const void*>(moe_kernel<MX, MP, UP>);
+  lpq_status st = set_smem_attr(kernel, 216 * 1024);
+  if (st != LPQ_OK) return st;
+  g.x_words = (g.k + kChunk - 1) / kChunk * (kChunk / 8);
+  const int smem = smem_bytes(g.k, MP, g.experts);
+  const int resident = std::max(1, std::min(2, 226 * 1024 / (smem + 8 * 1024)));
+  const int64_t items = (int64_t)g.m * g.top * g.tiles;  // at most
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)resident * device_sms()));
+  return cuda_check(launch_dependent(moe_kernel<MX, MP, UP>, dim3(grid), dim3(kThreads), smem, s, g), UP ? "moe up launch" : "moe down launch");
+}
+
+template <bool UP>
+lpq_status run_tokens(MoeKernelArgs& g, bool mx, int mp, cudaStream_t s) {
+  switch (mp) {
+    case 1: return mx ? run<true, 1, UP>(g, s) : run<false, 1, UP>(g, s);
+    case 2: return mx ? run<true, 2, UP>(g, s) : run<false, 2, UP>(g, s);
+    case 4: return mx ? run<true, 4, UP>(g, s) : run<false, 4, UP>(g, s);
+    default: return mx ? run<true, 8, UP>(g, s) : run<false, 8, UP>(g, s);
+  }
+}
+
+constexpr int kXBytes = 128 * 1024;  // most shared memory for an item's vectors
+
+// Columns of an item: enough for an expert's tokens as a rule, and what fits.
+int columns(int64_t m, int64_t top, int64_t experts, int64_t k) {
+  int mp = m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 || m * top <= 2 * experts ? 4 : 8;
+  while (mp > 1 && (k + kChunk - 1) / kChunk * kChunk * 2 * mp > kXBytes) mp /= 2;
+  return mp;
+}
+int64_t tokens_of_launch(int64_t top) { return std::max<int64_t>(1, kMostPairs / std::max<int64_t>(top, 1)); }
+int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
+size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
+
+}  // namespace
+
+lpq_status launch_moe_route(const RouteArgs& g, cudaStream_t s) {
+  if (g.m == 0) return LPQ_OK;
+  return g.m <= 1 ? route<1>(g, s) : g.m <= 2 ? route<2>(g, s) : g.m <= 4 ? route<4>(g, s) : route<8>(g, s);
+}
+
+size_t moe_workspace(int64_t m, int64_t top, int64_t hidden, int64_t inter) {
+  const size_t pairs = (size_t)(std::min(m, tokens_of_launch(top)) * top);
+  return round16(pairs * (size_t)inter * 4) + round16(pairs * (size_t)hidden * 4) + round16((size_t)tiles_of(hidden) * 4);
+}
+
+lpq_status launch_moe(const MoeArgs& a, cudaStream_t s) {
+  if (a.m == 0) return LPQ_OK;
+  const int64_t hidden = a.up->cols, inter = a.down->cols;
+  if (a.top == 0)  // no expert
+    return cuda_check(cudaMemsetAsync(a.y, 0, (size_t)a.m * (size_t)hidden * 2, s), "cudaMemsetAsync(y)");
+  for (int64_t m0 = 0; m0 < a.m; m0 += tokens_of_launch(a.top)) {
+    MoeKernelArgs g{};
+    g.m = (int)std::min(a.m - m0, tokens_of_launch(a.top));
+    const size_t pairs = (size_t)g.m * (size_t)a.top;
+    g.top = (int)a.top;
+    g.experts = (int)a.experts;
+    g.ids = a.ids + m0 * a.top;
+    g.probs = a.probs + m0 * a.top;
+    g.x = static_cast<const __nv_bfloat16*>(a.x) + m0 * a.ldx;
+    g.ldx = a.ldx;
+    g.y = static_cast<__nv_bfloat16*>(a.y) + m0 * hidden;
+    g.hidden = reinterpret_cast<float*>(a.workspace);
+    g.results = reinterpret_cast<float*>(a.workspace + round16(pairs * (size_t)inter * 4));
+    g.arrived = reinterpret_cast<int*>(a.workspace + round16(pairs * (size_t)inter * 4) + round16(pairs * (size_t)hidden * 4));
+    g.down_tiles = (int)tiles_of(hidden);
+    const bool mx = a.up->fmt == LPQ_MXFP4;
+    auto weights = [&](const lpq_qview* w) {
+      g.codes = static_cast<const uint8_t*>(w->codes);
+      g.scales = static_cast<const uint8_t*>(w->scales);
+      g.tensor_scale = w->tensor_scale;
+      g.k = (int)w->cols;
+      g.kt = sf_kt_atoms(w->fmt, w->cols);
+    };
+    weights(a.up);
+    g.rows = (int)inter;
+    // (the second half of a 128-value group has work where the group's 16 first rows do not hold all)
+    g.tiles = (int)(inter / 128 * 2 + (inter % 128 == 0 ? 0 : inter % 128 <= 16 ? 1 : 2));
+    lpq_status st = run_tokens<true>(g, mx, columns(g.m, a.top, a.experts, g.k), s);
+    if (st != LPQ_OK) return st;
+    weights(a.down);
+    g.rows = (int)hidden;
+    g.tiles = g.down_tiles;
+    st = run_tokens<false>(g, a.down->fmt == LPQ_MXFP4, columns(g.m, a.top, a.experts, g.k), s);
+    if (st != LPQ_OK) return st;
+  }
+  return LPQ_OK;
+}
+
+}  // namespace lpq

@@ -93,6 +93,11 @@ class LogitControls(ctypes.Structure):
                 ("allowed", ctypes.c_void_p), ("ld_allowed", ctypes.c_int64)]
 
 
+class AdaptersC(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("rank", ctypes.c_int64)]
+
+
 class TransformerCfg(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int64), ("intermediate", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("layers", ctypes.c_int64), ("micro_batch", ctypes.c_int64), ("seq", ctypes.c_int64)]
@@ -140,6 +145,11 @@ def lib():
         L.lpq_qk_norm_rope_backward.argtypes = [P, I64, P, I64, I32, I64, I64, I64, I64, P, P, I32, P, PD, I64, I32, F, P, I64,
                                                 P, P, P, SZ, P]
         L.lpq_adjust_logits.argtypes = [P, I64, I32, I64, I64, P, P, I64, P]  # (the controls as their bytes)
+        L.lpq_matvec_adapted.argtypes = [P, P, I64, I64, P, I32, ctypes.POINTER(AdaptersC), P, P, SZ, P]
+        L.lpq_matvec_adapted_workspace.argtypes = [I64, I64, PSZ]
+        L.lpq_moe_route.argtypes = [P, I64, P, I64, I64, I64, I64, I64, I32, P, P, P]
+        L.lpq_moe_workspace.argtypes = [I64, I64, I64, I64, PSZ]
+        L.lpq_moe.argtypes = [P, P, I64, P, I64, I64, P, P, I64, P, P, SZ, P]  # (the views as pointers or as their bytes)
         L.lpq_layer_shapes.argtypes = [ctypes.POINTER(TransformerCfg), ctypes.POINTER(GemmShape),
                                        ctypes.POINTER(I32)]
         L.lpq_last_error.restype = ctypes.c_char_p
@@ -152,7 +162,8 @@ def lib():
                      "lpq_device_status", "lpq_selftest_wait", "lpq_mma_peak", "lpq_selftest_arith", "lpq_layer_norm",
                      "lpq_layer_norm_workspace", "lpq_layer_norm_backward", "lpq_linear_ce_workspace", "lpq_linear_ce",
                      "lpq_linear_ce_backward", "lpq_linear_ce_backward_ex", "lpq_matvec", "lpq_qk_norm_rope",
-                     "lpq_qk_norm_rope_workspace", "lpq_qk_norm_rope_backward", "lpq_adjust_logits"):
+                     "lpq_qk_norm_rope_workspace", "lpq_qk_norm_rope_backward", "lpq_adjust_logits",
+                     "lpq_matvec_adapted", "lpq_matvec_adapted_workspace", "lpq_moe_route", "lpq_moe_workspace", "lpq_moe"):
             getattr(L, name).restype = I32
         _lib = L
     return _lib
@@ -531,18 +542,40 @@ def linear_cross_entropy_backward(h, w, labels, lse, dloss, out_fp32=False, voca
     return dh, dw
 
 
-def matvec(x, w, out_fp32=False, stream=None):
+def matvec(x, w, out_fp32=False, stream=None, adapters=None, index=None):
     """lpq_matvec: x [m, k] bf16 (a few tokens, not quantized) times the 4-bit
-    weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n]."""
+    weights of the row-wise Copy w [n, k] (NVFP4, NVFP4_2D or MXFP4); [m, n].
+
+    With `adapters` (an Adapters) and `index` [m] int64, token i gains the product of
+    its low-rank pair index[i] (outside 0 .. count - 1: none), lpq_matvec_adapted."""
     if stream is not None:
-        return on_stream(stream, matvec, x, w, out_fp32)
+        return on_stream(stream, matvec, x, w, out_fp32, adapters=adapters, index=index)
     m, k = x.shape
     assert x.dtype is _BF16 and k == w.cols, "x must be bf16 [m, k]"
     device = x.get_device()
     assert device == w.codes.get_device(), "x must lie where the weights do"
+    if adapters is not None:
+        return _matvec_adapted(x, w, out_fp32, adapters, index)
+    assert index is None, "index goes with adapters"
     y = torch.empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device)
     _check(lib().lpq_matvec(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _raw_stream(device)))
     return y
+
+
+class Adapters:
+    """Low-rank pairs of one linear layer: a [count, rank, k], b [count, n, rank] bf16
+    (rank a multiple of 8 up to 256; pad smaller ones with zeros), scale [count] fp32
+    (None: 1)."""
+
+    def __init__(self, a, b, scale=None):
+        assert a.dtype is torch.bfloat16 and b.dtype is torch.bfloat16 and a.dim() == 3 and b.dim() == 3, \
+            "a and b must be bf16 [count, rank, k] and [count, n, rank]"
+        assert a.shape[0] == b.shape[0] and a.shape[1] == b.shape[2], "a and b must have one count and one rank"
+        assert a.is_contiguous() and b.is_contiguous() and a.is_cuda and a.get_device() == b.get_device(), \
+            "a and b must be contiguous on one CUDA device"
+        assert scale is None or (_is_vector(scale, a.shape[0], torch.float32) and scale.get_device() == a.get_device()), \
+            f"scale must be {a.shape[0]} fp32"
+        self.a, self.b, self.scale = a, b, scale
 
 
 # ----------------------------------------------------------------- around attention
@@ -645,6 +678,71 @@ def qk_norm_rope_backward(dy, x, q_heads, k_heads, head_dim, positions, q_weight
                                            positions.data_ptr(), f, rotary_dim, int(interleaved), eps, dx.data_ptr(), lddx, _ptr(dq),
                                            _ptr(dk), _ptr(ws), need, _stream_of(x)))
     return dx, dq, dk
+
+
+@functools.lru_cache(maxsize=256)
+def _adapted_workspace(m, rank):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_matvec_adapted_workspace(m, rank, ctypes.byref(n)))
+    return n.value
+
+
+@_on_its_device
+def _matvec_adapted(x, w, out_fp32, adapters, index):
+    m, k = x.shape
+    count, rank, ka = adapters.a.shape
+    assert ka == k and adapters.b.shape[1] == w.rows, f"the adapters must be of a layer {k} -> {w.rows}"
+    assert index is not None and _is_vector(index, m, torch.int64), f"index must be {m} int64"
+    _beside(x, adapters=adapters.a, index=index)
+    need = _adapted_workspace(m, rank)
+    y, ws = _new(x, (m, w.rows), _FP32 if out_fp32 else _BF16), _new(x, need, torch.uint8)
+    c = AdaptersC(_ptr(adapters.a), _ptr(adapters.b), _ptr(adapters.scale), count, rank)
+    _check(lib().lpq_matvec_adapted(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), ctypes.byref(c),
+                                    index.data_ptr(), ws.data_ptr(), need, _stream_of(x)))
+    return y
+
+
+@_on_its_device
+def moe_route(x, w, k, renormalize=True):
+    """lpq_moe_route: the k experts of every token of x [m, d] with the largest logits x
+    w^T for the router's weights w [experts, d] (bf16); returns (ids [m, k] int64 in
+    descending order, probs [m, k] fp32: the softmax over the chosen, or over all
+    without `renormalize`).  `stream`: see the module."""
+    (m, d), (experts, dw) = x.shape, w.shape
+    assert x.dtype is _BF16 and w.dtype is _BF16 and d == dw, "x and w must be bf16 with the same number of columns"
+    _beside(x, w=w)
+    ids, probs = _new(x, (m, k), _I64), _new(x, (m, k), _FP32)
+    _check(lib().lpq_moe_route(x.data_ptr(), _ld(x, m, d), w.data_ptr(), _ld(w, experts, d), m, d, experts, k, int(renormalize), ids.data_ptr(),
+                               probs.data_ptr(), _stream_of(x)))
+    return ids, probs
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_workspace(m, k, d, f):
+    n = ctypes.c_size_t()
+    _check(lib().lpq_moe_workspace(m, k, d, f, ctypes.byref(n)))
+    return n.value
+
+
+@_on_its_device
+def moe(x, up, down, experts, ids, probs):
+    """lpq_moe: y[i] = sum_j probs[i, j] W2_e (silu(W1g_e x[i]) * (W1u_e x[i])), e =
+    ids[i, j], for a few tokens x [m, d] (bf16, not quantized) on 4-bit weights: the
+    row-wise Copies up [experts * 2 f, d] (each expert's gate rows, then its up rows)
+    and down [experts * d, f] with SF_GEMM scales.  ids [m, k] int64 (outside 0 ..
+    experts - 1: no expert), probs [m, k] fp32; returns bf16 [m, d].  `stream`: see the
+    module."""
+    m, d = x.shape
+    assert x.dtype is _BF16 and d == up.cols, "x must be bf16 [m, d]"
+    assert ids.dim() == 2 and ids.shape[0] == m and ids.shape == probs.shape, f"ids and probs must be [{m}, k]"
+    k = ids.shape[1]
+    assert _is_vector(ids, m * k, _I64) and _is_vector(probs, m * k, _FP32), "ids must be int64 and probs fp32, contiguous"
+    _beside(x, up=up.codes, down=down.codes, ids=ids, probs=probs)
+    need = _moe_workspace(m, k, d, down.cols)
+    y, ws = _new(x, (m, d), _BF16), _new(x, need, torch.uint8)
+    _check(lib().lpq_moe(up.packed_view(), down.packed_view(), experts, x.data_ptr(), _ld(x, m, d), m, ids.data_ptr(), probs.data_ptr(), k,
+                         y.data_ptr(), ws.data_ptr(), need, _stream_of(x)))
+    return y
 
 
 _pack_controls = struct.Struct("@PqqPPPPPPPPqPq").pack  # LogitControls' fields

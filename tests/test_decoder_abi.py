@@ -99,3 +99,88 @@ def test_logits_refusals(kw, status):
                                 dict(v=0, ld=0, ldo=0, x=None, out=None), dict(out=A + 4, ldo=117)])
 def test_logits_accepts(kw):
     assert adjust(**kw) in VALID
+
+
+def adapted(a=A, b=A, scale=A, count=2, rank=16, index=A, ws=A, wsb=1 << 20, null=False, fmt=lpq.NVFP4, rows=32, cols=64, x=A, ldx=64, m=1, y=A, fp32=0):
+    w = lpq.QView(A, A, A, None, rows, cols, fmt, lpq.SF_GEMM, 0, 0)
+    ad = lpq.AdaptersC(a, b, scale, count, rank)
+    return lpq.lib().lpq_matvec_adapted(ctypes.byref(w), x, ldx, m, y, fp32, None if null else ctypes.byref(ad), index, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(null=True), lpq.ERR_INVALID_ARG), (dict(rank=0), lpq.ERR_SHAPE), (dict(rank=12), lpq.ERR_SHAPE), (dict(rank=264), lpq.ERR_SHAPE),
+    (dict(rank=-8), lpq.ERR_SHAPE), (dict(count=-1), lpq.ERR_SHAPE), (dict(a=None), lpq.ERR_INVALID_ARG), (dict(b=None), lpq.ERR_INVALID_ARG),
+    (dict(index=None), lpq.ERR_INVALID_ARG), (dict(a=A + 8), lpq.ERR_ALIGN), (dict(b=A + 2), lpq.ERR_ALIGN), (dict(scale=A + 2), lpq.ERR_ALIGN),
+    (dict(index=A + 4), lpq.ERR_ALIGN), (dict(ws=None), lpq.ERR_INVALID_ARG), (dict(wsb=63), lpq.ERR_INVALID_ARG), (dict(ws=A + 8), lpq.ERR_ALIGN),
+    (dict(fmt=lpq.BF16), lpq.ERR_UNSUPPORTED), (dict(m=-1), lpq.ERR_SHAPE), (dict(y=None), lpq.ERR_INVALID_ARG), (dict(ldx=56), lpq.ERR_SHAPE)])
+def test_adapted_refusals(kw, status):
+    assert adapted(**kw) == status
+
+
+@on_cpu
+@pytest.mark.parametrize("kw", [dict(), dict(scale=None), dict(count=0, a=None, b=None, index=None, ws=None, wsb=0), dict(m=0, ws=None, wsb=0, x=None, y=None, index=None)])
+def test_adapted_accepts(kw):
+    assert adapted(**kw) in VALID
+
+
+def test_adapted_workspace():
+    n = ctypes.c_size_t(7)
+    assert lpq.lib().lpq_matvec_adapted_workspace(3, 16, ctypes.byref(n)) == 0 and n.value == 3 * 16 * 4
+    assert lpq.lib().lpq_matvec_adapted_workspace(-1, 16, ctypes.byref(n)) == lpq.ERR_SHAPE
+    assert lpq.lib().lpq_matvec_adapted_workspace(1, 16, None) == lpq.ERR_INVALID_ARG
+
+
+def route(x=A, ldx=64, w=A, ldw=64, m=2, d=64, e=8, k=2, renormalize=1, ids=A, probs=A):
+    return lpq.lib().lpq_moe_route(x, ldx, w, ldw, m, d, e, k, renormalize, ids, probs, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(renormalize=2), lpq.ERR_INVALID_ARG), (dict(m=-1), lpq.ERR_SHAPE), (dict(d=0), lpq.ERR_SHAPE), (dict(d=60), lpq.ERR_SHAPE), (dict(e=0), lpq.ERR_SHAPE),
+    (dict(e=1025), lpq.ERR_SHAPE), (dict(k=0), lpq.ERR_SHAPE), (dict(k=9), lpq.ERR_SHAPE), (dict(e=64, k=33), lpq.ERR_SHAPE), (dict(ldx=56), lpq.ERR_SHAPE),
+    (dict(ldw=68), lpq.ERR_SHAPE), (dict(x=None), lpq.ERR_INVALID_ARG), (dict(w=None), lpq.ERR_INVALID_ARG), (dict(ids=None), lpq.ERR_INVALID_ARG),
+    (dict(probs=None), lpq.ERR_INVALID_ARG), (dict(x=A + 8), lpq.ERR_ALIGN), (dict(w=A + 2), lpq.ERR_ALIGN), (dict(ids=A + 4), lpq.ERR_ALIGN),
+    (dict(probs=A + 2), lpq.ERR_ALIGN)])
+def test_route_refusals(kw, status):
+    assert route(**kw) == status
+
+
+@on_cpu
+@pytest.mark.parametrize("kw", [dict(), dict(m=0, x=None, ids=None, probs=None), dict(e=1024, k=32), dict(e=1, k=1)])
+def test_route_accepts(kw):
+    assert route(**kw) in VALID
+
+
+def moe(fmt=lpq.NVFP4, fmt2=None, layout=lpq.SF_GEMM, colwise=0, d=64, f=96, e=4, rows=None, rows2=None, codes=A, scales=A, ts=A, x=A, ldx=64, m=2, ids=A, probs=A, k=2,
+        y=A, ws=A, wsb=1 << 30, null=False):
+    up = lpq.QView(codes, scales, ts, None, e * 2 * f if rows is None else rows, d, fmt, layout, colwise, 0)
+    down = lpq.QView(codes, scales, ts, None, e * d if rows2 is None else rows2, f, fmt if fmt2 is None else fmt2, layout, colwise, 0)
+    return lpq.lib().lpq_moe(None if null else ctypes.addressof(up), ctypes.addressof(down), e, x, ldx, m, ids, probs, k, y, ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(null=True), lpq.ERR_INVALID_ARG), (dict(fmt=lpq.MXFP8), lpq.ERR_UNSUPPORTED), (dict(fmt2=lpq.BF16), lpq.ERR_UNSUPPORTED), (dict(layout=lpq.SF_PLAIN), lpq.ERR_UNSUPPORTED),
+    (dict(layout=3), lpq.ERR_UNSUPPORTED), (dict(colwise=1), lpq.ERR_INVALID_ARG), (dict(d=48, ldx=48), lpq.ERR_SHAPE), (dict(f=40), lpq.ERR_SHAPE), (dict(f=0), lpq.ERR_SHAPE),
+    (dict(d=65568, ldx=65568), lpq.ERR_SHAPE), (dict(e=0), lpq.ERR_SHAPE), (dict(e=1025), lpq.ERR_SHAPE), (dict(rows=700), lpq.ERR_SHAPE), (dict(rows2=128), lpq.ERR_SHAPE),
+    (dict(codes=None), lpq.ERR_INVALID_ARG), (dict(scales=None), lpq.ERR_INVALID_ARG), (dict(ts=None), lpq.ERR_INVALID_ARG), (dict(codes=A + 8), lpq.ERR_ALIGN),
+    (dict(scales=A + 4), lpq.ERR_ALIGN), (dict(ts=A + 2), lpq.ERR_ALIGN), (dict(x=None), lpq.ERR_INVALID_ARG), (dict(x=A + 8), lpq.ERR_ALIGN), (dict(ldx=56), lpq.ERR_SHAPE),
+    (dict(ldx=68), lpq.ERR_SHAPE), (dict(m=-1), lpq.ERR_SHAPE), (dict(k=-1), lpq.ERR_SHAPE), (dict(k=33), lpq.ERR_SHAPE), (dict(ids=None), lpq.ERR_INVALID_ARG),
+    (dict(probs=None), lpq.ERR_INVALID_ARG), (dict(ids=A + 4), lpq.ERR_ALIGN), (dict(probs=A + 2), lpq.ERR_ALIGN), (dict(y=None), lpq.ERR_INVALID_ARG), (dict(y=A + 1), lpq.ERR_ALIGN),
+    (dict(ws=None), lpq.ERR_INVALID_ARG), (dict(wsb=100), lpq.ERR_INVALID_ARG), (dict(ws=A + 8), lpq.ERR_ALIGN)])
+def test_moe_refusals(kw, status):
+    assert moe(**kw) == status
+    assert lpq.last_error()
+
+
+@on_cpu
+@pytest.mark.parametrize("kw", [dict(), dict(fmt=lpq.MXFP4, fmt2=lpq.NVFP4_2D), dict(fmt=lpq.MXFP4, ts=None), dict(k=0, ids=None, probs=None), dict(m=0, x=None, y=None, ids=None, probs=None, ws=None, wsb=0)])
+def test_moe_accepts(kw):
+    assert moe(**kw) in VALID
+
+
+def test_moe_workspace():
+    n = ctypes.c_size_t(7)
+    size = lambda *a: (lpq.lib().lpq_moe_workspace(*a, ctypes.byref(n)), n.value)
+    assert size(8, 8, 4096, 1536)[1] >= 64 * (4096 + 1536) * 4
+    assert size(100000, 8, 4096, 1536)[1] < 16 << 20  # the tokens of one launch
+    assert size(1, 1, 40, 32)[0] == lpq.ERR_SHAPE and size(1, 33, 32, 32)[0] == lpq.ERR_SHAPE and size(-1, 1, 32, 32)[0] == lpq.ERR_SHAPE
+    assert lpq.lib().lpq_moe_workspace(1, 1, 32, 32, None) == lpq.ERR_INVALID_ARG
