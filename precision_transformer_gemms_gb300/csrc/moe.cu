@@ -215,9 +215,14 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g, int* 
     if (tid == 0) p.entries = entries_before;
   }
   __syncthreads();
-  // (the order of an expert's pairs is that of the atomics; each has a column of its own)
-  for (int i = tid; i < pairs; i += kThreads)
-    if (p.id[i] >= 0) p.pair[atomicAdd(&start[p.id[i]], 1)] = (uint16_t)i;
+  // An expert's pairs in their own order: all CTAs have to put the same ones into an entry.
+  for (int i = tid; i < pairs; i += kThreads) {
+    const int16_t e = p.id[i];
+    if (e < 0) continue;
+    int before = 0;
+    for (int j = 0; j < i; ++j) before += p.id[j] == e;
+    p.pair[start[e] + before] = (uint16_t)i;
+  }
   __syncthreads();
 }
 

@@ -31,6 +31,17 @@ namespace {
 constexpr int kWarps = 8;                    // per CTA
 constexpr int kMaxPairs = kQkMaxDim / 2;
 
+// Head groups on their way per warp in the vector form (1 or 2 KB each way, FP32
+// twice that), and CTAs per SM.
+template <typename T, bool BACKWARD>
+struct Ring {
+  static constexpr int kDepth = sizeof(T) == 4 ? 3 : 4;
+  static constexpr int kPieces = 2 * 8 * sizeof(T) / 16 * (BACKWARD ? 2 : 1);  // 16-byte pieces of a lane
+  static constexpr int kStage = kPieces * 512;
+  static constexpr int kBytes = kWarps * kDepth * kStage;
+  static constexpr int kCtas = BACKWARD ? 2 : 3;
+};
+
 struct QkKernelArgs {
   const void* x;
   const void* dy;
@@ -39,6 +50,7 @@ struct QkKernelArgs {
   const void* weight[2];  // of the query heads, of the key heads; NULL: 1
   const int64_t* positions;
   float* parts;  // backward: [CTA][2][D], or NULL
+  int64_t rows;
   int64_t groups;  // of heads: tokens * (those of the queries and of the keys)
   int heads[2];    // query heads, key heads
   int runs[2];     // groups of 32 / lanes heads
@@ -69,6 +81,19 @@ struct Raw {
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
     for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+  }
+  // Through a lane's places in shared memory, 512 bytes apart.
+  static __device__ __forceinline__ void copy(uint32_t to, const T* p, bool there) {
+#pragma unroll
+    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(reinterpret_cast<const uint4*>(p) + i),
+                   "r"(there ? 16 : 0) : "memory");
+  }
+  __device__ __forceinline__ void take(uint32_t from) {
+#pragma unroll
+    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                   : "r"(from + i * 512) : "memory");
   }
   __device__ __forceinline__ float get(int i) const {  // i is a constant after unrolling
     if constexpr (sizeof(T) == 4) {
@@ -131,6 +156,17 @@ struct Slice {
         b[j] = Raw<T, V>{};
       }
     }
+  }
+  // The same through the ring (V > 1); `head` is any address of the tensor where nothing is there.
+  static __device__ __forceinline__ void copy(const QkKernelArgs& g, uint32_t to, const T* head, int lane, bool there) {
+    int at, bt;
+    there = place(g, lane, 0, at, bt) && there;
+    Raw<T, V>::copy(to, there ? head + at : head, there);
+    Raw<T, V>::copy(to + V * sizeof(T) / 16 * 512, there ? head + bt : head, there);
+  }
+  __device__ __forceinline__ void take(uint32_t from) {
+    a[0].take(from);
+    b[0].take(from + V * sizeof(T) / 16 * 512);
   }
   // Pair i of the thread as its two values.
   __device__ __forceinline__ void pair(int i, float& p, float& q) const {
@@ -195,8 +231,11 @@ __device__ __forceinline__ float lanes_sum(float v, int lanes) {
 template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD>
 __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(const __grid_constant__ QkKernelArgs g) {
   using S = Slice<T, V, NU, NEIGHBOURS>;
+  using R = Ring<T, BACKWARD>;
   constexpr int P = S::P;
-  extern __shared__ float sh[];  // weights [2][dim]; backward, at the end: sums [warp][2][dim]
+  constexpr bool kRing = V > 1;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* sh = reinterpret_cast<float*>(smem + (kRing ? R::kBytes : 0));  // weights [2][dim]; backward, at the end: sums [warp][2][dim]
   __shared__ uint64_t turns[kMaxPairs];
   let_dependents_start();
   wait_for_stream();
@@ -235,19 +274,45 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
     head += kind ? g.heads[0] : 0;
     return there;
   };
-  S nx, ny;  // the group that comes next
-  auto fetch = [&](int64_t t, int r) {
-    int kind, head;
-    const bool there = head_of(r, kind, head);
-    nx.load(g, x + t * g.ldx + (int64_t)head * g.dim, lane, there);
-    if constexpr (BACKWARD) ny.load(g, dy + t * g.lddy + (int64_t)head * g.dim, lane, there);
+  // The groups to come: in registers, or in the warp's ring (a lane reads back what it copied itself).
+  S nx, ny;
+  int64_t f_left = end - begin, f_token = token;
+  int f_run = run;
+  uint32_t f_at = 0, at = 0;
+  const uint32_t ring = smem_u32(smem) + warp * (R::kDepth * R::kStage) + (threadIdx.x & 31) * 16;
+  auto fetch = [&]() {
+    if (f_left > 0) {
+      --f_left;
+      int kind, head;
+      const bool there = head_of(f_run, kind, head);
+      const T* px = x + f_token * g.ldx + (there ? (int64_t)head * g.dim : 0);
+      const T* py = BACKWARD ? dy + f_token * g.lddy + (there ? (int64_t)head * g.dim : 0) : nullptr;
+      if constexpr (kRing) {
+        S::copy(g, ring + f_at, px, lane, there);
+        if constexpr (BACKWARD) S::copy(g, ring + f_at + R::kStage / 2, py, lane, there);
+      } else {
+        nx.load(g, px, lane, there);
+        if constexpr (BACKWARD) ny.load(g, py, lane, there);
+      }
+      if (++f_run == per_token) {
+        f_run = 0;
+        ++f_token;
+      }
+    }
+    if constexpr (kRing) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      f_at = f_at == (R::kDepth - 1) * R::kStage ? 0 : f_at + R::kStage;
+    }
   };
-  if (begin < end) fetch(token, run);
+#pragma unroll
+  for (int i = 0; i < (kRing ? R::kDepth : 1); ++i) fetch();
   int held = -1;  // the kind whose weights are in registers
   bool new_token = true;
+  int64_t next_position = begin < end ? g.positions[token] : 0;
   for (int64_t i = begin; i < end; ++i) {
     if (new_token) {
-      const int64_t position = g.positions[token];
+      const int64_t position = next_position;
+      if (token + 1 < g.rows) next_position = g.positions[token + 1];
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         const int u = lane + (k / V) * g.lanes, f = u * V + k % V;
@@ -271,15 +336,23 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
         wq[k] = in ? sh[kind * g.dim + q] : 0.f;
       }
     }
-    S cx = nx, cy;
-    if constexpr (BACKWARD) cy = ny;
+    S cx, cy;
+    if constexpr (kRing) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
+      cx.take(ring + at);
+      if constexpr (BACKWARD) cy.take(ring + at + R::kStage / 2);
+      at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
+    } else {
+      cx = nx;
+      if constexpr (BACKWARD) cy = ny;
+      fetch();
+    }
     const int64_t this_token = token;
     new_token = ++run == per_token;
     if (new_token) {
       run = 0;
       ++token;
     }
-    if (i + 1 < end) fetch(token, run);
 
     float p[P], q[P];
     float square = 0.f;
@@ -292,6 +365,7 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
     T* to = out + this_token * g.ldo + (int64_t)head * g.dim;
     if constexpr (!BACKWARD) {
       const float rstd = __frsqrt_rn(fmaf(lanes_sum(square, g.lanes), inv_dim, g.eps));
+      if constexpr (kRing) fetch();  // into the place whose values have entered the sum
 #pragma unroll
       for (int k = 0; k < P; ++k) {
         const float a = p[k] * rstd * wp[k], b = q[k] * rstd * wq[k];
@@ -314,6 +388,7 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
         square += __shfl_xor_sync(0xFFFFFFFFu, square, o);
         dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
       }
+      if constexpr (kRing) fetch();  // into the place whose values have entered the sums
       const float rstd = __frsqrt_rn(fmaf(square, inv_dim, g.eps));
       const float back = dot * inv_dim * rstd * rstd;
 #pragma unroll
@@ -337,6 +412,7 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
   if constexpr (BACKWARD) {
     if (!g.parts) return;
     // the warp's groups of lanes, then the warps, in a fixed order
+    if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind)
@@ -387,8 +463,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qk_join_kernel(const float* p
   }
 }
 
-// CTAs of the backward pass, each of which leaves a part of the weights' gradients.
-constexpr int kBackwardCtas = 2;  // per SM
+// Most CTAs of the backward pass, each of which leaves a part of the weights' gradients.
 int64_t most_parts() { return 2 * 160; }
 
 template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD>
@@ -399,10 +474,12 @@ lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t
   while (g.lanes < 32 && g.lanes < units) g.lanes *= 2;
   for (int i = 0; i < 2; ++i) g.runs[i] = (g.heads[i] * g.lanes + 31) / 32;
   g.groups = rows * (g.runs[0] + g.runs[1]);
-  const int smem = (BACKWARD ? kWarps : 1) * 2 * g.dim * (int)sizeof(float);
-  lpq_status st = set_smem_attr(kernel, (BACKWARD ? kWarps : 1) * 2 * kQkMaxDim * (int)sizeof(float));
+  g.rows = rows;
+  const int ring = V > 1 ? Ring<T, BACKWARD>::kBytes : 0;
+  const int smem = ring + (BACKWARD ? kWarps : 1) * 2 * g.dim * (int)sizeof(float);
+  lpq_status st = set_smem_attr(kernel, ring + (BACKWARD ? kWarps : 1) * 2 * kQkMaxDim * (int)sizeof(float));
   if (st != LPQ_OK) return st;
-  int64_t most = (int64_t)device_sms() * (BACKWARD ? kBackwardCtas : resident_ctas(kernel, 32 * kWarps, 2 * kQkMaxDim * 4));
+  int64_t most = (int64_t)device_sms() * std::max(1, std::min(Ring<T, BACKWARD>::kCtas, 226 * 1024 / (smem + 4 * 1024)));
   if (BACKWARD) most = std::min(most, most_parts());
   const int64_t grid = std::max<int64_t>(1, std::min(most, (g.groups + kWarps - 1) / kWarps));
   st = cuda_check(launch_dependent(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD>, dim3((unsigned)grid), dim3(32 * kWarps), smem, s, g),

@@ -186,7 +186,7 @@ def test_route(m, d, e, k, renormalize):
     assert ids.dtype == torch.int64 and probs.dtype == torch.float32 and ids.shape == probs.shape == (m, k)
     logits = x.double() @ w.double().T
     off = ((d / 32 + 13) * U * (x.double().abs() @ w.double().abs().T)).amax(1, keepdim=True)
-    best, order = logits.sort(1, descending=True, stable=True)
+    best, order = logits.sort(dim=1, descending=True, stable=True)
     clear = torch.ones_like(ids, dtype=torch.bool)
     if e > 1:
         gap = best[:, :-1] - best[:, 1:] > 2 * off
@@ -207,7 +207,7 @@ def test_route_ties_and_special_values():
     w = torch.randint(-1, 2, (96, 64), generator=g, device="cuda").bfloat16()
     w[48:] = w[:48]
     ids, _ = lpq.moe_route(x, w, 10)
-    assert torch.equal(ids, (x.double() @ w.double().T).sort(1, descending=True, stable=True).indices[:, :10])
+    assert torch.equal(ids, (x.double() @ w.double().T).sort(dim=1, descending=True, stable=True).indices[:, :10])
     ids, probs = lpq.moe_route(torch.zeros_like(x), w, 3)  # -0 and 0 alike
     assert torch.equal(ids, torch.arange(3, device="cuda").expand(40, 3)) and bool((probs - 1 / 3).abs().max() < 1e-6)
     bad = w.clone()
