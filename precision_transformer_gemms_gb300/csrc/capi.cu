@@ -565,7 +565,7 @@ lpq_status lpq_moe_route(const void* x, int64_t ldx, const void* w, int64_t ldw,
                          int32_t renormalize, int64_t* ids, float* probs, lpq_stream_t stream) {
   if (renormalize < 0 || renormalize > 1) return set_error(LPQ_ERR_INVALID_ARG, "renormalize %d", renormalize);
   if (m < 0 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "m %lld", (long long)m);
-  if (d < 8 || d % 8 || d > (int64_t)1 << 20) return set_error(LPQ_ERR_SHAPE, "d %lld not a multiple of 8, 8 to 2^20", (long long)d);
+  if (d < 8 || d % 8 || d > 65536) return set_error(LPQ_ERR_SHAPE, "d %lld not a multiple of 8, 8 to 65536", (long long)d);
   if (experts < 1 || experts > kMoeMostExperts) return set_error(LPQ_ERR_SHAPE, "experts %lld, at most %d", (long long)experts, kMoeMostExperts);
   if (k < 1 || k > kMoeMostChoices || k > experts)
     return set_error(LPQ_ERR_SHAPE, "k %lld of %lld experts, at most %d", (long long)k, (long long)experts, kMoeMostChoices);
@@ -647,7 +647,7 @@ lpq_status check_qk(QkArgs& a, const void* x, int64_t ldx, int32_t type, int64_t
   if (rotary_dim < 0 || rotary_dim > head_dim || rotary_dim % 2)
     return set_error(LPQ_ERR_SHAPE, "rotary_dim %lld must be even, 0 to head_dim", (long long)rotary_dim);
   const int64_t most = (int64_t)1 << 20;
-  if (rows < 0 || q_heads < 0 || k_heads < 0 || rows > (int64_t)1 << 40 || q_heads > most || k_heads > most)
+  if (rows < 0 || q_heads < 0 || k_heads < 0 || rows > (int64_t)1 << 30 || q_heads > most || k_heads > most)
     return set_error(LPQ_ERR_SHAPE, "rows %lld, heads %lld and %lld", (long long)rows, (long long)q_heads, (long long)k_heads);
   const int64_t cols = (q_heads + k_heads) * head_dim;
   lpq_status st = check_matrix(cols ? x : &a, "x", ldx, rows, cols, type_bytes(type));

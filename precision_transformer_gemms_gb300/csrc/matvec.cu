@@ -102,6 +102,14 @@ __device__ __forceinline__ float adapter_row(const MatvecArgs& g, int64_t token,
   return sum;
 }
 
+// Brings that row of B_e to the L2.
+__device__ __forceinline__ void prefetch_adapter_row(const MatvecArgs& g, int64_t token, int row) {
+  const int64_t e = g.index[token];
+  if ((uint64_t)e >= (uint64_t)g.count || row >= g.n) return;
+  const char* b = reinterpret_cast<const char*>(g.b + (e * g.n + row) * g.rank);
+  for (int i = 0; i < g.rank * 2; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
+}
+
 // inner[token, r] = s A_e[r] . x: a CTA for four rows of a token.
 constexpr int kInnerRows = 4, kInnerThreads = 256;
 __global__ void __launch_bounds__(kInnerThreads) adapter_inner_kernel(const __nv_bfloat16* a, const float* scale, const int64_t* index,
@@ -330,6 +338,13 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const Ma
   int jbuf = 0;
   for (int item = first_item; item < g.items; item += item_step, jbuf ^= 1) {
     float* mine = sums + (jbuf * W + warp) * kSums;
+    if constexpr (ADAPTED) {  // the rows that this CTA finishes, for the end of the item
+      const int per = shared_k ? 16 * W / g.cluster : 16 * slots;
+      for (int e = threadIdx.x; e < per * mm; e += kThreads) {
+        const int r = rank * per + e / mm;
+        prefetch_adapter_row(g, m0 + e % mm, row_of(item, r >> 4, r & 15));
+      }
+    }
     float acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -438,19 +453,21 @@ lpq_status run_matvec(MatvecArgs g, int passes, cudaStream_t s) {
     return cuda_check(launch_dependent(matvec_kernel<MX, SFG, MP, W, ADAPTED>, grid, 32 * W, smem, s, g), "matvec launch");
   // Clusters start when the stream is done: an early start would place them
   // around the kernel ahead and leave the SMs unevenly loaded (16384 -> 4096:
-  // 19.9 us, 14.7 us so).
+  // 19.9 us, 14.7 us so).  The inner vectors' kernel is too small for that.
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * W);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)g.cluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ADAPTED ? 2 : 1;
   return cuda_check(cudaLaunchKernelEx(&cfg, matvec_kernel<MX, SFG, MP, W, ADAPTED>, g), "matvec launch");
 }
 

@@ -25,10 +25,13 @@ namespace lpq {
 namespace {
 
 // ------------------------------------------------------------------ the router
-// A cluster takes up to T tokens: its warps share the experts (and the columns,
-// where there are few experts), the logits meet in shared memory, and CTA i picks
-// token i's experts.
+// A cluster takes up to T tokens, each of its CTAs an eighth of the columns for all
+// experts, so that every load is on its way at once; the parts of the logits meet in
+// shared memory, and CTA i adds those of token i up, in order, and picks its experts.
+// Products are FP32 FMAs: the tensor core's cut of its sum every 16 products would
+// move choices between experts that are nearly equal.
 constexpr int kRouteCtas = 8, kRouteWarps = 16;
+constexpr int kAtOnce = 4;  // experts of a warp
 
 // Floats in the order of their values, from 1 (NaN, below -infinity) up; -0 = +0.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -36,53 +39,83 @@ __device__ __forceinline__ uint32_t ordered(float v) {
   return v != v ? 1u : b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// The warp's sums of N values per lane (N a power of two up to 32): value i lands in
+// the lanes i * 32 / N ..; each step halves the values a lane holds.
+template <int N>
+__device__ __forceinline__ float warp_sums(float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = N / 2; n > 0; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float other = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + n], o);
+      v[i] = (up ? v[i + n] : v[i]) + other;
+    }
+  }
+  for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+  return v[0];
+}
+
 template <int T>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs g, int split) {
-  extern __shared__ float logits[];  // [split][T][experts of this CTA]; then, in CTA i, all of token i's: [experts]
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const RouteArgs g) {
+  extern __shared__ uint4 route_sh[];
   let_dependents_start();
+  wait_for_stream();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int64_t m0 = (int64_t)(blockIdx.x / kRouteCtas) * T;
   const int mm = (int)min((int64_t)T, g.m - m0);
-  const int mine = (g.experts + kRouteCtas - 1) / kRouteCtas;  // experts rank, rank + 8, ...
-  for (int task = warp; task < mine * split; task += kRouteWarps) {
-    const int local = task / split, part = task - local * split;
-    const int e = rank + local * kRouteCtas;
-    if (e >= g.experts) continue;
-    const __nv_bfloat16* w = g.w + (int64_t)e * g.ldw;
-    float sum[T] = {};
-#pragma unroll 4
-    for (int c = (part * 32 + lane) * 8; c < g.d; c += split * 256) {
-      float f[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w + c)), f);
+  const int words = g.d >> 3, most = (words + kRouteCtas - 1) / kRouteCtas;  // of 8 columns
+  const int first = min(rank * most, words), mine = min(most, words - first);
+  uint4* xs = route_sh;                                    // [T][most]
+  float* parts = reinterpret_cast<float*>(xs + T * most);  // [T][experts], of these columns
+  float* row = parts + T * g.experts;                      // [experts]: all of token `rank`'s
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(row + ((g.experts + 1) & ~1) + (T * g.experts & 1));
+  for (int i = threadIdx.x; i < T * mine; i += 32 * kRouteWarps) {
+    const int t = i / mine, c = i - t * mine;
+    xs[t * most + c] = __ldg(reinterpret_cast<const uint4*>(g.x + (m0 + min(t, mm - 1)) * g.ldx) + first + c);
+  }
+  __syncthreads();
+  for (int e0 = warp * kAtOnce; e0 < g.experts; e0 += kRouteWarps * kAtOnce) {
+    float sum[kAtOnce * T] = {};
+#pragma unroll 2
+    for (int c = lane; c < mine; c += 32) {
+      uint4 w[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        w[i] = __ldg(reinterpret_cast<const uint4*>(g.w + (int64_t)min(e0 + i, g.experts - 1) * g.ldw) + first + c);
 #pragma unroll
       for (int t = 0; t < T; ++t) {
         float x[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(g.x + (m0 + min(t, mm - 1)) * g.ldx + c)), x);
+        unpack8(xs[t * most + c], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[t] = fmaf(f[i], x[i], sum[t]);
+        for (int i = 0; i < kAtOnce; ++i) {
+          float f[8];
+          unpack8(w[i], f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[i * T + t] = fmaf(f[j], x[j], sum[i * T + t]);
+        }
       }
     }
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xFFFFFFFFu, sum[t], o);
-      if (lane == 0) logits[(part * T + t) * mine + local] = sum[t];
-    }
+    constexpr int kLanes = 32 / (kAtOnce * T);  // that end with the same value
+    const float v = warp_sums(sum);
+    const int i = lane / kLanes / T, t = lane / kLanes % T;
+    if (lane % kLanes == 0 && e0 + i < g.experts) parts[t * g.experts + e0 + i] = v;
   }
   cluster_sync_all();
-  float* row = logits + ((split * T * mine + 1) & ~1);
-  unsigned long long* keys = reinterpret_cast<unsigned long long*>(row + ((g.experts + 1) & ~1));
   if (rank < mm) {
     for (int e = threadIdx.x; e < g.experts; e += 32 * kRouteWarps) {
-      const uint32_t from = mapa_shared(smem_u32(logits + rank * mine + e / kRouteCtas), (uint32_t)(e % kRouteCtas));
+      const uint32_t from = smem_u32(parts + rank * g.experts + e);
       float v = 0.f;
-      for (int p = 0; p < split; ++p) v += ld_shared_cluster(from + p * T * mine * 4);
+#pragma unroll
+      for (int p = 0; p < kRouteCtas; ++p) v += ld_shared_cluster(mapa_shared(from, (uint32_t)p));
       row[e] = v;
       keys[e] = (unsigned long long)ordered(v) << 32 | (0xFFFFFFFFu - (uint32_t)e);
     }
   }
-  cluster_sync_all();  // (no CTA leaves while another may still read its logits)
+  cluster_sync_all();  // (no CTA leaves while another may still read its parts)
   if (rank >= mm || warp != 0) return;
   int pick = 0;
   float value = 0.f, top = 0.f;  // lane j: the j-th choice
@@ -118,31 +151,32 @@ __global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(const Route
 
 template <int T>
 lpq_status route(const RouteArgs& g, cudaStream_t s) {
-  const int mine = (g.experts + kRouteCtas - 1) / kRouteCtas;
-  int split = 1;  // while warps idle and a part keeps two loads a lane
-  while (mine * split < kRouteWarps && split * 1024 <= g.d) split *= 2;
-  const int smem = (((split * T * mine + 1) & ~1) + ((g.experts + 1) & ~1)) * 4 + g.experts * 8;
+  const int words = g.d / 8, most = (words + kRouteCtas - 1) / kRouteCtas;
+  const int smem = T * most * 16 + (T * g.experts + ((g.experts + 1) & ~1) + (T * g.experts & 1)) * 4 + g.experts * 8;
   const void* kernel = reinterpret_cast<const void*>(moe_route_kernel<T>);
-  lpq_status st = set_smem_attr(kernel, 96 * 1024);
+  lpq_status st = set_smem_attr(kernel, 200 * 1024);
   if (st != LPQ_OK) return st;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((g.m + T - 1) / T * kRouteCtas));
   cfg.blockDim = dim3(32 * kRouteWarps);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kRouteCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cuda_check(cudaLaunchKernelEx(&cfg, moe_route_kernel<T>, g, split), "route launch");
+  cfg.numAttrs = 2;
+  return cuda_check(cudaLaunchKernelEx(&cfg, moe_route_kernel<T>, g), "route launch");
 }
 
 // ------------------------------------------------------------------ the experts
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRing = 4;          // chunks of a warp on their way
+constexpr int kRing = 3;          // chunks of a warp on their way
+constexpr int kCtas = 3;          // per SM, where their vectors fit
 constexpr int kMostPairs = 512;   // (token, choice) pairs of a launch
 
 struct MoeKernelArgs {
@@ -152,7 +186,7 @@ struct MoeKernelArgs {
   int64_t kt;       // scale atoms per 128-row group
   int k;            // columns of the weights
   int rows;         // results of an expert: hidden values (up), rows (down)
-  int tiles;        // items of an expert
+  int tiles;        // of an expert: warps' shares of its rows
   int m, top, experts;
   const int64_t* ids;    // [m, top]
   const float* probs;    // down
@@ -227,12 +261,11 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g, int* 
 }
 
 template <bool MX, int MP, bool UP>
-__global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g) {
+__global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArgs g) {
   extern __shared__ uint4 sx[];
   __shared__ Plan plan;
   __shared__ uint32_t red[2][kTokens][kWarps];
   __shared__ float back_sh[kTokens];
-  __shared__ int last_sh;
   constexpr int kSums = kTokens * 16;
   float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -248,19 +281,23 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
     let_dependents_start();
   }
   make_plan<MP>(plan, g, numbers, numbers + g.experts);
-  const int items = plan.entries * g.tiles;
+  // This CTA's run of tiles, which its warps take in turn: all CTAs have equally many,
+  // and neighbours find their vectors staged.
+  const int64_t all_tiles = (int64_t)plan.entries * g.tiles;
+  const int begin = (int)(all_tiles * blockIdx.x / gridDim.x), end = (int)(all_tiles * (blockIdx.x + 1) / gridDim.x);
   const int chunks = (g.k + kChunk - 1) / kChunk;
 
   // ---- the weight stream
   const uint32_t codes_sh = ring + lane * 16, scales_sh = ring + 1024 + lane * 4;
   constexpr int kChunkS = MX ? 512 : 1024;
-  // The tile's rows for this lane: up, a gate and an up row of one hidden value; down, two rows.
-  auto value_of = [&](int tile, int r) {  // place in the expert's results of row r of 16 (up: of 8) of this warp's tile
-    return UP ? (tile >> 1) * 128 + 32 * (r & 3) + 16 * (tile & 1) + 2 * warp + (r >> 2)
-              : tile * 128 + 32 * (r & 3) + 4 * warp + (r >> 2);
+  // The tile's rows for this lane: up, a gate and an up row of one hidden value; down,
+  // two rows.  A tile's rows are runs of 2 or 4 neighbours 32 apart, whose scales of 4
+  // blocks lie side by side where the expert begins with a 128-row group.
+  auto value_of = [&](int tile, int r) {  // place in the expert's results of row r of 16 (up: of 8)
+    return UP ? (tile >> 4) * 128 + 32 * (r & 3) + 2 * (tile & 15) + (r >> 2) : (tile >> 3) * 128 + 32 * (r & 3) + 4 * (tile & 7) + (r >> 2);
   };
   const uint8_t *pc = nullptr, *pc2 = nullptr, *ps = nullptr, *ps2 = nullptr;
-  int a_item = blockIdx.x, a_chunk = 0;
+  int a_item = begin + warp, a_chunk = 0;
   uint32_t a_slot = 0;
   auto set_item = [&]() {
     const int entry = a_item / g.tiles, tile = a_item - entry * g.tiles;
@@ -280,32 +317,39 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
     ps2 = g.scales + sf_gemm_offset(r2, 0, g.kt) + (MX ? 0 : (t >> 1) * 512);
   };
   auto copy = [&]() {  // the next chunk of the stream
-    if (a_item < items) {
+    if (a_item < end) {
       const uint32_t c = codes_sh + a_slot, sc = scales_sh + a_slot;
-      const bool in = a_chunk * kChunk + t * 32 < g.k;
-      cp_async_or_zero<16>(c, in ? pc : g.codes, in);
-      cp_async_or_zero<16>(c + 512, in ? pc2 : g.codes, in);
-      cp_async_or_zero<4>(sc, in ? ps : g.scales, in);
-      cp_async_or_zero<4>(sc + 128, in ? ps2 : g.scales, in);
+      if ((a_chunk + 1) * kChunk <= g.k) {
+        cp_async<16>(c, pc);
+        cp_async<16>(c + 512, pc2);
+        cp_async<4>(sc, ps);
+        cp_async<4>(sc + 128, ps2);
+      } else {
+        const bool in = a_chunk * kChunk + t * 32 < g.k;
+        cp_async_or_zero<16>(c, in ? pc : g.codes, in);
+        cp_async_or_zero<16>(c + 512, in ? pc2 : g.codes, in);
+        cp_async_or_zero<4>(sc, in ? ps : g.scales, in);
+        cp_async_or_zero<4>(sc + 128, in ? ps2 : g.scales, in);
+      }
       pc += kChunk / 2;
       pc2 += kChunk / 2;
       ps += kChunkS;
       ps2 += kChunkS;
       if (++a_chunk == chunks) {
         a_chunk = 0;
-        a_item += gridDim.x;
-        if (a_item < items) set_item();
+        a_item += kWarps;
+        if (a_item < end) set_item();
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     a_slot = a_slot == (kRing - 1) * kSlot ? 0 : a_slot + kSlot;
   };
-  if (a_item < items) set_item();
+  if (a_item < end) set_item();
 #pragma unroll
   for (int i = 0; i < kRing; ++i) copy();
   if constexpr (!UP) {
     wait_for_stream();  // the hidden values are there
-    if (items == 0)     // no token has an expert
+    if (all_tiles == 0)  // no token has an expert
       for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (int64_t)g.m * g.rows; i += (int64_t)gridDim.x * kThreads)
         g.y[i] = __float2bfloat16_rn(0.f);
   }
@@ -315,8 +359,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
   auto place = [&](int c, int i) { return (((i >> 4) * 4 + (i & 3)) * MP + c) * 4 + ((i >> 2) & 3); };
   float* mine = sums + warp * kSums;
   uint32_t slot = 0;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int entry = item / g.tiles, tile = item - entry * g.tiles;
+  bool f16 = true;
+  int item = begin + warp;  // this warp's next tile
+  for (int entry = begin / g.tiles; entry * (int64_t)g.tiles < end; ++entry) {
     const int n = plan.count[entry];
     const uint16_t* pair = plan.pair + plan.first[entry];
     // ---- the entry's vectors as operand entries: their range, then their values
@@ -364,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
         red[1][c][warp] = least;
       }
     }
-    __syncthreads();  // (the last item's products are done, too)
-    bool f16 = true;
+    __syncthreads();  // (the products with the vectors that were there are done, too)
+    f16 = true;
     float up_by[MP];
 #pragma unroll
     for (int c = 0; c < MP; ++c) {
@@ -425,6 +470,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
     __syncthreads();
 
     // ---- the products
+    const int last_item = min(end, (entry + 1) * g.tiles);
+    for (; item < last_item; item += kWarps) {
+    const int tile = item - entry * g.tiles;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (MX) {
 #pragma unroll
@@ -475,22 +523,27 @@ __global__ void __launch_bounds__(kThreads, 2) moe_kernel(const MoeKernelArgs g)
         const int c = 2 * t + (i & 1), v = value_of(tile, gid + (i >> 1) * 8);
         if (c < n && v < g.rows) g.results[(int64_t)pair[c] * g.rows + v] = acc[i];
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) last_sh = atomicAdd(&g.arrived[tile], 1) == plan.entries - 1;
-      __syncthreads();
-      if (last_sh) {  // all experts' results of these rows are there
+      // The warp that finds all experts' results of its rows there adds them up.
+      __syncwarp();
+      int before = 0;
+      if (lane == 0) {
         __threadfence();
-        const int v = tile * 128 + (tid & 127);
+        before = atomicAdd(&g.arrived[tile], 1);
+      }
+      if (__shfl_sync(0xFFFFFFFFu, before, 0) == plan.entries - 1) {
+        __threadfence();
+        const int v = value_of(tile, lane & 15);
         if (v < g.rows)
-          for (int i = tid >> 7; i < g.m; i += kThreads / 128) {
+          for (int i = lane >> 4; i < g.m; i += 2) {
             float sum = 0.f;
 #pragma unroll 4
             for (int j = i * g.top; j < (i + 1) * g.top; ++j)
               if (plan.id[j] >= 0) sum = fmaf(__ldcg(g.probs + j), __ldcg(g.results + (int64_t)j * g.rows + v), sum);
             g.y[(int64_t)i * g.rows + v] = __float2bfloat16_rn(sum);
           }
+        __syncwarp();
       }
+    }
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -508,9 +561,9 @@ lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   if (st != LPQ_OK) return st;
   g.x_words = (g.k + kChunk - 1) / kChunk * (kChunk / 8);
   const int smem = smem_bytes(g.k, MP, g.experts);
-  const int resident = std::max(1, std::min(2, 226 * 1024 / (smem + 8 * 1024)));
-  const int64_t items = (int64_t)g.m * g.top * g.tiles;  // at most
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, (int64_t)resident * device_sms()));
+  const int resident = std::max(1, std::min(kCtas, 227 * 1024 / (smem + 7 * 1024)));
+  const int64_t tiles = (int64_t)g.m * g.top * g.tiles;  // at most
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tiles + kWarps - 1) / kWarps, (int64_t)resident * device_sms()));
   return cuda_check(launch_dependent(moe_kernel<MX, MP, UP>, dim3(grid), dim3(kThreads), smem, s, g), UP ? "moe up launch" : "moe down launch");
 }
 
@@ -533,19 +586,21 @@ int columns(int64_t m, int64_t top, int64_t experts, int64_t k) {
   return mp;
 }
 int64_t tokens_of_launch(int64_t top) { return std::max<int64_t>(1, kMostPairs / std::max<int64_t>(top, 1)); }
-int64_t tiles_of(int64_t rows) { return (rows + 127) / 128; }
+// Tiles of an expert: those with a row of it (a tile's first row is the lowest).
+int64_t up_tiles(int64_t inter) { return inter / 128 * 16 + std::min<int64_t>(16, (inter % 128 + 1) / 2); }
+int64_t down_tiles(int64_t hidden) { return hidden / 128 * 8 + std::min<int64_t>(8, (hidden % 128 + 3) / 4); }
 size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
 }  // namespace
 
 lpq_status launch_moe_route(const RouteArgs& g, cudaStream_t s) {
   if (g.m == 0) return LPQ_OK;
-  return g.m <= 1 ? route<1>(g, s) : g.m <= 2 ? route<2>(g, s) : g.m <= 4 ? route<4>(g, s) : route<8>(g, s);
+  return g.m <= 1 ? route<1>(g, s) : g.m <= 2 ? route<2>(g, s) : route<4>(g, s);
 }
 
 size_t moe_workspace(int64_t m, int64_t top, int64_t hidden, int64_t inter) {
   const size_t pairs = (size_t)(std::min(m, tokens_of_launch(top)) * top);
-  return round16(pairs * (size_t)inter * 4) + round16(pairs * (size_t)hidden * 4) + round16((size_t)tiles_of(hidden) * 4);
+  return round16(pairs * (size_t)inter * 4) + round16(pairs * (size_t)hidden * 4) + round16((size_t)down_tiles(hidden) * 4);
 }
 
 lpq_status launch_moe(const MoeArgs& a, cudaStream_t s) {
@@ -567,7 +622,7 @@ lpq_status launch_moe(const MoeArgs& a, cudaStream_t s) {
     g.hidden = reinterpret_cast<float*>(a.workspace);
     g.results = reinterpret_cast<float*>(a.workspace + round16(pairs * (size_t)inter * 4));
     g.arrived = reinterpret_cast<int*>(a.workspace + round16(pairs * (size_t)inter * 4) + round16(pairs * (size_t)hidden * 4));
-    g.down_tiles = (int)tiles_of(hidden);
+    g.down_tiles = (int)down_tiles(hidden);
     const bool mx = a.up->fmt == LPQ_MXFP4;
     auto weights = [&](const lpq_qview* w) {
       g.codes = static_cast<const uint8_t*>(w->codes);
@@ -578,8 +633,7 @@ lpq_status launch_moe(const MoeArgs& a, cudaStream_t s) {
     };
     weights(a.up);
     g.rows = (int)inter;
-    // (the second half of a 128-value group has work where the group's 16 first rows do not hold all)
-    g.tiles = (int)(inter / 128 * 2 + (inter % 128 == 0 ? 0 : inter % 128 <= 16 ? 1 : 2));
+    g.tiles = (int)up_tiles(inter);
     lpq_status st = run_tokens<true>(g, mx, columns(g.m, a.top, a.experts, g.k), s);
     if (st != LPQ_OK) return st;
     weights(a.down);

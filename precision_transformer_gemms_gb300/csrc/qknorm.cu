@@ -35,7 +35,7 @@ constexpr int kMaxPairs = kQkMaxDim / 2;
 // twice that), and CTAs per SM.
 template <typename T, bool BACKWARD>
 struct Ring {
-  static constexpr int kDepth = sizeof(T) == 4 ? 3 : 4;
+  static constexpr int kDepth = sizeof(T) == 4 ? (BACKWARD ? 2 : 3) : 4;
   static constexpr int kPieces = 2 * 8 * sizeof(T) / 16 * (BACKWARD ? 2 : 1);  // 16-byte pieces of a lane
   static constexpr int kStage = kPieces * 512;
   static constexpr int kBytes = kWarps * kDepth * kStage;
@@ -56,6 +56,7 @@ struct QkKernelArgs {
   int runs[2];     // groups of 32 / lanes heads
   int dim, rotary;
   int lanes;       // that hold a head
+  int neighbours;  // the pairs are neighbours
   int w_fp32;
   float eps;
   uint64_t turns[kMaxPairs];  // frequency / 2 pi in units of 2^-64
@@ -95,25 +96,26 @@ struct Raw {
       asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
                    : "r"(from + i * 512) : "memory");
   }
-  __device__ __forceinline__ float get(int i) const {  // i is a constant after unrolling
+  // Values 2 i and 2 i + 1 (i is a constant after unrolling).
+  __device__ __forceinline__ float2 get2(int i) const {
     if constexpr (sizeof(T) == 4) {
-      const uint4& u = v[i >> 2];
-      return __uint_as_float((i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w);
+      const uint4& u = v[i >> 1];
+      return i & 1 ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w)) : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
     } else {
-      const uint4& u = v[i >> 3];
-      const uint32_t p = ((i >> 1) & 3) == 0 ? u.x : ((i >> 1) & 3) == 1 ? u.y : ((i >> 1) & 3) == 2 ? u.z : u.w;
-      return i & 1 ? bf16_hi(p) : bf16_lo(p);
+      const uint4& u = v[i >> 2];
+      const uint32_t p = (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
+      return make_float2(bf16_lo(p), bf16_hi(p));
     }
   }
-  __device__ __forceinline__ void set2(int i, float a, float b) {  // values i and i + 1, i even
-    uint4& u = v[sizeof(T) == 4 ? i >> 2 : i >> 3];
+  __device__ __forceinline__ void set2(int i, float a, float b) {
+    uint4& u = v[sizeof(T) == 4 ? i >> 1 : i >> 2];
     if constexpr (sizeof(T) == 4) {
-      if ((i & 3) == 0) { u.x = __float_as_uint(a); u.y = __float_as_uint(b); }
-      else { u.z = __float_as_uint(a); u.w = __float_as_uint(b); }
+      if (i & 1) { u.z = __float_as_uint(a); u.w = __float_as_uint(b); }
+      else { u.x = __float_as_uint(a); u.y = __float_as_uint(b); }
     } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
       const uint32_t p = *reinterpret_cast<const uint32_t*>(&h);
-      if (((i >> 1) & 3) == 0) u.x = p; else if (((i >> 1) & 3) == 1) u.y = p; else if (((i >> 1) & 3) == 2) u.z = p; else u.w = p;
+      if ((i & 3) == 0) u.x = p; else if ((i & 3) == 1) u.y = p; else if ((i & 3) == 2) u.z = p; else u.w = p;
     }
   }
 };
@@ -124,8 +126,9 @@ struct Raw<T, 1> {
   __device__ __forceinline__ void store(T* p) const { *p = v; }
 };
 
-// A thread's part of a head: P pairs, as NU units of V pairs.  Vectors: V = 8,
-// one unit.  Any alignment and sizes: V = 1, units 32 apart.
+// A thread's part of a head: P pairs (even), as NU units of V pairs.  Vectors: V =
+// 8, one unit.  Any alignment and sizes: V = 1, units 32 apart.  Pairs 2 j and 2 j +
+// 1 lie in one float2 of firsts and one of seconds, for the two-wide operations.
 template <typename T, int V, int NU, bool NEIGHBOURS>
 struct Slice {
   static constexpr int P = V * NU;
@@ -135,7 +138,7 @@ struct Slice {
   static __device__ __forceinline__ bool place(const QkKernelArgs& g, int lane, int j, int& at, int& bt) {
     const int u = lane + j * g.lanes;
     const int turned = g.rotary / (2 * V);
-    if (NEIGHBOURS || u >= turned) {  // (values that are not turned lie side by side)
+    if (V == 1 ? g.neighbours || u >= turned : NEIGHBOURS || u >= turned) {  // (values that are not turned lie side by side)
       at = u * 2 * V;
       bt = at + V;
     } else {
@@ -144,6 +147,7 @@ struct Slice {
     }
     return u * 2 * V < g.dim;
   }
+  // Value by value (V = 1).
   __device__ __forceinline__ void load(const QkKernelArgs& g, const T* head, int lane, bool there) {
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
@@ -157,52 +161,46 @@ struct Slice {
       }
     }
   }
-  // The same through the ring (V > 1); `head` is any address of the tensor where nothing is there.
-  static __device__ __forceinline__ void copy(const QkKernelArgs& g, uint32_t to, const T* head, int lane, bool there) {
-    int at, bt;
-    there = place(g, lane, 0, at, bt) && there;
-    Raw<T, V>::copy(to, there ? head + at : head, there);
-    Raw<T, V>::copy(to + V * sizeof(T) / 16 * 512, there ? head + bt : head, there);
-  }
-  __device__ __forceinline__ void take(uint32_t from) {
-    a[0].take(from);
-    b[0].take(from + V * sizeof(T) / 16 * 512);
-  }
-  // Pair i of the thread as its two values.
-  __device__ __forceinline__ void pair(int i, float& p, float& q) const {
-    const int j = i / V, k = i % V;
-    if constexpr (V == 1) {
-      p = to_f32(a[j].v);
-      q = to_f32(b[j].v);
-    } else if constexpr (NEIGHBOURS) {
-      const Raw<T, V>& r = k < V / 2 ? a[j] : b[j];
-      p = r.get(2 * k % V);
-      q = r.get(2 * k % V + 1);
-    } else {
-      p = a[j].get(k);
-      q = b[j].get(k);
+  __device__ __forceinline__ void values(float2 (&p)[P / 2], float2 (&q)[P / 2]) const {
+#pragma unroll
+    for (int j = 0; j < P / 2; ++j) {
+      if constexpr (V == 1) {
+        p[j] = make_float2(to_f32(a[2 * j].v), to_f32(a[2 * j + 1].v));
+        q[j] = make_float2(to_f32(b[2 * j].v), to_f32(b[2 * j + 1].v));
+      } else if constexpr (NEIGHBOURS) {
+        const Raw<T, V>& r = j < V / 4 ? a[0] : b[0];
+        const float2 u = r.get2(2 * j % (V / 2)), v = r.get2(2 * j % (V / 2) + 1);
+        p[j] = make_float2(u.x, v.x);
+        q[j] = make_float2(u.y, v.y);
+      } else {
+        p[j] = a[0].get2(j);
+        q[j] = b[0].get2(j);
+      }
     }
   }
-  __device__ __forceinline__ void store(const QkKernelArgs& g, T* head, int lane, const float (&p)[P], const float (&q)[P]) {
+  __device__ __forceinline__ void set(const float2 (&p)[P / 2], const float2 (&q)[P / 2]) {
+#pragma unroll
+    for (int j = 0; j < P / 2; ++j) {
+      if constexpr (V == 1) {
+        a[2 * j].v = from_f32<T>(p[j].x);
+        a[2 * j + 1].v = from_f32<T>(p[j].y);
+        b[2 * j].v = from_f32<T>(q[j].x);
+        b[2 * j + 1].v = from_f32<T>(q[j].y);
+      } else if constexpr (NEIGHBOURS) {
+        Raw<T, V>& r = j < V / 4 ? a[0] : b[0];
+        r.set2(2 * j % (V / 2), p[j].x, q[j].x);
+        r.set2(2 * j % (V / 2) + 1, p[j].y, q[j].y);
+      } else {
+        a[0].set2(j, p[j].x, p[j].y);
+        b[0].set2(j, q[j].x, q[j].y);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const QkKernelArgs& g, T* head, int lane) const {
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       int at, bt;
       if (!place(g, lane, j, at, bt)) continue;
-      if constexpr (V == 1) {
-        a[j].v = from_f32<T>(p[j]);
-        b[j].v = from_f32<T>(q[j]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          if constexpr (NEIGHBOURS) {
-            a[j].set2(k, p[k / 2], q[k / 2]);
-            b[j].set2(k, p[V / 2 + k / 2], q[V / 2 + k / 2]);
-          } else {
-            a[j].set2(k, p[k], p[k + 1]);
-            b[j].set2(k, q[k], q[k + 1]);
-          }
-        }
-      }
       a[j].store(head + at);
       b[j].store(head + bt);
     }
@@ -222,82 +220,114 @@ struct Slice {
   }
 };
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
+__device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
-// A warp takes a run of the head groups (32 / lanes heads each), in token order.
-template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD>
-__global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(const __grid_constant__ QkKernelArgs g) {
+// A warp takes a run of the head groups (32 / lanes heads each): those of all
+// tokens' queries in token order, then those of the keys, so that the weights change
+// once at most.  LANES > 0: heads of 16 LANES values in whole groups, every lane with
+// a unit of every group.
+template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD, int LANES>
+__global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm_kernel(const __grid_constant__ QkKernelArgs g) {
   using S = Slice<T, V, NU, NEIGHBOURS>;
   using R = Ring<T, BACKWARD>;
-  constexpr int P = S::P;
+  constexpr int P = S::P, H = P / 2;
   constexpr bool kRing = V > 1;
   extern __shared__ __align__(16) uint8_t smem[];
-  float* sh = reinterpret_cast<float*>(smem + (kRing ? R::kBytes : 0));  // weights [2][dim]; backward, at the end: sums [warp][2][dim]
+  // behind the ring: weights [2][dim], cos and sin [warp][rotary / 2]; backward, sums [warp][2][dim]
+  float* sh = reinterpret_cast<float*>(smem + (kRing ? R::kBytes : 0));
   __shared__ uint64_t turns[kMaxPairs];
   let_dependents_start();
   wait_for_stream();
   const int warp = threadIdx.x >> 5;
-  const int lane = (threadIdx.x & 31) & (g.lanes - 1), sub = (threadIdx.x & 31) / g.lanes;
-  for (int i = threadIdx.x; i < g.rotary / 2; i += 32 * kWarps) turns[i] = g.turns[i];
+  const int lanes = LANES ? LANES : g.lanes;
+  const int lane = (threadIdx.x & 31) & (lanes - 1), sub = (threadIdx.x & 31) / lanes;
+  const int half = g.rotary / 2;
+  float2* trig = reinterpret_cast<float2*>(sh + 2 * g.dim) + warp * half;
+  float* sums = sh + 2 * g.dim + kWarps * g.rotary;
+  for (int i = threadIdx.x; i < half; i += 32 * kWarps) turns[i] = g.turns[i];
   for (int i = threadIdx.x; i < 2 * g.dim; i += 32 * kWarps) {
     const void* w = g.weight[i >= g.dim];
     const int c = i >= g.dim ? i - g.dim : i;
     sh[i] = !w ? 1.0f : g.w_fp32 ? static_cast<const float*>(w)[c] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[c]);
   }
+  if constexpr (BACKWARD)
+    for (int i = threadIdx.x; i < kWarps * 2 * g.dim; i += 32 * kWarps) sums[i] = 0.f;
   __syncthreads();
 
   const int64_t workers = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t each = g.groups / workers, more = g.groups % workers;
-  const int64_t begin = me * each + min(me, more), end = begin + each + (me < more);
-  const int per_token = g.runs[0] + g.runs[1];
+  const int64_t begin = me * each + min(me, more), count64 = each + (me < more);
+  const int count = (int)count64;
   const float inv_dim = 1.0f / (float)g.dim;
-  const T* x = static_cast<const T*>(g.x);
-  const T* dy = static_cast<const T*>(g.dy);
-  T* out = static_cast<T*>(g.out);
+  const int per_group = 32 / lanes, step = per_group * g.dim;  // heads, and values from a group to the next
+  int unit_a = 0, unit_b = 0;  // the lane's vectors in a head
+  const bool unit = S::place(g, lane, 0, unit_a, unit_b);
 
-  float cs[P], sn[P], wp[P], wq[P];
-  float dwp[BACKWARD ? 2 : 1][P], dwq[BACKWARD ? 2 : 1][P];
-  if constexpr (BACKWARD) {
-#pragma unroll
-    for (int i = 0; i < P; ++i) dwp[0][i] = dwp[1][i] = dwq[0][i] = dwq[1][i] = 0.f;
-  }
-  int64_t token = begin / per_token;
-  int run = (int)(begin - token * per_token);
-  // The head of a group that this thread's lanes take; false: the group has no such head.
-  auto head_of = [&](int r, int& kind, int& head) {
-    kind = r >= g.runs[0];
-    head = (r - (kind ? g.runs[0] : 0)) * (32 / g.lanes) + sub;
-    const bool there = head < g.heads[kind];
-    head += kind ? g.heads[0] : 0;
-    return there;
+  // A place in the run: the group, and where its heads begin in a tensor.
+  struct Place {
+    int token, kind, run;
   };
+  auto next = [&](Place& p, auto&& same, auto&& token, auto&& kind) {  // moves on; tells by how much
+    if (++p.run < g.runs[p.kind]) return same();
+    p.run = 0;
+    if (++p.token < g.rows) return token();
+    p.token = 0;
+    p.kind = 1;
+    kind();
+  };
+  Place here{};
+  here.kind = begin >= g.rows * g.runs[0];
+  const int64_t first = begin - (here.kind ? g.rows * g.runs[0] : 0);
+  here.token = g.runs[here.kind] ? (int)(first / g.runs[here.kind]) : 0;
+  here.run = (int)(first - (int64_t)here.token * g.runs[here.kind]);
+  auto start = [&](int64_t ld) {  // of this place's group in a tensor, at this lane's head
+    return (int64_t)here.token * ld + (int64_t)(here.kind ? g.heads[0] : 0) * g.dim + (int64_t)here.run * step + sub * g.dim;
+  };
+  auto has_head = [&](const Place& p) { return LANES > 0 || p.run * per_group + sub < g.heads[p.kind]; };
+
   // The groups to come: in registers, or in the warp's ring (a lane reads back what it copied itself).
   S nx, ny;
-  int64_t f_left = end - begin, f_token = token;
-  int f_run = run;
+  int f_left = count;
+  Place f = here;
+  const T* fx = static_cast<const T*>(g.x) + start(g.ldx);
+  const T* fy = BACKWARD ? static_cast<const T*>(g.dy) + start(g.lddy) : nullptr;
   uint32_t f_at = 0, at = 0;
   const uint32_t ring = smem_u32(smem) + warp * (R::kDepth * R::kStage) + (threadIdx.x & 31) * 16;
+  constexpr uint32_t kHalf = V * sizeof(T) / 16 * 512;  // of a head's slice in a stage
   auto fetch = [&]() {
     if (f_left > 0) {
       --f_left;
-      int kind, head;
-      const bool there = head_of(f_run, kind, head);
-      const T* px = x + f_token * g.ldx + (there ? (int64_t)head * g.dim : 0);
-      const T* py = BACKWARD ? dy + f_token * g.lddy + (there ? (int64_t)head * g.dim : 0) : nullptr;
+      const bool there = has_head(f);
       if constexpr (kRing) {
-        S::copy(g, ring + f_at, px, lane, there);
-        if constexpr (BACKWARD) S::copy(g, ring + f_at + R::kStage / 2, py, lane, there);
+        const bool in = LANES > 0 || (there && unit);
+        const T* px = in ? fx : static_cast<const T*>(g.x);
+        Raw<T, V>::copy(ring + f_at, in ? px + unit_a : px, in);
+        Raw<T, V>::copy(ring + f_at + kHalf, in ? px + unit_b : px, in);
+        if constexpr (BACKWARD) {
+          const T* py = in ? fy : static_cast<const T*>(g.dy);
+          Raw<T, V>::copy(ring + f_at + R::kStage / 2, in ? py + unit_a : py, in);
+          Raw<T, V>::copy(ring + f_at + R::kStage / 2 + kHalf, in ? py + unit_b : py, in);
+        }
       } else {
-        nx.load(g, px, lane, there);
-        if constexpr (BACKWARD) ny.load(g, py, lane, there);
+        nx.load(g, fx, lane, there);
+        if constexpr (BACKWARD) ny.load(g, fy, lane, there);
       }
-      if (++f_run == per_token) {
-        f_run = 0;
-        ++f_token;
-      }
+      const int run = f.run;
+      next(
+          f,
+          [&]() {
+            fx += step;
+            if constexpr (BACKWARD) fy += step;
+          },
+          [&]() {
+            fx += g.ldx - run * step;
+            if constexpr (BACKWARD) fy += g.lddy - run * step;
+          },
+          [&]() {
+            const int64_t keys = (int64_t)g.heads[0] * g.dim + sub * g.dim;
+            fx = static_cast<const T*>(g.x) + keys;
+            if constexpr (BACKWARD) fy = static_cast<const T*>(g.dy) + keys;
+          });
     }
     if constexpr (kRing) {
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -306,134 +336,197 @@ __global__ void __launch_bounds__(32 * kWarps, BACKWARD ? 2 : 3) qk_norm_kernel(
   };
 #pragma unroll
   for (int i = 0; i < (kRing ? R::kDepth : 1); ++i) fetch();
-  int held = -1;  // the kind whose weights are in registers
-  bool new_token = true;
-  int64_t next_position = begin < end ? g.positions[token] : 0;
-  for (int64_t i = begin; i < end; ++i) {
-    if (new_token) {
-      const int64_t position = next_position;
-      if (token + 1 < g.rows) next_position = g.positions[token + 1];
+
+  // Forward: w1 cos, -w2 sin, w2 cos, w1 sin of the thread's pairs.  Backward: w1, w2, cos, sin.
+  float2 wa[H], wb[H], wc[H], wd[H];
+  float2 dwp[BACKWARD ? H : 1], dwq[BACKWARD ? H : 1];
+  if constexpr (BACKWARD) {
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int u = lane + (k / V) * g.lanes, f = u * V + k % V;
-        cs[k] = 1.0f;
-        sn[k] = 0.0f;
-        if (f < g.rotary / 2) {
-          const int32_t half_turns = (int32_t)((turns[f] * (uint64_t)position) >> 32);  // of 2^-31
-          sincospif((float)half_turns * 4.65661287e-10f, &sn[k], &cs[k]);
-        }
+    for (int i = 0; i < H; ++i) dwp[i] = dwq[i] = twice(0.f);
+  }
+  auto leave_sums = [&](int kind) {  // the warp's groups of lanes, in a fixed order
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      float a = k & 1 ? dwp[k / 2].y : dwp[k / 2].x, b = k & 1 ? dwq[k / 2].y : dwq[k / 2].x;
+      for (int o = 16; o >= lanes; o >>= 1) {
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+        b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+      }
+      int pa, pb;
+      if (S::where(g, lane, k, pa, pb) && sub == 0) {
+        sums[(warp * 2 + kind) * g.dim + pa] += a;
+        sums[(warp * 2 + kind) * g.dim + pb] += b;
       }
     }
-    int kind, head;
-    const bool there = head_of(run, kind, head);
-    if (kind != held) {
-      held = kind;
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        int p, q;
-        const bool in = S::where(g, lane, k, p, q);
-        wp[k] = in ? sh[kind * g.dim + p] : 0.f;
-        wq[k] = in ? sh[kind * g.dim + q] : 0.f;
+    for (int i = 0; i < H; ++i) dwp[i] = dwq[i] = twice(0.f);
+  };
+  bool new_token = true;
+  int64_t next_position = count > 0 ? g.positions[here.token] : 0;
+  T* to = static_cast<T*>(g.out) + start(g.ldo);
+  for (int i = 0; i < count; ++i) {
+    if (new_token) {  // the warp's lanes share the angles
+      const uint64_t position = (uint64_t)next_position;
+      next_position = g.positions[here.token + 1 < g.rows ? here.token + 1 : 0];
+      __syncwarp();
+      for (int j = threadIdx.x & 31; j < half; j += 32) {
+        const int32_t half_turns = (int32_t)((turns[j] * position) >> 32);  // of 2^-31
+        float s, c;
+        sincospif((float)half_turns * 4.65661287e-10f, &s, &c);
+        trig[j] = make_float2(c, s);
+      }
+      __syncwarp();
+      float2 turn[P];  // (cos, sin)
+      float w[2 * P];  // of the firsts, of the seconds
+      if constexpr (V > 1) {
+        const float* ws = sh + here.kind * g.dim;
+#pragma unroll
+        for (int k = 0; k < P; k += 4) {
+          const bool in = LANES > 0 || unit;
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 u = in ? *reinterpret_cast<const float4*>(ws + unit_a + k) : zero;
+          const float4 v = in ? *reinterpret_cast<const float4*>(ws + unit_b + k) : zero;
+          const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {  // (neighbours: the unit's 16 values one after another)
+            w[NEIGHBOURS ? (k + h) / 2 + (h & 1 ? P : 0) : k + h] = a[h];
+            w[NEIGHBOURS ? (P + k + h) / 2 + (h & 1 ? P : 0) : P + k + h] = b[h];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+          const float4 r = lane * V < half ? *reinterpret_cast<const float4*>(trig + lane * V + k) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+          turn[k] = make_float2(r.x, r.y);
+          turn[k + 1] = make_float2(r.z, r.w);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const int j = lane + k * lanes;
+          turn[k] = j < half ? trig[j] : make_float2(1.0f, 0.0f);
+          int p, q;
+          const bool in = S::where(g, lane, k, p, q);
+          w[k] = in ? sh[here.kind * g.dim + p] : 0.f;
+          w[P + k] = in ? sh[here.kind * g.dim + q] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+        const float2 c = make_float2(turn[2 * k].x, turn[2 * k + 1].x), n = make_float2(turn[2 * k].y, turn[2 * k + 1].y);
+        const float2 w1 = make_float2(w[2 * k], w[2 * k + 1]), w2 = make_float2(w[P + 2 * k], w[P + 2 * k + 1]);
+        if constexpr (BACKWARD) {
+          wa[k] = w1;
+          wb[k] = w2;
+          wc[k] = c;
+          wd[k] = n;
+        } else {
+          wa[k] = __fmul2_rn(w1, c);
+          wb[k] = __fmul2_rn(make_float2(-w2.x, -w2.y), n);
+          wc[k] = __fmul2_rn(w2, c);
+          wd[k] = __fmul2_rn(w1, n);
+        }
       }
     }
     S cx, cy;
     if constexpr (kRing) {
       asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-      cx.take(ring + at);
-      if constexpr (BACKWARD) cy.take(ring + at + R::kStage / 2);
+      cx.a[0].take(ring + at);
+      cx.b[0].take(ring + at + kHalf);
+      if constexpr (BACKWARD) {
+        cy.a[0].take(ring + at + R::kStage / 2);
+        cy.b[0].take(ring + at + R::kStage / 2 + kHalf);
+      }
       at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
     } else {
       cx = nx;
       if constexpr (BACKWARD) cy = ny;
       fetch();
     }
-    const int64_t this_token = token;
-    new_token = ++run == per_token;
-    if (new_token) {
-      run = 0;
-      ++token;
-    }
 
-    float p[P], q[P];
-    float square = 0.f;
+    float2 p[H], q[H];
+    cx.values(p, q);
+    float2 squares = twice(0.f);
 #pragma unroll
-    for (int k = 0; k < P; ++k) {
-      cx.pair(k, p[k], q[k]);
-      square = fmaf(p[k], p[k], square);
-      square = fmaf(q[k], q[k], square);
+    for (int k = 0; k < H; ++k) {
+      squares = __ffma2_rn(p[k], p[k], squares);
+      squares = __ffma2_rn(q[k], q[k], squares);
     }
-    T* to = out + this_token * g.ldo + (int64_t)head * g.dim;
+    float square = squares.x + squares.y;
+    const bool there = has_head(here);
     if constexpr (!BACKWARD) {
-      const float rstd = __frsqrt_rn(fmaf(lanes_sum(square, g.lanes), inv_dim, g.eps));
+      #pragma unroll
+      for (int o = lanes >> 1; o > 0; o >>= 1) square += __shfl_xor_sync(0xFFFFFFFFu, square, o);
       if constexpr (kRing) fetch();  // into the place whose values have entered the sum
+      const float2 rstd = twice(rsqrtf(fmaf(square, inv_dim, g.eps)));
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const float a = p[k] * rstd * wp[k], b = q[k] * rstd * wq[k];
-        p[k] = fmaf(a, cs[k], -(b * sn[k]));
-        q[k] = fmaf(b, cs[k], a * sn[k]);
+      for (int k = 0; k < H; ++k) {
+        const float2 a = __fmul2_rn(p[k], rstd), b = __fmul2_rn(q[k], rstd);
+        p[k] = __ffma2_rn(b, wb[k], __fmul2_rn(a, wa[k]));
+        q[k] = __ffma2_rn(a, wd[k], __fmul2_rn(b, wc[k]));
       }
-      if (there) cx.store(g, to, lane, p, q);
     } else {
-      float gp[P], gq[P], dot = 0.f;
+      float2 gp[H], gq[H], dots = twice(0.f);
+      cy.values(gp, gq);
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        float u, v;
-        cy.pair(k, u, v);
-        gp[k] = fmaf(u, cs[k], v * sn[k]);
-        gq[k] = fmaf(v, cs[k], -(u * sn[k]));
-        dot = fmaf(gp[k] * wp[k], p[k], dot);
-        dot = fmaf(gq[k] * wq[k], q[k], dot);
+      for (int k = 0; k < H; ++k) {
+        const float2 u = gp[k], v = gq[k];
+        gp[k] = __ffma2_rn(v, wd[k], __fmul2_rn(u, wc[k]));
+        gq[k] = __ffma2_rn(make_float2(-u.x, -u.y), wd[k], __fmul2_rn(v, wc[k]));
+        dots = __ffma2_rn(__fmul2_rn(gp[k], wa[k]), p[k], dots);
+        dots = __ffma2_rn(__fmul2_rn(gq[k], wb[k]), q[k], dots);
       }
-      for (int o = g.lanes >> 1; o > 0; o >>= 1) {
+      float dot = dots.x + dots.y;
+      #pragma unroll
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
         square += __shfl_xor_sync(0xFFFFFFFFu, square, o);
         dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
       }
       if constexpr (kRing) fetch();  // into the place whose values have entered the sums
-      const float rstd = __frsqrt_rn(fmaf(square, inv_dim, g.eps));
-      const float back = dot * inv_dim * rstd * rstd;
+      const float r = rsqrtf(fmaf(square, inv_dim, g.eps));
+      const float2 rstd = twice(r), back = twice(-(dot * inv_dim * r * r));
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const float a = gp[k] * (p[k] * rstd), b = gq[k] * (q[k] * rstd);
+      for (int k = 0; k < H; ++k) {
         if (there) {
-          if (kind == 0) {
-            dwp[0][k] += a;
-            dwq[0][k] += b;
-          } else {
-            dwp[1][k] += a;
-            dwq[1][k] += b;
-          }
+          dwp[k] = __ffma2_rn(gp[k], __fmul2_rn(p[k], rstd), dwp[k]);
+          dwq[k] = __ffma2_rn(gq[k], __fmul2_rn(q[k], rstd), dwq[k]);
         }
-        p[k] = rstd * fmaf(gp[k], wp[k], -(p[k] * back));
-        q[k] = rstd * fmaf(gq[k], wq[k], -(q[k] * back));
+        p[k] = __fmul2_rn(rstd, __ffma2_rn(p[k], back, __fmul2_rn(gp[k], wa[k])));
+        q[k] = __fmul2_rn(rstd, __ffma2_rn(q[k], back, __fmul2_rn(gq[k], wb[k])));
       }
-      if (there) cx.store(g, to, lane, p, q);
     }
+    if (there) {
+      cx.set(p, q);
+      if constexpr (kRing) {
+        if (LANES > 0 || unit) {
+          cx.a[0].store(to + unit_a);
+          cx.b[0].store(to + unit_b);
+        }
+      } else {
+        cx.store(g, to, lane);
+      }
+    }
+    const int run = here.run, kind = here.kind;
+    new_token = true;
+    next(
+        here,
+        [&]() {
+          new_token = false;
+          to += step;
+        },
+        [&]() { to += g.ldo - run * step; },
+        [&]() {
+          to = static_cast<T*>(g.out) + (int64_t)g.heads[0] * g.dim + sub * g.dim;
+          if constexpr (BACKWARD) leave_sums(kind);
+        });
   }
   if constexpr (BACKWARD) {
     if (!g.parts) return;
-    // the warp's groups of lanes, then the warps, in a fixed order
-    if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        float a = dwp[kind][k], b = dwq[kind][k];
-        for (int o = 16; o >= g.lanes; o >>= 1) {
-          a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-          b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-        }
-        int pa, pb;
-        if (S::where(g, lane, k, pa, pb) && sub == 0) {
-          sh[(warp * 2 + kind) * g.dim + pa] = a;
-          sh[(warp * 2 + kind) * g.dim + pb] = b;
-        }
-      }
+    leave_sums(here.kind);
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * g.dim; i += 32 * kWarps) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += sh[w * 2 * g.dim + i];
+      for (int w = 0; w < kWarps; ++w) s += sums[w * 2 * g.dim + i];
       g.parts[(int64_t)blockIdx.x * 2 * g.dim + i] = s;
     }
   }
@@ -466,9 +559,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qk_join_kernel(const float* p
 // Most CTAs of the backward pass, each of which leaves a part of the weights' gradients.
 int64_t most_parts() { return 2 * 160; }
 
-template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD>
+template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD, int LANES>
 lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t s) {
-  const void* kernel = reinterpret_cast<const void*>(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD>);
+  const void* kernel = reinterpret_cast<const void*>(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD, LANES>);
   const int units = (g.dim / 2 + V - 1) / V;
   g.lanes = 1;
   while (g.lanes < 32 && g.lanes < units) g.lanes *= 2;
@@ -476,13 +569,15 @@ lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t
   g.groups = rows * (g.runs[0] + g.runs[1]);
   g.rows = rows;
   const int ring = V > 1 ? Ring<T, BACKWARD>::kBytes : 0;
-  const int smem = ring + (BACKWARD ? kWarps : 1) * 2 * g.dim * (int)sizeof(float);
-  lpq_status st = set_smem_attr(kernel, ring + (BACKWARD ? kWarps : 1) * 2 * kQkMaxDim * (int)sizeof(float));
+  auto rest = [](int dim, int rotary) { return 2 * dim * 4 + kWarps * rotary / 2 * 8 + (BACKWARD ? kWarps * 2 * dim * 4 : 0); };
+  const int smem = ring + rest(g.dim, g.rotary);
+  lpq_status st = set_smem_attr(kernel, ring + rest(kQkMaxDim, kQkMaxDim));
   if (st != LPQ_OK) return st;
   int64_t most = (int64_t)device_sms() * std::max(1, std::min(Ring<T, BACKWARD>::kCtas, 226 * 1024 / (smem + 4 * 1024)));
   if (BACKWARD) most = std::min(most, most_parts());
   const int64_t grid = std::max<int64_t>(1, std::min(most, (g.groups + kWarps - 1) / kWarps));
-  st = cuda_check(launch_dependent(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD>, dim3((unsigned)grid), dim3(32 * kWarps), smem, s, g),
+  if (g.groups / (grid * kWarps) >= 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "qk norm: too large");
+  st = cuda_check(launch_dependent(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD, LANES>, dim3((unsigned)grid), dim3(32 * kWarps), smem, s, g),
                   BACKWARD ? "qk norm backward launch" : "qk norm launch");
   if (st != LPQ_OK || !BACKWARD || !g.parts) return st;
   return cuda_check(launch_dependent(qk_join_kernel, dim3((2 * g.dim + 31) / 32), dim3(32 * kJoinWarps), 0, s, g.parts, (int)grid, g.dim,
@@ -493,13 +588,21 @@ lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t
 template <typename T, bool BACKWARD>
 lpq_status dispatch(QkKernelArgs& g, int64_t rows, bool neighbours, float* dq, float* dk, cudaStream_t s) {
   auto whole = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * sizeof(T) % 16 == 0; };
-  if (g.dim % 16 == 0 && g.rotary % 16 == 0 && whole(g.x, g.ldx) && whole(g.out, g.ldo) && (!BACKWARD || whole(g.dy, g.lddy)))
-    return neighbours ? run<T, 8, 1, true, BACKWARD>(g, rows, dq, dk, s) : run<T, 8, 1, false, BACKWARD>(g, rows, dq, dk, s);
+  g.neighbours = neighbours;
+  if (g.dim % 16 == 0 && g.rotary % 16 == 0 && whole(g.x, g.ldx) && whole(g.out, g.ldo) && (!BACKWARD || whole(g.dy, g.lddy))) {
+    if (neighbours) return run<T, 8, 1, true, BACKWARD, 0>(g, rows, dq, dk, s);
+    const int per_group = 512 / g.dim;  // whole groups of the usual head sizes
+    if (per_group > 0 && g.heads[0] % per_group == 0 && g.heads[1] % per_group == 0) {
+      if (g.dim == 64) return run<T, 8, 1, false, BACKWARD, 4>(g, rows, dq, dk, s);
+      if (g.dim == 128) return run<T, 8, 1, false, BACKWARD, 8>(g, rows, dq, dk, s);
+      if (g.dim == 256) return run<T, 8, 1, false, BACKWARD, 16>(g, rows, dq, dk, s);
+    }
+    return run<T, 8, 1, false, BACKWARD, 0>(g, rows, dq, dk, s);
+  }
   // value by value
-  if (g.dim <= 64) return neighbours ? run<T, 1, 1, true, BACKWARD>(g, rows, dq, dk, s) : run<T, 1, 1, false, BACKWARD>(g, rows, dq, dk, s);
-  if (g.dim <= 128) return neighbours ? run<T, 1, 2, true, BACKWARD>(g, rows, dq, dk, s) : run<T, 1, 2, false, BACKWARD>(g, rows, dq, dk, s);
-  if (g.dim <= 256) return neighbours ? run<T, 1, 4, true, BACKWARD>(g, rows, dq, dk, s) : run<T, 1, 4, false, BACKWARD>(g, rows, dq, dk, s);
-  return neighbours ? run<T, 1, 8, true, BACKWARD>(g, rows, dq, dk, s) : run<T, 1, 8, false, BACKWARD>(g, rows, dq, dk, s);
+  if (g.dim <= 128) return run<T, 1, 2, false, BACKWARD, 0>(g, rows, dq, dk, s);
+  if (g.dim <= 256) return run<T, 1, 4, false, BACKWARD, 0>(g, rows, dq, dk, s);
+  return run<T, 1, 8, false, BACKWARD, 0>(g, rows, dq, dk, s);
 }
 
 QkKernelArgs kernel_args(const QkArgs& a) {

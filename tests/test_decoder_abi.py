@@ -135,7 +135,7 @@ def route(x=A, ldx=64, w=A, ldw=64, m=2, d=64, e=8, k=2, renormalize=1, ids=A, p
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(renormalize=2), lpq.ERR_INVALID_ARG), (dict(m=-1), lpq.ERR_SHAPE), (dict(d=0), lpq.ERR_SHAPE), (dict(d=60), lpq.ERR_SHAPE), (dict(e=0), lpq.ERR_SHAPE),
+    (dict(renormalize=2), lpq.ERR_INVALID_ARG), (dict(m=-1), lpq.ERR_SHAPE), (dict(d=0), lpq.ERR_SHAPE), (dict(d=60), lpq.ERR_SHAPE), (dict(d=65544, ldx=65544, ldw=65544), lpq.ERR_SHAPE), (dict(e=0), lpq.ERR_SHAPE),
     (dict(e=1025), lpq.ERR_SHAPE), (dict(k=0), lpq.ERR_SHAPE), (dict(k=9), lpq.ERR_SHAPE), (dict(e=64, k=33), lpq.ERR_SHAPE), (dict(ldx=56), lpq.ERR_SHAPE),
     (dict(ldw=68), lpq.ERR_SHAPE), (dict(x=None), lpq.ERR_INVALID_ARG), (dict(w=None), lpq.ERR_INVALID_ARG), (dict(ids=None), lpq.ERR_INVALID_ARG),
     (dict(probs=None), lpq.ERR_INVALID_ARG), (dict(x=A + 8), lpq.ERR_ALIGN), (dict(w=A + 2), lpq.ERR_ALIGN), (dict(ids=A + 4), lpq.ERR_ALIGN),
