@@ -187,6 +187,7 @@ struct MoeKernelArgs {
   int k;            // columns of the weights
   int rows;         // results of an expert: hidden values (up), rows (down)
   int tiles;        // of an expert: warps' shares of its rows
+  int run;          // tiles of a CTA
   int m, top, experts;
   const int64_t* ids;    // [m, top]
   const float* probs;    // down
@@ -200,62 +201,57 @@ struct MoeKernelArgs {
   int x_words;      // 16-byte words of a vector in shared memory
 };
 
-// Which experts a launch reads, and the pairs of each, in shared memory.
+// Which experts a launch reads, and for which pairs: entries of up to MP pairs of one
+// expert, in the order of their first pairs.  All CTAs make the same.
 struct Plan {
-  int16_t id[kMostPairs];        // of a pair: its expert, or -1
-  uint16_t pair[kMostPairs];     // the pairs, by expert
-  uint16_t expert[kMostPairs];   // entries: up to MP pairs of one expert
-  uint16_t first[kMostPairs];    // of an entry: its place in `pair`
-  uint8_t count[kMostPairs];
+  int16_t id[kMostPairs];      // of a pair: its expert, or -1
+  uint16_t next[kMostPairs];   // the expert's next pair
+  uint16_t first[kMostPairs];  // of an entry: its first pair
+  uint8_t count[kMostPairs];   // and how many it has
+  uint8_t heads[kMostPairs / 32];  // entries that begin in 32 pairs
   int entries;
 };
 
-// count and start: room for the experts' numbers.
 template <int MP>
-__device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g, int* count, int* start) {
+__device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
   const int pairs = g.m * g.top, tid = threadIdx.x;
-  for (int e = tid; e < g.experts; e += kThreads) count[e] = 0;
-  __syncthreads();
   for (int i = tid; i < pairs; i += kThreads) {
     const int64_t e = g.ids[i];
-    const bool there = (uint64_t)e < (uint64_t)g.experts;
-    p.id[i] = there ? (int16_t)e : -1;
-    if (there) atomicAdd(&count[e], 1);
+    p.id[i] = (uint64_t)e < (uint64_t)g.experts ? (int16_t)e : -1;
   }
   __syncthreads();
-  if (tid < 32) {  // running sums over the experts
-    int pairs_before = 0, entries_before = 0;
-    for (int e0 = 0; e0 < g.experts; e0 += 32) {
-      const int e = e0 + tid, n = e < g.experts ? count[e] : 0, c = (n + MP - 1) / MP;
-      int np = n, nc = c;
+  constexpr int kEach = kMostPairs / kThreads;  // pairs of a thread
+  int before[kEach], total[kEach];
+  uint32_t begin[kEach];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xFFFFFFFFu, np, o), b = __shfl_up_sync(0xFFFFFFFFu, nc, o);
-        if (tid >= o) {
-          np += a;
-          nc += b;
-        }
+  for (int k = 0; k < kEach; ++k) {
+    const int i = k * kThreads + tid;
+    before[k] = total[k] = 0;
+    const int16_t e = i < pairs ? p.id[i] : -1;
+    if (e >= 0) {
+      int next = 0;
+      for (int j = pairs - 1; j >= 0; --j) {
+        const bool same = p.id[j] == e;
+        total[k] += same;
+        before[k] += same && j < i;
+        if (same && j > i) next = j;
       }
-      if (e < g.experts) start[e] = pairs_before + np - n;
-      for (int i = 0; i < c; ++i) {
-        const int at = entries_before + nc - c + i;
-        p.expert[at] = (uint16_t)e;
-        p.first[at] = (uint16_t)(pairs_before + np - n + i * MP);
-        p.count[at] = (uint8_t)min(MP, n - i * MP);
-      }
-      pairs_before += __shfl_sync(0xFFFFFFFFu, np, 31);
-      entries_before += __shfl_sync(0xFFFFFFFFu, nc, 31);
+      p.next[i] = (uint16_t)next;
     }
-    if (tid == 0) p.entries = entries_before;
+    begin[k] = __ballot_sync(0xFFFFFFFFu, e >= 0 && before[k] % MP == 0);
+    if ((tid & 31) == 0) p.heads[i >> 5] = (uint8_t)__popc(begin[k]);
   }
   __syncthreads();
-  // An expert's pairs in their own order: all CTAs have to put the same ones into an entry.
-  for (int i = tid; i < pairs; i += kThreads) {
-    const int16_t e = p.id[i];
-    if (e < 0) continue;
-    int before = 0;
-    for (int j = 0; j < i; ++j) before += p.id[j] == e;
-    p.pair[start[e] + before] = (uint16_t)i;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int i = k * kThreads + tid;
+    int at = __popc(begin[k] & ((1u << (tid & 31)) - 1));
+    for (int c = 0; c < i >> 5; ++c) at += p.heads[c];
+    if (begin[k] >> (tid & 31) & 1) {
+      p.first[at] = (uint16_t)i;
+      p.count[at] = (uint8_t)min(MP, total[k] - before[k]);
+    }
+    if (i == kMostPairs - 1) p.entries = at + (begin[k] >> 31);
   }
   __syncthreads();
 }
@@ -271,7 +267,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int gid = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(sums + kWarps * kSums) + warp * (kRing * kSlot);
-  int* numbers = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sums + kWarps * kSums) + kWarps * kRing * kSlot);
   if constexpr (UP) {
     wait_for_stream();
     let_dependents_start();  // not before: down reads the ids and the weights without a wait of its own
@@ -280,11 +275,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   } else {
     let_dependents_start();
   }
-  make_plan<MP>(plan, g, numbers, numbers + g.experts);
-  // This CTA's run of tiles, which its warps take in turn: all CTAs have equally many,
-  // and neighbours find their vectors staged.
+  make_plan<MP>(plan, g);
+  // This CTA's run of tiles, which its warps take in turn.  The grid has a CTA for
+  // every run that there may be; those beyond the entries have none.
   const int64_t all_tiles = (int64_t)plan.entries * g.tiles;
-  const int begin = (int)(all_tiles * blockIdx.x / gridDim.x), end = (int)(all_tiles * (blockIdx.x + 1) / gridDim.x);
+  const int begin = (int)min(all_tiles, (int64_t)blockIdx.x * g.run), end = (int)min(all_tiles, (int64_t)begin + g.run);
   const int chunks = (g.k + kChunk - 1) / kChunk;
 
   // ---- the weight stream
@@ -301,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   uint32_t a_slot = 0;
   auto set_item = [&]() {
     const int entry = a_item / g.tiles, tile = a_item - entry * g.tiles;
-    const int64_t e = plan.expert[entry];
+    const int64_t e = plan.id[plan.first[entry]];
     const int last = g.rows - 1;  // rows beyond the expert read its last one; their results are not stored
     int64_t r1, r2;
     if constexpr (UP) {
@@ -361,9 +356,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   uint32_t slot = 0;
   bool f16 = true;
   int item = begin + warp;  // this warp's next tile
-  for (int entry = begin / g.tiles; entry * (int64_t)g.tiles < end; ++entry) {
+  for (int entry = begin / g.tiles; begin < end && entry * (int64_t)g.tiles < end; ++entry) {
     const int n = plan.count[entry];
-    const uint16_t* pair = plan.pair + plan.first[entry];
+    uint16_t pair[MP];
+    pair[0] = plan.first[entry];
+#pragma unroll
+    for (int c = 1; c < MP; ++c) pair[c] = c < n ? plan.next[pair[c - 1]] : pair[c - 1];
     // ---- the entry's vectors as operand entries: their range, then their values
     const uint4* xs[MP];
 #pragma unroll
@@ -470,6 +468,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
     __syncthreads();
 
     // ---- the products
+    auto pair_of = [&](int c) {  // (c is not a constant)
+      int p = pair[0];
+      for (int i = 0; i < c; ++i) p = plan.next[p];
+      return p;
+    };
     const int last_item = min(end, (entry + 1) * g.tiles);
     for (; item < last_item; item += kWarps) {
     const int tile = item - entry * g.tiles;
@@ -515,13 +518,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
       for (int i = 0; i < 2; ++i) {
         const int c = 2 * t + i;
         const float gate = acc[i], lin = acc[2 + i];
-        if (c < n && v < g.rows) g.hidden[(int64_t)pair[c] * g.rows + v] = __fdiv_rn(gate, 1.0f + expf(-gate)) * lin;
+        if (c < n && v < g.rows) g.hidden[(int64_t)pair_of(c) * g.rows + v] = __fdiv_rn(gate, 1.0f + expf(-gate)) * lin;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = 2 * t + (i & 1), v = value_of(tile, gid + (i >> 1) * 8);
-        if (c < n && v < g.rows) g.results[(int64_t)pair[c] * g.rows + v] = acc[i];
+        if (c < n && v < g.rows) g.results[(int64_t)pair_of(c) * g.rows + v] = acc[i];
       }
       // The warp that finds all experts' results of its rows there adds them up.
       __syncwarp();
@@ -549,21 +552,24 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-int smem_bytes(int k, int mp, int experts) {
+int smem_bytes(int k, int mp) {
   const int chunks = (k + kChunk - 1) / kChunk;
-  return chunks * (kChunk / 8) * 16 * mp + kWarps * kTokens * 16 * 4 + kWarps * kRing * kSlot + 2 * experts * 4;
+  return chunks * (kChunk / 8) * 16 * mp + kWarps * kTokens * 16 * 4 + kWarps * kRing * kSlot;
 }
 
+#ifndef PERW
+#define PERW 1
+#endif
 template <bool MX, int MP, bool UP>
 lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   const void* kernel = reinterpret_cast<const void*>(moe_kernel<MX, MP, UP>);
   lpq_status st = set_smem_attr(kernel, 216 * 1024);
   if (st != LPQ_OK) return st;
   g.x_words = (g.k + kChunk - 1) / kChunk * (kChunk / 8);
-  const int smem = smem_bytes(g.k, MP, g.experts);
-  const int resident = std::max(1, std::min(kCtas, 227 * 1024 / (smem + 7 * 1024)));
+  const int smem = smem_bytes(g.k, MP);
   const int64_t tiles = (int64_t)g.m * g.top * g.tiles;  // at most
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((tiles + kWarps - 1) / kWarps, (int64_t)resident * device_sms()));
+  g.run = kWarps * PERW;
+  const unsigned grid = (unsigned)std::max<int64_t>(1, (tiles + g.run - 1) / g.run);
   return cuda_check(launch_dependent(moe_kernel<MX, MP, UP>, dim3(grid), dim3(kThreads), smem, s, g), UP ? "moe up launch" : "moe down launch");
 }
 

@@ -556,6 +556,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qk_join_kernel(const float* p
   }
 }
 
+// CTAs per place for one: SMs are not equally fast at memory, and an even split over
+// the CTAs that fit at once waits for the slowest (15872 x 64 x 128 bf16: 95.4 us with
+// one round, 82.7 with four, 80.1 with eight).  Backward each CTA leaves a part to
+// join, which costs more than it gains (130 us with one round, 133 with two).
+constexpr int kWaves = 8;
 // Most CTAs of the backward pass, each of which leaves a part of the weights' gradients.
 int64_t most_parts() { return 2 * 160; }
 
@@ -574,7 +579,7 @@ lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t
   lpq_status st = set_smem_attr(kernel, ring + rest(kQkMaxDim, kQkMaxDim));
   if (st != LPQ_OK) return st;
   int64_t most = (int64_t)device_sms() * std::max(1, std::min(Ring<T, BACKWARD>::kCtas, 226 * 1024 / (smem + 4 * 1024)));
-  if (BACKWARD) most = std::min(most, most_parts());
+  if (BACKWARD) most = std::min(most, most_parts()); else most *= kWaves;
   const int64_t grid = std::max<int64_t>(1, std::min(most, (g.groups + kWarps - 1) / kWarps));
   if (g.groups / (grid * kWarps) >= 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "qk norm: too large");
   st = cuda_check(launch_dependent(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD, LANES>, dim3((unsigned)grid), dim3(32 * kWarps), smem, s, g),
