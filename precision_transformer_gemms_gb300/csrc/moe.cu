@@ -176,7 +176,6 @@ lpq_status route(const RouteArgs& g, cudaStream_t s) {
 // ------------------------------------------------------------------ the experts
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRing = 3;          // chunks of a warp on their way
-constexpr int kCtas = 3;          // per SM, where their vectors fit
 constexpr int kMostPairs = 512;   // (token, choice) pairs of a launch
 
 struct MoeKernelArgs {
@@ -187,7 +186,7 @@ struct MoeKernelArgs {
   int k;            // columns of the weights
   int rows;         // results of an expert: hidden values (up), rows (down)
   int tiles;        // of an expert: warps' shares of its rows
-  int run;          // tiles of a CTA
+  int split;        // warps that share a tile's columns
   int m, top, experts;
   const int64_t* ids;    // [m, top]
   const float* probs;    // down
@@ -256,13 +255,13 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
   __syncthreads();
 }
 
-template <bool MX, int MP, bool UP>
-__global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArgs g) {
+template <bool MX, int MP, bool UP, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(const MoeKernelArgs g) {
   extern __shared__ uint4 sx[];
   __shared__ Plan plan;
   __shared__ uint32_t red[2][kTokens][kWarps];
   __shared__ float back_sh[kTokens];
-  constexpr int kSums = kTokens * 16;
+  constexpr int kSums = MX ? kTokens * 16 : 0;
   float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int gid = lane >> 2, t = lane & 3;
@@ -279,8 +278,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   // This CTA's run of tiles, which its warps take in turn.  The grid has a CTA for
   // every run that there may be; those beyond the entries have none.
   const int64_t all_tiles = (int64_t)plan.entries * g.tiles;
-  const int begin = (int)min(all_tiles, (int64_t)blockIdx.x * g.run), end = (int)min(all_tiles, (int64_t)begin + g.run);
+  const int split = SPLIT ? g.split : 1;
+  const int slots = kWarps / split, slot = warp / split, part = SPLIT ? warp % split : 0;  // tiles at once, this warp's, its part of it
+  const int begin = (int)min(all_tiles, (int64_t)blockIdx.x * slots), end = (int)min(all_tiles, (int64_t)begin + slots);
   const int chunks = (g.k + kChunk - 1) / kChunk;
+  const int chunk0 = part * chunks / split, chunk1 = (part + 1) * chunks / split;
 
   // ---- the weight stream
   const uint32_t codes_sh = ring + lane * 16, scales_sh = ring + 1024 + lane * 4;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
     return UP ? (tile >> 4) * 128 + 32 * (r & 3) + 2 * (tile & 15) + (r >> 2) : (tile >> 3) * 128 + 32 * (r & 3) + 4 * (tile & 7) + (r >> 2);
   };
   const uint8_t *pc = nullptr, *pc2 = nullptr, *ps = nullptr, *ps2 = nullptr;
-  int a_item = begin + warp, a_chunk = 0;
+  int a_item = begin + slot, a_chunk = chunk0;
   uint32_t a_slot = 0;
   auto set_item = [&]() {
     const int entry = a_item / g.tiles, tile = a_item - entry * g.tiles;
@@ -306,10 +308,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
       r1 = e * g.rows + min(value_of(tile, gid), last);
       r2 = e * g.rows + min(value_of(tile, gid + 8), last);
     }
-    pc = g.codes + r1 * (g.k >> 1) + t * 16;
-    pc2 = g.codes + r2 * (g.k >> 1) + t * 16;
-    ps = g.scales + sf_gemm_offset(r1, 0, g.kt) + (MX ? 0 : (t >> 1) * 512);
-    ps2 = g.scales + sf_gemm_offset(r2, 0, g.kt) + (MX ? 0 : (t >> 1) * 512);
+    const int at = chunk0 * (kChunk / 2) + t * 16, scale_at = chunk0 * kChunkS + (MX ? 0 : (t >> 1) * 512);
+    pc = g.codes + r1 * (g.k >> 1) + at;
+    pc2 = g.codes + r2 * (g.k >> 1) + at;
+    ps = g.scales + sf_gemm_offset(r1, 0, g.kt) + scale_at;
+    ps2 = g.scales + sf_gemm_offset(r2, 0, g.kt) + scale_at;
   };
   auto copy = [&]() {  // the next chunk of the stream
     if (a_item < end) {
@@ -330,11 +333,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
       pc2 += kChunk / 2;
       ps += kChunkS;
       ps2 += kChunkS;
-      if (++a_chunk == chunks) {
-        a_chunk = 0;
-        a_item += kWarps;
-        if (a_item < end) set_item();
-      }
+      if (++a_chunk == chunk1) a_item = end;  // (a tile a warp)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     a_slot = a_slot == (kRing - 1) * kSlot ? 0 : a_slot + kSlot;
@@ -353,9 +352,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
   const int words = g.k >> 3, all_words = chunks * (kChunk / 8);
   auto place = [&](int c, int i) { return (((i >> 4) * 4 + (i & 3)) * MP + c) * 4 + ((i >> 2) & 3); };
   float* mine = sums + warp * kSums;
-  uint32_t slot = 0;
+  uint32_t place_at = 0;
   bool f16 = true;
-  int item = begin + warp;  // this warp's next tile
+  int item = begin + slot;  // this warp's tile
   for (int entry = begin / g.tiles; begin < end && entry * (int64_t)g.tiles < end; ++entry) {
     const int n = plan.count[entry];
     uint16_t pair[MP];
@@ -473,26 +472,25 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
       for (int i = 0; i < c; ++i) p = plan.next[p];
       return p;
     };
-    const int last_item = min(end, (entry + 1) * g.tiles);
-    for (; item < last_item; item += kWarps) {
+    if (item >= min(end, (entry + 1) * g.tiles)) continue;  // (the tile is of the next entry, or there is none)
     const int tile = item - entry * g.tiles;
+    item = end;
+    const int col = min(gid, MP - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
+    const uint4* e = sx + (size_t)chunk0 * (kChunk / 8) * MP;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (MX) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) mine[(2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = 0.f;  // far_chunk adds to it
-      __syncwarp();
     }
-    const int col = min(gid, MP - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
     auto stream = [&](auto f16_path) {
       constexpr bool F16 = decltype(f16_path)::value;
-      const uint4* e = sx;
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c, e += (kChunk / 8) * MP) {
+      for (int c = chunk0; c < chunk1; ++c, e += (kChunk / 8) * MP) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
         Load l;
-        l.lo = ld_shared_16(codes_sh + slot);
-        l.hi = ld_shared_16(codes_sh + slot + 512);
-        const uint32_t at = scales_sh + slot + (MX ? t : (t & 1) * 2);
+        l.lo = ld_shared_16(codes_sh + place_at);
+        l.hi = ld_shared_16(codes_sh + place_at + 512);
+        const uint32_t at = scales_sh + place_at + (MX ? t : (t & 1) * 2);
         l.slo = ld_shared_scale<MX>(at);
         l.shi = ld_shared_scale<MX>(at + 128);
         if (MX && F16 && mx_far(l))
@@ -500,18 +498,31 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
         else
           chunk_products<MX, F16, MP>(l, e + col, acc);
         copy();  // into the slot whose values have just been used
-        slot = slot == (kRing - 1) * kSlot ? 0 : slot + kSlot;
+        place_at = place_at == (kRing - 1) * kSlot ? 0 : place_at + kSlot;
       }
     };
     if (!UP || f16) stream(std::true_type{}); else stream(std::false_type{});
-    if constexpr (MX) __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = 2 * t + (i & 1);
       acc[i] *= !UP || f16 ? back_sh[min(c, n - 1)] : MX ? 1.0f : 256.0f;
       if constexpr (MX) acc[i] += mine[c * 16 + gid + (i >> 1) * 8];
-      acc[i] *= tensor;
     }
+    if constexpr (SPLIT) {  // the parts' sums in order, through their rings, which are done with
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      float* left = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sums + kWarps * kSums) + warp * (kRing * kSlot)) + lane;
+      if (part > 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) left[i * 32] = acc[i];
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(32 * split) : "memory");
+      if (part > 0) continue;
+      for (int p = 1; p < split; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += left[p * (kRing * kSlot / 4) + i * 32];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] *= tensor;
     if constexpr (UP) {
       const int v = value_of(tile, gid);
 #pragma unroll
@@ -547,30 +558,39 @@ __global__ void __launch_bounds__(kThreads, kCtas) moe_kernel(const MoeKernelArg
         __syncwarp();
       }
     }
-    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-int smem_bytes(int k, int mp) {
+int smem_bytes(int k, int mp, bool mx) {
   const int chunks = (k + kChunk - 1) / kChunk;
-  return chunks * (kChunk / 8) * 16 * mp + kWarps * kTokens * 16 * 4 + kWarps * kRing * kSlot;
+  return chunks * (kChunk / 8) * 16 * mp + (mx ? kWarps * kTokens * 16 * 4 : 0) + kWarps * kRing * kSlot;
 }
 
-#ifndef PERW
-#define PERW 1
-#endif
+template <bool MX, int MP, bool UP, bool SPLIT>
+lpq_status launch(const MoeKernelArgs& g, int64_t tiles, cudaStream_t s) {
+  const void* kernel = reinterpret_cast<const void*>(moe_kernel<MX, MP, UP, SPLIT>);
+  lpq_status st = set_smem_attr(kernel, 200 * 1024);
+  if (st != LPQ_OK) return st;
+  const int slots = kWarps / g.split;
+  return cuda_check(launch_dependent(moe_kernel<MX, MP, UP, SPLIT>, dim3((unsigned)((tiles + slots - 1) / slots)), dim3(kThreads),
+                                     smem_bytes(g.k, MP, MX), s, g),
+                    UP ? "moe up launch" : "moe down launch");
+}
+
 template <bool MX, int MP, bool UP>
 lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
-  const void* kernel = reinterpret_cast<const void*>(moe_kernel<MX, MP, UP>);
-  lpq_status st = set_smem_attr(kernel, 216 * 1024);
-  if (st != LPQ_OK) return st;
-  g.x_words = (g.k + kChunk - 1) / kChunk * (kChunk / 8);
-  const int smem = smem_bytes(g.k, MP);
+  const int chunks = (g.k + kChunk - 1) / kChunk;
+  g.x_words = chunks * (kChunk / 8);
   const int64_t tiles = (int64_t)g.m * g.top * g.tiles;  // at most
-  g.run = kWarps * PERW;
-  const unsigned grid = (unsigned)std::max<int64_t>(1, (tiles + g.run - 1) / g.run);
-  return cuda_check(launch_dependent(moe_kernel<MX, MP, UP>, dim3(grid), dim3(kThreads), smem, s, g), UP ? "moe up launch" : "moe down launch");
+  // Warps share a tile's columns while there are fewer tiles than places for warps (24
+  // an SM, and some pairs will have an expert in common) and each gets a few chunks:
+  // one token of 8 experts of 4096 x 1536 45.5 -> 37.0 us; with two warps a tile
+  // beyond that, 43.4.
+  const int most = chunks >= 16 ? 4 : chunks >= 8 ? 2 : 1;
+  g.split = 1;
+  while (g.split < most && tiles * g.split * 2 <= 26 * device_sms()) g.split *= 2;
+  return g.split > 1 ? launch<MX, MP, UP, true>(g, tiles, s) : launch<MX, MP, UP, false>(g, tiles, s);
 }
 
 template <bool UP>
