@@ -622,10 +622,9 @@ QkKernelArgs kernel_args(const QkArgs& a) {
   g.eps = a.eps;
   g.parts = a.parts;
   for (int i = 0; i < a.rotary / 2; ++i) {
-    double whole;  // (modf leaves the fraction with the value's sign)
-    double turn = std::modf(a.freqs[i] * 0.15915494309189535, &whole);  // 1 / (2 pi)
-    if (turn < 0) turn += 1.0;
-    g.turns[i] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0;
+    double turn = a.freqs[i] * 0.15915494309189535;  // 1 / (2 pi)
+    turn -= std::floor(turn);
+    g.turns[i] = turn < 1.0 ? (uint64_t)(turn * 18446744073709551616.0) : 0;
   }
   return g;
 }

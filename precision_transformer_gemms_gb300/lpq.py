@@ -145,7 +145,7 @@ def lib():
         L.lpq_qk_norm_rope_backward.argtypes = [P, I64, P, I64, I32, I64, I64, I64, I64, P, P, I32, P, PD, I64, I32, F, P, I64,
                                                 P, P, P, SZ, P]
         L.lpq_adjust_logits.argtypes = [P, I64, I32, I64, I64, P, P, I64, P]  # (the controls as their bytes)
-        L.lpq_matvec_adapted.argtypes = [P, P, I64, I64, P, I32, ctypes.POINTER(AdaptersC), P, P, SZ, P]
+        L.lpq_matvec_adapted.argtypes = [P, P, I64, I64, P, I32, P, P, P, SZ, P]  # (view and adapters as pointers or bytes)
         L.lpq_matvec_adapted_workspace.argtypes = [I64, I64, PSZ]
         L.lpq_moe_route.argtypes = [P, I64, P, I64, I64, I64, I64, I64, I32, P, P, P]
         L.lpq_moe_workspace.argtypes = [I64, I64, I64, I64, PSZ]
@@ -209,6 +209,8 @@ def layer_shapes(hidden, intermediate, micro_batch, seq, heads=32, layers=1):
 # ----------------------------------------------------------------- device buffers
 _TENSOR_SCALED = (FP8_E4M3, FP8_E5M2, NVFP4, NVFP4_2D)  # formats with a factor per tensor
 _pack_view = struct.Struct("@PPPPqqiiii").pack  # QView's fields
+_pack_adapters = struct.Struct("@PPPqq").pack  # AdaptersC's
+_pack_controls = struct.Struct("@PqqPPPPPPPPqPq").pack  # LogitControls'
 
 
 @functools.lru_cache(maxsize=256)
@@ -555,7 +557,7 @@ def matvec(x, w, out_fp32=False, stream=None, adapters=None, index=None):
     device = x.get_device()
     assert device == w.codes.get_device(), "x must lie where the weights do"
     if adapters is not None:
-        return _matvec_adapted(x, w, out_fp32, adapters, index)
+        return _matvec_adapted(x, w, out_fp32, adapters, index, m, k, device)
     assert index is None, "index goes with adapters"
     y = torch.empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device)
     _check(lib().lpq_matvec(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), _raw_stream(device)))
@@ -576,30 +578,24 @@ class Adapters:
         assert scale is None or (_is_vector(scale, a.shape[0], torch.float32) and scale.get_device() == a.get_device()), \
             f"scale must be {a.shape[0]} fp32"
         self.a, self.b, self.scale = a, b, scale
+        self.count, self.rank, self.k = a.shape
+        self.rows, self.device = b.shape[1], a.get_device()
+        self.packed = _pack_adapters(a.data_ptr(), b.data_ptr(), 0 if scale is None else scale.data_ptr(), self.count, self.rank)
 
 
 # ----------------------------------------------------------------- around attention
+_I64, _I32, _U8 = torch.int64, torch.int32, torch.uint8
 _current_device = torch._C._cuda_getDevice
+_empty = torch.empty
 
 
-def _on_its_device(call):
-    """The call with the device of its first tensor current, which the library launches on."""
-    @functools.wraps(call)
-    def at(x, *args, stream=None, **kw):
-        if stream is not None:
-            return on_stream(stream, at, x, *args, **kw)
-        assert x.is_cuda, "a CUDA tensor is needed"
-        if x.get_device() == _current_device():
-            return call(x, *args, **kw)
-        with torch.cuda.device(x.device):
-            return call(x, *args, **kw)
-    return at
-
-
-def _beside(x, **tensors):
-    """All tensors lie on x's device."""
-    for name, t in tensors.items():
-        assert t is None or t.get_device() == x.get_device(), f"{name} must lie where the first argument does"
+def _elsewhere(call, stream, x, *args):
+    """The call on `stream`, or with the device of x current, which the library launches on."""
+    if stream is not None:
+        return on_stream(stream, call, x, *args)
+    assert x.is_cuda, "CUDA tensors are needed"
+    with torch.cuda.device(x.device):
+        return call(x, *args)
 
 
 @functools.lru_cache(maxsize=64)
@@ -611,147 +607,149 @@ def _freqs(rotary_dim, base, freqs):
     return (ctypes.c_double * max(1, len(freqs)))(*freqs)
 
 
-@functools.lru_cache(maxsize=64)
-def _qk_workspace(rows, head_dim):
+@functools.lru_cache(maxsize=256)
+def _workspace(call, *sizes):
+    """Bytes that a workspace query of the library asks for."""
     n = ctypes.c_size_t()
-    _check(lib().lpq_qk_norm_rope_workspace(rows, head_dim, ctypes.byref(n)))
+    _check(getattr(lib(), call)(*sizes, ctypes.byref(n)))
     return n.value
 
 
-def _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs):
-    rows, cols = x.shape
-    used = (q_heads + k_heads) * head_dim
+def _check_heads(x, rows, cols, used, device, positions, head_dim, q_weight, k_weight):
+    """lpq_types of x and of the weights."""
     assert x.dtype in _TYPES, "the head norm runs on bf16 and fp32"
-    assert 0 <= used <= cols, f"x must hold {q_heads} + {k_heads} heads of {head_dim}"
-    assert _is_vector(positions, rows, torch.int64), f"positions must be {rows} int64"
+    assert 0 <= used <= cols, f"x must hold {used} values of heads"
+    assert positions.dtype is _I64 and positions.shape == (rows,) and positions.is_contiguous() and positions.get_device() == device, \
+        f"positions must be {rows} int64 where x lies"
     w_type = _check_params(head_dim, q_weight, k_weight)
-    _beside(x, positions=positions, q_weight=q_weight, k_weight=k_weight)
-    rotary_dim = head_dim if rotary_dim is None else rotary_dim
-    return rows, used, w_type, rotary_dim, _freqs(rotary_dim, None if freqs is not None else base, None if freqs is None else tuple(freqs))
+    assert (q_weight is None or q_weight.get_device() == device) and (k_weight is None or k_weight.get_device() == device), \
+        "the weights must lie where x does"
+    return _TYPES[x.dtype], w_type
 
 
-def _heads_out(out, x, rows, used, name):
-    """The result's tensor and its leading dimension."""
-    if out is None:
-        return _new(x, (rows, used), x.dtype), used
-    assert out.dtype is x.dtype and out.dim() == 2 and out.shape[0] == rows and out.shape[1] >= used, \
-        f"{name} must be of x's type, {rows} rows of at least {used}"
-    _beside(x, out=out)
-    return out, _ld(out, rows, out.shape[1])
+def _heads_out(out, x, rows, used, device):
+    """Leading dimension of a result that the caller gives."""
+    assert out.dtype is x.dtype and out.dim() == 2 and out.shape[0] == rows and out.shape[1] >= used and out.get_device() == device, \
+        f"out must be of x's type where x lies, {rows} rows of at least {used}"
+    return _ld(out, rows, out.shape[1])
 
 
-@_on_its_device
 def qk_norm_rope(x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weight=None, rotary_dim=None, base=10000.0, freqs=None,
-                 interleaved=False, eps=1e-6, out=None):
+                 interleaved=False, eps=1e-6, out=None, stream=None):
     """lpq_qk_norm_rope: the RMS norm of every query and key head of x [t, >= (q_heads
     + k_heads) * head_dim] (bf16 or fp32: a token's query heads, then its key heads),
     turned by its position (positions [t] int64).  Pair i of the first `rotary_dim`
     values turns by freqs[i] (default base^(-2 i / rotary_dim)) radians a position.
     Returns `out` (a new [t, (q_heads + k_heads) * head_dim]; x itself: in place,
-    and what lies behind the key heads stays).  `stream`: see the module."""
-    rows, used, w_type, rotary_dim, f = _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs)
-    y, ldy = _heads_out(out, x, rows, used, "out")
-    _check(lib().lpq_qk_norm_rope(x.data_ptr(), _ld(x, rows, x.shape[1]), _TYPES[x.dtype], rows, q_heads, k_heads, head_dim, _ptr(q_weight),
-                                  _ptr(k_weight), w_type, positions.data_ptr(), f, rotary_dim, int(interleaved), eps, y.data_ptr(), ldy,
-                                  _stream_of(x)))
-    return y
+    and what lies behind the key heads stays)."""
+    device = x.get_device()
+    if stream is not None or device != _current_device():
+        return _elsewhere(qk_norm_rope, stream, x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs,
+                          interleaved, eps, out)
+    rows, cols = x.shape
+    used = (q_heads + k_heads) * head_dim
+    x_type, w_type = _check_heads(x, rows, cols, used, device, positions, head_dim, q_weight, k_weight)
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    if out is None:
+        out, ldo = _empty((rows, used), dtype=x.dtype, device=x.device), used
+    else:
+        ldo = _heads_out(out, x, rows, used, device)
+    _check(lib().lpq_qk_norm_rope(x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads, k_heads, head_dim, _ptr(q_weight),
+                                  _ptr(k_weight), w_type, positions.data_ptr(), _freqs(rotary_dim, base, freqs and tuple(freqs)), rotary_dim,
+                                  interleaved, eps, out.data_ptr(), ldo, _raw_stream(device)))
+    return out
 
 
-@_on_its_device
 def qk_norm_rope_backward(dy, x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weight=None, rotary_dim=None, base=10000.0,
-                          freqs=None, interleaved=False, eps=1e-6, param_grads=True, out=None):
+                          freqs=None, interleaved=False, eps=1e-6, param_grads=True, out=None, stream=None):
     """lpq_qk_norm_rope_backward: returns (dx, dq_weight, dk_weight) from dy [t, >=
     (q_heads + k_heads) * head_dim] and the forward's x; the weights' gradients are
     FP32 (None, None without `param_grads`).  dx goes to `out` (dy, x or a wider
-    tensor whose first columns it fills) or a new tensor.  `stream`: see the module."""
-    rows, used, w_type, rotary_dim, f = _qk_args(x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base, freqs)
-    assert dy.dtype is x.dtype and dy.dim() == 2 and dy.shape[0] == rows and dy.shape[1] >= used, "dy must be like x"
-    _beside(x, dy=dy)
-    dx, lddx = _heads_out(out, x, rows, used, "out")
-    dq = dk = ws = None
-    need = 0
+    tensor whose first columns it fills) or a new tensor."""
+    device = dy.get_device()
+    if stream is not None or device != _current_device():
+        return _elsewhere(qk_norm_rope_backward, stream, dy, x, q_heads, k_heads, head_dim, positions, q_weight, k_weight, rotary_dim, base,
+                          freqs, interleaved, eps, param_grads, out)
+    rows, cols = x.shape
+    used = (q_heads + k_heads) * head_dim
+    x_type, w_type = _check_heads(x, rows, cols, used, device, positions, head_dim, q_weight, k_weight)
+    assert dy.dtype is x.dtype and dy.dim() == 2 and dy.shape[0] == rows and dy.shape[1] >= used and x.get_device() == device, \
+        "dy must be like x"
+    rotary_dim = head_dim if rotary_dim is None else rotary_dim
+    if out is None:
+        out, ldo = _empty((rows, used), dtype=x.dtype, device=x.device), used
+    else:
+        ldo = _heads_out(out, x, rows, used, device)
+    dq = dk = None
+    dqp = dkp = wsp = need = 0
     if param_grads:
-        need = _qk_workspace(rows, head_dim)
-        dq, dk, ws = _new(x, head_dim, _FP32), _new(x, head_dim, _FP32), _new(x, need, torch.uint8)
-    _check(lib().lpq_qk_norm_rope_backward(dy.data_ptr(), _ld(dy, rows, dy.shape[1]), x.data_ptr(), _ld(x, rows, x.shape[1]),
-                                           _TYPES[x.dtype], rows, q_heads, k_heads, head_dim, _ptr(q_weight), _ptr(k_weight), w_type,
-                                           positions.data_ptr(), f, rotary_dim, int(interleaved), eps, dx.data_ptr(), lddx, _ptr(dq),
-                                           _ptr(dk), _ptr(ws), need, _stream_of(x)))
-    return dx, dq, dk
+        need = _workspace("lpq_qk_norm_rope_workspace", rows, head_dim)
+        dq, dk = _empty(head_dim, dtype=_FP32, device=x.device), _empty(head_dim, dtype=_FP32, device=x.device)
+        ws = _empty(need, dtype=_U8, device=x.device)
+        dqp, dkp, wsp = dq.data_ptr(), dk.data_ptr(), ws.data_ptr()
+    _check(lib().lpq_qk_norm_rope_backward(dy.data_ptr(), _ld(dy, rows, dy.shape[1]), x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads,
+                                           k_heads, head_dim, _ptr(q_weight), _ptr(k_weight), w_type, positions.data_ptr(),
+                                           _freqs(rotary_dim, base, freqs and tuple(freqs)), rotary_dim, interleaved, eps, out.data_ptr(), ldo,
+                                           dqp, dkp, wsp, need, _raw_stream(device)))
+    return out, dq, dk
 
 
-@functools.lru_cache(maxsize=256)
-def _adapted_workspace(m, rank):
-    n = ctypes.c_size_t()
-    _check(lib().lpq_matvec_adapted_workspace(m, rank, ctypes.byref(n)))
-    return n.value
-
-
-@_on_its_device
-def _matvec_adapted(x, w, out_fp32, adapters, index):
-    m, k = x.shape
-    count, rank, ka = adapters.a.shape
-    assert ka == k and adapters.b.shape[1] == w.rows, f"the adapters must be of a layer {k} -> {w.rows}"
-    assert index is not None and _is_vector(index, m, torch.int64), f"index must be {m} int64"
-    _beside(x, adapters=adapters.a, index=index)
-    need = _adapted_workspace(m, rank)
-    y, ws = _new(x, (m, w.rows), _FP32 if out_fp32 else _BF16), _new(x, need, torch.uint8)
-    c = AdaptersC(_ptr(adapters.a), _ptr(adapters.b), _ptr(adapters.scale), count, rank)
-    _check(lib().lpq_matvec_adapted(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), int(out_fp32), ctypes.byref(c),
-                                    index.data_ptr(), ws.data_ptr(), need, _stream_of(x)))
+def _matvec_adapted(x, w, out_fp32, adapters, index, m, k, device):
+    if device != _current_device():
+        return _elsewhere(_matvec_adapted, None, x, w, out_fp32, adapters, index, m, k, device)
+    assert adapters.k == k and adapters.rows == w.rows and adapters.device == device, \
+        f"the adapters must be of a layer {k} -> {w.rows}, where x lies"
+    assert index is not None and index.dtype is _I64 and index.shape == (m,) and index.is_contiguous() and index.get_device() == device, \
+        f"index must be {m} int64 where x lies"
+    need = _workspace("lpq_matvec_adapted_workspace", m, adapters.rank)
+    y, ws = _empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device), _empty(need, dtype=_U8, device=x.device)
+    _check(lib().lpq_matvec_adapted(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), out_fp32, adapters.packed, index.data_ptr(),
+                                    ws.data_ptr(), need, _raw_stream(device)))
     return y
 
 
-@_on_its_device
-def moe_route(x, w, k, renormalize=True):
+def moe_route(x, w, k, renormalize=True, stream=None):
     """lpq_moe_route: the k experts of every token of x [m, d] with the largest logits x
     w^T for the router's weights w [experts, d] (bf16); returns (ids [m, k] int64 in
     descending order, probs [m, k] fp32: the softmax over the chosen, or over all
-    without `renormalize`).  `stream`: see the module."""
+    without `renormalize`)."""
+    device = x.get_device()
+    if stream is not None or device != _current_device():
+        return _elsewhere(moe_route, stream, x, w, k, renormalize)
     (m, d), (experts, dw) = x.shape, w.shape
-    assert x.dtype is _BF16 and w.dtype is _BF16 and d == dw, "x and w must be bf16 with the same number of columns"
-    _beside(x, w=w)
-    ids, probs = _new(x, (m, k), _I64), _new(x, (m, k), _FP32)
-    _check(lib().lpq_moe_route(x.data_ptr(), _ld(x, m, d), w.data_ptr(), _ld(w, experts, d), m, d, experts, k, int(renormalize), ids.data_ptr(),
-                               probs.data_ptr(), _stream_of(x)))
+    assert x.dtype is _BF16 and w.dtype is _BF16 and d == dw and w.get_device() == device, \
+        "x and w must be bf16 with the same number of columns, on one device"
+    ids, probs = _empty((m, k), dtype=_I64, device=x.device), _empty((m, k), dtype=_FP32, device=x.device)
+    _check(lib().lpq_moe_route(x.data_ptr(), _ld(x, m, d), w.data_ptr(), _ld(w, experts, d), m, d, experts, k, renormalize, ids.data_ptr(),
+                               probs.data_ptr(), _raw_stream(device)))
     return ids, probs
 
 
-@functools.lru_cache(maxsize=256)
-def _moe_workspace(m, k, d, f):
-    n = ctypes.c_size_t()
-    _check(lib().lpq_moe_workspace(m, k, d, f, ctypes.byref(n)))
-    return n.value
-
-
-@_on_its_device
-def moe(x, up, down, experts, ids, probs):
+def moe(x, up, down, experts, ids, probs, stream=None):
     """lpq_moe: y[i] = sum_j probs[i, j] W2_e (silu(W1g_e x[i]) * (W1u_e x[i])), e =
     ids[i, j], for a few tokens x [m, d] (bf16, not quantized) on 4-bit weights: the
     row-wise Copies up [experts * 2 f, d] (each expert's gate rows, then its up rows)
     and down [experts * d, f] with SF_GEMM scales.  ids [m, k] int64 (outside 0 ..
-    experts - 1: no expert), probs [m, k] fp32; returns bf16 [m, d].  `stream`: see the
-    module."""
+    experts - 1: no expert), probs [m, k] fp32; returns bf16 [m, d]."""
+    device = x.get_device()
+    if stream is not None or device != _current_device():
+        return _elsewhere(moe, stream, x, up, down, experts, ids, probs)
     m, d = x.shape
     assert x.dtype is _BF16 and d == up.cols, "x must be bf16 [m, d]"
-    assert ids.dim() == 2 and ids.shape[0] == m and ids.shape == probs.shape, f"ids and probs must be [{m}, k]"
-    k = ids.shape[1]
-    assert _is_vector(ids, m * k, _I64) and _is_vector(probs, m * k, _FP32), "ids must be int64 and probs fp32, contiguous"
-    _beside(x, up=up.codes, down=down.codes, ids=ids, probs=probs)
-    need = _moe_workspace(m, k, d, down.cols)
-    y, ws = _new(x, (m, d), _BF16), _new(x, need, torch.uint8)
+    rows, k = ids.shape
+    assert rows == m and ids.dtype is _I64 and ids.is_contiguous() and probs.shape == ids.shape and probs.dtype is _FP32 and probs.is_contiguous(), \
+        f"ids must be int64 and probs fp32, [{m}, k], contiguous"
+    assert up.codes.get_device() == device and down.codes.get_device() == device and ids.get_device() == device and probs.get_device() == device, \
+        "all tensors must lie on one device"
+    need = _workspace("lpq_moe_workspace", m, k, d, down.cols)
+    y, ws = _empty((m, d), dtype=_BF16, device=x.device), _empty(need, dtype=_U8, device=x.device)
     _check(lib().lpq_moe(up.packed_view(), down.packed_view(), experts, x.data_ptr(), _ld(x, m, d), m, ids.data_ptr(), probs.data_ptr(), k,
-                         y.data_ptr(), ws.data_ptr(), need, _stream_of(x)))
+                         y.data_ptr(), ws.data_ptr(), need, _raw_stream(device)))
     return y
 
 
-_pack_controls = struct.Struct("@PqqPPPPPPPPqPq").pack  # LogitControls' fields
-_I64, _I32 = torch.int64, torch.int32
-
-
-@_on_its_device
 def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=None, frequency=None, presence=None, bias=None,
-                  allowed=None, out=None):
+                  allowed=None, out=None, stream=None):
     """lpq_adjust_logits on logits [t, v] (bf16 or fp32): penalties for words that
     stand in each row's context, biases and a mask; returns `out` (a new tensor;
     logits itself: in place).
@@ -759,40 +757,46 @@ def adjust_logits(logits, history=None, lengths=None, prompt=None, repetition=No
     `history` [t, n] int64 words, `lengths` [t] int64 of them valid, of which the first
     `prompt` [t] int64 are the prompt (default 0) and the others the answer;
     `repetition`, `frequency`, `presence` [t] fp32; `bias` (offsets [t + 1] int64, words
-    int64, values fp32); `allowed` [t, ceil(v / 32)] int32, one bit a word.  `stream`:
-    see the module."""
+    int64, values fp32); `allowed` [t, ceil(v / 32)] int32, one bit a word."""
+    device = logits.get_device()
+    if stream is not None or device != _current_device():
+        return _elsewhere(adjust_logits, stream, logits, history, lengths, prompt, repetition, frequency, presence, bias, allowed, out)
     rows, v = logits.shape
-    dtype, device = logits.dtype, logits.get_device()
+    dtype = logits.dtype
     assert dtype in _TYPES, "logits must be bf16 or fp32"
-    ld_history = max_len = bias_count = ld_allowed = 0
-    offsets = words = values = None
+
+    def at(t, shape, kind, name):
+        """Address of a control, 0 for None (an empty tensor has none: any other)."""
+        if t is None:
+            return 0
+        assert t.dtype is kind and t.shape == shape and t.is_contiguous() and t.get_device() == device, \
+            f"{name} must be {kind} {tuple(shape)}, contiguous, where the logits lie"
+        return t.data_ptr() or 8
+
+    row = (rows,)
+    words = ld_words = max_len = bias_count = offsets = ids = values = bits = ld_bits = 0
     if history is not None:
-        assert history.dtype is _I64 and history.dim() == 2 and history.shape[0] == rows, f"history must be int64 [{rows}, n]"
-        max_len = history.shape[1]
-        ld_history = _ld(history, rows, max_len)
+        assert history.dtype is _I64 and history.dim() == 2 and history.shape[0] == rows and history.get_device() == device, \
+            f"history must be int64 [{rows}, n] where the logits lie"
         assert lengths is not None, "history needs lengths"
+        max_len = history.shape[1]
+        words, ld_words = history.data_ptr() or 8, _ld(history, rows, max_len)
     if bias is not None:
-        offsets, words, values = bias
-        bias_count = words.numel()
-        assert _is_vector(offsets, rows + 1, _I64) and _is_vector(words, bias_count, _I64) and _is_vector(values, bias_count, _FP32), \
-            f"bias must be {rows + 1} int64 offsets, int64 words and as many fp32 values"
+        bias_count = bias[1].numel()
+        offsets = at(bias[0], (rows + 1,), _I64, "the biases' offsets")
+        ids, values = at(bias[1], (bias_count,), _I64, "the biases' words"), at(bias[2], (bias_count,), _FP32, "the biases")
     if allowed is not None:
-        assert allowed.dtype is _I32 and allowed.shape == (rows, (v + 31) // 32), f"allowed must be int32 [{rows}, {(v + 31) // 32}]"
-        ld_allowed = _ld(allowed, rows, allowed.shape[1])
-    for p, kind in ((lengths, _I64), (prompt, _I64), (repetition, _FP32), (frequency, _FP32), (presence, _FP32)):
-        assert p is None or _is_vector(p, rows, kind), f"lengths and prompt must be {rows} int64, the penalties {rows} fp32"
-    for p in (history, lengths, prompt, repetition, frequency, presence, offsets, words, values, allowed, out):
-        assert p is None or p.get_device() == device, "all tensors must lie where the logits do"
+        assert allowed.dtype is _I32 and allowed.shape == (rows, (v + 31) // 32) and allowed.get_device() == device, \
+            f"allowed must be int32 [{rows}, {(v + 31) // 32}] where the logits lie"
+        bits, ld_bits = allowed.data_ptr(), _ld(allowed, rows, (v + 31) // 32)
+    c = _pack_controls(words, ld_words, max_len, at(lengths, row, _I64, "lengths"), at(prompt, row, _I64, "prompt"),
+                       at(repetition, row, _FP32, "repetition"), at(frequency, row, _FP32, "frequency"), at(presence, row, _FP32, "presence"),
+                       offsets, ids, values, bias_count, bits, ld_bits)
     if out is None:
-        out, ldo = _new(logits, (rows, v), dtype), v
+        out, ldo = _empty((rows, v), dtype=dtype, device=logits.device), v
     else:
-        assert out.dtype is dtype and out.shape == logits.shape, "out must be like the logits"
+        assert out.dtype is dtype and out.shape == logits.shape and out.get_device() == device, "out must be like the logits"
         ldo = _ld(out, rows, v)
-    at = lambda t: 0 if t is None else t.data_ptr()
-    # an empty tensor has no address, which would read as one that is not given
-    some = lambda t: 0 if t is None else t.data_ptr() or 8
-    c = _pack_controls(some(history), ld_history, max_len, some(lengths), at(prompt), at(repetition), at(frequency), at(presence), at(offsets),
-                       at(words), at(values), bias_count, at(allowed), ld_allowed)
     _check(lib().lpq_adjust_logits(logits.data_ptr(), _ld(logits, rows, v), _TYPES[dtype], rows, v, c, out.data_ptr(), ldo, _raw_stream(device)))
     return out
 
