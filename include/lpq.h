@@ -495,7 +495,7 @@ lpq_status lpq_qk_norm_rope_backward(const void *dy, int64_t lddy, const void *x
 
 /* What changes the logits of the next words.  Device pointers; any group may be
  * NULL, which leaves its step out.
- *   history      [rows, max_len] int64 words of every request's context, rows
+ *   history      [rows, max_len <= 2^30] int64 words of every request's context, rows
  *                ld_history elements apart: lengths[row] of them (taken within 0 ..
  *                max_len), of which the first prompt[row] (NULL: 0) are the prompt
  *                and the others the answer so far.  Words outside 0 .. v - 1 count
@@ -528,7 +528,7 @@ typedef struct {
  * controls, in the order repetition, frequency and presence, bias, mask; FP32
  * arithmetic, rounded once.  out has the logits' type, rows ldo elements apart, and
  * may be the logits themselves (then ldo = ld), else they must not overlap.  Any
- * rows and v >= 0, v at most 2^31; rows that begin equally far from a 16-byte
+ * rows and v >= 0, v at most 2^30; rows that begin equally far from a 16-byte
  * boundary on both sides take 16-byte accesses. */
 lpq_status lpq_adjust_logits(const void *logits, int64_t ld, int32_t type, int64_t rows, int64_t v,
                              const lpq_logit_controls *controls, void *out, int64_t ldo, lpq_stream_t stream);

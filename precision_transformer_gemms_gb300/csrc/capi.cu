@@ -720,7 +720,7 @@ lpq_status lpq_adjust_logits(const void* logits, int64_t ld, int32_t type, int64
   if (!controls) return set_error(LPQ_ERR_INVALID_ARG, "controls is NULL");
   const lpq_logit_controls& c = *controls;
   if (!valid_type(type)) return set_error(LPQ_ERR_INVALID_ARG, "type %d", type);
-  if (rows < 0 || v < 0 || rows > (int64_t)1 << 30 || v > (int64_t)1 << 31)
+  if (rows < 0 || v < 0 || rows > (int64_t)1 << 30 || v > (int64_t)1 << 30)
     return set_error(LPQ_ERR_SHAPE, "rows %lld, v %lld", (long long)rows, (long long)v);
   const bool any = rows > 0 && v > 0;
   lpq_status st = check_matrix(any ? logits : &c, "logits", ld, rows, v, type_bytes(type));
@@ -728,7 +728,7 @@ lpq_status lpq_adjust_logits(const void* logits, int64_t ld, int32_t type, int64
   if ((st = check_matrix(any ? out : &c, "out", ldo, rows, v, type_bytes(type))) != LPQ_OK) return st;
   if (out == logits && rows > 1 && v > 0 && ld != ldo) return set_error(LPQ_ERR_SHAPE, "out in the logits' place needs their leading dimension");
   if (c.history) {
-    if (c.max_len < 0 || c.ld_history < c.max_len)
+    if (c.max_len < 0 || c.max_len > (int64_t)1 << 30 || c.ld_history < c.max_len)
       return set_error(LPQ_ERR_SHAPE, "history of %lld in rows of %lld", (long long)c.max_len, (long long)c.ld_history);
     if (!c.lengths) return set_error(LPQ_ERR_INVALID_ARG, "lengths is NULL");
   } else if (c.repetition || c.frequency || c.presence) {

@@ -8,9 +8,7 @@
 // run of words of a row: it loads them to registers, counts the context's words
 // that lie in its run in shared memory (integers: the order of the atomics does
 // not matter), adds the biases there in the list's order, and then works on its
-// registers.  Contexts of more than a few words are read by a cluster of CTAs
-// together, each a part, whose words it counts where they belong, in its own or
-// another CTA's shared memory.
+// registers.  Every CTA of a row reads the row's whole context, from the L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,24 +18,15 @@
 namespace lpq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int64_t kClusterContext = 512;  // words of a context that a CTA reads alone
 constexpr uint32_t kSeen = 0x80000000u;  // stands in the prompt; the other bits count the answer
 
-// Integer sums in the shared memory of a CTA of the cluster.
-__device__ __forceinline__ void count_at(uint32_t addr, bool prompt) {
-  if (prompt) asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(kSeen) : "memory");
-  else asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(1u) : "memory");
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// `segments` CTAs a row, a multiple of C, the CTAs of a cluster.
-template <typename T, int VEC, int NV, int C>
-__global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitsArgs g, int64_t segments) {
+// `segments` CTAs a row.  What a CTA reads at addresses that it knows, it asks for at once: the time of a CTA
+// is that of a few loads after one another, not of its bytes.
+template <typename T, int VEC, int NV, int kThreads>
+__global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 : 3) adjust_logits_kernel(const LogitsArgs g, int64_t segments) {
   constexpr int S = kThreads * VEC * NV;  // words of a CTA
-  __shared__ __align__(16) uint32_t counts[S];
-  __shared__ __align__(16) float biases[S];
+  extern __shared__ __align__(16) uint32_t counts[];  // [S], and with biases their sums [S]
+  float* biases = reinterpret_cast<float*>(counts + S);
   let_dependents_start();
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / segments;
@@ -45,149 +34,157 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitsArg
   T* out = static_cast<T*>(g.out) + row * g.ldo;
   // Word w of the row stands at w + lead, counted from a 16-byte boundary.
   const int lead = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(in) & 15u) / sizeof(T));
-  const int64_t first = (blockIdx.x - row * segments) * S - lead;  // word of the run's first place
-  const int rank = C > 1 ? (int)cluster_ctarank() : 0;
-  for (int i = tid; i < S / 4; i += kThreads) {
-    reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
-    reinterpret_cast<uint4*>(biases)[i] = make_uint4(0, 0, 0, 0);
+  const int v = (int)g.v;
+  const int first = (int)(blockIdx.x - row * segments) * S - lead;  // word of the run's first place
+#pragma unroll
+  for (int i = 0; i < S / 4; i += kThreads) {
+    reinterpret_cast<uint4*>(counts)[i + tid] = make_uint4(0, 0, 0, 0);
+    if (g.c.bias_words) reinterpret_cast<uint4*>(biases)[i + tid] = make_uint4(0, 0, 0, 0);
   }
-  if constexpr (C > 1) cluster_arrive();  // this CTA's counts are ready
   wait_for_stream();
 
-  T val[NV][VEC];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int64_t w = first + (j * kThreads + tid) * VEC;
-    if (VEC > 1 && w >= 0 && w + VEC <= g.v) {
-      *reinterpret_cast<uint4*>(val[j]) = *reinterpret_cast<const uint4*>(in + w);
-    } else {
-#pragma unroll
-      for (int k = 0; k < VEC; ++k) val[j][k] = w + k >= 0 && w + k < g.v ? in[w + k] : T(0.f);
-    }
-  }
-  // The word's place among `count` from `from` on, or -1.
-  auto place = [&](int64_t word, int64_t from, int count) {
-    if ((uint64_t)word >= (uint64_t)g.v) return -1;
-    const int64_t at = word - from;
-    return at >= 0 && at < count ? (int)at : -1;
-  };
-  if constexpr (C == 1) __syncthreads();
+  int64_t n = 0, prompt = 0, from = 0, to = 0;
   if (g.c.history) {
-    const int64_t n = max((int64_t)0, min(g.c.lengths[row], g.c.max_len));
-    const int64_t prompt = g.c.prompt ? g.c.prompt[row] : 0;
-    const int64_t* h = g.c.history + row * g.c.ld_history;
-    const uint32_t table = smem_u32(counts);
-    constexpr int kAhead = 4;  // words of a thread on their way
-    int64_t word[kAhead];
-    auto load = [&](int64_t i0) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) word[j] = i0 + j * C * kThreads < n ? h[i0 + j * C * kThreads] : -1;
-    };
-    int64_t i0 = (int64_t)rank * kThreads + tid;
-    load(i0);
-    if constexpr (C > 1) {
-      __syncwarp();
-      cluster_wait();  // the others' counts are ready, too
-    }
-    for (; i0 < n; load(i0)) {
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int at = place(word[j], first - (int64_t)rank * S, C * S);
-        if (at < 0) continue;
-        const bool asked = i0 + j * C * kThreads < prompt;
-        if constexpr (C > 1) {
-          count_at(mapa_shared(table + (at % S) * 4, (uint32_t)(at / S)), asked);
-        } else {
-          if (asked) atomicOr(&counts[at], kSeen); else atomicAdd(&counts[at], 1u);
-        }
-      }
-      i0 += kAhead * C * kThreads;
-    }
-  } else if constexpr (C > 1) {
-    cluster_wait();
+    n = g.c.lengths[row];
+    if (g.c.prompt) prompt = g.c.prompt[row];
   }
-  if constexpr (C > 1) {
-    __syncwarp();
-    cluster_arrive();  // its words are counted
+  if (g.c.bias_words) {
+    from = g.c.bias_offsets[row];
+    to = g.c.bias_offsets[row + 1];
   }
-  if (g.c.bias_words && tid < 32) {
-    const int64_t from = max((int64_t)0, g.c.bias_offsets[row]), to = min(g.c.bias_offsets[row + 1], g.c.bias_count);
-    for (int64_t i = from; i < to; i += 32) {
-      const int at = i + tid < to ? place(g.c.bias_words[i + tid], first, S) : -1;
-      const float b = at >= 0 ? g.c.bias_values[i + tid] : 0.f;
-      for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0); left; left &= left - 1) {  // one after another
-        if (tid == __ffs(left) - 1) biases[at] += b;
-        __syncwarp();
-      }
-    }
-  }
-  __syncthreads();
-  if constexpr (C > 1) cluster_wait();
   const float rep = g.c.repetition ? g.c.repetition[row] : 1.f;
   const float freq = g.c.frequency ? g.c.frequency[row] : 0.f, pres = g.c.presence ? g.c.presence[row] : 0.f;
+  T val[NV][VEC];
+  uint32_t bits[NV];
   const uint32_t* allowed = g.c.allowed ? reinterpret_cast<const uint32_t*>(g.c.allowed) + row * g.c.ld_allowed : nullptr;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int p = (j * kThreads + tid) * VEC;
-    const int64_t w = first + p;
-    if (w >= g.v || w + VEC <= 0) continue;
-    uint32_t bits = 0xFFFFFFFFu;
-    if (allowed) {
-      const int64_t a = max(w, (int64_t)0), z = min(w + VEC, g.v) - 1;
-      bits = __funnelshift_r(allowed[a >> 5], allowed[z >> 5], (uint32_t)a & 31u) << (a - w);
+    const int w = first + (j * kThreads + tid) * VEC;
+    if (VEC > 1 && w >= 0 && w + VEC <= v) {
+      *reinterpret_cast<uint4*>(val[j]) = *reinterpret_cast<const uint4*>(in + w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) val[j][k] = w + k >= 0 && w + k < v ? in[w + k] : T(0.f);
+    }
+    bits[j] = 0xFFFFFFFFu;
+    if (allowed && w < v && w + VEC > 0) {
+      const int a = max(w, 0), z = min(w + VEC, v) - 1;
+      bits[j] = __funnelshift_r(allowed[a >> 5], allowed[z >> 5], (uint32_t)a & 31u) << (a - w);
+    }
+  }
+  // The word's place among `count` from `at` on, or -1.  (A word just below 0 may be
+  // given a place in front of the row's first, which nothing reads.)
+  auto place = [&](int64_t word, int at, int count) {
+    const uint64_t p = (uint64_t)word - (uint64_t)(int64_t)at;
+    return p < (uint64_t)count ? (int)p : -1;
+  };
+  const int words = min(S, v - first);
+
+  // The context's words, and the biases by the last warp.
+  const int len = (int)max((int64_t)0, min(n, g.c.max_len));
+  const int asked = (int)max((int64_t)0, min(prompt, (int64_t)len));  // words of the prompt
+  from = max((int64_t)0, from);
+  to = min(to, g.c.bias_count);
+  constexpr int kAhead = 4;  // words of a thread on their way
+  constexpr int stride = kThreads;
+  int i0 = tid;
+  const int64_t* h = g.c.history + row * g.c.ld_history + i0;
+  int64_t word[kAhead];
+  auto load = [&]() {
+    if (i0 + (kAhead - 1) * stride < len) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) word[j] = h[j * stride];
+    } else {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) word[j] = i0 + j * stride < len ? h[j * stride] : INT64_MIN;
+    }
+    h += kAhead * stride;
+  };
+  const int lane = tid & 31;
+  const bool biasing = g.c.bias_words && tid >= kThreads - 32;
+  int64_t bias_word = -1;
+  float bias = 0.f;
+  auto load_bias = [&]() {
+    bias_word = from + lane < to ? g.c.bias_words[from + lane] : -1;
+    bias = from + lane < to ? g.c.bias_values[from + lane] : 0.f;
+  };
+  load();
+  if (biasing) load_bias();
+  __syncthreads();  // (the tables are clear)
+  while (i0 < len) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int at = place(word[j], first, words);
+      if (at < 0) continue;
+      if (i0 + j * stride < asked) atomicOr(&counts[at], kSeen); else atomicAdd(&counts[at], 1u);
+    }
+    i0 += kAhead * stride;
+    load();
+  }
+  if (biasing) {
+    for (; from < to; load_bias()) {
+      const int at = place(bias_word, first, words);
+      for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0); left; left &= left - 1) {  // one after another, in the list's order
+        if (lane == __ffs(left) - 1) biases[at] += bias;
+        __syncwarp();
+      }
+      from += 32;
+    }
+  }
+  __syncthreads();
+  const float inverse = __fdiv_rn(1.f, rep);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int p = (j * kThreads + tid) * VEC, w = first + p;
+    if (w >= v || w + VEC <= 0) continue;
+    float x[VEC];
+    uint32_t c[VEC], any = 0;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      if constexpr (sizeof(T) == 4) x[k] = val[j][k]; else x[k] = __bfloat162float(val[j][k]);
+      c[k] = counts[p + k];
+      any |= c[k];
+    }
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        // x / rep by its reciprocal and one correction with the exact remainder (where that is a number)
+        float q = x[k] * inverse;
+        if (fabsf(q) <= 3.402823466e38f) q = fmaf(fmaf(-q, rep, x[k]), inverse, q);
+        const float seen = x[k] > 0.f ? q : x[k] * rep;
+        if (c[k]) x[k] = seen;
+        const uint32_t times = c[k] & ~kSeen;
+        if (times) x[k] = x[k] - freq * (float)times - pres;
+      }
     }
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
-      float x;
-      if constexpr (sizeof(T) == 4) x = val[j][k]; else x = __bfloat162float(val[j][k]);
-      const uint32_t c = counts[p + k];
-      if (c) {
-        x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-        const uint32_t times = c & ~kSeen;
-        if (times) x = x - freq * (float)times - pres;
-      }
-      if (g.c.bias_words) x += biases[p + k];
-      if (!((bits >> k) & 1u)) x = -__int_as_float(0x7F800000);
-      if constexpr (sizeof(T) == 4) val[j][k] = x; else val[j][k] = __float2bfloat16_rn(x);
+      if (g.c.bias_words) x[k] += biases[p + k];
+      if (!((bits[j] >> k) & 1u)) x[k] = -__int_as_float(0x7F800000);
+      if constexpr (sizeof(T) == 4) val[j][k] = x[k]; else val[j][k] = __float2bfloat16_rn(x[k]);
     }
-    if (VEC > 1 && w >= 0 && w + VEC <= g.v) {
+    if (VEC > 1 && w >= 0 && w + VEC <= v) {
       *reinterpret_cast<uint4*>(out + w) = *reinterpret_cast<const uint4*>(val[j]);
     } else {
 #pragma unroll
       for (int k = 0; k < VEC; ++k)
-        if (w + k >= 0 && w + k < g.v) out[w + k] = val[j][k];
+        if (w + k >= 0 && w + k < v) out[w + k] = val[j][k];
     }
   }
 }
 
-template <typename T, int VEC, int NV, int C>
+template <typename T, int VEC, int NV, int kThreads>
 lpq_status run(const LogitsArgs& g, cudaStream_t s) {
   constexpr int S = kThreads * VEC * NV;
-  const int64_t segments = ((g.v + VEC - 1 + S - 1) / S + C - 1) / C * C;  // (a row may begin VEC - 1 places in)
+  const int64_t segments = (g.v + VEC - 1 + S - 1) / S;  // (a row may begin VEC - 1 places in)
   const int64_t grid = g.rows * segments;
   if (grid > 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "logits: too large");
-  if constexpr (C == 1)
-    return cuda_check(launch_dependent(adjust_logits_kernel<T, VEC, NV, 1>, dim3((unsigned)grid), dim3(kThreads), 0, s, g, segments),
-                      "logits launch");
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cuda_check(cudaLaunchKernelEx(&cfg, adjust_logits_kernel<T, VEC, NV, C>, g, segments), "logits launch");
-}
-
-template <typename T, int VEC, int NV>
-lpq_status run_context(const LogitsArgs& g, cudaStream_t s) {
-  return g.c.history && g.c.max_len > kClusterContext ? run<T, VEC, NV, 8>(g, s) : run<T, VEC, NV, 1>(g, s);
+  const void* kernel = reinterpret_cast<const void*>(adjust_logits_kernel<T, VEC, NV, kThreads>);
+  lpq_status st = set_smem_attr(kernel, 8 * S);
+  if (st != LPQ_OK) return st;
+  return cuda_check(launch_dependent(adjust_logits_kernel<T, VEC, NV, kThreads>, dim3((unsigned)grid), dim3(kThreads),
+                                     (g.c.bias_words ? 8 : 4) * S, s, g, segments),
+                    "logits launch");
 }
 
 template <typename T>
@@ -196,9 +193,13 @@ lpq_status dispatch(const LogitsArgs& g, cudaStream_t s) {
   // every row must begin equally far from a 16-byte boundary on both sides
   const uintptr_t in = reinterpret_cast<uintptr_t>(g.logits), out = reinterpret_cast<uintptr_t>(g.out);
   const bool vectors = (in - out) % 16 == 0 && (g.rows == 1 || (g.ld - g.ldo) * (int64_t)sizeof(T) % 16 == 0);
+  // Small runs of words while they give every SM a few CTAs; large ones else, and of
+  // twice the words where the context, which every CTA reads, may be long (64 x 131073
+  // FP32, contexts of up to 8192: 26.6 -> 24.6 us, of 32768 50.9 -> 34.8, of 1000 18.5 -> 20.0).
   const bool small = g.rows * g.v < (int64_t)device_sms() * 2 * 4096;
-  if (vectors) return small ? run_context<T, VEC, 1>(g, s) : run_context<T, VEC, 16 / VEC>(g, s);
-  return small ? run_context<T, 1, 4>(g, s) : run_context<T, 1, 16>(g, s);
+  const bool long_context = g.c.history && g.c.max_len >= 2048;
+  if (vectors) return small ? run<T, VEC, 1, 256>(g, s) : long_context ? run<T, VEC, 16 / VEC, 512>(g, s) : run<T, VEC, 16 / VEC, 256>(g, s);
+  return small ? run<T, 1, 4, 256>(g, s) : run<T, 1, 16, 256>(g, s);
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ def adjust(x=A, ld=100, t=1, rows=3, v=100, out=A, ldo=100, null=False, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(null=True), lpq.ERR_INVALID_ARG), (dict(t=2), lpq.ERR_INVALID_ARG), (dict(rows=-1), lpq.ERR_SHAPE), (dict(v=-1), lpq.ERR_SHAPE),
-    (dict(v=(1 << 31) + 1, ld=1 << 32, ldo=1 << 32), lpq.ERR_SHAPE), (dict(ld=99), lpq.ERR_SHAPE), (dict(ldo=99), lpq.ERR_SHAPE), (dict(x=None), lpq.ERR_INVALID_ARG),
+    (dict(v=(1 << 30) + 1, ld=1 << 32, ldo=1 << 32), lpq.ERR_SHAPE), (dict(ld=99), lpq.ERR_SHAPE), (dict(ldo=99), lpq.ERR_SHAPE), (dict(x=None), lpq.ERR_INVALID_ARG),
     (dict(out=None), lpq.ERR_INVALID_ARG), (dict(x=A + 2), lpq.ERR_ALIGN), (dict(t=0, out=A + 1), lpq.ERR_ALIGN), (dict(ld=104), lpq.ERR_SHAPE),
     (dict(max_len=9), lpq.ERR_SHAPE), (dict(max_len=-1), lpq.ERR_SHAPE), (dict(lengths=None), lpq.ERR_INVALID_ARG),
     (dict(history=None, lengths=None, prompt=None), lpq.ERR_INVALID_ARG), (dict(bias_offsets=None), lpq.ERR_INVALID_ARG),
