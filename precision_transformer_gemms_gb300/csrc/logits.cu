@@ -20,22 +20,23 @@ namespace {
 
 constexpr uint32_t kSeen = 0x80000000u;  // stands in the prompt; the other bits count the answer
 
-// `segments` CTAs a row.  What a CTA reads at addresses that it knows, it asks for at once: the time of a CTA
-// is that of a few loads after one another, not of its bytes.
+// `segments` CTAs a row.  What a CTA reads at addresses that it knows, it asks for at
+// once: the time of a CTA is that of a few loads after one another, not of its bytes.
 template <typename T, int VEC, int NV, int kThreads>
-__global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 : 3) adjust_logits_kernel(const LogitsArgs g, int64_t segments) {
+__global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 : 3) adjust_logits_kernel(const LogitsArgs g, uint32_t segments) {
   constexpr int S = kThreads * VEC * NV;  // words of a CTA
   extern __shared__ __align__(16) uint32_t counts[];  // [S], and with biases their sums [S]
   float* biases = reinterpret_cast<float*>(counts + S);
   let_dependents_start();
   const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x / segments;
+  const uint32_t row32 = blockIdx.x / segments;
+  const int64_t row = row32;
   const T* in = static_cast<const T*>(g.logits) + row * g.ld;
   T* out = static_cast<T*>(g.out) + row * g.ldo;
   // Word w of the row stands at w + lead, counted from a 16-byte boundary.
   const int lead = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(in) & 15u) / sizeof(T));
   const int v = (int)g.v;
-  const int first = (int)(blockIdx.x - row * segments) * S - lead;  // word of the run's first place
+  const int first = (int)(blockIdx.x - row32 * segments) * S - lead;  // word of the run's first place
 #pragma unroll
   for (int i = 0; i < S / 4; i += kThreads) {
     reinterpret_cast<uint4*>(counts)[i + tid] = make_uint4(0, 0, 0, 0);
@@ -183,7 +184,7 @@ lpq_status run(const LogitsArgs& g, cudaStream_t s) {
   lpq_status st = set_smem_attr(kernel, 8 * S);
   if (st != LPQ_OK) return st;
   return cuda_check(launch_dependent(adjust_logits_kernel<T, VEC, NV, kThreads>, dim3((unsigned)grid), dim3(kThreads),
-                                     (g.c.bias_words ? 8 : 4) * S, s, g, segments),
+                                     (g.c.bias_words ? 8 : 4) * S, s, g, (uint32_t)segments),
                     "logits launch");
 }
 

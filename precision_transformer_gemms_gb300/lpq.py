@@ -621,10 +621,14 @@ def _check_heads(x, rows, cols, used, device, positions, head_dim, q_weight, k_w
     assert 0 <= used <= cols, f"x must hold {used} values of heads"
     assert positions.dtype is _I64 and positions.shape == (rows,) and positions.is_contiguous() and positions.get_device() == device, \
         f"positions must be {rows} int64 where x lies"
-    w_type = _check_params(head_dim, q_weight, k_weight)
-    assert (q_weight is None or q_weight.get_device() == device) and (k_weight is None or k_weight.get_device() == device), \
-        "the weights must lie where x does"
-    return _TYPES[x.dtype], w_type
+    w_dtype = None
+    for w in (q_weight, k_weight):
+        if w is not None:
+            assert w.dtype in _TYPES and w.numel() == head_dim and w.is_contiguous() and w.get_device() == device, \
+                f"the weights must be contiguous bf16 or fp32 vectors of {head_dim} where x lies"
+            assert w_dtype is None or w_dtype is w.dtype, "the weights must have one type"
+            w_dtype = w.dtype
+    return _TYPES[x.dtype], _TYPES.get(w_dtype, TYPE_FP32)
 
 
 def _heads_out(out, x, rows, used, device):
@@ -655,7 +659,7 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weig
     else:
         ldo = _heads_out(out, x, rows, used, device)
     _check(lib().lpq_qk_norm_rope(x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads, k_heads, head_dim, _ptr(q_weight),
-                                  _ptr(k_weight), w_type, positions.data_ptr(), _freqs(rotary_dim, base, freqs and tuple(freqs)), rotary_dim,
+                                  _ptr(k_weight), w_type, positions.data_ptr(), _freqs(rotary_dim, base, None if freqs is None else tuple(map(float, freqs))), rotary_dim,
                                   interleaved, eps, out.data_ptr(), ldo, _raw_stream(device)))
     return out
 
@@ -689,7 +693,7 @@ def qk_norm_rope_backward(dy, x, q_heads, k_heads, head_dim, positions, q_weight
         dqp, dkp, wsp = dq.data_ptr(), dk.data_ptr(), ws.data_ptr()
     _check(lib().lpq_qk_norm_rope_backward(dy.data_ptr(), _ld(dy, rows, dy.shape[1]), x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads,
                                            k_heads, head_dim, _ptr(q_weight), _ptr(k_weight), w_type, positions.data_ptr(),
-                                           _freqs(rotary_dim, base, freqs and tuple(freqs)), rotary_dim, interleaved, eps, out.data_ptr(), ldo,
+                                           _freqs(rotary_dim, base, None if freqs is None else tuple(map(float, freqs))), rotary_dim, interleaved, eps, out.data_ptr(), ldo,
                                            dqp, dkp, wsp, need, _raw_stream(device)))
     return out, dq, dk
 

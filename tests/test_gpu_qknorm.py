@@ -243,3 +243,24 @@ def test_same_bits_streams_and_graphs():
         graph.replay()
         assert torch.equal(yg, lpq.qk_norm_rope(xs, hq, hk, d, pos, *w))
         assert all(torch.equal(a, b) for a, b in zip(back, lpq.qk_norm_rope_backward(dys, xs, hq, hk, d, pos, *w)))
+
+
+def test_refusals():
+    t, hq, hk, d = 5, 2, 1, 64
+    x, w, pos, dy = make(t, hq, hk, d, BF, BF)
+    good = dict(x=x, q_heads=hq, k_heads=hk, head_dim=d, positions=pos, q_weight=w[0], k_weight=w[1])
+    for bad in (dict(x=x.half()), dict(x=x.cpu()), dict(x=x.t()), dict(q_heads=3), dict(positions=pos.int()), dict(positions=pos[:4]), dict(positions=pos.cpu()),
+                dict(q_weight=w[0][:32]), dict(q_weight=w[0].float()), dict(k_weight=w[1].cpu()), dict(freqs=[1.0]), dict(out=x.float()), dict(out=x[:4])):
+        with pytest.raises(AssertionError):
+            lpq.qk_norm_rope(**{**good, **bad})
+        with pytest.raises(AssertionError):
+            lpq.qk_norm_rope_backward(dy, **{**good, **bad})
+    for bad in (dict(rotary_dim=66, head_dim=64), dict(rotary_dim=31), dict(eps=-1.0), dict(freqs=[float("nan")] * 32), dict(x=x[:1].expand(5, -1))):
+        with pytest.raises(lpq.LpqError):
+            lpq.qk_norm_rope(**{**good, **bad})
+    with pytest.raises(AssertionError):
+        lpq.qk_norm_rope_backward(dy.float(), **good)
+    y = lpq.qk_norm_rope(x, hq, hk, d, pos, rotary_dim=0, freqs=[])
+    check(x, (None, None), hq, hk, d, pos, y, 0)
+    own = torch.tensor([0.5 ** i for i in range(32)], dtype=torch.float64)  # frequencies of any kind that float() takes
+    check(x, w, hq, hk, d, pos % 1000, lpq.qk_norm_rope(**{**good, "positions": pos % 1000, "freqs": own}), d, freqs=own.tolist())
