@@ -8,16 +8,27 @@
 //
 // HBM bounds both: one read and one write forward, two reads and one write
 // backward.  A pair's two values lie in one thread, so the rotation needs no
-// exchange: a thread holds V values of the first half and V of the second (or
-// 2 V neighbours, where neighbours are turned together), and D / (2 V) lanes
-// hold a head, whose sums take log2 of that many shuffles.  The statistics are
-// taken again backward rather than kept: x is read anyway.
+// exchange: a thread holds 16-byte vectors from both halves of a head (or whole pairs,
+// where neighbours are turned together), 8 pairs in all; D / 16 lanes hold a head,
+// whose sums take log2 of that many shuffles.  Rows stream through per-lane rings of
+// asynchronous copies; arithmetic is two-wide.  The statistics are taken again backward
+// rather than kept: x is read anyway.
 //
 // The angle in turns is position * (frequency / 2 pi), of which only the
 // fraction matters: as a 64-bit integer product modulo 2^64 that is exact but
 // for the frequency's own rounding (2^-53 of it), so an angle at position 2^20
-// is as near as one at 0.  cos and sin are taken once per token, thread and
-// pair, and serve all heads that a warp takes of the token.
+// is as near as one at 0.  cos and sin are taken once per token, shared by a warp's
+// lanes, and serve all heads that the warp takes of the token.
+//
+// Measured against the copy bandwidth of 6677 GB/s, 15872 tokens, bf16 unless said:
+//   forward   64 heads of 128 78.5 us (99%), of 64 78.2, 32 of 256 with 64 turned 79.5,
+//             neighbours turned 78.6, 8192 tokens FP32 81.7 (98%), 32 + 8 heads of 128
+//             54.6 (89%), 16 of 512 110 (71%)
+//   backward  64 heads of 128 129 us (90%; 4 of it the join of the parts), of 64 132,
+//             32 of 256 135, 8192 tokens FP32 154 (78%: a ring of two), 32 + 8 106 (69%)
+// Heads that are no power of two times 16 leave lanes idle (96 of 80: 118 us, 62%);
+// those that 16 values or 16 bytes do not divide go value by value (64 of 130: 260 us,
+// 30%; backward 370, 32%), bound by the count of accesses.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -50,7 +61,7 @@ struct QkKernelArgs {
   const void* weight[2];  // of the query heads, of the key heads; NULL: 1
   const int64_t* positions;
   float* parts;  // backward: [CTA][2][D], or NULL
-  int64_t rows;
+  int rows;
   int64_t groups;  // of heads: tokens * (those of the queries and of the keys)
   int heads[2];    // query heads, key heads
   int runs[2];     // groups of 32 / lanes heads
@@ -71,51 +82,36 @@ __device__ __forceinline__ T from_f32(float v) {
   if constexpr (sizeof(T) == 4) return v; else return __float2bfloat16_rn(v);
 }
 
-// V values as they lie in memory.
+// V values as they lie in memory: 16 bytes, or one value.
 template <typename T, int V>
 struct Raw {
-  uint4 v[V * sizeof(T) / 16];
-  __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void store(T* p) const {
-#pragma unroll
-    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
-  }
-  // Through a lane's places in shared memory, 512 bytes apart.
+  static_assert(V * sizeof(T) == 16, "a vector is 16 bytes");
+  uint4 v;
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  // Through a lane's place in shared memory.
   static __device__ __forceinline__ void copy(uint32_t to, const T* p, bool there) {
-#pragma unroll
-    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * 512), "l"(reinterpret_cast<const uint4*>(p) + i),
-                   "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(there ? 16 : 0) : "memory");
   }
   __device__ __forceinline__ void take(uint32_t from) {
-#pragma unroll
-    for (int i = 0; i < (int)(V * sizeof(T) / 16); ++i)
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                   : "r"(from + i * 512) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
   }
   // Values 2 i and 2 i + 1 (i is a constant after unrolling).
   __device__ __forceinline__ float2 get2(int i) const {
     if constexpr (sizeof(T) == 4) {
-      const uint4& u = v[i >> 1];
-      return i & 1 ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w)) : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      return i & 1 ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
     } else {
-      const uint4& u = v[i >> 2];
-      const uint32_t p = (i & 3) == 0 ? u.x : (i & 3) == 1 ? u.y : (i & 3) == 2 ? u.z : u.w;
+      const uint32_t p = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
       return make_float2(bf16_lo(p), bf16_hi(p));
     }
   }
   __device__ __forceinline__ void set2(int i, float a, float b) {
-    uint4& u = v[sizeof(T) == 4 ? i >> 1 : i >> 2];
     if constexpr (sizeof(T) == 4) {
-      if (i & 1) { u.z = __float_as_uint(a); u.w = __float_as_uint(b); }
-      else { u.x = __float_as_uint(a); u.y = __float_as_uint(b); }
+      if (i & 1) { v.z = __float_as_uint(a); v.w = __float_as_uint(b); }
+      else { v.x = __float_as_uint(a); v.y = __float_as_uint(b); }
     } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
       const uint32_t p = *reinterpret_cast<const uint32_t*>(&h);
-      if ((i & 3) == 0) u.x = p; else if ((i & 3) == 1) u.y = p; else if ((i & 3) == 2) u.z = p; else u.w = p;
+      if ((i & 3) == 0) v.x = p; else if ((i & 3) == 1) v.y = p; else if ((i & 3) == 2) v.z = p; else v.w = p;
     }
   }
 };
@@ -126,106 +122,108 @@ struct Raw<T, 1> {
   __device__ __forceinline__ void store(T* p) const { *p = v; }
 };
 
-// A thread's part of a head: P pairs (even), as NU units of V pairs.  Vectors: V =
-// 8, one unit.  Any alignment and sizes: V = 1, units 32 apart.  Pairs 2 j and 2 j +
-// 1 lie in one float2 of firsts and one of seconds, for the two-wide operations.
+// A thread's part of a head: P pairs (even), as NU units of two vectors of V values.
+// Neighbouring lanes' vectors are neighbours, so that a warp's accesses take whole
+// sectors: the two vectors lie half a head apart, or half of the turned values, where
+// the pairs are made of their halves.  Vectors of 16 bytes hold 8 pairs a thread; any
+// alignment and sizes: V = 1, units 32 apart.  Pairs 2 j and 2 j + 1 lie in one float2
+// of firsts and one of seconds, for the two-wide operations.
 template <typename T, int V, int NU, bool NEIGHBOURS>
 struct Slice {
   static constexpr int P = V * NU;
   Raw<T, V> a[NU], b[NU];
 
-  // Offsets in a head of a unit's two halves; false: the thread holds no such unit.
-  static __device__ __forceinline__ bool place(const QkKernelArgs& g, int lane, int j, int& at, int& bt) {
-    const int u = lane + j * g.lanes;
-    const int turned = g.rotary / (2 * V);
-    if (V == 1 ? g.neighbours || u >= turned : NEIGHBOURS || u >= turned) {  // (values that are not turned lie side by side)
-      at = u * 2 * V;
-      bt = at + V;
-    } else {
+  // Offsets in a head of unit j's two vectors; false: the thread holds no such unit.
+  static __device__ __forceinline__ bool place(const QkKernelArgs& g, int lanes, int lane, int j, int& at, int& bt) {
+    const int u = lane + j * lanes, turned = g.rotary / (2 * V);
+    if (V == 1 && g.neighbours) {
+      at = 2 * u;
+      bt = at + 1;
+    } else if (V > 1 && NEIGHBOURS) {
+      at = u * V;
+      bt = g.dim / 2 + at;
+    } else if (u < turned) {
       at = u * V;
       bt = g.rotary / 2 + at;
+    } else {
+      at = g.rotary + (u - turned) * V;
+      bt = at + (g.dim - g.rotary) / 2;
     }
     return u * 2 * V < g.dim;
   }
-  // Value by value (V = 1).
-  __device__ __forceinline__ void load(const QkKernelArgs& g, const T* head, int lane, bool there) {
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      int at, bt;
-      if (place(g, lane, j, at, bt) && there) {
-        a[j].load(head + at);
-        b[j].load(head + bt);
-      } else {
-        a[j] = Raw<T, V>{};
-        b[j] = Raw<T, V>{};
-      }
+  // Places in the head of pair i's two values.
+  static __device__ __forceinline__ bool where(const QkKernelArgs& g, int lanes, int lane, int i, int& p, int& q) {
+    int at, bt;
+    const bool in = place(g, lanes, lane, i / V, at, bt);
+    const int k = i % V;
+    if (NEIGHBOURS && V > 1) {
+      p = k < V / 2 ? at + 2 * k : bt + 2 * k - V;
+      q = p + 1;
+    } else {
+      p = at + k;
+      q = bt + k;
     }
+    return in;
+  }
+  // Which pair of the head that is, among those that are turned (beyond half of `rotary`: it is not).
+  static __device__ __forceinline__ int turn_of(const QkKernelArgs& g, int lanes, int lane, int i) {
+    if (NEIGHBOURS && V > 1) {
+      int p, q;
+      where(g, lanes, lane, i, p, q);
+      return p / 2;
+    }
+    return (lane + i / V * lanes) * V + i % V;
   }
   __device__ __forceinline__ void values(float2 (&p)[P / 2], float2 (&q)[P / 2]) const {
 #pragma unroll
-    for (int j = 0; j < P / 2; ++j) {
+    for (int i = 0; i < P / 2; ++i) {
       if constexpr (V == 1) {
-        p[j] = make_float2(to_f32(a[2 * j].v), to_f32(a[2 * j + 1].v));
-        q[j] = make_float2(to_f32(b[2 * j].v), to_f32(b[2 * j + 1].v));
-      } else if constexpr (NEIGHBOURS) {
-        const Raw<T, V>& r = j < V / 4 ? a[0] : b[0];
-        const float2 u = r.get2(2 * j % (V / 2)), v = r.get2(2 * j % (V / 2) + 1);
-        p[j] = make_float2(u.x, v.x);
-        q[j] = make_float2(u.y, v.y);
+        p[i] = make_float2(to_f32(a[2 * i].v), to_f32(a[2 * i + 1].v));
+        q[i] = make_float2(to_f32(b[2 * i].v), to_f32(b[2 * i + 1].v));
       } else {
-        p[j] = a[0].get2(j);
-        q[j] = b[0].get2(j);
+        const int j = i / (V / 2), k = i % (V / 2);
+        if constexpr (NEIGHBOURS) {
+          const Raw<T, V>& r = k < V / 4 ? a[j] : b[j];
+          const float2 u = r.get2(2 * k % (V / 2)), v = r.get2(2 * k % (V / 2) + 1);
+          p[i] = make_float2(u.x, v.x);
+          q[i] = make_float2(u.y, v.y);
+        } else {
+          p[i] = a[j].get2(k);
+          q[i] = b[j].get2(k);
+        }
       }
     }
   }
   __device__ __forceinline__ void set(const float2 (&p)[P / 2], const float2 (&q)[P / 2]) {
 #pragma unroll
-    for (int j = 0; j < P / 2; ++j) {
+    for (int i = 0; i < P / 2; ++i) {
       if constexpr (V == 1) {
-        a[2 * j].v = from_f32<T>(p[j].x);
-        a[2 * j + 1].v = from_f32<T>(p[j].y);
-        b[2 * j].v = from_f32<T>(q[j].x);
-        b[2 * j + 1].v = from_f32<T>(q[j].y);
-      } else if constexpr (NEIGHBOURS) {
-        Raw<T, V>& r = j < V / 4 ? a[0] : b[0];
-        r.set2(2 * j % (V / 2), p[j].x, q[j].x);
-        r.set2(2 * j % (V / 2) + 1, p[j].y, q[j].y);
+        a[2 * i].v = from_f32<T>(p[i].x);
+        a[2 * i + 1].v = from_f32<T>(p[i].y);
+        b[2 * i].v = from_f32<T>(q[i].x);
+        b[2 * i + 1].v = from_f32<T>(q[i].y);
       } else {
-        a[0].set2(j, p[j].x, p[j].y);
-        b[0].set2(j, q[j].x, q[j].y);
+        const int j = i / (V / 2), k = i % (V / 2);
+        if constexpr (NEIGHBOURS) {
+          Raw<T, V>& r = k < V / 4 ? a[j] : b[j];
+          r.set2(2 * k % (V / 2), p[i].x, q[i].x);
+          r.set2(2 * k % (V / 2) + 1, p[i].y, q[i].y);
+        } else {
+          a[j].set2(k, p[i].x, p[i].y);
+          b[j].set2(k, q[i].x, q[i].y);
+        }
       }
     }
-  }
-  __device__ __forceinline__ void store(const QkKernelArgs& g, T* head, int lane) const {
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      int at, bt;
-      if (!place(g, lane, j, at, bt)) continue;
-      a[j].store(head + at);
-      b[j].store(head + bt);
-    }
-  }
-  // Places in the head of pair i's two values.
-  static __device__ __forceinline__ bool where(const QkKernelArgs& g, int lane, int i, int& p, int& q) {
-    int at, bt;
-    const bool in = place(g, lane, i / V, at, bt);
-    if (NEIGHBOURS && V > 1) {
-      p = at + 2 * (i % V);
-      q = p + 1;
-    } else {
-      p = at + i % V;
-      q = bt + i % V;
-    }
-    return in;
   }
 };
 
 __device__ __forceinline__ float2 twice(float v) { return make_float2(v, v); }
 
-// A warp takes a run of the head groups (32 / lanes heads each): those of all
-// tokens' queries in token order, then those of the keys, so that the weights change
-// once at most.  LANES > 0: heads of 16 LANES values in whole groups, every lane with
-// a unit of every group.
+// A warp takes a run of the head groups (32 / lanes heads each).  Forward they come
+// token by token, queries then keys, so that a token's angles serve both; backward the
+// queries of all tokens, then the keys, so that the sums of the weight's gradient
+// change hands once at most.  LANES > 0: heads of 16 LANES values in whole groups,
+// every lane with all its units of every group.
 template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD, int LANES>
 __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm_kernel(const __grid_constant__ QkKernelArgs g) {
   using S = Slice<T, V, NU, NEIGHBOURS>;
@@ -256,32 +254,50 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
 
   const int64_t workers = (int64_t)gridDim.x * kWarps, me = (int64_t)blockIdx.x * kWarps + warp;
   const int64_t each = g.groups / workers, more = g.groups % workers;
-  const int64_t begin = me * each + min(me, more), count64 = each + (me < more);
-  const int count = (int)count64;
+  const int64_t begin = me * each + min(me, more);
+  const int count = (int)(each + (me < more));
   const float inv_dim = 1.0f / (float)g.dim;
   const int per_group = 32 / lanes, step = per_group * g.dim;  // heads, and values from a group to the next
-  int unit_a = 0, unit_b = 0;  // the lane's vectors in a head
-  const bool unit = S::place(g, lane, 0, unit_a, unit_b);
+  int unit_a[NU], unit_b[NU];  // the lane's vectors in a head
+  bool unit[NU];
+#pragma unroll
+  for (int j = 0; j < NU; ++j) unit[j] = S::place(g, lanes, lane, j, unit_a[j], unit_b[j]) || LANES > 0;
 
-  // A place in the run: the group, and where its heads begin in a tensor.
+  // A place in the run: a group of a token's query or key heads.
   struct Place {
     int token, kind, run;
   };
-  auto next = [&](Place& p, auto&& same, auto&& token, auto&& kind) {  // moves on; tells by how much
-    if (++p.run < g.runs[p.kind]) return same();
+  Place here;
+  if constexpr (BACKWARD) {
+    here.kind = begin >= (int64_t)g.rows * g.runs[0];
+    const int64_t first = begin - (here.kind ? (int64_t)g.rows * g.runs[0] : 0);
+    here.token = g.runs[here.kind] ? (int)(first / g.runs[here.kind]) : 0;
+    here.run = (int)(first - (int64_t)here.token * g.runs[here.kind]);
+  } else {
+    const int per_token = g.runs[0] + g.runs[1];
+    here.token = (int)(begin / per_token);
+    here.run = (int)(begin - (int64_t)here.token * per_token);
+    here.kind = here.run >= g.runs[0];
+    here.run -= here.kind ? g.runs[0] : 0;
+  }
+  auto next = [&](Place& p) {  // true: the next group of the same heads' kind and token
+    if (++p.run < g.runs[p.kind]) return true;
     p.run = 0;
-    if (++p.token < g.rows) return token();
-    p.token = 0;
-    p.kind = 1;
-    kind();
+    if (BACKWARD) {
+      if (++p.token == g.rows) {
+        p.token = 0;
+        p.kind = 1;
+      }
+    } else if (p.kind == 0 && g.runs[1] > 0) {
+      p.kind = 1;
+    } else {
+      ++p.token;
+      p.kind = g.runs[0] == 0;
+    }
+    return false;
   };
-  Place here{};
-  here.kind = begin >= g.rows * g.runs[0];
-  const int64_t first = begin - (here.kind ? g.rows * g.runs[0] : 0);
-  here.token = g.runs[here.kind] ? (int)(first / g.runs[here.kind]) : 0;
-  here.run = (int)(first - (int64_t)here.token * g.runs[here.kind]);
-  auto start = [&](int64_t ld) {  // of this place's group in a tensor, at this lane's head
-    return (int64_t)here.token * ld + (int64_t)(here.kind ? g.heads[0] : 0) * g.dim + (int64_t)here.run * step + sub * g.dim;
+  auto start = [&](const Place& p, int64_t ld) {  // of its group in a tensor, at this lane's head
+    return (int64_t)p.token * ld + (int64_t)(p.kind ? g.heads[0] : 0) * g.dim + (int64_t)p.run * step + sub * g.dim;
   };
   auto has_head = [&](const Place& p) { return LANES > 0 || p.run * per_group + sub < g.heads[p.kind]; };
 
@@ -289,45 +305,46 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
   S nx, ny;
   int f_left = count;
   Place f = here;
-  const T* fx = static_cast<const T*>(g.x) + start(g.ldx);
-  const T* fy = BACKWARD ? static_cast<const T*>(g.dy) + start(g.lddy) : nullptr;
+  const T* const x = static_cast<const T*>(g.x);
+  const T* const dy = static_cast<const T*>(g.dy);
+  const T* fx = x + start(f, g.ldx);
+  const T* fy = BACKWARD ? dy + start(f, g.lddy) : nullptr;
   uint32_t f_at = 0, at = 0;
   const uint32_t ring = smem_u32(smem) + warp * (R::kDepth * R::kStage) + (threadIdx.x & 31) * 16;
-  constexpr uint32_t kHalf = V * sizeof(T) / 16 * 512;  // of a head's slice in a stage
   auto fetch = [&]() {
     if (f_left > 0) {
       --f_left;
       const bool there = has_head(f);
-      if constexpr (kRing) {
-        const bool in = LANES > 0 || (there && unit);
-        const T* px = in ? fx : static_cast<const T*>(g.x);
-        Raw<T, V>::copy(ring + f_at, in ? px + unit_a : px, in);
-        Raw<T, V>::copy(ring + f_at + kHalf, in ? px + unit_b : px, in);
-        if constexpr (BACKWARD) {
-          const T* py = in ? fy : static_cast<const T*>(g.dy);
-          Raw<T, V>::copy(ring + f_at + R::kStage / 2, in ? py + unit_a : py, in);
-          Raw<T, V>::copy(ring + f_at + R::kStage / 2 + kHalf, in ? py + unit_b : py, in);
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        const bool in = LANES > 0 || (there && unit[j]);
+        if constexpr (kRing) {
+          const uint32_t to = ring + f_at + j * 1024;
+          Raw<T, V>::copy(to, in ? fx + unit_a[j] : x, in);
+          Raw<T, V>::copy(to + 512, in ? fx + unit_b[j] : x, in);
+          if constexpr (BACKWARD) {
+            Raw<T, V>::copy(to + R::kStage / 2, in ? fy + unit_a[j] : dy, in);
+            Raw<T, V>::copy(to + R::kStage / 2 + 512, in ? fy + unit_b[j] : dy, in);
+          }
+        } else {
+          nx.a[j] = nx.b[j] = ny.a[j] = ny.b[j] = Raw<T, V>{};
+          if (in) {
+            nx.a[j].load(fx + unit_a[j]);
+            nx.b[j].load(fx + unit_b[j]);
+            if constexpr (BACKWARD) {
+              ny.a[j].load(fy + unit_a[j]);
+              ny.b[j].load(fy + unit_b[j]);
+            }
+          }
         }
-      } else {
-        nx.load(g, fx, lane, there);
-        if constexpr (BACKWARD) ny.load(g, fy, lane, there);
       }
-      const int run = f.run;
-      next(
-          f,
-          [&]() {
-            fx += step;
-            if constexpr (BACKWARD) fy += step;
-          },
-          [&]() {
-            fx += g.ldx - run * step;
-            if constexpr (BACKWARD) fy += g.lddy - run * step;
-          },
-          [&]() {
-            const int64_t keys = (int64_t)g.heads[0] * g.dim + sub * g.dim;
-            fx = static_cast<const T*>(g.x) + keys;
-            if constexpr (BACKWARD) fy = static_cast<const T*>(g.dy) + keys;
-          });
+      if (next(f)) {
+        fx += step;
+        if constexpr (BACKWARD) fy += step;
+      } else {
+        fx = x + start(f, g.ldx);
+        if constexpr (BACKWARD) fy = dy + start(f, g.lddy);
+      }
     }
     if constexpr (kRing) {
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
         b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
       }
       int pa, pb;
-      if (S::where(g, lane, k, pa, pb) && sub == 0) {
+      if (S::where(g, lanes, lane, k, pa, pb) && sub == 0) {
         sums[(warp * 2 + kind) * g.dim + pa] += a;
         sums[(warp * 2 + kind) * g.dim + pb] += b;
       }
@@ -361,9 +378,9 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
 #pragma unroll
     for (int i = 0; i < H; ++i) dwp[i] = dwq[i] = twice(0.f);
   };
-  bool new_token = true;
+  bool new_token = true, new_kind = true;
   int64_t next_position = count > 0 ? g.positions[here.token] : 0;
-  T* to = static_cast<T*>(g.out) + start(g.ldo);
+  T* to = static_cast<T*>(g.out) + start(here, g.ldo);
   for (int i = 0; i < count; ++i) {
     if (new_token) {  // the warp's lanes share the angles
       const uint64_t position = (uint64_t)next_position;
@@ -376,38 +393,39 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
         trig[j] = make_float2(c, s);
       }
       __syncwarp();
+    }
+    if (new_token || new_kind) {
       float2 turn[P];  // (cos, sin)
       float w[2 * P];  // of the firsts, of the seconds
+      const float* ws = sh + here.kind * g.dim;
       if constexpr (V > 1) {
-        const float* ws = sh + here.kind * g.dim;
-#pragma unroll
-        for (int k = 0; k < P; k += 4) {
-          const bool in = LANES > 0 || unit;
-          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 u = in ? *reinterpret_cast<const float4*>(ws + unit_a + k) : zero;
-          const float4 v = in ? *reinterpret_cast<const float4*>(ws + unit_b + k) : zero;
-          const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {  // (neighbours: the unit's 16 values one after another)
-            w[NEIGHBOURS ? (k + h) / 2 + (h & 1 ? P : 0) : k + h] = a[h];
-            w[NEIGHBOURS ? (P + k + h) / 2 + (h & 1 ? P : 0) : P + k + h] = b[h];
-          }
-        }
 #pragma unroll
         for (int k = 0; k < P; k += 2) {
-          const float4 r = lane * V < half ? *reinterpret_cast<const float4*>(trig + lane * V + k) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+          const int t = S::turn_of(g, lanes, lane, k);  // (even, and so is half)
+          const float4 r = t < half ? *reinterpret_cast<const float4*>(trig + t) : make_float4(1.0f, 0.0f, 1.0f, 0.0f);
           turn[k] = make_float2(r.x, r.y);
           turn[k + 1] = make_float2(r.z, r.w);
+        }
+#pragma unroll
+        for (int k = 0; k < P; k += 4) {
+          const int j = k / V, i0 = k % V;
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 u = unit[j] ? *reinterpret_cast<const float4*>(ws + unit_a[j] + i0) : zero;
+          const float4 v = unit[j] ? *reinterpret_cast<const float4*>(ws + unit_b[j] + i0) : zero;
+          const float a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {  // (neighbours: value 2 i and 2 i + 1 of a vector are pair i's)
+            w[NEIGHBOURS ? j * V + (i0 + h) / 2 + (h & 1 ? P : 0) : k + h] = a[h];
+            w[NEIGHBOURS ? j * V + (V + i0 + h) / 2 + (h & 1 ? P : 0) : P + k + h] = b[h];
+          }
         }
       } else {
 #pragma unroll
         for (int k = 0; k < P; ++k) {
-          const int j = lane + k * lanes;
-          turn[k] = j < half ? trig[j] : make_float2(1.0f, 0.0f);
-          int p, q;
-          const bool in = S::where(g, lane, k, p, q);
-          w[k] = in ? sh[here.kind * g.dim + p] : 0.f;
-          w[P + k] = in ? sh[here.kind * g.dim + q] : 0.f;
+          const int t = S::turn_of(g, lanes, lane, k);
+          turn[k] = t < half ? trig[t] : make_float2(1.0f, 0.0f);
+          w[k] = unit[k] ? ws[unit_a[k]] : 0.f;
+          w[P + k] = unit[k] ? ws[unit_b[k]] : 0.f;
         }
       }
 #pragma unroll
@@ -430,11 +448,15 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
     S cx, cy;
     if constexpr (kRing) {
       asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-      cx.a[0].take(ring + at);
-      cx.b[0].take(ring + at + kHalf);
-      if constexpr (BACKWARD) {
-        cy.a[0].take(ring + at + R::kStage / 2);
-        cy.b[0].take(ring + at + R::kStage / 2 + kHalf);
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        const uint32_t from = ring + at + j * 1024;
+        cx.a[j].take(from);
+        cx.b[j].take(from + 512);
+        if constexpr (BACKWARD) {
+          cy.a[j].take(from + R::kStage / 2);
+          cy.b[j].take(from + R::kStage / 2 + 512);
+        }
       }
       at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
     } else {
@@ -454,7 +476,7 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
     float square = squares.x + squares.y;
     const bool there = has_head(here);
     if constexpr (!BACKWARD) {
-      #pragma unroll
+#pragma unroll
       for (int o = lanes >> 1; o > 0; o >>= 1) square += __shfl_xor_sync(0xFFFFFFFFu, square, o);
       if constexpr (kRing) fetch();  // into the place whose values have entered the sum
       const float2 rstd = twice(rsqrtf(fmaf(square, inv_dim, g.eps)));
@@ -476,7 +498,7 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
         dots = __ffma2_rn(__fmul2_rn(gq[k], wb[k]), q[k], dots);
       }
       float dot = dots.x + dots.y;
-      #pragma unroll
+#pragma unroll
       for (int o = lanes >> 1; o > 0; o >>= 1) {
         square += __shfl_xor_sync(0xFFFFFFFFu, square, o);
         dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
@@ -496,28 +518,24 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
     }
     if (there) {
       cx.set(p, q);
-      if constexpr (kRing) {
-        if (LANES > 0 || unit) {
-          cx.a[0].store(to + unit_a);
-          cx.b[0].store(to + unit_b);
+#pragma unroll
+      for (int j = 0; j < NU; ++j)
+        if (LANES > 0 || unit[j]) {
+          cx.a[j].store(to + unit_a[j]);
+          cx.b[j].store(to + unit_b[j]);
         }
-      } else {
-        cx.store(g, to, lane);
-      }
     }
-    const int run = here.run, kind = here.kind;
-    new_token = true;
-    next(
-        here,
-        [&]() {
-          new_token = false;
-          to += step;
-        },
-        [&]() { to += g.ldo - run * step; },
-        [&]() {
-          to = static_cast<T*>(g.out) + (int64_t)g.heads[0] * g.dim + sub * g.dim;
-          if constexpr (BACKWARD) leave_sums(kind);
-        });
+    const int token = here.token, kind = here.kind;
+    if (next(here)) {
+      new_token = new_kind = false;
+      to += step;
+    } else {
+      new_kind = here.kind != kind;
+      new_token = here.token != token || (BACKWARD && new_kind);
+      to = static_cast<T*>(g.out) + start(here, g.ldo);
+      if constexpr (BACKWARD)
+        if (new_kind || here.token == 0) leave_sums(kind);
+    }
   }
   if constexpr (BACKWARD) {
     if (!g.parts) return;
@@ -558,8 +576,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) qk_join_kernel(const float* p
 
 // CTAs per place for one: SMs are not equally fast at memory, and an even split over
 // the CTAs that fit at once waits for the slowest (15872 x 64 x 128 bf16: 95.4 us with
-// one round, 82.7 with four, 80.1 with eight).  Backward each CTA leaves a part to
-// join, which costs more than it gains (130 us with one round, 133 with two).
+// one round, 82.7 with four, 80.1 with eight).  Backward each CTA leaves a part to join,
+// which costs more than rounds gain (130 us with one, 133 with two).
 constexpr int kWaves = 8;
 // Most CTAs of the backward pass, each of which leaves a part of the weights' gradients.
 int64_t most_parts() { return 2 * 160; }
@@ -567,19 +585,22 @@ int64_t most_parts() { return 2 * 160; }
 template <typename T, int V, int NU, bool NEIGHBOURS, bool BACKWARD, int LANES>
 lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t s) {
   const void* kernel = reinterpret_cast<const void*>(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD, LANES>);
-  const int units = (g.dim / 2 + V - 1) / V;
+  const int units = g.dim / 2 / V;  // of a head; value by value a warp has a head
   g.lanes = 1;
-  while (g.lanes < 32 && g.lanes < units) g.lanes *= 2;
+  while (g.lanes < 32 && g.lanes * (V > 1 ? NU : 1) < units) g.lanes *= 2;
   for (int i = 0; i < 2; ++i) g.runs[i] = (g.heads[i] * g.lanes + 31) / 32;
   g.groups = rows * (g.runs[0] + g.runs[1]);
-  g.rows = rows;
+  g.rows = (int)rows;
   const int ring = V > 1 ? Ring<T, BACKWARD>::kBytes : 0;
   auto rest = [](int dim, int rotary) { return 2 * dim * 4 + kWarps * rotary / 2 * 8 + (BACKWARD ? kWarps * 2 * dim * 4 : 0); };
   const int smem = ring + rest(g.dim, g.rotary);
   lpq_status st = set_smem_attr(kernel, ring + rest(kQkMaxDim, kQkMaxDim));
   if (st != LPQ_OK) return st;
   int64_t most = (int64_t)device_sms() * std::max(1, std::min(Ring<T, BACKWARD>::kCtas, 226 * 1024 / (smem + 4 * 1024)));
-  if (BACKWARD) most = std::min(most, most_parts()); else most *= kWaves;
+  // Forward more rounds of CTAs while every warp keeps a few groups (2000 tokens of 32 +
+  // 8 heads of 128: 20.0 us with one group a warp, 9.9 with five).
+  if (BACKWARD) most = std::min(most, most_parts());
+  else most = std::max(most, std::min(most * kWaves, g.groups / (kWarps * 8)));
   const int64_t grid = std::max<int64_t>(1, std::min(most, (g.groups + kWarps - 1) / kWarps));
   if (g.groups / (grid * kWarps) >= 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "qk norm: too large");
   st = cuda_check(launch_dependent(qk_norm_kernel<T, V, NU, NEIGHBOURS, BACKWARD, LANES>, dim3((unsigned)grid), dim3(32 * kWarps), smem, s, g),
@@ -590,19 +611,23 @@ lpq_status run(QkKernelArgs& g, int64_t rows, float* dq, float* dk, cudaStream_t
                     "qk norm join launch");
 }
 
+template <typename T, bool NEIGHBOURS, bool BACKWARD>
+lpq_status vectors(QkKernelArgs& g, int64_t rows, bool usual, float* dq, float* dk, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T), NU = 8 / V;
+  if (usual && g.dim == 64) return run<T, V, NU, NEIGHBOURS, BACKWARD, 4>(g, rows, dq, dk, s);
+  if (usual && g.dim == 128) return run<T, V, NU, NEIGHBOURS, BACKWARD, 8>(g, rows, dq, dk, s);
+  if (usual && g.dim == 256) return run<T, V, NU, NEIGHBOURS, BACKWARD, 16>(g, rows, dq, dk, s);
+  return run<T, V, NU, NEIGHBOURS, BACKWARD, 0>(g, rows, dq, dk, s);
+}
+
 template <typename T, bool BACKWARD>
 lpq_status dispatch(QkKernelArgs& g, int64_t rows, bool neighbours, float* dq, float* dk, cudaStream_t s) {
   auto whole = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * sizeof(T) % 16 == 0; };
   g.neighbours = neighbours;
   if (g.dim % 16 == 0 && g.rotary % 16 == 0 && whole(g.x, g.ldx) && whole(g.out, g.ldo) && (!BACKWARD || whole(g.dy, g.lddy))) {
-    if (neighbours) return run<T, 8, 1, true, BACKWARD, 0>(g, rows, dq, dk, s);
     const int per_group = 512 / g.dim;  // whole groups of the usual head sizes
-    if (per_group > 0 && g.heads[0] % per_group == 0 && g.heads[1] % per_group == 0) {
-      if (g.dim == 64) return run<T, 8, 1, false, BACKWARD, 4>(g, rows, dq, dk, s);
-      if (g.dim == 128) return run<T, 8, 1, false, BACKWARD, 8>(g, rows, dq, dk, s);
-      if (g.dim == 256) return run<T, 8, 1, false, BACKWARD, 16>(g, rows, dq, dk, s);
-    }
-    return run<T, 8, 1, false, BACKWARD, 0>(g, rows, dq, dk, s);
+    const bool usual = per_group > 0 && g.heads[0] % per_group == 0 && g.heads[1] % per_group == 0;
+    return neighbours ? vectors<T, true, BACKWARD>(g, rows, usual, dq, dk, s) : vectors<T, false, BACKWARD>(g, rows, usual, dq, dk, s);
   }
   // value by value
   if (g.dim <= 128) return run<T, 1, 2, false, BACKWARD, 0>(g, rows, dq, dk, s);
