@@ -5,18 +5,31 @@
 //
 // The chosen experts' weights, read once, are the traffic there is; their rows
 // stream, decode and multiply as in the plain products of a few tokens.  Two
-// launches.  Up: an item is 64 hidden values of an expert, whose gate and up rows
-// share a warp's 16 MMA rows, so that a lane ends with both and stores silu(g) u;
-// the MMA's columns are the tokens that chose the expert.  Down: an item is 128
-// rows of an expert, whose results lie in a workspace until the last expert of
-// those rows has come: that CTA adds them up per token, in the order of the
-// token's choice.  Which experts there are, and for whom, every CTA reads from
-// the ids by itself.
+// launches.  Up: a warp's tile is 8 hidden values of an expert, whose gate and up rows
+// share its 16 MMA rows, so that a lane ends with both and stores silu(g) u; the
+// MMA's columns are the tokens that chose the expert.  Down: a tile is 16 rows of an
+// expert, whose results lie in a workspace until the last expert of those rows has
+// come: that warp adds them up per token, in the order of the token's choice.  Which
+// experts there are, and for whom, every CTA reads from the ids by itself.  The grid
+// is not resident at once: SMs are not equally fast at memory, and runs handed out as
+// CTAs end even that out.
 //
 // Hidden values enter the second product as f16 times a power of two per vector
-// (the largest in [2^14, 2^15)): 11 significant bits, a thirty-second of y's own
-// bf16 rounding.  Everything else is exact or FP32.
+// (the largest in [2^14, 2^15)): 11 significant bits, an eighth of y's own bf16
+// rounding.  Everything else is exact or FP32.
+//
+// Measured (router, up and down in one graph; in brackets the weights' bytes at the copy
+// bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 120 us (67),
+// MXFP4 124; one token of them 34 (13); 4 tokens, 4 of 32 of 2048 x 768 24 (5.3); 24
+// tokens, 2 of 16 of 2048 x 1024 39 (8.5); 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
+// (5.6); one token, 2 of 8 of 512 x 384 11.7 (0.1), the three launches whose parts wait
+// for one another.  What bounds the large ones: of an earlier state's 126 us the stream
+// without a product took 102, the products without the stream 97 and what a CTA does
+// before and after its tiles 58 by itself (the plan 15, the vectors' conversion 11, the
+// rest launches, the router and the joining of the results); the three overlap in the
+// CTAs that share an SM.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fp4_rows.cuh"
@@ -175,7 +188,6 @@ lpq_status route(const RouteArgs& g, cudaStream_t s) {
 
 // ------------------------------------------------------------------ the experts
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRing = 3;          // chunks of a warp on their way
 constexpr int kMostPairs = 512;   // (token, choice) pairs of a launch
 
 struct MoeKernelArgs {
@@ -203,7 +215,7 @@ struct MoeKernelArgs {
 // Which experts a launch reads, and for which pairs: entries of up to MP pairs of one
 // expert, in the order of their first pairs.  All CTAs make the same.
 struct Plan {
-  int16_t id[kMostPairs];      // of a pair: its expert, or -1
+  alignas(16) int16_t id[kMostPairs];  // of a pair: its expert, or -1
   uint16_t next[kMostPairs];   // the expert's next pair
   uint16_t first[kMostPairs];  // of an entry: its first pair
   uint8_t count[kMostPairs];   // and how many it has
@@ -214,8 +226,8 @@ struct Plan {
 template <int MP>
 __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
   const int pairs = g.m * g.top, tid = threadIdx.x;
-  for (int i = tid; i < pairs; i += kThreads) {
-    const int64_t e = g.ids[i];
+  for (int i = tid; i < ((pairs + 31) & ~31); i += kThreads) {
+    const int64_t e = i < pairs ? g.ids[i] : -1;
     p.id[i] = (uint64_t)e < (uint64_t)g.experts ? (int16_t)e : -1;
   }
   __syncthreads();
@@ -229,11 +241,25 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
     const int16_t e = i < pairs ? p.id[i] : -1;
     if (e >= 0) {
       int next = 0;
-      for (int j = pairs - 1; j >= 0; --j) {
-        const bool same = p.id[j] == e;
-        total[k] += same;
-        before[k] += same && j < i;
-        if (same && j > i) next = j;
+      const uint32_t both = (uint32_t)e * 0x00010001u;
+      for (int w = (pairs - 1) >> 5; w >= 0; --w) {  // 32 pairs: which of them have the expert
+        const uint4* ids = reinterpret_cast<const uint4*>(p.id) + w * 4;
+        uint32_t same = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 v = ids[q];
+          const uint32_t u[4] = {v.x ^ both, v.y ^ both, v.z ^ both, v.w ^ both};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            if (!(u[h] & 0xFFFFu)) same |= 1u << (8 * q + 2 * h);
+            if (!(u[h] >> 16)) same |= 2u << (8 * q + 2 * h);
+          }
+        }
+        total[k] += __popc(same);
+        const int at = i - 32 * w;  // below 0: the pair comes before these; above 31: after them
+        before[k] += at > 31 ? __popc(same) : at > 0 ? __popc(same & ((1u << at) - 1)) : 0;
+        const uint32_t later = at < 0 ? same : at < 31 ? same & (0xFFFFFFFEu << at) : 0u;
+        if (later) next = 32 * w + __ffs(later) - 1;
       }
       p.next[i] = (uint16_t)next;
     }
@@ -255,11 +281,14 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
   __syncthreads();
 }
 
-template <bool MX, int MP, bool UP, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(const MoeKernelArgs g) {
+constexpr int ring_of(int ctas) { return ctas > 2 ? 3 : 4; }  // chunks of a warp on their way
+
+template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs g) {
+  constexpr int kRing = ring_of(CTAS);
   extern __shared__ uint4 sx[];
   __shared__ Plan plan;
-  __shared__ uint32_t red[2][kTokens][kWarps];
+  __shared__ uint32_t red[2][kWarps];
   __shared__ float back_sh[kTokens];
   constexpr int kSums = MX ? kTokens * 16 : 0;
   float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
@@ -354,27 +383,31 @@ __global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(cons
   float* mine = sums + warp * kSums;
   uint32_t place_at = 0;
   bool f16 = true;
+  float up_by = 1.f;
   int item = begin + slot;  // this warp's tile
   for (int entry = begin / g.tiles; begin < end && entry * (int64_t)g.tiles < end; ++entry) {
     const int n = plan.count[entry];
-    uint16_t pair[MP];
-    pair[0] = plan.first[entry];
-#pragma unroll
-    for (int c = 1; c < MP; ++c) pair[c] = c < n ? plan.next[pair[c - 1]] : pair[c - 1];
-    // ---- the entry's vectors as operand entries: their range, then their values
-    const uint4* xs[MP];
-#pragma unroll
-    for (int c = 0; c < MP; ++c)
-      if (c < n)
-        xs[c] = UP ? reinterpret_cast<const uint4*>(g.x + (int64_t)(pair[c] / g.top) * g.ldx)
-                   : reinterpret_cast<const uint4*>(g.hidden + (int64_t)pair[c] * g.k);
-#pragma unroll
-    for (int c = 0; c < MP; ++c) {
-      if (c >= n) break;
-      uint32_t top = 0, least = 0xFFFFFFFFu;
-      for (int i = tid; i < words; i += kThreads) {
+    auto pair_of = [&](int c) {
+      int p = plan.first[entry];
+      for (int i = 0; i < c; ++i) p = plan.next[p];
+      return p;
+    };
+    // ---- the entry's vectors as operand entries: their range, then their values.  The
+    // warps share the vectors out, so that all loads are on their way together.
+    const int lg = MP <= 1 || n <= 1 ? 0 : MP <= 2 || n <= 2 ? 1 : MP <= 4 || n <= 4 ? 2 : 3;
+    const int vec = warp & ((1 << lg) - 1), first = (warp >> lg) * 32 + lane, step = kThreads >> lg;
+    const uint4* xs = nullptr;
+    if (vec < n) {
+      const int p = pair_of(vec);
+      xs = UP ? reinterpret_cast<const uint4*>(g.x + (int64_t)(p / g.top) * g.ldx)
+              : reinterpret_cast<const uint4*>(g.hidden + (int64_t)p * g.k);
+    }
+    uint32_t top = 0, least = 0xFFFFFFFFu;
+    if (vec < n) {
+#pragma unroll 4
+      for (int i = first; i < words; i += step) {
         if constexpr (UP) {
-          const uint4 v = __ldg(xs[c] + i);
+          const uint4 v = __ldg(xs + i);
           const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -385,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(cons
         } else {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint4 v = xs[c][2 * i + h];
+            const uint4 v = xs[2 * i + h];
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -395,53 +428,50 @@ __global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(cons
           }
         }
       }
-      if constexpr (UP) {
-        top = max(top >> 16, top & 0xFFFFu);
-        least = min(least >> 16, least & 0xFFFFu);
-      }
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-      least = __reduce_min_sync(0xFFFFFFFFu, least);
-      if (lane == 0) {
-        red[0][c][warp] = top;
-        red[1][c][warp] = least;
-      }
+    }
+    if constexpr (UP) {
+      top = max(top >> 16, top & 0xFFFFu);
+      least = min(least >> 16, least & 0xFFFFu);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    least = __reduce_min_sync(0xFFFFFFFFu, least);
+    if (lane == 0) {
+      red[0][warp] = top;
+      red[1][warp] = least;
     }
     __syncthreads();  // (the products with the vectors that were there are done, too)
-    f16 = true;
-    float up_by[MP];
-#pragma unroll
-    for (int c = 0; c < MP; ++c) {
-      if (c >= n) break;
-      uint32_t top = 0, least = 0xFFFFFFFFu;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        top = max(top, red[0][c][w]);
-        least = min(least, red[1][c][w]);
+    {                 // lane c: vector c
+      const int c = lane & ((1 << lg) - 1);
+      top = 0, least = 0xFFFFFFFFu;
+      for (int w = c; w < kWarps; w += 1 << lg) {
+        top = max(top, red[0][w]);
+        least = min(least, red[1][w]);
       }
       int shift;
+      bool holds = true;
       if constexpr (UP) {  // (bf16 bits; as in the plain products: exact or not in f16)
         least = (least & 0xFFFFu) + 1u;
         shift = top ? min(141 - (int)max(top >> 7, 1u), 126) : 0;
-        f16 = f16 && top < 0x7F80u && (least > 0xFFFFu || (least >> 7 ? (int)(least >> 7) : -6) + shift >= 110);
+        holds = top < 0x7F80u && (least > 0xFFFFu || (least >> 7 ? (int)(least >> 7) : -6) + shift >= 110);
       } else {
         shift = top ? min(141 - (int)max(top >> 23, 1u), 126) : 0;
       }
-      up_by[c] = __uint_as_float((uint32_t)(127 + shift) << 23);
-      if (tid == 0) back_sh[c] = __uint_as_float((uint32_t)(127 - shift) << 23);
+      f16 = __all_sync(0xFFFFFFFFu, c >= n || holds);
+      up_by = __uint_as_float((uint32_t)(127 + __shfl_sync(0xFFFFFFFFu, shift, vec)) << 23);
+      if (tid < n) back_sh[tid] = __uint_as_float((uint32_t)(127 - shift) << 23);
     }
-#pragma unroll
-    for (int c = 0; c < MP; ++c) {
-      if (c >= n) break;
-      for (int i = tid; i < all_words; i += kThreads) {
+    if (vec < n) {
+#pragma unroll 2
+      for (int i = first; i < all_words; i += step) {
         uint32_t r[4] = {0, 0, 0, 0};
         if (i < words) {
           if constexpr (UP) {
-            const uint4 v = __ldg(xs[c] + i);
+            const uint4 v = __ldg(xs + i);
             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
             if (f16) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * up_by[c], bf16_hi(u[j]) * up_by[c]);
+                const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * up_by, bf16_hi(u[j]) * up_by);
                 r[j] = *reinterpret_cast<const uint32_t*>(&h2);
               }
             } else {
@@ -453,25 +483,20 @@ __global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(cons
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint4 v = xs[c][2 * i + h];
-              const __half2 lo = __floats2half2_rn(__uint_as_float(v.x) * up_by[c], __uint_as_float(v.y) * up_by[c]);
-              const __half2 hi = __floats2half2_rn(__uint_as_float(v.z) * up_by[c], __uint_as_float(v.w) * up_by[c]);
+              const uint4 v = xs[2 * i + h];
+              const __half2 lo = __floats2half2_rn(__uint_as_float(v.x) * up_by, __uint_as_float(v.y) * up_by);
+              const __half2 hi = __floats2half2_rn(__uint_as_float(v.z) * up_by, __uint_as_float(v.w) * up_by);
               r[2 * h] = *reinterpret_cast<const uint32_t*>(&lo);
               r[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&hi);
             }
           }
         }
-        sx[place(c, i)] = make_uint4(r[0], r[1], r[2], r[3]);
+        sx[place(vec, i)] = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
     __syncthreads();
 
     // ---- the products
-    auto pair_of = [&](int c) {  // (c is not a constant)
-      int p = pair[0];
-      for (int i = 0; i < c; ++i) p = plan.next[p];
-      return p;
-    };
     if (item >= min(end, (entry + 1) * g.tiles)) continue;  // (the tile is of the next entry, or there is none)
     const int tile = item - entry * g.tiles;
     item = end;
@@ -562,20 +587,21 @@ __global__ void __launch_bounds__(kThreads, MX && SPLIT ? 2 : 3) moe_kernel(cons
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-int smem_bytes(int k, int mp, bool mx) {
-  const int chunks = (k + kChunk - 1) / kChunk;
-  return chunks * (kChunk / 8) * 16 * mp + (mx ? kWarps * kTokens * 16 * 4 : 0) + kWarps * kRing * kSlot;
-}
-
-template <bool MX, int MP, bool UP, bool SPLIT>
+template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
 lpq_status launch(const MoeKernelArgs& g, int64_t tiles, cudaStream_t s) {
-  const void* kernel = reinterpret_cast<const void*>(moe_kernel<MX, MP, UP, SPLIT>);
-  lpq_status st = set_smem_attr(kernel, 200 * 1024);
+  auto kernel = moe_kernel<MX, MP, UP, SPLIT, CTAS>;
+  const int smem = g.x_words * 16 * MP + (MX ? kWarps * kTokens * 16 * 4 : 0) + kWarps * ring_of(CTAS) * kSlot;
+  lpq_status st = set_smem_attr(reinterpret_cast<const void*>(kernel), 200 * 1024);
   if (st != LPQ_OK) return st;
   const int slots = kWarps / g.split;
-  return cuda_check(launch_dependent(moe_kernel<MX, MP, UP, SPLIT>, dim3((unsigned)((tiles + slots - 1) / slots)), dim3(kThreads),
-                                     smem_bytes(g.k, MP, MX), s, g),
+  return cuda_check(launch_dependent(kernel, dim3((unsigned)((tiles + slots - 1) / slots)), dim3(kThreads), smem, s, g),
                     UP ? "moe up launch" : "moe down launch");
+}
+
+// Experts that m tokens with `top` of them each choose, were all equally likely.
+double expected_experts(int64_t m, int64_t top, int64_t experts) {
+  const double others = 1.0 - std::min(1.0, (double)top / (double)experts);
+  return (double)experts * (1.0 - std::pow(others, (double)m));
 }
 
 template <bool MX, int MP, bool UP>
@@ -583,14 +609,19 @@ lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   const int chunks = (g.k + kChunk - 1) / kChunk;
   g.x_words = chunks * (kChunk / 8);
   const int64_t tiles = (int64_t)g.m * g.top * g.tiles;  // at most
+  const double likely = expected_experts(g.m, g.top, g.experts) * g.tiles;
   // Warps share a tile's columns while there are fewer tiles than places for warps (24
-  // an SM, and some pairs will have an expert in common) and each gets a few chunks:
-  // one token of 8 experts of 4096 x 1536 45.5 -> 37.0 us; with two warps a tile
-  // beyond that, 43.4.
+  // an SM) and each gets a few chunks: one token of 8 experts of 4096 x 1536 45.5 ->
+  // 36.0 us, with the second product split too, beyond that number, 38.4; 5 tokens, 3
+  // of 21 of 2080 x 992 37.0 -> 29.8 us.
   const int most = chunks >= 16 ? 4 : chunks >= 8 ? 2 : 1;
   g.split = 1;
-  while (g.split < most && tiles * g.split * 2 <= 26 * device_sms()) g.split *= 2;
-  return g.split > 1 ? launch<MX, MP, UP, true>(g, tiles, s) : launch<MX, MP, UP, false>(g, tiles, s);
+  while (g.split < most && likely * g.split * 2 <= 3 * kWarps * device_sms()) g.split *= 2;
+  if (g.split > 1) return launch<MX, MP, UP, true, 3>(g, tiles, s);
+  // Where two CTAs an SM hold all tiles, each has more registers and chunks on their way
+  // (24 tokens, 2 of 16 of 2048 x 1024 43.5 -> 38.8 us; with more tiles three are
+  // better: 8 tokens, 8 of 64 of 4096 x 1536 120 against 131).
+  return likely <= 2 * kWarps * device_sms() ? launch<MX, MP, UP, false, 2>(g, tiles, s) : launch<MX, MP, UP, false, 3>(g, tiles, s);
 }
 
 template <bool UP>
@@ -603,9 +634,9 @@ lpq_status run_tokens(MoeKernelArgs& g, bool mx, int mp, cudaStream_t s) {
   }
 }
 
-constexpr int kXBytes = 128 * 1024;  // most shared memory for an item's vectors
+constexpr int kXBytes = 128 * 1024;  // most shared memory for an entry's vectors
 
-// Columns of an item: enough for an expert's tokens as a rule, and what fits.
+// Columns of an entry: enough for an expert's tokens as a rule, and what fits.
 int columns(int64_t m, int64_t top, int64_t experts, int64_t k) {
   int mp = m <= 1 ? 1 : m <= 2 ? 2 : m <= 4 || m * top <= 2 * experts ? 4 : 8;
   while (mp > 1 && (k + kChunk - 1) / kChunk * kChunk * 2 * mp > kXBytes) mp /= 2;
