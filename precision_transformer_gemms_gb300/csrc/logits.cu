@@ -9,6 +9,14 @@
 // that lie in its run in shared memory (integers: the order of the atomics does
 // not matter), adds the biases there in the list's order, and then works on its
 // registers.  Every CTA of a row reads the row's whole context, from the L2.
+//
+// Measured, 64 rows of 131073 FP32 (floor 10.5 us at the copy bandwidth of 6677 GB/s):
+// contexts of up to 1000 words 18.5 us, 8192 24.6, 16384 28, 32768 35; bf16, 4000 words
+// 17.7; 8 rows 4.6; one row of 32000 words 2.1.  What bounds it is the chain of a CTA's
+// loads (lengths, context, counts, then words) and the scan of the context, whose 8192
+// words take a CTA's 512 threads 4 loads each for the 8192 words that it writes;
+// clusters that share the scan through distributed shared memory gained for one row
+// with a long context alone.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -133,7 +141,10 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
     }
   }
   __syncthreads();
-  const float inverse = __fdiv_rn(1.f, rep);
+  // rep scaled to where its reciprocal is a normal number (infinity: to 0, whose reciprocal is taken to be 0)
+  const float size = fabsf(rep), scale = size < 0x1p-100f ? 0x1p64f : size > 0x1p100f ? 0x1p-64f : 1.f;
+  const bool endless = size > 3.402823466e38f;
+  const float divisor = endless ? 0.f : rep * scale, inverse = endless ? 0.f : __fdiv_rn(1.f, divisor);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int p = (j * kThreads + tid) * VEC, w = first + p;
@@ -149,9 +160,10 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
     if (any) {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
-        // x / rep by its reciprocal and one correction with the exact remainder (where that is a number)
+        // x / rep by the reciprocal and one correction with the exact remainder (where that is a number)
         float q = x[k] * inverse;
-        if (fabsf(q) <= 3.402823466e38f) q = fmaf(fmaf(-q, rep, x[k]), inverse, q);
+        if (fabsf(q) <= 3.402823466e38f) q = fmaf(fmaf(-q, divisor, x[k]), inverse, q);
+        q *= scale;
         const float seen = x[k] > 0.f ? q : x[k] * rep;
         if (c[k]) x[k] = seen;
         const uint32_t times = c[k] & ~kSeen;

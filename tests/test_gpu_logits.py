@@ -151,6 +151,23 @@ def test_special_values_and_bad_entries():
     check(logits, c, lpq.adjust_logits(logits, **c))
 
 
+def test_repetition_of_any_size():
+    """Divisors without a reciprocal among the normal numbers, too: a correctly rounded
+    quotient or product is off by half a step, or half of 2^-149 below 2^-126."""
+    r = torch.tensor([1e-40, 2.0 ** -126, 2.0 ** -127, 3e38, 2.0 ** 126, math.inf, 0.0, -1.5], device="cuda")
+    v = 600
+    g = torch.Generator(device="cuda")
+    g.manual_seed(11)
+    logits = 1e-3 * torch.randn(len(r), v, generator=g, device="cuda")
+    words = torch.arange(v, device="cuda").repeat(len(r), 1)
+    got = lpq.adjust_logits(logits, words, torch.full((len(r),), v, device="cuda"), repetition=r).double()
+    x, d = logits.double(), r.double()[:, None]
+    want = torch.where(x > 0, x / d, x * d)
+    fine = want.isfinite()
+    assert torch.equal(got[~fine], want[~fine])
+    assert torch.all((got - want).abs()[fine] <= (2 * U * want.abs() + 2.0 ** -149)[fine])
+
+
 def test_biases_of_one_word_add_in_order():
     logits = torch.zeros(2, 700, device="cuda")
     values = torch.tensor([1e8, 1.0, -1e8, 5.0, 3.0] * 20, device="cuda")
