@@ -19,10 +19,10 @@
 // rounding.  Everything else is exact or FP32.
 //
 // Measured (router, up and down in one graph; in brackets the weights' bytes at the copy
-// bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 120 us (67),
-// MXFP4 124; one token of them 34 (13); 4 tokens, 4 of 32 of 2048 x 768 24 (5.3); 24
-// tokens, 2 of 16 of 2048 x 1024 39 (8.5); 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
-// (5.6); one token, 2 of 8 of 512 x 384 11.7 (0.1), the three launches whose parts wait
+// bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 115 us (67),
+// MXFP4 121; one token of them 33 (13); 4 tokens, 4 of 32 of 2048 x 768 23 (5.3); 24
+// tokens, 2 of 16 of 2048 x 1024 38 (8.5); 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
+// (5.6); one token, 2 of 8 of 512 x 384 11.5 (0.1), the three launches whose parts wait
 // for one another.  What bounds the large ones: of an earlier state's 126 us the stream
 // without a product took 102, the products without the stream 97 and what a CTA does
 // before and after its tiles 58 by itself (the plan 15, the vectors' conversion 11, the
@@ -281,11 +281,18 @@ __device__ __forceinline__ void make_plan(Plan& p, const MoeKernelArgs& g) {
   __syncthreads();
 }
 
-constexpr int ring_of(int ctas) { return ctas > 2 ? 3 : 4; }  // chunks of a warp on their way
+// A step is 256 codes of a tile's 16 rows: whole lines of memory, whose copies take half
+// the L1's time that two chunks' half lines take.  A row has 128 bytes of codes in a
+// ring's slot, their 16-byte units exchanged across the middle in odd rows (eight lanes
+// read two rows' units without a conflict), and behind them a word of scales for every
+// 4 blocks.
+constexpr int kStepCodes = 2 * kChunk;
+constexpr int kRing = 2;  // steps of a warp on their way
+constexpr int slot_bytes(bool mx) { return 16 * 128 + 16 * (mx ? 8 : 16); }
 
 template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs g) {
-  constexpr int kRing = ring_of(CTAS);
+  constexpr int kStepSlot = slot_bytes(MX), kRingBytes = kRing * kStepSlot;
   extern __shared__ uint4 sx[];
   __shared__ Plan plan;
   __shared__ uint32_t red[2][kWarps];
@@ -294,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
   float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int gid = lane >> 2, t = lane & 3;
-  const uint32_t ring = smem_u32(sums + kWarps * kSums) + warp * (kRing * kSlot);
+  const uint32_t ring = smem_u32(sums + kWarps * kSums) + warp * kRingBytes;
   if constexpr (UP) {
     wait_for_stream();
     let_dependents_start();  // not before: down reads the ids and the weights without a wait of its own
@@ -311,61 +318,57 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
   const int slots = kWarps / split, slot = warp / split, part = SPLIT ? warp % split : 0;  // tiles at once, this warp's, its part of it
   const int begin = (int)min(all_tiles, (int64_t)blockIdx.x * slots), end = (int)min(all_tiles, (int64_t)begin + slots);
   const int chunks = (g.k + kChunk - 1) / kChunk;
-  const int chunk0 = part * chunks / split, chunk1 = (part + 1) * chunks / split;
+  const int steps = (chunks + 1) / 2, step0 = part * steps / split, step1 = (part + 1) * steps / split;
 
   // ---- the weight stream
-  const uint32_t codes_sh = ring + lane * 16, scales_sh = ring + 1024 + lane * 4;
-  constexpr int kChunkS = MX ? 512 : 1024;
-  // The tile's rows for this lane: up, a gate and an up row of one hidden value; down,
-  // two rows.  A tile's rows are runs of 2 or 4 neighbours 32 apart, whose scales of 4
-  // blocks lie side by side where the expert begins with a 128-row group.
+  constexpr int kScaleStep = MX ? 1024 : 2048;  // bytes of scales per step: 2 or 4 atoms
+  // The tile's 16 rows: up, 8 gate rows and their up rows; down, 16 rows.  They are
+  // runs of 2 or 4 neighbours 32 apart, whose scales of 4 blocks lie side by side where
+  // the expert begins with a 128-row group.
   auto value_of = [&](int tile, int r) {  // place in the expert's results of row r of 16 (up: of 8)
     return UP ? (tile >> 4) * 128 + 32 * (r & 3) + 2 * (tile & 15) + (r >> 2) : (tile >> 3) * 128 + 32 * (r & 3) + 4 * (tile & 7) + (r >> 2);
   };
-  const uint8_t *pc = nullptr, *pc2 = nullptr, *ps = nullptr, *ps2 = nullptr;
-  int a_item = begin + slot, a_chunk = chunk0;
+  const uint8_t *pc = nullptr, *ps = nullptr, *ps2 = nullptr;
+  uint32_t next_row[3] = {};  // from the lane's first row of codes to its others
+  int a_item = begin + slot, a_step = step0;
   uint32_t a_slot = 0;
   auto set_item = [&]() {
     const int entry = a_item / g.tiles, tile = a_item - entry * g.tiles;
     const int64_t e = plan.id[plan.first[entry]];
-    const int last = g.rows - 1;  // rows beyond the expert read its last one; their results are not stored
-    int64_t r1, r2;
-    if constexpr (UP) {
-      r1 = e * 2 * g.rows + min(value_of(tile, gid), last);
-      r2 = r1 + g.rows;
-    } else {
-      r1 = e * g.rows + min(value_of(tile, gid), last);
-      r2 = e * g.rows + min(value_of(tile, gid + 8), last);
-    }
-    const int at = chunk0 * (kChunk / 2) + t * 16, scale_at = chunk0 * kChunkS + (MX ? 0 : (t >> 1) * 512);
-    pc = g.codes + r1 * (g.k >> 1) + at;
-    pc2 = g.codes + r2 * (g.k >> 1) + at;
-    ps = g.scales + sf_gemm_offset(r1, 0, g.kt) + scale_at;
-    ps2 = g.scales + sf_gemm_offset(r2, 0, g.kt) + scale_at;
+    auto row_of = [&](int r) {  // rows beyond the expert read its last one; their results are not stored
+      if constexpr (UP) return e * 2 * g.rows + min(value_of(tile, r & 7), g.rows - 1) + (r >> 3) * g.rows;
+      else return e * g.rows + min(value_of(tile, r), g.rows - 1);
+    };
+    const int64_t first = row_of(lane >> 3);
+    pc = g.codes + first * (g.k >> 1) + step0 * (kStepCodes / 2) + (lane & 7) * 16;
+#pragma unroll
+    for (int q = 1; q < 4; ++q) next_row[q - 1] = (uint32_t)(row_of((lane >> 3) + 4 * q) - first) * (uint32_t)(g.k >> 1);
+    ps = g.scales + sf_gemm_offset(row_of(MX ? lane >> 1 : gid), 0, g.kt) + step0 * kScaleStep + (MX ? lane & 1 : t) * 512;
+    if constexpr (!MX) ps2 = g.scales + sf_gemm_offset(row_of(gid + 8), 0, g.kt) + step0 * kScaleStep + t * 512;
   };
-  auto copy = [&]() {  // the next chunk of the stream
+  const uint32_t codes_to = ring + (lane >> 3) * 128 + ((lane & 7) ^ ((lane >> 3 & 1) << 2)) * 16, scales_to = ring + 2048 + lane * 4;
+  auto copy = [&]() {  // the next step of the stream
     if (a_item < end) {
-      const uint32_t c = codes_sh + a_slot, sc = scales_sh + a_slot;
-      if ((a_chunk + 1) * kChunk <= g.k) {
+      const uint32_t c = codes_to + a_slot;
+      if ((a_step + 1) * kStepCodes <= g.k) {
         cp_async<16>(c, pc);
-        cp_async<16>(c + 512, pc2);
-        cp_async<4>(sc, ps);
-        cp_async<4>(sc + 128, ps2);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) cp_async<16>(c + q * 512, pc + next_row[q - 1]);
       } else {
-        const bool in = a_chunk * kChunk + t * 32 < g.k;
+        const bool in = a_step * kStepCodes + (lane & 7) * 32 < g.k;
         cp_async_or_zero<16>(c, in ? pc : g.codes, in);
-        cp_async_or_zero<16>(c + 512, in ? pc2 : g.codes, in);
-        cp_async_or_zero<4>(sc, in ? ps : g.scales, in);
-        cp_async_or_zero<4>(sc + 128, in ? ps2 : g.scales, in);
+#pragma unroll
+        for (int q = 1; q < 4; ++q) cp_async_or_zero<16>(c + q * 512, in ? pc + next_row[q - 1] : g.codes, in);
       }
-      pc += kChunk / 2;
-      pc2 += kChunk / 2;
-      ps += kChunkS;
-      ps2 += kChunkS;
-      if (++a_chunk == chunk1) a_item = end;  // (a tile a warp)
+      cp_async<4>(scales_to + a_slot, ps);
+      if constexpr (!MX) cp_async<4>(scales_to + a_slot + 128, ps2);
+      pc += kStepCodes / 2;
+      ps += kScaleStep;
+      ps2 += kScaleStep;
+      if (++a_step == step1) a_item = end;  // (a tile a warp)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-    a_slot = a_slot == (kRing - 1) * kSlot ? 0 : a_slot + kSlot;
+    a_slot = a_slot == (kRing - 1) * kStepSlot ? 0 : a_slot + kStepSlot;
   };
   if (a_item < end) set_item();
 #pragma unroll
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
     const int tile = item - entry * g.tiles;
     item = end;
     const int col = min(gid, MP - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
-    const uint4* e = sx + (size_t)chunk0 * (kChunk / 8) * MP;
+    const uint4* e = sx + (size_t)step0 * (kStepCodes / 8) * MP;
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (MX) {
 #pragma unroll
@@ -509,21 +512,35 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
     }
     auto stream = [&](auto f16_path) {
       constexpr bool F16 = decltype(f16_path)::value;
-#pragma unroll 1
-      for (int c = chunk0; c < chunk1; ++c, e += (kChunk / 8) * MP) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      auto read = [&](int h, bool tail, int s) {  // chunk h of the step
         Load l;
-        l.lo = ld_shared_16(codes_sh + place_at);
-        l.hi = ld_shared_16(codes_sh + place_at + 512);
-        const uint32_t at = scales_sh + place_at + (MX ? t : (t & 1) * 2);
+        const uint32_t c = ring + place_at + gid * 128 + ((h * 4 + t) ^ ((gid & 1) << 2)) * 16;
+        l.lo = ld_shared_16(c);
+        l.hi = ld_shared_16(c + 1024);
+        const uint32_t at = ring + place_at + 2048 + (MX ? gid * 8 + h * 4 + t : gid * 16 + h * 8 + t * 2);
         l.slo = ld_shared_scale<MX>(at);
-        l.shi = ld_shared_scale<MX>(at + 128);
+        l.shi = ld_shared_scale<MX>(at + (MX ? 64 : 128));
+        if (tail && s * kStepCodes + h * kChunk + t * 32 >= g.k) l.slo = l.shi = 0;  // (anything may stand there)
+        return l;
+      };
+      auto products = [&](const Load& l) {
         if (MX && F16 && mx_far(l))
           far_chunk(l.lo, l.hi, l.slo, l.shi, e + t, MP, n, back_sh, mine);
         else
           chunk_products<MX, F16, MP>(l, e + col, acc);
-        copy();  // into the slot whose values have just been used
-        place_at = place_at == (kRing - 1) * kSlot ? 0 : place_at + kSlot;
+        e += (kChunk / 8) * MP;
+      };
+#pragma unroll 1
+      for (int s = step0; s < step1; ++s) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        __syncwarp();
+        const bool tail = (s + 1) * kStepCodes > g.k;
+        products(read(0, tail, s));
+        const Load l = read(1, tail, s);
+        __syncwarp();
+        copy();  // into the slot whose values have just been read
+        place_at = place_at == (kRing - 1) * kStepSlot ? 0 : place_at + kStepSlot;
+        if (2 * s + 1 < chunks) products(l);
       }
     };
     if (!UP || f16) stream(std::true_type{}); else stream(std::false_type{});
@@ -535,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
     }
     if constexpr (SPLIT) {  // the parts' sums in order, through their rings, which are done with
       asm volatile("cp.async.wait_all;" ::: "memory");
-      float* left = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sums + kWarps * kSums) + warp * (kRing * kSlot)) + lane;
+      float* left = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sums + kWarps * kSums) + warp * kRingBytes) + lane;
       if (part > 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) left[i * 32] = acc[i];
@@ -544,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
       if (part > 0) continue;
       for (int p = 1; p < split; ++p)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += left[p * (kRing * kSlot / 4) + i * 32];
+        for (int i = 0; i < 4; ++i) acc[i] += left[p * (kRingBytes / 4) + i * 32];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] *= tensor;
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
 template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
 lpq_status launch(const MoeKernelArgs& g, int64_t tiles, cudaStream_t s) {
   auto kernel = moe_kernel<MX, MP, UP, SPLIT, CTAS>;
-  const int smem = g.x_words * 16 * MP + (MX ? kWarps * kTokens * 16 * 4 : 0) + kWarps * ring_of(CTAS) * kSlot;
+  const int smem = g.x_words * 16 * MP + (MX ? kWarps * kTokens * 16 * 4 : 0) + kWarps * kRing * slot_bytes(MX);
   lpq_status st = set_smem_attr(reinterpret_cast<const void*>(kernel), 200 * 1024);
   if (st != LPQ_OK) return st;
   const int slots = kWarps / g.split;
@@ -612,15 +629,15 @@ lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   const double likely = expected_experts(g.m, g.top, g.experts) * g.tiles;
   // Warps share a tile's columns while there are fewer tiles than places for warps (24
   // an SM) and each gets a few chunks: one token of 8 experts of 4096 x 1536 45.5 ->
-  // 36.0 us, with the second product split too, beyond that number, 38.4; 5 tokens, 3
-  // of 21 of 2080 x 992 37.0 -> 29.8 us.
+  // 36.0 us (32.7 now; with the second product split too, beyond that number, 36.3); 5
+  // tokens, 3 of 21 of 2080 x 992 37.0 -> 29.8 us.
   const int most = chunks >= 16 ? 4 : chunks >= 8 ? 2 : 1;
   g.split = 1;
   while (g.split < most && likely * g.split * 2 <= 3 * kWarps * device_sms()) g.split *= 2;
   if (g.split > 1) return launch<MX, MP, UP, true, 3>(g, tiles, s);
-  // Where two CTAs an SM hold all tiles, each has more registers and chunks on their way
-  // (24 tokens, 2 of 16 of 2048 x 1024 43.5 -> 38.8 us; with more tiles three are
-  // better: 8 tokens, 8 of 64 of 4096 x 1536 120 against 131).
+  // Where two CTAs an SM hold all tiles, each has more registers, which hide more of the
+  // loads' time (24 tokens, 2 of 16 of 2048 x 1024 42.0 -> 37.7 us; with more tiles three
+  // are better: 8 tokens, 8 of 64 of 4096 x 1536 120 against 131).
   return likely <= 2 * kWarps * device_sms() ? launch<MX, MP, UP, false, 2>(g, tiles, s) : launch<MX, MP, UP, false, 3>(g, tiles, s);
 }
 
