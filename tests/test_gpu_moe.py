@@ -8,6 +8,8 @@ each (the tensor core adds 16 at once).  h = silu(g) l moves by 1.1 |l| of g's e
 and |silu(g)| of l's and its own 8 u, and is rounded to 11 bits (2^-11 of itself, 2^-38
 of its vector's largest).  y is the products of that with the down weights, weighted
 and added in FP32 ((k + 2) u), and rounded to bf16 (2^-8)."""
+import functools
+
 import pytest
 import torch
 
@@ -74,6 +76,38 @@ def test_sizes(shape, fmt):
     y = lpq.moe(x, up, down, e, ids, probs)
     assert y.dtype == torch.bfloat16 and y.shape == (m, d)
     check(x, up, down, e, ids, probs, y)
+
+
+@functools.lru_cache(maxsize=1)
+def many_rows(d, f, fmt):
+    return weights(16, f, d, fmt, seed=d)
+
+
+@pytest.mark.parametrize("d,f,fmt", [(d, f, fmt) for d, f in ((320, 2048), (4000, 96)) for fmt in (lpq.NVFP4, lpq.MXFP4)])
+@pytest.mark.parametrize("m,k", [(1, 12), (2, 10), (3, 6), (9, 6)])
+def test_more_rows_than_warps(d, f, fmt, m, k):
+    """Experts whose rows fill every SM more than once, for all counts of tokens a tile."""
+    up, down = many_rows(d, f, fmt)
+    ids, probs = choices(m, k, 16, seed=m)
+    x = synth.bf16_normal((m, d), 1.0, m, "cuda", 0.01, 30.0)
+    check(x, up, down, 16, ids, probs, lpq.moe(x, up, down, 16, ids, probs))
+
+
+@pytest.mark.parametrize("fmt", [lpq.NVFP4, lpq.MXFP4])
+def test_what_lies_behind_the_last_block_does_not_count(fmt):
+    m, d, f, e, k = 4, 288, 96, 3, 2
+    up, down = weights(e, f, d, fmt)
+    ids, probs = choices(m, k, e)
+    x = synth.bf16_normal((m, d), 1.0, 1, "cuda")
+    y = lpq.moe(x, up, down, e, ids, probs)
+    for w in (up, down):
+        blocks, atoms = w.cols // (32 if fmt == lpq.MXFP4 else 16), (w.cols + 255) // 256 * (2 if fmt == lpq.MXFP4 else 4)
+        r, b = torch.arange(w.rows, device="cuda")[:, None], torch.arange(blocks, device="cuda")
+        held = torch.zeros(w.scales.numel(), device="cuda", dtype=torch.bool)
+        held[((r >> 7) * atoms + (b >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (b & 3)] = True
+        flat = w.scales.view(torch.uint8).view(-1)
+        flat[~held] = 255 if fmt == lpq.MXFP4 else 127  # no number
+    assert torch.equal(lpq.moe(x, up, down, e, ids, probs), y)
 
 
 @pytest.mark.parametrize("fmts", [(lpq.NVFP4, lpq.MXFP4), (lpq.MXFP4, lpq.NVFP4_2D)])
