@@ -21,7 +21,7 @@
 // Measured (router, up and down in one graph; in brackets the weights' bytes at the copy
 // bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 115 us (67),
 // MXFP4 121; one token of them 33 (13); 4 tokens, 4 of 32 of 2048 x 768 23 (5.3); 24
-// tokens, 2 of 16 of 2048 x 1024 38 (8.5); 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
+// tokens, 2 of 16 of 2048 x 1024 36 (8.5), 200 tokens 207; 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
 // (5.6); one token, 2 of 8 of 512 x 384 11.5 (0.1), the three launches whose parts wait
 // for one another.  What bounds the large ones: of an earlier state's 126 us the stream
 // without a product took 102, the products without the stream 97 and what a CTA does
@@ -615,7 +615,7 @@ lpq_status launch(const MoeKernelArgs& g, int64_t tiles, cudaStream_t s) {
                     UP ? "moe up launch" : "moe down launch");
 }
 
-// Experts that m tokens with `top` of them each choose, were all equally likely.
+// Experts that m tokens with `top` of them each choose, if all are equally likely.
 double expected_experts(int64_t m, int64_t top, int64_t experts) {
   const double others = 1.0 - std::min(1.0, (double)top / (double)experts);
   return (double)experts * (1.0 - std::pow(others, (double)m));
@@ -625,8 +625,12 @@ template <bool MX, int MP, bool UP>
 lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   const int chunks = (g.k + kChunk - 1) / kChunk;
   g.x_words = chunks * (kChunk / 8);
-  const int64_t tiles = (int64_t)g.m * g.top * g.tiles;  // at most
-  const double likely = expected_experts(g.m, g.top, g.experts) * g.tiles;
+  // Entries, at most: one for every expert, and for every MP pairs beyond the experts'
+  // first ones.  (CTAs without an entry cost a plan each: with one for every pair, 200
+  // tokens, 2 of 16 of 2048 x 1024, took 427 us, 223 so.)
+  const int64_t pairs = (int64_t)g.m * g.top, firsts = std::min<int64_t>(pairs, g.experts);
+  const int64_t tiles = (firsts + (pairs - firsts) / MP) * g.tiles;
+  const double likely = std::max(expected_experts(g.m, g.top, g.experts), (double)pairs / MP) * g.tiles;
   // Warps share a tile's columns while there are fewer tiles than places for warps (24
   // an SM) and each gets a few chunks: one token of 8 experts of 4096 x 1536 45.5 ->
   // 36.0 us (32.7 now; with the second product split too, beyond that number, 36.3); 5
