@@ -466,9 +466,10 @@ lpq_status lpq_moe_workspace(int64_t m, int64_t k, int64_t d, int64_t f, size_t 
  * Angles are reduced modulo a turn in 64 bits: off by at most 2^-26 turns (1e-7
  * radians) and 2^-52 |position freqs[i]|; any int64 position is valid.
  * Statistics are FP32 and y is rounded once.  head_dim is even, 2 ..
- * 512; rotary_dim even, 0 .. head_dim; any rows, heads >= 0; eps >= 0.  Heads
- * and a rotary_dim of a multiple of 16 values, with 16-byte aligned rows, take
- * 16-byte accesses; others go value by value. */
+ * 512; rotary_dim even, 0 .. head_dim; any rows, heads >= 0; eps >= 0.  Rows
+ * that begin at 16 bytes, with head_dim and rotary_dim multiples of 16 values (FP32:
+ * 8; interleaved: rotary_dim of 4), take 16-byte accesses; bf16 with 8 in place of 16
+ * takes 8-byte ones; others go value by value. */
 lpq_status lpq_qk_norm_rope(const void *x, int64_t ldx, int32_t type, int64_t rows, int64_t q_heads, int64_t k_heads,
                             int64_t head_dim, const void *q_weight, const void *k_weight, int32_t w_type,
                             const int64_t *positions, const double *freqs, int64_t rotary_dim, int32_t interleaved,

@@ -26,13 +26,15 @@
 //             54.6 (89%), 16 of 512 110 (71%)
 //   backward  64 heads of 128 129 us (90%; 4 of it the join of the parts), of 64 132,
 //             32 of 256 135, 8192 tokens FP32 154 (78%: a ring of two), 32 + 8 106 (69%)
-// Heads that are no power of two times 16 leave lanes idle (96 of 80: 118 us, 62%);
-// those that 16 values or 16 bytes do not divide go value by value (64 of 130: 260 us,
-// 30%; backward 370, 32%), bound by the count of accesses.
+// Heads that are no power of two times 16 leave lanes idle (96 of 80: 118 us, 62%).
+// bf16 that goes in 8-byte vectors: 112 heads of 72 142 us (54%, backward 268), 96 of 80
+// with halves of 20 turned 126 (value by value 348, 499 and 302).  What goes value by
+// value (64 of 130: 260 us, 30%; backward 370, 32%) is bound by the count of accesses.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "lpq_device.cuh"
 
@@ -47,8 +49,7 @@ constexpr int kMaxPairs = kQkMaxDim / 2;
 template <typename T, bool BACKWARD>
 struct Ring {
   static constexpr int kDepth = sizeof(T) == 4 ? (BACKWARD ? 2 : 3) : 4;
-  static constexpr int kPieces = 2 * 8 * sizeof(T) / 16 * (BACKWARD ? 2 : 1);  // 16-byte pieces of a lane
-  static constexpr int kStage = kPieces * 512;
+  static constexpr int kStage = 32 * 2 * 8 * sizeof(T) * (BACKWARD ? 2 : 1);  // 8 pairs a lane
   static constexpr int kBytes = kWarps * kDepth * kStage;
   static constexpr int kCtas = BACKWARD ? 2 : 3;
 };
@@ -82,36 +83,43 @@ __device__ __forceinline__ T from_f32(float v) {
   if constexpr (sizeof(T) == 4) return v; else return __float2bfloat16_rn(v);
 }
 
-// V values as they lie in memory: 16 bytes, or one value.
+// V values as they lie in memory: 16 bytes (8 of 4 bf16 values), or one value.
 template <typename T, int V>
 struct Raw {
-  static_assert(V * sizeof(T) == 16, "a vector is 16 bytes");
-  uint4 v;
-  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
+  static constexpr int kBytes = V * sizeof(T);
+  static_assert(kBytes == 16 || kBytes == 8, "a vector is 8 or 16 bytes");
+  using Word = std::conditional_t<kBytes == 16, uint4, uint2>;
+  Word v;
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<Word*>(p) = v; }
   // Through a lane's place in shared memory.
   static __device__ __forceinline__ void copy(uint32_t to, const T* p, bool there) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(there ? 16 : 0) : "memory");
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(there ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(there ? 8 : 0) : "memory");
   }
   __device__ __forceinline__ void take(uint32_t from) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    if constexpr (kBytes == 16)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    else
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(from) : "memory");
   }
-  // Values 2 i and 2 i + 1 (i is a constant after unrolling).
+  // 32-bit word i (a constant after unrolling).
+  __device__ __forceinline__ uint32_t& word(int i) {
+    if constexpr (kBytes == 16) return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    else return i == 0 ? v.x : v.y;
+  }
+  __device__ __forceinline__ uint32_t word(int i) const { return const_cast<Raw*>(this)->word(i); }
+  // Values 2 i and 2 i + 1.
   __device__ __forceinline__ float2 get2(int i) const {
-    if constexpr (sizeof(T) == 4) {
-      return i & 1 ? make_float2(__uint_as_float(v.z), __uint_as_float(v.w)) : make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
-    } else {
-      const uint32_t p = (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
-      return make_float2(bf16_lo(p), bf16_hi(p));
-    }
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(word(2 * i)), __uint_as_float(word(2 * i + 1)));
+    else return make_float2(bf16_lo(word(i)), bf16_hi(word(i)));
   }
   __device__ __forceinline__ void set2(int i, float a, float b) {
     if constexpr (sizeof(T) == 4) {
-      if (i & 1) { v.z = __float_as_uint(a); v.w = __float_as_uint(b); }
-      else { v.x = __float_as_uint(a); v.y = __float_as_uint(b); }
+      word(2 * i) = __float_as_uint(a);
+      word(2 * i + 1) = __float_as_uint(b);
     } else {
       const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      const uint32_t p = *reinterpret_cast<const uint32_t*>(&h);
-      if ((i & 3) == 0) v.x = p; else if ((i & 3) == 1) v.y = p; else if ((i & 3) == 2) v.z = p; else v.w = p;
+      word(i) = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
 };
@@ -125,8 +133,8 @@ struct Raw<T, 1> {
 // A thread's part of a head: P pairs (even), as NU units of two vectors of V values.
 // Neighbouring lanes' vectors are neighbours, so that a warp's accesses take whole
 // sectors: the two vectors lie half a head apart, or half of the turned values, where
-// the pairs are made of their halves.  Vectors of 16 bytes hold 8 pairs a thread; any
-// alignment and sizes: V = 1, units 32 apart.  Pairs 2 j and 2 j + 1 lie in one float2
+// the pairs are made of their halves.  Vectors hold 8 pairs a thread; any alignment and
+// sizes: V = 1, units 32 apart.  Pairs 2 j and 2 j + 1 lie in one float2
 // of firsts and one of seconds, for the two-wide operations.
 template <typename T, int V, int NU, bool NEIGHBOURS>
 struct Slice {
@@ -310,7 +318,8 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
   const T* fx = x + start(f, g.ldx);
   const T* fy = BACKWARD ? dy + start(f, g.lddy) : nullptr;
   uint32_t f_at = 0, at = 0;
-  const uint32_t ring = smem_u32(smem) + warp * (R::kDepth * R::kStage) + (threadIdx.x & 31) * 16;
+  constexpr int kVector = V * sizeof(T);
+  const uint32_t ring = smem_u32(smem) + warp * (R::kDepth * R::kStage) + (threadIdx.x & 31) * kVector;
   auto fetch = [&]() {
     if (f_left > 0) {
       --f_left;
@@ -319,12 +328,12 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
       for (int j = 0; j < NU; ++j) {
         const bool in = LANES > 0 || (there && unit[j]);
         if constexpr (kRing) {
-          const uint32_t to = ring + f_at + j * 1024;
+          const uint32_t to = ring + f_at + j * 64 * kVector;
           Raw<T, V>::copy(to, in ? fx + unit_a[j] : x, in);
-          Raw<T, V>::copy(to + 512, in ? fx + unit_b[j] : x, in);
+          Raw<T, V>::copy(to + 32 * kVector, in ? fx + unit_b[j] : x, in);
           if constexpr (BACKWARD) {
             Raw<T, V>::copy(to + R::kStage / 2, in ? fy + unit_a[j] : dy, in);
-            Raw<T, V>::copy(to + R::kStage / 2 + 512, in ? fy + unit_b[j] : dy, in);
+            Raw<T, V>::copy(to + R::kStage / 2 + 32 * kVector, in ? fy + unit_b[j] : dy, in);
           }
         } else {
           nx.a[j] = nx.b[j] = ny.a[j] = ny.b[j] = Raw<T, V>{};
@@ -450,12 +459,12 @@ __global__ void __launch_bounds__(32 * kWarps, Ring<T, BACKWARD>::kCtas) qk_norm
       asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
 #pragma unroll
       for (int j = 0; j < NU; ++j) {
-        const uint32_t from = ring + at + j * 1024;
+        const uint32_t from = ring + at + j * 64 * kVector;
         cx.a[j].take(from);
-        cx.b[j].take(from + 512);
+        cx.b[j].take(from + 32 * kVector);
         if constexpr (BACKWARD) {
           cy.a[j].take(from + R::kStage / 2);
-          cy.b[j].take(from + R::kStage / 2 + 512);
+          cy.b[j].take(from + R::kStage / 2 + 32 * kVector);
         }
       }
       at = at == (R::kDepth - 1) * R::kStage ? 0 : at + R::kStage;
@@ -622,13 +631,21 @@ lpq_status vectors(QkKernelArgs& g, int64_t rows, bool usual, float* dq, float* 
 
 template <typename T, bool BACKWARD>
 lpq_status dispatch(QkKernelArgs& g, int64_t rows, bool neighbours, float* dq, float* dk, cudaStream_t s) {
-  auto whole = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * sizeof(T) % 16 == 0; };
   g.neighbours = neighbours;
-  if (g.dim % 16 == 0 && g.rotary % 16 == 0 && whole(g.x, g.ldx) && whole(g.out, g.ldo) && (!BACKWARD || whole(g.dy, g.lddy))) {
+  // Vectors of v values: both halves of what is turned begin with one, or every vector
+  // holds whole pairs, and two lie in a float4 of angles.
+  auto fits = [&](int v) {
+    auto whole = [&](const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (v * sizeof(T)) == 0 && ld % v == 0; };
+    return g.dim % (2 * v) == 0 && g.rotary % (neighbours ? 4 : 2 * v) == 0 && whole(g.x, g.ldx) && whole(g.out, g.ldo) &&
+           (!BACKWARD || whole(g.dy, g.lddy));
+  };
+  if (fits(16 / sizeof(T))) {
     const int per_group = 512 / g.dim;  // whole groups of the usual head sizes
     const bool usual = per_group > 0 && g.heads[0] % per_group == 0 && g.heads[1] % per_group == 0;
     return neighbours ? vectors<T, true, BACKWARD>(g, rows, usual, dq, dk, s) : vectors<T, false, BACKWARD>(g, rows, usual, dq, dk, s);
   }
+  if constexpr (sizeof(T) == 2)
+    if (fits(4)) return neighbours ? run<T, 4, 2, true, BACKWARD, 0>(g, rows, dq, dk, s) : run<T, 4, 2, false, BACKWARD, 0>(g, rows, dq, dk, s);
   // value by value
   if (g.dim <= 128) return run<T, 1, 2, false, BACKWARD, 0>(g, rows, dq, dk, s);
   if (g.dim <= 256) return run<T, 1, 4, false, BACKWARD, 0>(g, rows, dq, dk, s);

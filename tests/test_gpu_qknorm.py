@@ -115,6 +115,25 @@ def test_forward_and_backward(case, dt):
     check_backward(dy, x, w, hq, hk, d, pos, dx, dq, dk, rot, inter)
 
 
+@pytest.mark.parametrize("case", [  # vectors of 8 bytes; neighbours whose turned part is no multiple of 16
+    (50, 5, 3, 80, 40, False), (21, 9, 2, 72, 24, False), (6, 3, 2, 8, 8, False), (5, 2, 1, 24, 8, False), (4, 1, 1, 8, 0, False),
+    (400, 7, 2, 104, 52, True), (3, 2, 1, 504, 248, False), (3, 1, 1, 512, 252, True), (9, 8, 4, 128, 52, True), (30, 16, 8, 64, 20, True),
+    (2, 3, 1, 488, 484, True), (1500, 4, 4, 40, 24, False)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_smaller_vectors(case, dt):
+    test_forward_and_backward(case, dt)
+
+
+@pytest.mark.parametrize("lead", [4, 12])
+def test_rows_that_begin_at_8_bytes(lead):
+    t, hq, hk, d = 19, 5, 2, 96
+    wide, w, pos, dy = make(t, hq, hk, d, BF, F32, extra=lead, pad=4, seed=8)
+    x = wide[:, lead:]
+    check(x, w, hq, hk, d, pos, lpq.qk_norm_rope(x, hq, hk, d, pos, *w), d)
+    dx, dq, dk = lpq.qk_norm_rope_backward(dy, x, hq, hk, d, pos, *w)
+    check_backward(dy, x, w, hq, hk, d, pos, dx, dq, dk, d)
+
+
 @pytest.mark.parametrize("pad,lead", [(0, 0), (8, 0), (3, 0), (16, 5), (1, 1)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_strides_and_alignment(dt, pad, lead):
