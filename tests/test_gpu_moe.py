@@ -93,6 +93,16 @@ def test_more_rows_than_warps(d, f, fmt, m, k):
     check(x, up, down, 16, ids, probs, lpq.moe(x, up, down, 16, ids, probs))
 
 
+@pytest.mark.parametrize("d,f", [(65536, 32), (32, 65536), (65504, 64), (64, 40928)])
+@pytest.mark.parametrize("fmt", [lpq.NVFP4, lpq.MXFP4])
+def test_the_longest_rows(d, f, fmt):
+    """Vectors of which shared memory holds one or two, for tokens that share an expert."""
+    up, down = weights(2, f, d, fmt)
+    ids, probs = torch.tensor([[0, 1], [1, 0], [1, -1]], device="cuda"), torch.rand(3, 2, device="cuda")
+    x = synth.bf16_normal((3, d), 1.0, 4, "cuda")
+    check(x, up, down, 2, ids, probs, lpq.moe(x, up, down, 2, ids, probs))
+
+
 @pytest.mark.parametrize("fmt", [lpq.NVFP4, lpq.MXFP4])
 def test_what_lies_behind_the_last_block_does_not_count(fmt):
     m, d, f, e, k = 4, 288, 96, 3, 2
