@@ -434,9 +434,9 @@ lpq_status lpq_moe_route(const void *x, int64_t ldx, const void *w, int64_t ldw,
  * x [m, d] bf16 (rows ldx elements apart, a multiple of 8; 16-byte aligned), not
  * quantized; ids [m, k] int64 (outside 0 .. experts - 1: the place counts for nothing;
  * one expert may stand twice), probs [m, k] FP32; y [m, d] bf16, contiguous.  Sums are
- * FP32; hidden values enter the second product with 11 significant bits of their
- * vector's range; y is rounded once, its sum taken in the order of j.  d and f are
- * multiples of 32 up to 65536; 0 <= k <= 32, experts <= 1024; any m >= 0, but m is meant
+ * FP32; hidden values enter the second product off by at most 2^-22 of themselves or
+ * 2^-39 of their vector's largest; y is rounded once, its sum taken in the order of j.
+ * d and f are multiples of 32 up to 65536; 0 <= k <= 32, experts <= 1024; any m >= 0, but m is meant
  * to be small: an expert's weights are read once for up to 8 of its tokens. */
 lpq_status lpq_moe(const lpq_qview *up, const lpq_qview *down, int64_t experts, const void *x, int64_t ldx, int64_t m,
                    const int64_t *ids, const float *probs, int64_t k, void *y, void *workspace, size_t workspace_bytes,

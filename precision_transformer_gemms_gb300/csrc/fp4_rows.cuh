@@ -111,7 +111,7 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
 }
 
 // The chunk's products.  e: the lane's x entries (16 bytes per word, words 4 *
-// MP entries apart).
+// MP entries apart; of 16 columns, those from 8 on add to the sums of the first 8).
 template <bool MX, bool F16, int MP>
 __device__ __forceinline__ void chunk_products(const Load& l, const uint4* e, float (&acc)[4]) {
   uint32_t sl[2], sh[2], xl = 0, xh = 0;
@@ -147,13 +147,20 @@ __device__ __forceinline__ void chunk_products(const Load& l, const uint4* e, fl
     const uint4 b = e[w * 4 * MP];
     mma<F16>(acc, pl[0], ph[0], pl[1], ph[1], b.x, b.y);
     mma<F16>(acc, pl[2], ph[2], pl[3], ph[3], b.z, b.w);
+    if constexpr (MP > kTokens) {
+      const uint4 c = e[w * 4 * MP + kTokens * 4];
+      mma<F16>(acc, pl[0], ph[0], pl[1], ph[1], c.x, c.y);
+      mma<F16>(acc, pl[2], ph[2], pl[3], ph[3], c.z, c.w);
+    }
   }
 }
 
 // A chunk with MXFP4 groups that f16 cannot hold: plain FP32 dot products of
 // the lane's 32 codes with each token, joined over the 4 lanes of a row and
 // added to the warp's sums in shared memory ([token][row], in x's own scale).
-// back: per token 2^-shift of the entries at e.
+// back: per token 2^-shift of the entries at e.  TERMS == 2: x is the sum of the
+// columns token and token + mp / 2.
+template <int TERMS>
 __device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_t shi, const uint4* e, int mp, int mm,
                                        const float* back, float* sums) {
   const int lane = threadIdx.x & 31, t = lane & 3, gid = lane >> 2;
@@ -167,12 +174,19 @@ __device__ __noinline__ void far_chunk(uint4 lo, uint4 hi, uint32_t slo, uint32_
     for (int w = 0; w < 4; ++w) {
       const uint4 b = e[(w * mp + token) * 4];
       const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+      const uint4 b2 = TERMS == 2 ? e[(w * mp + mp / 2 + token) * 4] : b;
+      const uint32_t u2[4] = {b2.x, b2.y, b2.z, b2.w};
       const uint32_t cl = w == 0 ? lo.x : w == 1 ? lo.y : w == 2 ? lo.z : lo.w;
       const uint32_t ch = w == 0 ? hi.x : w == 1 ? hi.y : w == 2 ? hi.z : hi.w;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[i >> 1]));
-        const float xv = (i & 1 ? p.y : p.x) * f;
+        float xv = i & 1 ? p.y : p.x;
+        if constexpr (TERMS == 2) {
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u2[i >> 1]));
+          xv += i & 1 ? q.y : q.x;
+        }
+        xv *= f;
         dl += e2m1_value(cl >> (4 * i)) * xv;
         dh += e2m1_value(ch >> (4 * i)) * xv;
       }

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) matvec_kernel(const Ma
           }
           const uint4* eh = e + h * (kChunk / 8) * MP;
           if (MX && F16 && mx_far(l))
-            far_chunk(l.lo, l.hi, l.slo, l.shi, eh + t, MP, mm, back_sh + seg * kTokens, mine);
+            far_chunk<1>(l.lo, l.hi, l.slo, l.shi, eh + t, MP, mm, back_sh + seg * kTokens, mine);
           else
             chunk_products<MX, F16, MP>(l, eh + col, acc);
           copy(h);  // into the slot whose values have just been used

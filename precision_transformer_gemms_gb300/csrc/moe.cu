@@ -14,9 +14,11 @@
 // is not resident at once: SMs are not equally fast at memory, and runs handed out as
 // CTAs end even that out.
 //
-// Hidden values enter the second product as f16 times a power of two per vector
-// (the largest in [2^14, 2^15)): 11 significant bits, an eighth of y's own bf16
-// rounding.  Everything else is exact or FP32.
+// Hidden values enter the second product as the sum of two f16 values times a power of
+// two per vector (the largest in [2^14, 2^15)), off by 2^-23 of themselves or 2^-39 of the
+// largest; one f16 would round to 11 bits what the first product left in FP32.  Up to 4
+// tokens the second terms take columns of the MMA that would stand empty, of 8 tokens an
+// MMA of their own on the same decoded weights.  Everything else is exact or FP32.
 //
 // Measured (router, up and down in one graph; in brackets the weights' bytes at the copy
 // bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 115 us (67),
@@ -209,7 +211,7 @@ struct MoeKernelArgs {
   int* arrived;     // [tiles], down; set to 0 by up
   int down_tiles;
   __nv_bfloat16* y;  // [m, rows], down
-  int x_words;      // 16-byte words of a vector in shared memory
+  int x_words;      // 16-byte words of a vector's window in shared memory
 };
 
 // Which experts a launch reads, and for which pairs: entries of up to MP pairs of one
@@ -290,15 +292,28 @@ constexpr int kStepCodes = 2 * kChunk;
 constexpr int kRing = 2;  // steps of a warp on their way
 constexpr int slot_bytes(bool mx) { return 16 * 128 + 16 * (mx ? 8 : 16); }
 
+// Two values as two f16 terms each: what the first leaves of a number goes to the second.
+__device__ __forceinline__ void two_terms(float a, float b, uint32_t& first, uint32_t& second) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(fabsf(f.x) < 0x1p16f ? a - f.x : 0.f, fabsf(f.y) < 0x1p16f ? b - f.y : 0.f);
+  first = *reinterpret_cast<const uint32_t*>(&h);
+  second = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Operand columns of an entry of mp pairs: the first terms of the vectors, then (down) the second ones.
+constexpr int columns_of(bool up, int mp) { return up ? mp : 2 * mp; }
+
 template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs g) {
   constexpr int kStepSlot = slot_bytes(MX), kRingBytes = kRing * kStepSlot;
+  constexpr int C = columns_of(UP, MP);
   extern __shared__ uint4 sx[];
   __shared__ Plan plan;
   __shared__ uint32_t red[2][kWarps];
   __shared__ float back_sh[kTokens];
   constexpr int kSums = MX ? kTokens * 16 : 0;
-  float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * MP);  // of chunks that f16 cannot hold
+  float* sums = reinterpret_cast<float*>(sx + (size_t)g.x_words * C);  // of chunks that f16 cannot hold
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const int gid = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(sums + kWarps * kSums) + warp * kRingBytes;
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
 
   const float tensor = MX ? 1.0f : *g.tensor_scale;
   const int words = g.k >> 3, all_words = chunks * (kChunk / 8);
-  auto place = [&](int c, int i) { return (((i >> 4) * 4 + (i & 3)) * MP + c) * 4 + ((i >> 2) & 3); };
+  auto place = [&](int c, int i) { return (((i >> 4) * 4 + (i & 3)) * C + c) * 4 + ((i >> 2) & 3); };
   float* mine = sums + warp * kSums;
   uint32_t place_at = 0;
   bool f16 = true;
@@ -463,54 +478,17 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
       up_by = __uint_as_float((uint32_t)(127 + __shfl_sync(0xFFFFFFFFu, shift, vec)) << 23);
       if (tid < n) back_sh[tid] = __uint_as_float((uint32_t)(127 - shift) << 23);
     }
-    if (vec < n) {
-#pragma unroll 2
-      for (int i = first; i < all_words; i += step) {
-        uint32_t r[4] = {0, 0, 0, 0};
-        if (i < words) {
-          if constexpr (UP) {
-            const uint4 v = __ldg(xs + i);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-            if (f16) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * up_by, bf16_hi(u[j]) * up_by);
-                r[j] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-            } else {
-              r[0] = __byte_perm(v.x, v.z, 0x5410);
-              r[1] = __byte_perm(v.x, v.z, 0x7632);
-              r[2] = __byte_perm(v.y, v.w, 0x5410);
-              r[3] = __byte_perm(v.y, v.w, 0x7632);
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 v = xs[2 * i + h];
-              const __half2 lo = __floats2half2_rn(__uint_as_float(v.x) * up_by, __uint_as_float(v.y) * up_by);
-              const __half2 hi = __floats2half2_rn(__uint_as_float(v.z) * up_by, __uint_as_float(v.w) * up_by);
-              r[2 * h] = *reinterpret_cast<const uint32_t*>(&lo);
-              r[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&hi);
-            }
-          }
-        }
-        sx[place(vec, i)] = make_uint4(r[0], r[1], r[2], r[3]);
-      }
-    }
-    __syncthreads();
-
-    // ---- the products
-    if (item >= min(end, (entry + 1) * g.tiles)) continue;  // (the tile is of the next entry, or there is none)
+    // The warp's tile, if it is of this entry.
+    const bool has = item < min(end, (entry + 1) * g.tiles);
     const int tile = item - entry * g.tiles;
-    item = end;
-    const int col = min(gid, MP - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
-    const uint4* e = sx + (size_t)step0 * (kStepCodes / 8) * MP;
+    if (has) item = end;
+    const int col = min(gid, C - 1) * 4 + t;  // columns beyond the entry's hold anything: their sums are not stored
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (MX) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) mine[(2 * t + (i & 1)) * 16 + gid + (i >> 1) * 8] = 0.f;  // far_chunk adds to it
     }
-    auto stream = [&](auto f16_path) {
+    auto stream = [&](auto f16_path, const uint4* e, int from, int to) {  // the products of steps from .. to - 1
       constexpr bool F16 = decltype(f16_path)::value;
       auto read = [&](int h, bool tail, int s) {  // chunk h of the step
         Load l;
@@ -525,13 +503,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
       };
       auto products = [&](const Load& l) {
         if (MX && F16 && mx_far(l))
-          far_chunk(l.lo, l.hi, l.slo, l.shi, e + t, MP, n, back_sh, mine);
+          far_chunk<C / MP>(l.lo, l.hi, l.slo, l.shi, e + t, C, n, back_sh, mine);
         else
-          chunk_products<MX, F16, MP>(l, e + col, acc);
-        e += (kChunk / 8) * MP;
+          chunk_products<MX, F16, C>(l, e + col, acc);
+        e += (kChunk / 8) * C;
       };
 #pragma unroll 1
-      for (int s = step0; s < step1; ++s) {
+      for (int s = from; s < to; ++s) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
         __syncwarp();
         const bool tail = (s + 1) * kStepCodes > g.k;
@@ -543,7 +521,62 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
         if (2 * s + 1 < chunks) products(l);
       }
     };
-    if (!UP || f16) stream(std::true_type{}); else stream(std::false_type{});
+    // Window by window of the vectors (up: all of them at once): their values, and the products.
+    for (int w0 = 0;; w0 += g.x_words) {
+      const int w1 = UP ? all_words : min(all_words, w0 + g.x_words);
+      if (vec < n) {
+#pragma unroll 2
+        for (int i = w0 + first; i < w1; i += step) {
+          uint32_t r[4] = {0, 0, 0, 0}, q[4] = {0, 0, 0, 0};
+          if (i < words) {
+            if constexpr (UP) {
+              const uint4 v = __ldg(xs + i);
+              const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+              if (f16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const __half2 h2 = __floats2half2_rn(bf16_lo(u[j]) * up_by, bf16_hi(u[j]) * up_by);
+                  r[j] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+              } else {
+                r[0] = __byte_perm(v.x, v.z, 0x5410);
+                r[1] = __byte_perm(v.x, v.z, 0x7632);
+                r[2] = __byte_perm(v.y, v.w, 0x5410);
+                r[3] = __byte_perm(v.y, v.w, 0x7632);
+              }
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint4 v = xs[2 * i + h];
+                two_terms(__uint_as_float(v.x) * up_by, __uint_as_float(v.y) * up_by, r[2 * h], q[2 * h]);
+                two_terms(__uint_as_float(v.z) * up_by, __uint_as_float(v.w) * up_by, r[2 * h + 1], q[2 * h + 1]);
+              }
+            }
+          }
+          sx[place(vec, i - w0)] = make_uint4(r[0], r[1], r[2], r[3]);
+          if constexpr (!UP) sx[place(vec + MP, i - w0)] = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      }
+      __syncthreads();
+      if (has) {
+        constexpr int kStepWords = kStepCodes / 8;
+        const int from = UP ? step0 : max(step0, w0 / kStepWords), to = UP ? step1 : min(step1, (w1 + kStepWords - 1) / kStepWords);
+        const uint4* e = sx + (size_t)(from - w0 / kStepWords) * kStepWords * C;
+        if (!UP || f16) stream(std::true_type{}, e, from, to); else stream(std::false_type{}, e, from, to);
+      }
+      if (UP || w1 == all_words) break;
+      __syncthreads();  // the window's products are done
+    }
+    if (!has) continue;
+    if constexpr (!UP) {  // the second terms' sums, in other columns
+      if constexpr (MP == 1) {
+        acc[0] += acc[1];
+        acc[2] += acc[3];
+      } else if constexpr (MP < kTokens) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], MP / 2);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = 2 * t + (i & 1);
@@ -607,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) moe_kernel(const MoeKernelArgs
 template <bool MX, int MP, bool UP, bool SPLIT, int CTAS>
 lpq_status launch(const MoeKernelArgs& g, int64_t tiles, cudaStream_t s) {
   auto kernel = moe_kernel<MX, MP, UP, SPLIT, CTAS>;
-  const int smem = g.x_words * 16 * MP + (MX ? kWarps * kTokens * 16 * 4 : 0) + kWarps * kRing * slot_bytes(MX);
+  const int smem = g.x_words * 16 * columns_of(UP, MP) + (MX ? kWarps * kTokens * 16 * 4 : 0) + kWarps * kRing * slot_bytes(MX);
   lpq_status st = set_smem_attr(reinterpret_cast<const void*>(kernel), 200 * 1024);
   if (st != LPQ_OK) return st;
   const int slots = kWarps / g.split;
@@ -621,10 +654,18 @@ double expected_experts(int64_t m, int64_t top, int64_t experts) {
   return (double)experts * (1.0 - std::pow(others, (double)m));
 }
 
+// Most shared memory for a window of the hidden values, whole steps of them.  With 16
+// columns small ones, beside which three CTAs fit an SM (64 tokens, 2 of 8 of 4096 x 1536:
+// 108.5 us with 32 KB, 113.5 with 64; 32 tokens, 2 of 8 of 2048 x 4096 80.9, 85.5 and 88.4
+// with 128); with fewer one window for most sizes, since the warps that share a tile's
+// columns work in different ones (4 tokens, 2 of 8 of 2048 x 8192: 65.8, 59.0 and 57.2).
+constexpr int window_bytes(int columns) { return (columns > kTokens ? 32 : 128) * 1024; }
+
 template <bool MX, int MP, bool UP>
 lpq_status run(MoeKernelArgs& g, cudaStream_t s) {
   const int chunks = (g.k + kChunk - 1) / kChunk;
   g.x_words = chunks * (kChunk / 8);
+  if (!UP) g.x_words = std::min(g.x_words, window_bytes(columns_of(UP, MP)) / (16 * columns_of(UP, MP)));
   // Entries, at most: one for every expert, and for every MP pairs beyond the experts'
   // first ones.  (CTAs without an entry cost a plan each: with one for every pair, 200
   // tokens, 2 of 16 of 2048 x 1024, took 427 us, 223 so.)
