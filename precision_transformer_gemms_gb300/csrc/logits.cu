@@ -21,6 +21,7 @@
 
 #include <algorithm>
 
+#include "logit_runs.h"
 #include "lpq_device.cuh"
 
 namespace lpq {
@@ -44,7 +45,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
   // Word w of the row stands at w + lead, counted from a 16-byte boundary.
   const int lead = VEC == 1 ? 0 : (int)((reinterpret_cast<uintptr_t>(in) & 15u) / sizeof(T));
   const int v = (int)g.v;
-  const int first = (int)(blockIdx.x - row32 * segments) * S - lead;  // word of the run's first place
+  const int first = run_first((int)(blockIdx.x - row32 * segments), S, lead);
 #pragma unroll
   for (int i = 0; i < S / 4; i += kThreads) {
     reinterpret_cast<uint4*>(counts)[i + tid] = make_uint4(0, 0, 0, 0);
@@ -81,13 +82,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
       bits[j] = __funnelshift_r(allowed[a >> 5], allowed[z >> 5], (uint32_t)a & 31u) << (a - w);
     }
   }
-  // The word's place among `count` from `at` on, or -1.  (A word just below 0 may be
-  // given a place in front of the row's first, which nothing reads.)
-  auto place = [&](int64_t word, int at, int count) {
-    const uint64_t p = (uint64_t)word - (uint64_t)(int64_t)at;
-    return p < (uint64_t)count ? (int)p : -1;
-  };
-  const int words = min(S, v - first);
+  const int words = run_words(first, S, v);
 
   // The context's words, and the biases by the last warp.
   const int len = (int)max((int64_t)0, min(n, g.c.max_len));
@@ -123,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
   while (i0 < len) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int at = place(word[j], first, words);
+      const int at = run_place(word[j], first, words);
       if (at < 0) continue;
       if (i0 + j * stride < asked) atomicOr(&counts[at], kSeen); else atomicAdd(&counts[at], 1u);
     }
@@ -132,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
   }
   if (biasing) {
     for (; from < to; load_bias()) {
-      const int at = place(bias_word, first, words);
+      const int at = run_place(bias_word, first, words);
       for (uint32_t left = __ballot_sync(0xFFFFFFFFu, at >= 0); left; left &= left - 1) {  // one after another, in the list's order
         if (lane == __ffs(left) - 1) biases[at] += bias;
         __syncwarp();
@@ -189,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
 template <typename T, int VEC, int NV, int kThreads>
 lpq_status run(const LogitsArgs& g, cudaStream_t s) {
   constexpr int S = kThreads * VEC * NV;
-  const int64_t segments = (g.v + VEC - 1 + S - 1) / S;  // (a row may begin VEC - 1 places in)
+  const int64_t segments = run_count(g.v, VEC, S);
   const int64_t grid = g.rows * segments;
   if (grid > 0x7FFFFFFF) return set_error(LPQ_ERR_SHAPE, "logits: too large");
   const void* kernel = reinterpret_cast<const void*>(adjust_logits_kernel<T, VEC, NV, kThreads>);
