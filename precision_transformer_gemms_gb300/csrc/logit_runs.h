@@ -31,4 +31,7 @@ LPQ_HOST_DEVICE int run_place(int64_t word, int first, int words) {
   return p < (uint64_t)words ? (int)p : -1;
 }
 
+// A control's number of entries or place among `count` of them, whatever it holds.
+LPQ_HOST_DEVICE int64_t within(int64_t n, int64_t count) { return n < 0 ? 0 : n < count ? n : count; }
+
 }  // namespace lpq

@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(kThreads, VEC == 1 ? 3 : kThreads == 256 ? 5 :
   // The context's words, and the biases by the last warp.
   const int len = (int)max((int64_t)0, min(n, g.c.max_len));
   const int asked = (int)max((int64_t)0, min(prompt, (int64_t)len));  // words of the prompt
-  from = max((int64_t)0, from);
-  to = min(to, g.c.bias_count);
+  // Both ends: the last warp's lanes read from + lane at once, which beyond 2^63 would be
+  // in front of the list.
+  from = within(from, g.c.bias_count);
+  to = within(to, g.c.bias_count);
   constexpr int kAhead = 4;  // words of a thread on their way
   constexpr int stride = kThreads;
   int i0 = tid;

@@ -48,3 +48,19 @@ def test_words_outside_the_vocabulary(dt, v, t, n, lead):
     for x in (c["history"], words):
         x[(x < 0) | (x >= v)] = -1
     assert torch.equal(lpq.adjust_logits(logits, **c), got)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_bias_offsets_of_any_size(dt):
+    """Offsets are taken within the list: no bias where a row's begin beyond it or end before they begin."""
+    top, v, t = (1 << 63) - 1, 700, 12
+    logits, c = make(t, v, 20, dt, seed=3)
+    words, values = torch.arange(100, device="cuda"), torch.linspace(1, 3, 100, device="cuda")
+    offsets = [0, top, top - 5, top - 31, 40, -top - 1, 30, 1 << 32, 100, 101, -1, 3, top]
+    c["bias"] = torch.tensor(offsets, device="cuda"), words, values
+    got = lpq.adjust_logits(logits, **c)
+    within = lambda n: min(max(n, 0), 100)
+    for i in range(t):
+        ends = [within(offsets[i]), max(within(offsets[i]), within(offsets[i + 1]))]
+        row = {k: x[i:i + 1] for k, x in c.items() if k != "bias"}
+        check(logits[i:i + 1], {**row, "bias": (torch.tensor(ends, device="cuda"), words, values)}, got[i:i + 1])

@@ -30,23 +30,46 @@ extern "C" int check_row(int v, int lead, int vec, int s, int every) {
   }
   return held == v ? 0 : 4;
 }
+// Entries that lane `lane` of a warp reads of a list of `count` from `from` to `to`, the
+// first and every one of its steps: 0, or 1 where one lies outside the list.
+extern "C" int check_list(int64_t from, int64_t to, int64_t count, int lane) {
+  from = within(from, count), to = within(to, count);
+  for (int step = 0;; ++step) {
+    const uint64_t at = (uint64_t)from + (uint64_t)lane;  // (as the device adds: modulo 2^64)
+    if ((int64_t)at < to && ((int64_t)at < 0 || (int64_t)at >= count)) return 1;
+    if (from >= to) return 0;
+    from += 32;
+  }
+}
 """
 
 
 @pytest.fixture(scope="module")
-def check_row(tmp_path_factory):
+def host(tmp_path_factory):
     folder = tmp_path_factory.mktemp("runs")
     (folder / "runs.cpp").write_text(SOURCE)
     subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I" + build.CSRC, str(folder / "runs.cpp"), "-o",
                     str(folder / "runs.so")], check=True)
-    return ctypes.CDLL(os.path.join(folder, "runs.so")).check_row
+    return ctypes.CDLL(os.path.join(folder, "runs.so"))
 
 
 @pytest.mark.parametrize("vec,s", [(4, 1024), (4, 4096), (4, 8192), (8, 2048), (8, 4096), (8, 8192), (1, 1024), (1, 4096)])
-def test_every_length_and_lead(check_row, vec, s):
+def test_every_length_and_lead(host, vec, s):
     for v in list(range(1, 3 * s + 2 * vec)) + [50174, 50175, 131071, 131072, 131073, (1 << 30) - 1, 1 << 30]:
         near = v % s < 2 * vec or v % s > s - 2 * vec
         if v > 1 << 20 or near or v % 7 == 0:
             for lead in range(vec):
                 every = 1 if near and v < 1 << 20 else 5 if v < 1 << 20 else 1001
-                assert check_row(v, lead, vec, s, every) == 0, (v, lead)
+                assert host.check_row(v, lead, vec, s, every) == 0, (v, lead)
+
+
+@pytest.mark.parametrize("count", [0, 1, 31, 100])
+def test_offsets_beyond_the_list(host, count):
+    top = (1 << 63) - 1
+    ends = [-top - 1, -top, -1000, -1, 0, 1, 31, count - 1, count, count + 1, 1 << 31, 1 << 32, top - 32, top - 31, top - 5, top]
+    i64 = ctypes.c_int64
+    for a in ends:
+        for b in ends:
+            if min(max(b, 0), count) - max(a, 0) < 1 << 20:
+                for lane in (0, 5, 31):
+                    assert host.check_list(i64(a), i64(b), i64(count), lane) == 0, (a, b, lane)
