@@ -598,11 +598,16 @@ def _elsewhere(call, stream, x, *args):
         return call(x, *args)
 
 
+def _frequencies(rotary_dim, base, freqs):
+    """Radians per position of every pair, as the library's array: kept for the numbers
+    that base and freqs hold now."""
+    return _freqs(rotary_dim, float(base), None if freqs is None else tuple(map(float, freqs)))
+
+
 @functools.lru_cache(maxsize=64)
 def _freqs(rotary_dim, base, freqs):
-    """Radians per position of every pair, as the library's array."""
     if freqs is None:
-        freqs = [float(base) ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+        freqs = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
     assert len(freqs) == rotary_dim // 2, f"freqs must hold {rotary_dim // 2} values"
     return (ctypes.c_double * max(1, len(freqs)))(*freqs)
 
@@ -659,7 +664,7 @@ def qk_norm_rope(x, q_heads, k_heads, head_dim, positions, q_weight=None, k_weig
     else:
         ldo = _heads_out(out, x, rows, used, device)
     _check(lib().lpq_qk_norm_rope(x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads, k_heads, head_dim, _ptr(q_weight),
-                                  _ptr(k_weight), w_type, positions.data_ptr(), _freqs(rotary_dim, base, None if freqs is None else tuple(map(float, freqs))), rotary_dim,
+                                  _ptr(k_weight), w_type, positions.data_ptr(), _frequencies(rotary_dim, base, freqs), rotary_dim,
                                   interleaved, eps, out.data_ptr(), ldo, _raw_stream(device)))
     return out
 
@@ -693,7 +698,7 @@ def qk_norm_rope_backward(dy, x, q_heads, k_heads, head_dim, positions, q_weight
         dqp, dkp, wsp = dq.data_ptr(), dk.data_ptr(), ws.data_ptr()
     _check(lib().lpq_qk_norm_rope_backward(dy.data_ptr(), _ld(dy, rows, dy.shape[1]), x.data_ptr(), _ld(x, rows, cols), x_type, rows, q_heads,
                                            k_heads, head_dim, _ptr(q_weight), _ptr(k_weight), w_type, positions.data_ptr(),
-                                           _freqs(rotary_dim, base, None if freqs is None else tuple(map(float, freqs))), rotary_dim, interleaved, eps, out.data_ptr(), ldo,
+                                           _frequencies(rotary_dim, base, freqs), rotary_dim, interleaved, eps, out.data_ptr(), ldo,
                                            dqp, dkp, wsp, need, _raw_stream(device)))
     return out, dq, dk
 
