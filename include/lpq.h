@@ -463,8 +463,8 @@ lpq_status lpq_moe_workspace(int64_t m, int64_t k, int64_t d, int64_t f, size_t 
  *                turned.
  *   y            rows ldy elements apart, same heads; y may be x itself (then
  *                ldy = ldx), else they must not overlap.
- * Angles are reduced modulo a turn in 64 bits: off by at most 2^-26 turns (1e-7
- * radians) and 2^-52 |position freqs[i]|; any int64 position is valid.
+ * Angles are reduced modulo a turn in integers: off by at most 1e-7 radians (they are
+ * rounded to 2^-26 turns) and 2^-52 |position freqs[i]|; any int64 position is valid.
  * Statistics are FP32 and y is rounded once.  head_dim is even, 2 ..
  * 512; rotary_dim even, 0 .. head_dim; any rows, heads >= 0; eps >= 0.  Rows
  * that begin at 16 bytes, with head_dim and rotary_dim multiples of 16 values (FP32:

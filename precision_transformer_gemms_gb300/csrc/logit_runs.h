@@ -3,10 +3,12 @@
 #pragma once
 #include <stdint.h>
 
+#ifndef LPQ_HOST_DEVICE
 #ifdef __CUDACC__
 #define LPQ_HOST_DEVICE __host__ __device__ __forceinline__
 #else
 #define LPQ_HOST_DEVICE inline
+#endif
 #endif
 
 namespace lpq {
