@@ -422,7 +422,7 @@ lpq_status lpq_matvec_adapted_workspace(int64_t m, int64_t rank, size_t *bytes);
  *   probs [m, k] FP32: the softmax over the chosen (renormalize = 1) or over all
  *   (renormalize = 0) at those places.
  * d is a multiple of 8 up to 65536, ldx and ldw multiples of 8, x and w 16-byte
- * aligned; 1 <= k <= 32, k <= experts <= 1024; any m >= 0 (made for few). */
+ * aligned; 1 <= k <= 32, k <= experts <= 1024; 0 <= m <= 2^30 - 4 (made for few). */
 lpq_status lpq_moe_route(const void *x, int64_t ldx, const void *w, int64_t ldw, int64_t m, int64_t d, int64_t experts,
                          int64_t k, int32_t renormalize, int64_t *ids, float *probs, lpq_stream_t stream);
 

@@ -564,7 +564,7 @@ lpq_status lpq_matvec_adapted(const lpq_qview* w, const void* x, int64_t ldx, in
 lpq_status lpq_moe_route(const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t m, int64_t d, int64_t experts, int64_t k,
                          int32_t renormalize, int64_t* ids, float* probs, lpq_stream_t stream) {
   if (renormalize < 0 || renormalize > 1) return set_error(LPQ_ERR_INVALID_ARG, "renormalize %d", renormalize);
-  if (m < 0 || m > (int64_t)1 << 30) return set_error(LPQ_ERR_SHAPE, "m %lld", (long long)m);
+  if (m < 0 || m > kRouteMostTokens) return set_error(LPQ_ERR_SHAPE, "m %lld", (long long)m);
   if (d < 8 || d % 8 || d > 65536) return set_error(LPQ_ERR_SHAPE, "d %lld not a multiple of 8, 8 to 65536", (long long)d);
   if (experts < 1 || experts > kMoeMostExperts) return set_error(LPQ_ERR_SHAPE, "experts %lld, at most %d", (long long)experts, kMoeMostExperts);
   if (k < 1 || k > kMoeMostChoices || k > experts)

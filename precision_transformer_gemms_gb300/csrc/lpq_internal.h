@@ -140,6 +140,7 @@ lpq_status launch_qk_norm_backward(const QkArgs& a, int32_t type, cudaStream_t s
 
 // Mixture-of-experts launchers (moe.cu).  Arguments validated.
 constexpr int kMoeMostExperts = 1024, kMoeMostChoices = 32;
+constexpr int64_t kRouteMostTokens = ((int64_t)1 << 30) - 4;  // 8 CTAs for 4 of them in one grid
 struct RouteArgs {
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
