@@ -11,11 +11,11 @@
 // registers.  Every CTA of a row reads the row's whole context, from the L2.
 //
 // Measured, 64 rows of 131073 FP32 (floor 10.5 us at the copy bandwidth of 6677 GB/s):
-// contexts of up to 1000 words 18.5 us, 8192 24.6, 16384 28, 32768 35; bf16, 4000 words
-// 17.7; 8 rows 4.6; one row of 32000 words 2.1.  What bounds it is the chain of a CTA's
+// contexts of up to 1000 words 18.6 us, 8192 25, 16384 29, 32768 36; bf16, 4000 words
+// 18; 8 rows 4.9; one row of 32000 words 2.1.  What bounds it is the chain of a CTA's
 // loads (lengths, context, counts, then words) and the scan of the context, whose 8192
-// words take a CTA's 512 threads 4 loads each for the 8192 words that it writes;
-// clusters that share the scan through distributed shared memory gained for one row
+// words take a CTA's 512 threads 16 loads each, in four rounds of four, for the 8192
+// words that it writes; clusters that share the scan through distributed shared memory gained for one row
 // with a long context alone.
 #include <cuda_bf16.h>
 

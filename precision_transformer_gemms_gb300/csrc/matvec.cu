@@ -71,15 +71,6 @@ struct MatvecArgs {
   int rank;
 };
 
-// A warp's tile is 16 weight rows: 4 runs of 4 neighbours, 32 apart (rows 32 j
-// + i of a 128-row group, i in a run of 4), whose scales of 4 neighbouring
-// blocks are 64 consecutive bytes of the tensor-core layout.  K is cut into
-// segments by its length alone and a warp sums one segment.  With many tiles a
-// CTA's warps take all segments of a few tiles, with x of all of K in shared
-// memory; with few a cluster of CTAs takes 8 tiles, one segment (and x of it)
-// per CTA, and joins the sums through distributed shared memory.  The segments'
-// sums are added in the same order either way: a row's result does not depend
-// on the number of rows.
 // Row `row` of B_e times the token's inner vector.
 __device__ __forceinline__ float adapter_row(const MatvecArgs& g, int64_t token, int row) {
   const int64_t e = g.index[token];
@@ -155,6 +146,15 @@ __global__ void __launch_bounds__(kInnerThreads) adapter_inner_kernel(const __nv
   }
 }
 
+// A warp's tile is 16 weight rows: 4 runs of 4 neighbours, 32 apart (rows 32 j
+// + i of a 128-row group, i in a run of 4), whose scales of 4 neighbouring
+// blocks are 64 consecutive bytes of the tensor-core layout.  K is cut into
+// segments by its length alone and a warp sums one segment.  With many tiles a
+// CTA's warps take all segments of a few tiles, with x of all of K in shared
+// memory; with few a cluster of CTAs takes 8 tiles, one segment (and x of it)
+// per CTA, and joins the sums through distributed shared memory.  The segments'
+// sums are added in the same order either way: a row's result does not depend
+// on the number of rows.
 // MP: tokens that x's place in shared memory is laid out for (g.m or more).
 // W warps per CTA: 8, four CTAs on an SM while x is small, else 24 that share x.
 template <bool MX, bool SFG, int MP, int W, bool ADAPTED>

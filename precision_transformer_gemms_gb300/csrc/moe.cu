@@ -25,11 +25,14 @@
 // Everything else is exact or FP32.
 //
 // Measured (router, up and down in one graph; in brackets the weights' bytes at the copy
-// bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 115 us (67),
-// MXFP4 121; one token of them 33 (13); 4 tokens, 4 of 32 of 2048 x 768 23 (5.3); 24
-// tokens, 2 of 16 of 2048 x 1024 36 (8.5), 200 tokens 207; 5 tokens, 3 of 21 of 2080 x 992 MXFP4 30
-// (5.6); one token, 2 of 8 of 512 x 384 11.5 (0.1), the three launches whose parts wait
-// for one another.  What bounds the large ones: of an earlier state's 126 us the stream
+// bandwidth of 6677 GB/s): 8 tokens, 8 of 64 experts of 4096 x 1536 NVFP4 117 us (67),
+// MXFP4 124; one token of them 33 (13); 4 tokens, 4 of 32 of 2048 x 768 24 (5.3); 24
+// tokens, 2 of 16 of 2048 x 1024 38 (8.5), 200 tokens 214; 5 tokens, 3 of 21 of 2080 x 992 MXFP4 31
+// (5.6); one token, 2 of 8 of 512 x 384 12 (0.1), the three launches whose parts wait
+// for one another.  The router by itself: 5.8 us for 8 tokens of 64 experts of 4096, of
+// which a choice is 0.25 (4.0 with one choice, 11.6 with 32: each is a pass of one warp over
+// the keys), 5.0 with 512 columns; the rest is a cluster's chain of loads, two barriers
+// and the parts' exchange.  What bounds the large ones: of an earlier state's 126 us the stream
 // without a product took 102, the products without the stream 97 and what a CTA does
 // before and after its tiles 58 by itself (the plan 15, the vectors' conversion 11, the
 // rest launches, the router and the joining of the results); the three overlap in the

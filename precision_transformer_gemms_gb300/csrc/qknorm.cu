@@ -26,10 +26,16 @@
 //             54.6 (89%), 16 of 512 110 (71%)
 //   backward  64 heads of 128 129 us (90%; 4 of it the join of the parts), of 64 132,
 //             32 of 256 135, 8192 tokens FP32 154 (78%: a ring of two), 32 + 8 106 (69%)
-// Heads that are no power of two times 16 leave lanes idle (96 of 80: 118 us, 62%).
-// bf16 that goes in 8-byte vectors: 112 heads of 72 142 us (54%, backward 268), 96 of 80
+// Heads that are no power of two times 16 leave lanes idle (96 of 80: 120 us, 61%).
+// bf16 that goes in 8-byte vectors: 112 heads of 72 145 us (53%, backward 273), 96 of 80
 // with halves of 20 turned 126 (value by value 348, 499 and 302).  What goes value by
-// value (64 of 130: 260 us, 30%; backward 370, 32%) is bound by the count of accesses.
+// value (64 of 130: 260 us, 30%; backward 370, 32%) is bound by the count of accesses;
+// beyond 256 values a head it spills, too (16 of 510 FP32 or bf16: 160 bytes a thread
+// forward, 240 to 280 backward, 205 and 301 us at 8192 tokens).  The vector forms spill 16
+// to 40 bytes a thread backward, those of 8 bytes 8 to 24 forward.
+// Grouped heads lose more backward (40 + 0 heads 87 us, 84%; 24 + 16 92; 32 + 8 106; 36 +
+// 4 123, 59%): warps have equal counts of head groups, and those with the keys set up a
+// token's angles and weights for two groups, or one, where queries have eight.
 #include <cuda_bf16.h>
 
 #include <algorithm>
