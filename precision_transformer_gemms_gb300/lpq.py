@@ -577,10 +577,15 @@ class Adapters:
             "a and b must be contiguous on one CUDA device"
         assert scale is None or (_is_vector(scale, a.shape[0], torch.float32) and scale.get_device() == a.get_device()), \
             f"scale must be {a.shape[0]} fp32"
-        self.a, self.b, self.scale = a, b, scale
-        self.count, self.rank, self.k = a.shape
-        self.rows, self.device = b.shape[1], a.get_device()
-        self.packed = _pack_adapters(a.data_ptr(), b.data_ptr(), 0 if scale is None else scale.data_ptr(), self.count, self.rank)
+        self._held = a, b, scale, *a.shape, b.shape[1], a.get_device()
+
+    # (other tensors make another object: these have been checked)
+    a, b, scale, count, rank, k, rows, device = (property(lambda self, i=i: self._held[i]) for i in range(8))
+
+    def packed(self):
+        """The bytes of the library's view."""
+        a, b, scale, count, rank = self._held[:5]
+        return _pack_adapters(a.data_ptr(), b.data_ptr(), 0 if scale is None else scale.data_ptr(), count, rank)
 
 
 # ----------------------------------------------------------------- around attention
@@ -712,7 +717,7 @@ def _matvec_adapted(x, w, out_fp32, adapters, index, m, k, device):
         f"index must be {m} int64 where x lies"
     need = _workspace("lpq_matvec_adapted_workspace", m, adapters.rank)
     y, ws = _empty((m, w.rows), dtype=_FP32 if out_fp32 else _BF16, device=x.device), _empty(need, dtype=_U8, device=x.device)
-    _check(lib().lpq_matvec_adapted(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), out_fp32, adapters.packed, index.data_ptr(),
+    _check(lib().lpq_matvec_adapted(w.packed_view(), x.data_ptr(), _ld(x, m, k), m, y.data_ptr(), out_fp32, adapters.packed(), index.data_ptr(),
                                     ws.data_ptr(), need, _raw_stream(device)))
     return y
 
