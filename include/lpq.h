@@ -465,7 +465,8 @@ lpq_status lpq_moe_workspace(int64_t m, int64_t k, int64_t d, int64_t f, size_t 
  *                ldy = ldx), else they must not overlap.
  * Angles are reduced modulo a turn in integers: off by at most 1e-7 radians (they are
  * rounded to 2^-26 turns) and 2^-52 |position freqs[i]|; any int64 position is valid.
- * Statistics are FP32 and y is rounded once.  head_dim is even, 2 ..
+ * Statistics are FP32 and y is rounded once: squares beyond that range (values from 2^60
+ * on; with eps = 0 below 2^-60, too) are not those of the formula.  head_dim is even, 2 ..
  * 512; rotary_dim even, 0 .. head_dim; any rows, heads >= 0; eps >= 0.  Rows
  * that begin at 16 bytes, with head_dim and rotary_dim multiples of 16 values (FP32:
  * 8; interleaved: rotary_dim of 4), take 16-byte accesses; bf16 with 8 in place of 16
